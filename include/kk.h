@@ -483,6 +483,128 @@ kk_status kk_hier_select_pool(const uint16_t* A, const uint16_t* M, const uint32
 kk_status kk_coarse_means(const float* vb, int32_t D, int32_t num_pages, const kk_block_table* bt,
                           int32_t group, float* out, cudaStream_t stream);
 
+/*
+ * ---- attention over the paged cache, and eviction by the weight it gives ----
+ *
+ * The blocks a request keeps are read by these calls: attention of one or
+ * several new nodes over the cache (all of it, or the blocks kk_compact_table
+ * listed), the attention weight each cached token received, and the removal
+ * of the tokens that received least. Values are a second paged cache (vc)
+ * with the K cache's type, sizes and page ids; its strides may differ.
+ */
+
+/*
+ * Nodes: the query tokens of each request. Request r owns rows
+ * node_offsets[r] .. node_offsets[r+1] of the query tensor (device int32
+ * [R+1]; NULL: max_nodes rows each, in order); no request has more than
+ * max_nodes (host value, 1..256), and total_nodes bounds every row. A decode
+ * token is one node. Drafted nodes that are not in the cache yet bring their
+ * own Keys and Values (k, v: device, the cache's element type, head h of node
+ * i at k + i*k_stride_node + h*k_stride_head, in elements; 16-byte aligned,
+ * nullable together): node i of a request also attends to its nodes j with
+ * bit j % 32 of mask[i][j / 32] set (device uint32 [total_nodes][ceil(max_nodes
+ * / 32)], rows as the queries'; NULL: every j <= i). Without k, nodes attend to
+ * the cache alone and mask is not read.
+ */
+typedef struct kk_tree {
+  const int32_t* node_offsets;
+  int32_t max_nodes;
+  int32_t total_nodes;
+  const uint32_t* mask;
+  const void* k;
+  const void* v;
+  int64_t k_stride_node, k_stride_head;
+  int64_t v_stride_node, v_stride_head;
+} kk_tree;
+
+/* The blocks of each request that attention reads, as kk_compact_table (or
+ * kk_step_options) writes them: device int32 pages[R][K], logical[R][K],
+ * count[R]; the first count[r] entries of row r. */
+typedef struct kk_selection {
+  const int32_t* pages;
+  const int32_t* logical;
+  const int32_t* count;
+  int32_t K;
+} kk_selection;
+
+/*
+ * kk_tree_attn - attention of every node over its request's cached tokens
+ * (layer `layer`; all seq_lens[r] of them, or with sel the valid tokens of the
+ * selected blocks) and the drafted nodes it may see. For node i and query
+ * head hq, with KV head h = hq / (num_q_heads / num_kv_heads):
+ *   s_t = scale * q . k_t,  lse = log sum_t e^{s_t},  out = sum_t e^{s_t - lse} v_t
+ * q: device, the cache's element type, head hq of node i at q + i*q_stride_node
+ * + hq*q_stride_head (elements; 16-byte aligned, strides multiples of 16
+ * bytes). out: device [total_nodes][num_q_heads][D] of the cache's type; lse:
+ * nullable device float [total_nodes][num_q_heads]. A node that sees no token
+ * gets 0 and -inf. Tokens past seq_lens[r] and drafted nodes a node does not
+ * see take no part, whatever those places hold. Sums and the softmax are
+ * float32; on bf16 caches the weights are rounded to bf16 before they multiply
+ * the Values. num_q_heads is a multiple of num_kv_heads; scale is finite.
+ * workspace: device, 256-byte aligned, of kk_tree_attn_workspace_bytes(); no
+ * initial contents; calls that may run at once need separate ones. The same
+ * call gives the same bits.
+ */
+size_t kk_tree_attn_workspace_bytes(const kk_kcache_desc* kc, const kk_block_table* bt, int32_t max_nodes,
+                                    int32_t num_q_heads);
+kk_status kk_tree_attn(const kk_kcache_desc* kc, const kk_kcache_desc* vc, const kk_block_table* bt, int32_t layer,
+                       const kk_selection* sel, const kk_tree* tree, const void* q, int64_t q_stride_node,
+                       int64_t q_stride_head, int32_t num_q_heads, float scale, void* out, float* lse,
+                       void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * kk_attn_mass - the attention weight every cached token received from a set
+ * of nodes, added to what it had. The weights live with the pages: device
+ * float [num_layers][num_pages][num_kv_heads][block_size]. For token t of
+ * request r, at page p and slot o, and every KV head h:
+ *   out[layer][p][h][o] = decay * (t < old_lens[r] ? in[layer][p][h][o] : 0)
+ *       + sum_i w_i * sum_{hq of h} [t < row_lens[i]] * e^{scale * q_i,hq . k_t - lse_i,hq}
+ * over the request's nodes i (tree: offsets and counts; its mask, k and v are
+ * not read), with q as in kk_tree_attn and lse as it wrote it. row_w: nullable
+ * device float [total_nodes] (1; nodes of weight 0, such as drafts that were
+ * rejected, take no part); row_lens: nullable device int32 [total_nodes] (all
+ * the request's tokens; for causal rows that are in the cache themselves);
+ * old_lens: nullable device int32 [R] (all): tokens from there on are new and
+ * had nothing. mass_in: nullable (nothing), may be mass_out. Only the slots of
+ * the requests' tokens are written. Nodes with lse -inf add nothing. No page
+ * may be in two requests' tables.
+ */
+kk_status kk_attn_mass(const kk_kcache_desc* kc, const kk_block_table* bt, int32_t layer, const kk_tree* tree,
+                       const void* q, int64_t q_stride_node, int64_t q_stride_head, int32_t num_q_heads, float scale,
+                       const float* lse, const float* row_w, const int32_t* row_lens, const int32_t* old_lens,
+                       float decay, const float* mass_in, float* mass_out, cudaStream_t stream);
+
+/*
+ * kk_evict_select - the tokens of every (request, layer, KV head) to keep:
+ * all of them when seq_lens[r] <= keep; else the first `sinks`, the last
+ * `recent`, and the keep - sinks - recent of the others with the largest
+ * weight (mass as kk_attn_mass writes it; equal weights to the lower index,
+ * -0 equals +0, NaN below everything). kept: device int32 [R][L][H][keep],
+ * token indices in ascending order, -1 past min(keep, seq_lens[r]), which also
+ * goes to new_lens[r] (nullable device int32 [R]). keep >= 1, sinks >= 0,
+ * recent >= 0, sinks + recent <= keep. kc gives the sizes (its base is not
+ * read).
+ */
+kk_status kk_evict_select(const kk_kcache_desc* kc, const kk_block_table* bt, const float* mass, int32_t sinks,
+                          int32_t recent, int32_t keep, int32_t* kept, int32_t* new_lens, cudaStream_t stream);
+
+/*
+ * kk_evict_compact - slot i of every (request, layer, KV head) becomes token
+ * kept[r][l][h][i], i < min(keep, seq_lens[r]), in both caches (vc nullable)
+ * and in the weights (mass_in / mass_out nullable together; they may be the
+ * same). Slot i is in block i / block_size of dst_pages[r] (device int32
+ * [R][ceil(keep / block_size)]; pages of no table of the call, and of no other
+ * request), or, with dst_pages NULL, of the request's own table: in place, for
+ * which kept must ascend in every row, as kk_evict_select writes it. Other
+ * slots keep what they held. The order of the tokens stays, so the last W
+ * slots are still the newest tokens as long as W <= recent. The caller then
+ * shortens its table to ceil(new_lens[r] / block_size) blocks (and pools them
+ * again: v_b of a compacted block is kk_pool_blocks').
+ */
+kk_status kk_evict_compact(const kk_kcache_desc* kc, const kk_kcache_desc* vc, const kk_block_table* bt,
+                           const int32_t* kept, int32_t keep, const float* mass_in, float* mass_out,
+                           const int32_t* dst_pages, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

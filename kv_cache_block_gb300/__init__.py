@@ -12,7 +12,8 @@ _BINDING = (
     "kk_head_variance", "kk_head_variance_workspace_bytes", "kk_pool_blocks", "kk_pool_blocks_weighted", "kk_pool_blocks_weighted_static",
     "kk_score", "kk_score_pool_batched", "kk_score_pool_batched_workspace_bytes", "kk_score_topk",
     "kk_select_step", "kk_topk", "AnchorRing", "kk_anchor_ring_fill", "kk_append_tokens",
-    "kk_select_step_workspace_bytes",
+    "kk_select_step_workspace_bytes", "Tree", "Selection", "kk_tree_attn", "kk_tree_attn_workspace_bytes",
+    "kk_attn_mass", "kk_evict_select", "kk_evict_compact",
 )
 __all__ = ["kk", *_BINDING]
 

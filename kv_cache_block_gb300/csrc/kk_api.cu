@@ -95,6 +95,11 @@ VarWorkspace carve(void* ws, int LH, int D, long long total_blocks) {
 
 }  // namespace
 
+namespace kk {
+kk_status check_kcache_desc(const kk_kcache_desc* kc, KCache* out) { return check_kcache(kc, out); }
+kk_status check_block_table(const kk_block_table* bt, Table* out) { return check_table(bt, true, out); }
+}  // namespace kk
+
 extern "C" {
 
 kk_status kk_debug_set_wait_limit(uint64_t ns) {

@@ -1,0 +1,326 @@
+// Attention of drafted nodes (one node: a decode token) over a paged cache,
+//   out = sum_t e^(s_t - lse) v_t,  s_t = scale * q . k_t,  lse = log sum_t e^s_t
+// over the cached tokens (or those of the selected blocks, "Key-Key Semantic
+// Affinity" page §5.2 step 4: only they are loaded) and the drafted nodes a
+// node may see. One pass over the tokens with a running maximum and sum per
+// row; the work division is kk_attn.cuh's.
+//  * attn_simt_kernel: float32 products on the CUDA cores;
+//  * attn_combine_kernel: adds up the parts of the items that were cut.
+#include "kk_attn.cuh"
+#include "kk_pdl.cuh"
+
+namespace kk {
+namespace {
+
+constexpr int kSimtThreads = 128;
+constexpr int kSimtM = 8;     // query rows per item
+constexpr int kSimtTK = 128;  // tokens per unit: 32 per warp
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const AttnArgs a) {
+  constexpr int EPV = Vec16<T>::kElems;
+  constexpr int ES = elem_bytes<T>();
+  constexpr int M = kSimtM, DL = D / 32;
+  __shared__ __align__(16) float s_q[M][D];
+  __shared__ __align__(16) float s_p[4][32][M];
+  __shared__ __align__(16) float s_o[4][M][D];
+  __shared__ float s_m[4][M], s_l[4][M];
+  __shared__ long long s_place[kSimtThreads / 32 + 4];
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  pdl_launch_dependents();
+  const AttnPlace pl = find_place<kSimtThreads>(a, blockIdx.x, M, kSimtTK, s_place, tid);
+  int r = pl.r;
+  long long base = pl.base;
+  for (long long u = pl.u0; u < pl.u1;) {
+    const AttnReq rq = load_req(a, r, M, kSimtTK, false);
+    const long long units = req_units(a, rq);
+    if (u >= base + units) {
+      base += units;
+      ++r;
+      continue;
+    }
+    const int item = (int)((u - base) / rq.tiles);
+    const int t0 = (int)((u - base) - (long long)item * rq.tiles);
+    const int t1 = (int)min((long long)rq.tiles, t0 + (pl.u1 - u));
+    const int h = item / rq.mt, row0 = (item - h * rq.mt) * M;
+    const int rows = min(M, rq.n * a.G - row0);
+    for (int i = tid; i < M * D; i += kSimtThreads) {
+      const int m = i / D, d = i - m * D, row = row0 + m;
+      float x = 0.f;
+      if (m < rows) {
+        const long long at = (rq.node0 + row / a.G) * a.q_sn + (long long)(h * a.G + row % a.G) * a.q_sh + d;
+        x = ES == 4 ? static_cast<const float*>(a.q)[at]
+                    : __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.q)[at] << 16);
+      }
+      s_q[m][d] = x;
+    }
+    __syncthreads();
+    float m_run[M], l_run[M], o[M][DL];
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      m_run[i] = -INFINITY;
+      l_run[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < DL; ++e) o[i][e] = 0.f;
+    }
+    for (int t = t0; t < t1; ++t) {
+      const bool draft = t >= rq.tiles_c;
+      const char *kp = nullptr, *vp = nullptr;
+      bool ok;
+      uint32_t vis = (1u << M) - 1u;  // rows that may see this lane's token
+      if (!draft) {
+        TokenAt at;
+        ok = token_at(a, r, rq, t * kSimtTK + tid, true, &at);
+        kp = static_cast<const char*>(a.kc.base) +
+             (a.layer * a.kc.sL + at.page * a.kc.sP + h * a.kc.sH + at.tok * a.kc.sT) * ES;
+        vp = static_cast<const char*>(a.vc.base) +
+             (a.layer * a.vc.sL + at.page * a.vc.sP + h * a.vc.sH + at.tok * a.vc.sT) * ES;
+      } else {
+        const int j = (t - rq.tiles_c) * kSimtTK + tid;
+        ok = a.dk && j < rq.n;
+        if (ok) {
+          kp = static_cast<const char*>(a.dk) + ((rq.node0 + j) * a.dk_sn + h * a.dk_sh) * ES;
+          vp = static_cast<const char*>(a.dv) + ((rq.node0 + j) * a.dv_sn + h * a.dv_sh) * ES;
+          vis = 0;
+          for (int i = 0; i < rows; ++i) vis |= sees(a, rq, (row0 + i) / a.G, j) ? 1u << i : 0u;
+        }
+      }
+      float s[M];
+#pragma unroll
+      for (int i = 0; i < M; ++i) s[i] = 0.f;
+      if (ok) {
+#pragma unroll 4
+        for (int c = 0; c < D / EPV; ++c) {
+          float k[EPV];
+          Vec16<T>::unpack(*reinterpret_cast<const uint4*>(kp + c * 16), k);
+#pragma unroll
+          for (int i = 0; i < M; ++i)
+#pragma unroll
+            for (int e = 0; e < EPV; e += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(&s_q[i][c * EPV + e]);
+              s[i] += k[e] * x.x;
+              s[i] += k[e + 1] * x.y;
+              s[i] += k[e + 2] * x.z;
+              s[i] += k[e + 3] * x.w;
+            }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < M; ++i) {
+        // selected, not added: what a hidden place holds (NaN, infinity) never enters
+        s[i] = (ok && ((vis >> i) & 1u)) ? s[i] * a.scale_log2 : -INFINITY;
+        float mx = s[i];
+#pragma unroll
+        for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
+        const float m_new = fmaxf(m_run[i], mx), ref = m_new == -INFINITY ? 0.f : m_new;
+        const float p = exp2f(s[i] - ref), al = exp2f(m_run[i] - ref);
+        m_run[i] = m_new;
+        l_run[i] = l_run[i] * al + p;  // this lane's share of the sum
+#pragma unroll
+        for (int e = 0; e < DL; ++e) o[i][e] *= al;
+        s_p[w][lane][i] = p;
+      }
+      __syncwarp();
+      const uint32_t live = __ballot_sync(kFull, ok);
+      for (uint32_t left = live; left; left &= left - 1) {
+        const int k = __ffs(left) - 1;
+        const char* v = reinterpret_cast<const char*>(__shfl_sync(kFull, (unsigned long long)vp, k));
+        float x[DL];
+#pragma unroll
+        for (int e = 0; e < DL; ++e)
+          x[e] = ES == 4 ? reinterpret_cast<const float*>(v)[lane * DL + e]
+                         : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(v)[lane * DL + e] << 16);
+        float pr[M];
+#pragma unroll
+        for (int i = 0; i < M; i += 4)
+          *reinterpret_cast<float4*>(&pr[i]) = *reinterpret_cast<const float4*>(&s_p[w][k][i]);
+        if (!draft) {
+#pragma unroll
+          for (int i = 0; i < M; ++i)
+#pragma unroll
+            for (int e = 0; e < DL; ++e) o[i][e] += pr[i] * x[e];
+        } else {  // a node hidden from some rows may hold anything
+          const uint32_t vk = __shfl_sync(kFull, vis, k);
+#pragma unroll
+          for (int i = 0; i < M; ++i)
+            if ((vk >> i) & 1u)
+#pragma unroll
+              for (int e = 0; e < DL; ++e) o[i][e] += pr[i] * x[e];
+        }
+      }
+      __syncwarp();
+    }
+    // the four warps' shares of the item
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      float l = l_run[i];
+#pragma unroll
+      for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(kFull, l, x);
+      if (lane == 0) {
+        s_m[w][i] = m_run[i];
+        s_l[w][i] = l;
+      }
+#pragma unroll
+      for (int e = 0; e < DL; ++e) s_o[w][i][lane * DL + e] = o[i][e];
+    }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == rq.tiles;
+    float* part = partial_slot(a, blockIdx.x, u == pl.u0 ? 0 : 1, M, D);
+    for (int i = tid; i < rows * D; i += kSimtThreads) {
+      const int m = i / D, d = i - m * D;
+      float mm = s_m[0][m];
+      for (int x = 1; x < 4; ++x) mm = fmaxf(mm, s_m[x][m]);
+      const float ref = mm == -INFINITY ? 0.f : mm;
+      float l = 0.f, acc = 0.f;
+      for (int x = 0; x < 4; ++x) {
+        const float al = exp2f(s_m[x][m] - ref);
+        l += s_l[x][m] * al;
+        acc += s_o[x][m][d] * al;
+      }
+      if (whole) {
+        const int row = row0 + m;
+        const long long at = (long long)(rq.node0 + row / a.G) * a.Hq + h * a.G + row % a.G;
+        store_elem<T>(a.out, at * D + d, acc * row_inv(l));
+        if (d == 0 && a.lse) a.lse[at] = row_lse(mm, l);
+      } else {
+        part[i] = acc;
+        if (d == 0) {
+          part[M * D + m] = mm;
+          part[M * D + M + m] = l;
+        }
+      }
+    }
+    __syncthreads();
+    u += t1 - t0;
+  }
+}
+
+// Block (item slot, row chunk): the rows of one item's partial results, added
+// up in CTA order. Whole items were written by the main kernel.
+constexpr int kCombineThreads = 128;
+constexpr int kCombineRows = 8;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const AttnArgs a, int M, int TK, int mt_max) {
+  __shared__ long long s_sum[2][kCombineThreads / 32];
+  const int tid = threadIdx.x;
+  const int mt = blockIdx.x % mt_max, h = (blockIdx.x / mt_max) % a.kc.H, r = blockIdx.x / (mt_max * a.kc.H);
+  const AttnReq rq = load_req(a, r, M, TK, false);
+  const int row0 = mt * M + blockIdx.y * kCombineRows, rows = min(kCombineRows, rq.n * a.G - row0);
+  const bool mine = mt < rq.mt && rows > 0;
+  long long before = 0, all = 0;
+  if (mine)
+    for (int i = tid; i < a.bt.R; i += kCombineThreads) {
+      const long long n = req_units(a, load_req(a, i, M, TK, false));
+      all += n;
+      if (i < r) before += n;
+    }
+#pragma unroll
+  for (int x = 16; x; x >>= 1) {
+    all += __shfl_xor_sync(kFull, all, x);
+    before += __shfl_xor_sync(kFull, before, x);
+  }
+  if ((tid & 31) == 0) {
+    s_sum[0][tid >> 5] = before;
+    s_sum[1][tid >> 5] = all;
+  }
+  __syncthreads();
+  if (!mine) return;
+  before = all = 0;
+  for (int x = 0; x < kCombineThreads / 32; ++x) {
+    before += s_sum[0][x];
+    all += s_sum[1][x];
+  }
+  const long long lo = before + (long long)(h * rq.mt + mt) * rq.tiles, hi = lo + rq.tiles - 1;
+  const int c0 = (int)(((lo + 1) * a.grid - 1) / all), c1 = (int)(((hi + 1) * a.grid - 1) / all);
+  if (c0 == c1) return;
+  pdl_wait();
+  constexpr int L = D / 4 < 32 ? D / 4 : 32;  // lanes of a row
+  constexpr int V = D / (4 * L);              // float4 of a lane
+  const int sub = tid / L, ln = tid % L;
+  const int first = (long long)c0 * all / a.grid == lo ? 0 : 1;  // c0's slot: its first item, or its last
+  for (int i = sub; i < rows; i += kCombineThreads / L) {
+    const int m = row0 + i - mt * M;
+    float mm = -INFINITY;
+    for (int c = c0; c <= c1; ++c) {
+      if ((long long)c * all / a.grid == (long long)(c + 1) * all / a.grid) continue;  // no units
+      mm = fmaxf(mm, partial_slot(a, c, c == c0 ? first : 0, M, D)[M * D + m]);
+    }
+    const float ref = mm == -INFINITY ? 0.f : mm;
+    float l = 0.f;
+    float4 acc[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+      if ((long long)c * all / a.grid == (long long)(c + 1) * all / a.grid) continue;
+      const float* part = partial_slot(a, c, c == c0 ? first : 0, M, D);
+      const float al = exp2f(part[M * D + m] - ref);
+      l += part[M * D + M + m] * al;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float4 x = *reinterpret_cast<const float4*>(part + m * D + (e * L + ln) * 4);
+        acc[e].x += x.x * al;
+        acc[e].y += x.y * al;
+        acc[e].z += x.z * al;
+        acc[e].w += x.w * al;
+      }
+    }
+    const float inv = row_inv(l);
+    const int row = row0 + i;
+    const long long at = (long long)(rq.node0 + row / a.G) * a.Hq + h * a.G + row % a.G;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const long long d = at * D + (e * L + ln) * 4;
+      store_elem<T>(a.out, d, acc[e].x * inv);
+      store_elem<T>(a.out, d + 1, acc[e].y * inv);
+      store_elem<T>(a.out, d + 2, acc[e].z * inv);
+      store_elem<T>(a.out, d + 3, acc[e].w * inv);
+    }
+    if (ln == 0 && a.lse) a.lse[at] = row_lse(mm, l);
+  }
+}
+
+template <typename T, int D>
+cudaError_t combine_t(const AttnArgs& a, int M, int TK, cudaStream_t s) {
+  const int mt_max = (int)(((long long)a.max_nodes * a.G + M - 1) / M);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.bt.R * a.kc.H * mt_max), (unsigned)((M + kCombineRows - 1) / kCombineRows));
+  cfg.blockDim = dim3(kCombineThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, D>, a, M, TK, mt_max);
+}
+
+template <typename T, int D>
+cudaError_t simt_t(AttnArgs a, cudaStream_t s) {
+  a.grid = attn_grid(a.kc, a.max_nodes, a.G);
+  attn_simt_kernel<T, D><<<a.grid, kSimtThreads, 0, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? combine_t<T, D>(a, kSimtM, kSimtTK, s) : e;
+}
+
+}  // namespace
+
+int attn_grid(const KCache&, int, int) { return sm_count() * 4; }
+
+size_t attn_workspace_bytes(const KCache& kc, int max_nodes, int G) {
+  return (size_t)attn_grid(kc, max_nodes, G) * 2 * kSimtM * (kc.D + 2) * sizeof(float);
+}
+
+cudaError_t launch_tree_attn(const AttnArgs& a, cudaStream_t s) {
+  const bool bf = a.kc.dtype == 1;
+  switch (a.kc.D) {
+    case 32: return bf ? simt_t<bf16_t, 32>(a, s) : simt_t<float, 32>(a, s);
+    case 64: return bf ? simt_t<bf16_t, 64>(a, s) : simt_t<float, 64>(a, s);
+    case 128: return bf ? simt_t<bf16_t, 128>(a, s) : simt_t<float, 128>(a, s);
+    case 256: return bf ? simt_t<bf16_t, 256>(a, s) : cudaErrorNotSupported;
+  }
+  return cudaErrorNotSupported;
+}
+
+}  // namespace kk

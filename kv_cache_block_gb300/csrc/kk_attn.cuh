@@ -1,0 +1,218 @@
+// Work division shared by the attention kernels over a paged cache.
+//
+// A query row of request r and KV head h is (node i, query head h*G + g) at
+// row i*G + g; rows are taken in tiles of M. An item is (r, h, row tile); its
+// tokens are cut into tiles of TK: those of the cached tokens first, then those
+// of the drafted nodes. Each (item, tile) is one unit of work, numbered request
+// by request, and CTA c of the grid takes the units [c*total/G, (c+1)*total/G):
+// the SMs stay level whatever the lengths are, without any work list from the
+// host. An item inside one CTA's range is written out by that CTA; an item
+// that ranges cut leaves one partial result per CTA (running maximum, sum and
+// accumulator) in the workspace, at most two per CTA (its first and its last
+// item), which the combine kernel adds up in CTA order: the same split gives
+// the same bits.
+#pragma once
+#include "kk_device.cuh"
+
+namespace kk {
+
+struct AttnArgs {
+  KCache kc, vc;
+  Table bt;
+  int layer;
+  const int* sel_pages;  // selected blocks (nullable): [R][selK]
+  const int* sel_logical;
+  const int* sel_count;
+  int selK;
+  const int* node_off;  // [R+1], or null: max_nodes of every request
+  int max_nodes, total_nodes;
+  const uint32_t* mask;  // [total_nodes][mask_words], or null: j <= i
+  int mask_words;
+  const void *dk, *dv;  // drafted Keys and Values (nullable)
+  long long dk_sn, dk_sh, dv_sn, dv_sh;
+  const void* q;
+  long long q_sn, q_sh;
+  int Hq, G;
+  float scale_log2;  // scale * log2(e)
+  void* out;         // [total_nodes][Hq][D]
+  float* lse;        // [total_nodes][Hq] or null
+  float* ws;
+  int grid;  // CTAs of the main kernel
+  // attention mass only
+  const float* row_w;
+  const int* row_lens;
+  const int* old_lens;
+  float decay;
+  const float* mass_in;
+  float* mass_out;
+  unsigned long long wait_ns;
+  int* err;
+};
+
+struct AttnReq {
+  int node0, n;      // first node, nodes
+  int off, T;        // table start, cached tokens
+  int ctx;           // token slots to visit: T, or block_size * selected blocks
+  int mt;            // row tiles
+  int tiles_c, tiles;  // token tiles: cached, all (at least 1 when there are nodes)
+};
+
+// Request r's sizes; bad metadata leaves it without cached tokens (or nodes).
+__device__ __forceinline__ AttnReq load_req(const AttnArgs& a, int r, int M, int TK, bool report) {
+  AttnReq q;
+  bool ok = true;
+  q.node0 = a.node_off ? a.node_off[r] : r * a.max_nodes;
+  const int n1 = a.node_off ? a.node_off[r + 1] : q.node0 + a.max_nodes;
+  q.n = n1 - q.node0;
+  if (q.node0 < 0 || n1 > a.total_nodes || q.n < 0 || q.n > a.max_nodes) {
+    ok = false;
+    q.n = 0;
+    q.node0 = 0;
+  }
+  q.off = a.bt.offsets[r];
+  const int nb = a.bt.offsets[r + 1] - q.off;
+  q.T = a.bt.seq_lens[r];
+  if (q.T < 0 || nb < 0 || nb > a.bt.max_blocks || nb != (int)(((long long)q.T + a.kc.bs - 1) / a.kc.bs)) {
+    ok = false;
+    q.T = 0;
+  }
+  long long ctx = q.T;
+  if (a.sel_pages) {
+    const int c = a.sel_count[r];
+    if (c < 0 || c > a.selK) ok = false;
+    ctx = (c < 0 || c > a.selK || q.T == 0) ? 0 : (long long)c * a.kc.bs;
+    if (ctx > 0x7FFFFF00ll) {
+      ok = false;
+      ctx = 0;
+    }
+  }
+  q.ctx = (int)ctx;
+  q.mt = (q.n * a.G + M - 1) / M;
+  q.tiles_c = (int)((ctx + TK - 1) / TK);
+  q.tiles = q.tiles_c + (a.dk ? (q.n + TK - 1) / TK : 0);
+  if (q.tiles == 0) q.tiles = 1;
+  if (a.mass_out) {  // attention mass: the unit is a token tile of one KV head, whatever its rows
+    q.mt = 1;
+    q.tiles = q.tiles_c;
+  }
+  if (report && !ok) flag_error(a.err, kErrBadIndex);
+  return q;
+}
+__device__ __forceinline__ long long req_units(const AttnArgs& a, const AttnReq& q) {
+  return (long long)a.kc.H * q.mt * q.tiles;
+}
+
+// Element offset (without head and layer) of token slot v of a request in the
+// K and V caches; false when the slot holds no valid token. `report`: tell
+// a page out of range.
+struct TokenAt {
+  int page, tok;
+};
+__device__ __forceinline__ bool token_at(const AttnArgs& a, int r, const AttnReq& q, int v, bool report, TokenAt* t) {
+  t->page = 0;
+  t->tok = 0;
+  if (v >= q.ctx) return false;
+  const int bs = a.kc.bs, b = v / bs, o = v - b * bs;
+  int page;
+  if (a.sel_pages) {
+    const int logical = a.sel_logical[(long long)r * a.selK + b];
+    page = a.sel_pages[(long long)r * a.selK + b];
+    if (logical < 0 || (long long)logical * bs >= q.T) {
+      if (report) flag_error(a.err, kErrBadIndex);
+      return false;
+    }
+    if ((long long)logical * bs + o >= q.T) return false;
+  } else {
+    page = a.bt.pages[q.off + b];
+  }
+  if (page < 0 || page >= a.kc.num_pages) {
+    if (report) flag_error(a.err, kErrBadIndex);
+    return false;
+  }
+  t->page = page;
+  t->tok = o;
+  return true;
+}
+
+// A CTA's place in the work: request `r` whose units start at `base`, and the
+// range [u0, u1) of all units. Called by NT threads (a multiple of 32, at most
+// 1024); `sh` is NT/32 + 4 long longs of shared memory.
+struct AttnPlace {
+  long long u0, u1, total, base;
+  int r;
+};
+template <int NT>
+__device__ __forceinline__ AttnPlace find_place(const AttnArgs& a, int cta, int M, int TK, long long* sh, int tid) {
+  const int R = a.bt.R, per = (R + NT - 1) / NT;
+  const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) mine += req_units(a, load_req(a, r, M, TK, cta == 0));
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(kFull, incl, o);
+    if ((tid & 31) >= o) incl += x;
+  }
+  if ((tid & 31) == 31) sh[tid >> 5] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < (tid >> 5)) before += sh[w];
+    total += sh[w];
+  }
+  long long lo = before + incl - mine;
+  AttnPlace p;
+  p.total = total;
+  p.u0 = (long long)cta * total / a.grid;
+  p.u1 = (long long)(cta + 1) * total / a.grid;
+  long long* found = sh + NT / 32;
+  if (p.u0 < p.u1 && lo <= p.u0 && p.u0 < lo + mine) {
+    int r = r0;
+    for (; r < r1; ++r) {
+      const long long n = req_units(a, load_req(a, r, M, TK, false));
+      if (p.u0 < lo + n) break;
+      lo += n;
+    }
+    found[0] = r;
+    found[1] = lo;
+  }
+  __syncthreads();
+  p.r = p.u0 < p.u1 ? (int)found[0] : 0;
+  p.base = p.u0 < p.u1 ? found[1] : 0;
+  __syncthreads();
+  return p;
+}
+
+// Partial results: slot s (two per CTA) holds M*D accumulators, then M running
+// maxima (log2 domain) and M sums.
+__device__ __forceinline__ float* partial_slot(const AttnArgs& a, int cta, int which, int M, int D) {
+  return a.ws + (size_t)(2 * cta + which) * M * (D + 2);
+}
+
+// 1 / sum and lse of a row with running maximum m (log2 domain) and sum l; a
+// row that saw nothing is 0 with lse -inf.
+__device__ __forceinline__ float row_inv(float l) { return l > 0.f || l != l ? 1.f / l : 0.f; }
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_elem(void* p, long long i, float v);
+template <>
+__device__ __forceinline__ void store_elem<float>(void* p, long long i, float v) {
+  static_cast<float*>(p)[i] = v;
+}
+template <>
+__device__ __forceinline__ void store_elem<bf16_t>(void* p, long long i, float v) {
+  uint16_t h;  // one rounding to nearest, the cache's own type
+  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
+  static_cast<uint16_t*>(p)[i] = h;
+}
+
+// Whether node i may see drafted node j (both inside the request).
+__device__ __forceinline__ bool sees(const AttnArgs& a, const AttnReq& q, int i, int j) {
+  if (!a.mask) return j <= i;
+  return (a.mask[(long long)(q.node0 + i) * a.mask_words + (j >> 5)] >> (j & 31)) & 1u;
+}
+
+}  // namespace kk

@@ -197,6 +197,22 @@ int* device_error_word();
 unsigned long long wait_limit_ns();
 long long take_skip_box();
 
+// kk_attn.cu: attention of drafted nodes over the paged cache (AttnArgs:
+// kk_attn.cuh). The workspace holds two partial results per CTA of the grid.
+struct AttnArgs;
+int attn_grid(const KCache& kc, int max_nodes, int G);
+size_t attn_workspace_bytes(const KCache& kc, int max_nodes, int G);
+cudaError_t launch_tree_attn(const AttnArgs& a, cudaStream_t s);
+// kk_mass.cu: the attention weight every cached token received
+cudaError_t launch_attn_mass(const AttnArgs& a, cudaStream_t s);
+// kk_evict.cu: the tokens to keep by that weight, and their move
+constexpr int kMaxNodes = 256;  // drafted nodes of a request
+cudaError_t launch_evict_select(const KCache& kc, const Table& bt, const float* mass, int sinks, int recent, int keep,
+                                int* kept, int* new_lens, int* err, cudaStream_t s);
+cudaError_t launch_evict_compact(const KCache& kc, const KCache& vc, const Table& bt, const int* kept, int keep,
+                                 const float* mass_in, float* mass_out, const int* dst_pages, int* err,
+                                 cudaStream_t s);
+
 // kk_coarse.cu
 cudaError_t launch_coarse(const float* vb, int D, int num_pages, const Table& bt, int group,
                           float* out, int* err, cudaStream_t s);

@@ -64,6 +64,18 @@ class kk_step_options(ctypes.Structure):
                 ("sel_pages", ctypes.c_void_p), ("sel_logical", ctypes.c_void_p), ("sel_count", ctypes.c_void_p)]
 
 
+class kk_tree(ctypes.Structure):
+    _fields_ = [("node_offsets", ctypes.c_void_p), ("max_nodes", ctypes.c_int32), ("total_nodes", ctypes.c_int32),
+                ("mask", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_stride_node", ctypes.c_int64), ("k_stride_head", ctypes.c_int64),
+                ("v_stride_node", ctypes.c_int64), ("v_stride_head", ctypes.c_int64)]
+
+
+class kk_selection(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("logical", ctypes.c_void_p), ("count", ctypes.c_void_p),
+                ("K", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m kv_cache_block_gb300.build`")
@@ -71,6 +83,7 @@ def _load():
     P, I32, I64, SZ, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     KC, BT = ctypes.POINTER(kk_kcache_desc), ctypes.POINTER(kk_block_table)
     RG, OP = ctypes.POINTER(kk_anchor_ring), ctypes.POINTER(kk_step_options)
+    TR, SL = ctypes.POINTER(kk_tree), ctypes.POINTER(kk_selection)
     sig = {
         "kk_status_str": (ctypes.c_char_p, [ctypes.c_int]),
         "kk_debug_set_wait_limit": (ctypes.c_int, [ctypes.c_uint64]),
@@ -102,6 +115,11 @@ def _load():
         "kk_hier_select_pool_workspace_bytes": (SZ, [I32, I32, I32, I32]),
         "kk_hier_select_pool": (ctypes.c_int, [P, P, P, I32, I32, I32, I32, I32, I32, I32, I32, I32, P, P, P, P,
                                                SZ, P]),
+        "kk_tree_attn_workspace_bytes": (SZ, [KC, BT, I32, I32]),
+        "kk_tree_attn": (ctypes.c_int, [KC, KC, BT, I32, SL, TR, P, I64, I64, I32, F, P, P, P, SZ, P]),
+        "kk_attn_mass": (ctypes.c_int, [KC, BT, I32, TR, P, I64, I64, I32, F, P, P, P, P, F, P, P, P]),
+        "kk_evict_select": (ctypes.c_int, [KC, BT, P, I32, I32, I32, P, P, P]),
+        "kk_evict_compact": (ctypes.c_int, [KC, KC, BT, P, I32, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -123,6 +141,7 @@ EXPORTS = (
     "kk_score_pool_batched_workspace_bytes",
     "kk_score_pool_batched", "kk_coarse_means", "kk_hier_pool_coarse_rows", "kk_hier_pool_reps",
     "kk_hier_select_pool_workspace_bytes", "kk_hier_select_pool",
+    "kk_tree_attn_workspace_bytes", "kk_tree_attn", "kk_attn_mass", "kk_evict_select", "kk_evict_compact",
 )
 
 
@@ -197,6 +216,69 @@ class AnchorRing:
     @property
     def slots(self) -> int:
         return self.c.slots
+
+
+def _strided(t, name):
+    """(address, node stride, head stride) of a [nodes][heads][D] CUDA tensor whose last dim is dense."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise ValueError(f"{name} must be [nodes][heads][D] with a dense last dimension")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _check_elems(kc, t, name):
+    """The element type and head_dim of a query-side tensor are the cache's."""
+    want = (torch.float32,) if kc.dtype == KK_F32 else (torch.bfloat16, torch.int16)
+    if t.dtype not in want:
+        raise TypeError(f"{name} has dtype {t.dtype}, the cache holds {want[0]}")
+    if t.shape[-1] != kc.head_dim:
+        raise ValueError(f"{name} has head_dim {t.shape[-1]}, the cache {kc.head_dim}")
+
+
+class Tree:
+    """The query nodes of each request (see kk_tree in include/kk.h); keeps its tensors alive.
+
+    ``node_offsets`` int32 [R+1] (None: ``max_nodes`` each); ``mask`` int32
+    [nodes][ceil(max_nodes / 32)] holding the uint32 words (None: causal);
+    ``k``, ``v``: [nodes][KV heads][D] of drafted nodes (may be strided)."""
+
+    def __init__(self, max_nodes: int, node_offsets=None, mask=None, k=None, v=None):
+        self.node_offsets, self.mask, self.k, self.v = node_offsets, mask, k, v
+        self.c = kk_tree(_ptr(node_offsets, torch.int32, "node_offsets"), int(max_nodes), 0,
+                         _ptr(mask, torch.int32, "mask"))
+        if mask is not None and (mask.dim() != 2 or mask.shape[1] != (int(max_nodes) + 31) // 32):
+            raise ValueError("mask must be [nodes][ceil(max_nodes / 32)]")
+        if (k is None) != (v is None):
+            raise ValueError("k and v come together")
+        if k is not None:
+            self.c.k, self.c.k_stride_node, self.c.k_stride_head = _strided(k, "k")
+            self.c.v, self.c.v_stride_node, self.c.v_stride_head = _strided(v, "v")
+
+    def bind(self, kc, q):
+        """The C struct for queries ``q`` [nodes][query heads][D]."""
+        n = q.shape[0]
+        for t, name in ((self.mask, "mask"), (self.k, "k"), (self.v, "v")):
+            if t is not None and t.shape[0] < n:
+                raise ValueError(f"{name} has fewer rows than q")
+        for t, name in ((self.k, "k"), (self.v, "v")):
+            if t is not None:
+                _check_elems(kc, t, name)
+                if t.shape[1] != kc.num_kv_heads:
+                    raise ValueError(f"{name} has {t.shape[1]} heads, the cache {kc.num_kv_heads}")
+        self.c.total_nodes = n
+        return ctypes.byref(self.c)
+
+
+class Selection:
+    """The blocks attention reads, as kk_compact_table writes them; keeps its tensors alive."""
+
+    def __init__(self, pages, logical, count):
+        if pages.shape != logical.shape or pages.dim() != 2 or count.shape != pages.shape[:1]:
+            raise ValueError("pages and logical are [R][K], count is [R]")
+        self.pages, self.logical, self.count = pages, logical, count
+        self.c = kk_selection(_ptr(pages, torch.int32, "pages"), _ptr(logical, torch.int32, "logical"),
+                              _ptr(count, torch.int32, "count"), pages.shape[1])
 
 
 def _options(ring=None, workspace=None, append=None, compact=None):
@@ -439,3 +521,74 @@ def kk_coarse_means(vb, bt: BlockTable, group: int, out, stream=None):
     _check("kk_coarse_means", _lib.kk_coarse_means(
         _ptr(vb, torch.float32, "vb"), vb.shape[1], vb.shape[0], ctypes.byref(bt.c), group,
         _ptr(out, torch.float32, "out"), _stream(stream)))
+
+
+def kk_tree_attn_workspace_bytes(kc, bt: BlockTable, max_nodes: int, num_q_heads: int) -> int:
+    return _lib.kk_tree_attn_workspace_bytes(ctypes.byref(kc), ctypes.byref(bt.c), max_nodes, num_q_heads)
+
+
+def kk_tree_attn(kc, vc, bt: BlockTable, layer: int, tree: Tree, q, scale: float, out, lse=None, sel=None,
+                 workspace=None, stream=None):
+    """Attention of the nodes of ``tree`` over layer ``layer`` of the cache (``sel``: a :class:`Selection`
+    of its blocks). ``q``: [nodes][query heads][D] (may be strided), ``out`` the same shape, contiguous."""
+    _check_elems(kc, q, "q")
+    qp, qn, qh = _strided(q, "q")
+    if out.shape != q.shape or out.element_size() != q.element_size():
+        raise ValueError("out must have q's shape and type")
+    if lse is not None and lse.numel() != q.shape[0] * q.shape[1]:
+        raise ValueError("lse must be [nodes][query heads]")
+    if sel is not None and sel.pages.shape[0] != bt.num_requests:
+        raise ValueError("the selection has another number of requests than the table")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("kk_tree_attn", _lib.kk_tree_attn(
+        ctypes.byref(kc), ctypes.byref(vc), ctypes.byref(bt.c), layer, None if sel is None else ctypes.byref(sel.c),
+        tree.bind(kc, q), qp, qn, qh, q.shape[1], float(scale), _ptr(out, name="out"),
+        _ptr(lse, torch.float32, "lse"), _ptr(workspace, name="workspace"), ws_bytes, _stream(stream)))
+
+
+def _mass_ptr(kc, mass, name):
+    n = kc.num_layers * kc.num_pages * kc.num_kv_heads * kc.block_size
+    if mass is not None and mass.numel() != n:
+        raise ValueError(f"{name} must be [layers][pages][KV heads][block_size]")
+    return _ptr(mass, torch.float32, name)
+
+
+def kk_attn_mass(kc, bt: BlockTable, layer: int, tree: Tree, q, scale: float, lse, mass_in, mass_out, row_w=None,
+                 row_lens=None, old_lens=None, decay: float = 1.0, stream=None):
+    """Adds the weight every cached token received from the nodes to ``mass_in`` (may be ``mass_out``)."""
+    _check_elems(kc, q, "q")
+    qp, qn, qh = _strided(q, "q")
+    for t, name, n in ((lse, "lse", q.shape[0] * q.shape[1]), (row_w, "row_w", q.shape[0]),
+                       (row_lens, "row_lens", q.shape[0]), (old_lens, "old_lens", bt.num_requests)):
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{name} must have {n} elements")
+    _check("kk_attn_mass", _lib.kk_attn_mass(
+        ctypes.byref(kc), ctypes.byref(bt.c), layer, tree.bind(kc, q), qp, qn, qh, q.shape[1], float(scale),
+        _ptr(lse, torch.float32, "lse"), _ptr(row_w, torch.float32, "row_w"),
+        _ptr(row_lens, torch.int32, "row_lens"), _ptr(old_lens, torch.int32, "old_lens"), float(decay),
+        _mass_ptr(kc, mass_in, "mass_in"), _mass_ptr(kc, mass_out, "mass_out"), _stream(stream)))
+
+
+def _kept_ptr(kc, bt, kept):
+    if kept.dim() != 4 or tuple(kept.shape[:3]) != (bt.num_requests, kc.num_layers, kc.num_kv_heads):
+        raise ValueError("kept must be [R][layers][KV heads][keep]")
+    return _ptr(kept, torch.int32, "kept")
+
+
+def kk_evict_select(kc, bt: BlockTable, mass, sinks: int, recent: int, kept, new_lens=None, stream=None):
+    """``kept``: int32 [R][layers][KV heads][keep]."""
+    _check("kk_evict_select", _lib.kk_evict_select(
+        ctypes.byref(kc), ctypes.byref(bt.c), _mass_ptr(kc, mass, "mass"), sinks, recent, kept.shape[-1],
+        _kept_ptr(kc, bt, kept), _ptr(new_lens, torch.int32, "new_lens"), _stream(stream)))
+
+
+def kk_evict_compact(kc, vc, bt: BlockTable, kept, mass_in=None, mass_out=None, dst_pages=None, stream=None):
+    """``dst_pages``: int32 [R][ceil(keep / block_size)] (None: in place)."""
+    if dst_pages is not None:
+        want = (bt.num_requests, (kept.shape[-1] + kc.block_size - 1) // kc.block_size)
+        if tuple(dst_pages.shape) != want:
+            raise ValueError(f"dst_pages must be {want}")
+    _check("kk_evict_compact", _lib.kk_evict_compact(
+        ctypes.byref(kc), None if vc is None else ctypes.byref(vc), ctypes.byref(bt.c), _kept_ptr(kc, bt, kept),
+        kept.shape[-1], _mass_ptr(kc, mass_in, "mass_in"), _mass_ptr(kc, mass_out, "mass_out"),
+        _ptr(dst_pages, torch.int32, "dst_pages"), _stream(stream)))
