@@ -4,7 +4,7 @@
 // Affinity" page §5.2 step 4: only they are loaded) and the drafted nodes a
 // node may see. One pass over the tokens with a running maximum and sum per
 // row; the work division is kk_attn.cuh's.
-//  * attn_simt_kernel: float32 products on the CUDA cores;
+//  * attn_simt_kernel: float32 caches, on the CUDA cores;
 //  * attn_combine_kernel: adds up the parts of the items that were cut.
 #include "kk_attn.cuh"
 #include "kk_pdl.cuh"
@@ -282,7 +282,8 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const Att
 }
 
 template <typename T, int D>
-cudaError_t combine_t(const AttnArgs& a, int M, int TK, cudaStream_t s) {
+cudaError_t combine_t(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
+  const int M = pl.M;
   const int mt_max = (int)(((long long)a.max_nodes * a.G + M - 1) / M);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.bt.R * a.kc.H * mt_max), (unsigned)((M + kCombineRows - 1) / kCombineRows));
@@ -293,34 +294,48 @@ cudaError_t combine_t(const AttnArgs& a, int M, int TK, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, D>, a, M, TK, mt_max);
+  return cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, D>, a, M, pl.TK, mt_max);
 }
 
-template <typename T, int D>
-cudaError_t simt_t(AttnArgs a, cudaStream_t s) {
-  a.grid = attn_grid(a.kc, a.max_nodes, a.G);
-  attn_simt_kernel<T, D><<<a.grid, kSimtThreads, 0, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? combine_t<T, D>(a, kSimtM, kSimtTK, s) : e;
+template <int D>
+cudaError_t simt_t(const AttnArgs& a, cudaStream_t s) {
+  attn_simt_kernel<float, D><<<a.grid, kSimtThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+AttnPlan plan(const KCache& kc, int max_nodes, int G) {
+  if (kc.dtype == 1) return attn_mma_plan(kc, max_nodes * G);
+  return AttnPlan{AttnPlan::kSimt, kSimtM, kSimtTK, sm_count() * 4};
 }
 
 }  // namespace
 
-int attn_grid(const KCache&, int, int) { return sm_count() * 4; }
-
 size_t attn_workspace_bytes(const KCache& kc, int max_nodes, int G) {
-  return (size_t)attn_grid(kc, max_nodes, G) * 2 * kSimtM * (kc.D + 2) * sizeof(float);
+  const AttnPlan pl = plan(kc, max_nodes, G);
+  return (size_t)pl.grid * 2 * pl.M * (kc.D + 2) * sizeof(float);
 }
 
-cudaError_t launch_tree_attn(const AttnArgs& a, cudaStream_t s) {
+cudaError_t launch_tree_attn(AttnArgs a, cudaStream_t s) {
+  const AttnPlan pl = plan(a.kc, a.max_nodes, a.G);
+  a.grid = pl.grid;
   const bool bf = a.kc.dtype == 1;
-  switch (a.kc.D) {
-    case 32: return bf ? simt_t<bf16_t, 32>(a, s) : simt_t<float, 32>(a, s);
-    case 64: return bf ? simt_t<bf16_t, 64>(a, s) : simt_t<float, 64>(a, s);
-    case 128: return bf ? simt_t<bf16_t, 128>(a, s) : simt_t<float, 128>(a, s);
-    case 256: return bf ? simt_t<bf16_t, 256>(a, s) : cudaErrorNotSupported;
+  cudaError_t e = cudaErrorNotSupported;
+  if (pl.kind == AttnPlan::kMma) {
+    e = launch_attn_mma(a, pl, s);
+  } else {
+    switch (a.kc.D) {
+      case 32: e = simt_t<32>(a, s); break;
+      case 64: e = simt_t<64>(a, s); break;
+      case 128: e = simt_t<128>(a, s); break;
+    }
   }
-  return cudaErrorNotSupported;
+  if (e != cudaSuccess) return e;
+  switch (a.kc.D) {
+    case 32: return bf ? combine_t<bf16_t, 32>(a, pl, s) : combine_t<float, 32>(a, pl, s);
+    case 64: return bf ? combine_t<bf16_t, 64>(a, pl, s) : combine_t<float, 64>(a, pl, s);
+    case 128: return bf ? combine_t<bf16_t, 128>(a, pl, s) : combine_t<float, 128>(a, pl, s);
+    default: return combine_t<bf16_t, 256>(a, pl, s);
+  }
 }
 
 }  // namespace kk

@@ -49,6 +49,16 @@ struct AttnArgs {
   int* err;
 };
 
+// How a call runs: which kernel, its row and token tiles, its grid.
+struct AttnPlan {
+  enum Kind { kSimt, kMma };
+  Kind kind;
+  int M, TK, grid;
+};
+// kk_attn_mma.cu (bf16; rows: query rows of a request and KV head, at most)
+AttnPlan attn_mma_plan(const KCache& kc, int rows);
+cudaError_t launch_attn_mma(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s);
+
 struct AttnReq {
   int node0, n;      // first node, nodes
   int off, T;        // table start, cached tokens
