@@ -195,26 +195,34 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const AttnArgs 
   }
 }
 
-// Block (item slot, row chunk): the rows of one item's partial results, added
-// up in CTA order. Whole items were written by the main kernel.
-constexpr int kCombineThreads = 128;
-constexpr int kCombineRows = 8;
+// Block (item, row chunk): rows of one item's partial results, added up.
+// Whole items were written by the main kernel. `wpr` of the eight warps share a
+// row (more when few items are cut into many parts): each group of lanes that
+// spans a row's D values adds every n-th part in CTA order, and the groups'
+// sums are joined in order, so the result does not depend on timing.
+constexpr int kCombineThreads = 256;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const AttnArgs a, int M, int TK, int mt_max) {
+__global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const AttnArgs a, int M, int TK, int mt_max,
+                                                                       int wpr) {
+  constexpr int L = D / 4 < 32 ? D / 4 : 32;  // lanes of a row
+  constexpr int V = D / (4 * L);              // float4 of a lane
+  constexpr int NG = kCombineThreads / L;     // lane groups of the block
   __shared__ long long s_sum[2][kCombineThreads / 32];
+  __shared__ __align__(16) float s_acc[NG][D];
+  __shared__ float s_m[NG], s_l[NG];
   const int tid = threadIdx.x;
   const int mt = blockIdx.x % mt_max, h = (blockIdx.x / mt_max) % a.kc.H, r = blockIdx.x / (mt_max * a.kc.H);
+  const int rpb = kCombineThreads / 32 / wpr;  // rows of a block
   const AttnReq rq = load_req(a, r, M, TK, false);
-  const int row0 = mt * M + blockIdx.y * kCombineRows, rows = min(kCombineRows, rq.n * a.G - row0);
-  const bool mine = mt < rq.mt && rows > 0;
+  const int row0 = mt * M + blockIdx.y * rpb;
+  if (mt >= rq.mt || row0 >= min(rq.n * a.G, (mt + 1) * M)) return;
   long long before = 0, all = 0;
-  if (mine)
-    for (int i = tid; i < a.bt.R; i += kCombineThreads) {
-      const long long n = req_units(a, load_req(a, i, M, TK, false));
-      all += n;
-      if (i < r) before += n;
-    }
+  for (int i = tid; i < a.bt.R; i += kCombineThreads) {
+    const long long n = req_units(a, load_req(a, i, M, TK, false));
+    all += n;
+    if (i < r) before += n;
+  }
 #pragma unroll
   for (int x = 16; x; x >>= 1) {
     all += __shfl_xor_sync(kFull, all, x);
@@ -225,68 +233,94 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const Att
     s_sum[1][tid >> 5] = all;
   }
   __syncthreads();
-  if (!mine) return;
   before = all = 0;
   for (int x = 0; x < kCombineThreads / 32; ++x) {
     before += s_sum[0][x];
     all += s_sum[1][x];
   }
+  const int G = (int)min((long long)a.grid, all);
   const long long lo = before + (long long)(h * rq.mt + mt) * rq.tiles, hi = lo + rq.tiles - 1;
-  const int c0 = (int)(((lo + 1) * a.grid - 1) / all), c1 = (int)(((hi + 1) * a.grid - 1) / all);
+  const int c0 = (int)(((lo + 1) * G - 1) / all), c1 = (int)(((hi + 1) * G - 1) / all);
   if (c0 == c1) return;
+  const int first = (long long)c0 * all / G == lo ? 0 : 1;  // c0's slot: its first item, or its last
+  const int grp = tid / L, ln = tid % L, gpr = NG / rpb;    // lane groups of a row
+  const int row = row0 + grp / gpr, gi = grp % gpr;
+  const bool real = row < min(rq.n * a.G, (mt + 1) * M);
+  const int m = real ? row - mt * M : 0;
   pdl_wait();
-  constexpr int L = D / 4 < 32 ? D / 4 : 32;  // lanes of a row
-  constexpr int V = D / (4 * L);              // float4 of a lane
-  const int sub = tid / L, ln = tid % L;
-  const int first = (long long)c0 * all / a.grid == lo ? 0 : 1;  // c0's slot: its first item, or its last
-  for (int i = sub; i < rows; i += kCombineThreads / L) {
-    const int m = row0 + i - mt * M;
-    float mm = -INFINITY;
-    for (int c = c0; c <= c1; ++c) {
-      if ((long long)c * all / a.grid == (long long)(c + 1) * all / a.grid) continue;  // no units
-      mm = fmaxf(mm, partial_slot(a, c, c == c0 ? first : 0, M, D)[M * D + m]);
-    }
-    const float ref = mm == -INFINITY ? 0.f : mm;
-    float l = 0.f;
-    float4 acc[V];
+  float mm = -INFINITY, l = 0.f;
+  float4 acc[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int e = 0; e < V; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      if ((long long)c * all / a.grid == (long long)(c + 1) * all / a.grid) continue;
-      const float* part = partial_slot(a, c, c == c0 ? first : 0, M, D);
-      const float al = exp2f(part[M * D + m] - ref);
-      l += part[M * D + M + m] * al;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float4 x = *reinterpret_cast<const float4*>(part + m * D + (e * L + ln) * 4);
-        acc[e].x += x.x * al;
-        acc[e].y += x.y * al;
-        acc[e].z += x.z * al;
-        acc[e].w += x.w * al;
-      }
-    }
-    const float inv = row_inv(l);
-    const int row = row0 + i;
-    const long long at = (long long)(rq.node0 + row / a.G) * a.Hq + h * a.G + row % a.G;
+  for (int c = c0 + gi; c <= c1; c += gpr) {
+    const float* part = partial_slot(a, c, c == c0 ? first : 0, M, D);
+    const float pm = part[M * D + m], pl = part[M * D + M + m];
+    const float m2 = fmaxf(mm, pm), ref = m2 == -INFINITY ? 0.f : m2;
+    const float f = exp2f(mm - ref), al = exp2f(pm - ref);
+    l = l * f + pl * al;
+    mm = m2;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const long long d = at * D + (e * L + ln) * 4;
-      store_elem<T>(a.out, d, acc[e].x * inv);
-      store_elem<T>(a.out, d + 1, acc[e].y * inv);
-      store_elem<T>(a.out, d + 2, acc[e].z * inv);
-      store_elem<T>(a.out, d + 3, acc[e].w * inv);
+      const float4 x = *reinterpret_cast<const float4*>(part + m * D + (e * L + ln) * 4);
+      acc[e].x = acc[e].x * f + x.x * al;
+      acc[e].y = acc[e].y * f + x.y * al;
+      acc[e].z = acc[e].z * f + x.z * al;
+      acc[e].w = acc[e].w * f + x.w * al;
     }
-    if (ln == 0 && a.lse) a.lse[at] = row_lse(mm, l);
   }
+  if (gpr > 1) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) *reinterpret_cast<float4*>(&s_acc[grp][(e * L + ln) * 4]) = acc[e];
+    if (ln == 0) {
+      s_m[grp] = mm;
+      s_l[grp] = l;
+    }
+    __syncthreads();
+    if (gi != 0) return;
+    for (int x = 1; x < gpr; ++x) mm = fmaxf(mm, s_m[grp + x]);
+    const float ref = mm == -INFINITY ? 0.f : mm;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = 0; x < gpr; ++x) {
+      const float al = exp2f(s_m[grp + x] - ref);
+      l += s_l[grp + x] * al;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float4 y = *reinterpret_cast<const float4*>(&s_acc[grp + x][(e * L + ln) * 4]);
+        acc[e].x += y.x * al;
+        acc[e].y += y.y * al;
+        acc[e].z += y.z * al;
+        acc[e].w += y.w * al;
+      }
+    }
+  }
+  if (!real) return;
+  const float inv = row_inv(l);
+  const long long at = (long long)(rq.node0 + row / a.G) * a.Hq + h * a.G + row % a.G;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const long long d = at * D + (e * L + ln) * 4;
+    store_elem<T>(a.out, d, acc[e].x * inv);
+    store_elem<T>(a.out, d + 1, acc[e].y * inv);
+    store_elem<T>(a.out, d + 2, acc[e].z * inv);
+    store_elem<T>(a.out, d + 3, acc[e].w * inv);
+  }
+  if (ln == 0 && a.lse) a.lse[at] = row_lse(mm, l);
 }
 
 template <typename T, int D>
 cudaError_t combine_t(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
   const int M = pl.M;
   const int mt_max = (int)(((long long)a.max_nodes * a.G + M - 1) / M);
+  const long long items = (long long)a.bt.R * a.kc.H * mt_max;
+  // warps of a row: about four parts each when every CTA works on few items
+  int wpr = 1;
+  while (wpr < 8 && pl.grid / items > 4 * wpr) wpr *= 2;
+  const int rows = min(M, a.max_nodes * a.G), rpb = kCombineThreads / 32 / wpr;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.bt.R * a.kc.H * mt_max), (unsigned)((M + kCombineRows - 1) / kCombineRows));
+  cfg.gridDim = dim3((unsigned)items, (unsigned)((rows + rpb - 1) / rpb));
   cfg.blockDim = dim3(kCombineThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -294,7 +328,7 @@ cudaError_t combine_t(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, D>, a, M, pl.TK, mt_max);
+  return cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, D>, a, M, pl.TK, mt_max, wpr);
 }
 
 template <int D>

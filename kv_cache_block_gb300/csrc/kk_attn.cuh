@@ -148,7 +148,7 @@ __device__ __forceinline__ bool token_at(const AttnArgs& a, int r, const AttnReq
 // range [u0, u1) of all units. Called by NT threads (a multiple of 32, at most
 // 1024); `sh` is NT/32 + 4 long longs of shared memory.
 struct AttnPlace {
-  long long u0, u1, total, base;
+  long long u0, u1, base;
   int r;
 };
 template <int NT>
@@ -172,9 +172,9 @@ __device__ __forceinline__ AttnPlace find_place(const AttnArgs& a, int cta, int 
   }
   long long lo = before + incl - mine;
   AttnPlace p;
-  p.total = total;
-  p.u0 = (long long)cta * total / a.grid;
-  p.u1 = (long long)(cta + 1) * total / a.grid;
+  const int G = (int)min((long long)a.grid, total);
+  p.u0 = cta < G ? (long long)cta * total / G : total;
+  p.u1 = cta < G ? (long long)(cta + 1) * total / G : total;
   long long* found = sh + NT / 32;
   if (p.u0 < p.u1 && lo <= p.u0 && p.u0 < lo + mine) {
     int r = r0;
