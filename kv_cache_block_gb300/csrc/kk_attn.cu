@@ -6,6 +6,8 @@
 // row; the work division is kk_attn.cuh's.
 //  * attn_simt_kernel: float32 caches, on the CUDA cores;
 //  * attn_combine_kernel: adds up the parts of the items that were cut.
+#include <algorithm>
+
 #include "kk_attn.cuh"
 #include "kk_pdl.cuh"
 
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const Att
   const int rpb = kCombineThreads / 32 / wpr;  // rows of a block
   const AttnReq rq = load_req(a, r, M, TK, false);
   const int row0 = mt * M + blockIdx.y * rpb;
-  if (mt >= rq.mt || row0 >= min(rq.n * a.G, (mt + 1) * M)) return;
+  if (mt >= rq.mt || blockIdx.y * rpb >= M || row0 >= rq.n * a.G) return;
   long long before = 0, all = 0;
   for (int i = tid; i < a.bt.R; i += kCombineThreads) {
     const long long n = req_units(a, load_req(a, i, M, TK, false));
@@ -239,13 +241,15 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const Att
     all += s_sum[1][x];
   }
   const int G = (int)min((long long)a.grid, all);
-  const long long lo = before + (long long)(h * rq.mt + mt) * rq.tiles, hi = lo + rq.tiles - 1;
+  const ItemAt it = item_of(rq, h, mt);
+  const long long lo = before + it.start, hi = lo + it.units - 1;
   const int c0 = (int)(((lo + 1) * G - 1) / all), c1 = (int)(((hi + 1) * G - 1) / all);
-  if (c0 == c1) return;
+  if (c0 == c1 && !it.single) return;
+  const int halves = it.single ? 2 : 1;  // a single's streams leave a part each, M/2 rows apart
   const int first = (long long)c0 * all / G == lo ? 0 : 1;  // c0's slot: its first item, or its last
   const int grp = tid / L, ln = tid % L, gpr = NG / rpb;    // lane groups of a row
   const int row = row0 + grp / gpr, gi = grp % gpr;
-  const bool real = row < min(rq.n * a.G, (mt + 1) * M);
+  const bool real = row < rq.n * a.G;
   const int m = real ? row - mt * M : 0;
   pdl_wait();
   float mm = -INFINITY, l = 0.f;
@@ -253,16 +257,17 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const Att
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int c = c0 + gi; c <= c1; c += gpr) {
+  for (int i = gi; i < (c1 - c0 + 1) * halves; i += gpr) {
+    const int c = c0 + i / halves, pr = m + (i % halves) * (M / 2);
     const float* part = partial_slot(a, c, c == c0 ? first : 0, M, D);
-    const float pm = part[M * D + m], pl = part[M * D + M + m];
+    const float pm = part[M * D + pr], pl = part[M * D + M + pr];
     const float m2 = fmaxf(mm, pm), ref = m2 == -INFINITY ? 0.f : m2;
     const float f = exp2f(mm - ref), al = exp2f(pm - ref);
     l = l * f + pl * al;
     mm = m2;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const float4 x = *reinterpret_cast<const float4*>(part + m * D + (e * L + ln) * 4);
+      const float4 x = *reinterpret_cast<const float4*>(part + (size_t)pr * D + (e * L + ln) * 4);
       acc[e].x = acc[e].x * f + x.x * al;
       acc[e].y = acc[e].y * f + x.y * al;
       acc[e].z = acc[e].z * f + x.z * al;
@@ -337,24 +342,37 @@ cudaError_t simt_t(const AttnArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-AttnPlan plan(const KCache& kc, int max_nodes, int G) {
-  if (kc.dtype == 1) return attn_mma_plan(kc, max_nodes * G);
-  return AttnPlan{AttnPlan::kSimt, kSimtM, kSimtTK, sm_count() * 4};
+// Rows per KV head from which the tensor-memory kernel is taken (where the
+// caches' layouts suit it).
+constexpr int kTcRows = 33;
+
+AttnPlan plan(const KCache& kc, const KCache& vc, int max_nodes, int G) {
+  const int rows = max_nodes * G;
+  if (kc.dtype != 1) return AttnPlan{AttnPlan::kSimt, kSimtM, kSimtTK, sm_count() * 4};
+  if (rows >= kTcRows && attn_tc_suits(kc) && attn_tc_suits(vc)) return attn_tc_plan();
+  return attn_mma_plan(kc, rows);
 }
+
+size_t plan_bytes(const AttnPlan& pl, int D) { return (size_t)pl.grid * 2 * pl.M * (D + 2) * sizeof(float); }
 
 }  // namespace
 
 size_t attn_workspace_bytes(const KCache& kc, int max_nodes, int G) {
-  const AttnPlan pl = plan(kc, max_nodes, G);
-  return (size_t)pl.grid * 2 * pl.M * (kc.D + 2) * sizeof(float);
+  // enough for either kernel: which one runs also depends on the V cache's strides
+  size_t n = plan_bytes(plan(kc, kc, max_nodes, G), kc.D);
+  if (kc.dtype == 1) n = std::max(n, plan_bytes(attn_mma_plan(kc, max_nodes * G), kc.D));
+  return n;
 }
 
 cudaError_t launch_tree_attn(AttnArgs a, cudaStream_t s) {
-  const AttnPlan pl = plan(a.kc, a.max_nodes, a.G);
+  const AttnPlan pl = plan(a.kc, a.vc, a.max_nodes, a.G);
   a.grid = pl.grid;
+  a.twin = pl.kind == AttnPlan::kTc;
   const bool bf = a.kc.dtype == 1;
   cudaError_t e = cudaErrorNotSupported;
-  if (pl.kind == AttnPlan::kMma) {
+  if (pl.kind == AttnPlan::kTc) {
+    e = launch_attn_tc(a, s);
+  } else if (pl.kind == AttnPlan::kMma) {
     e = launch_attn_mma(a, pl, s);
   } else {
     switch (a.kc.D) {

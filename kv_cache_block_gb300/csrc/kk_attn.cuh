@@ -38,6 +38,7 @@ struct AttnArgs {
   float* lse;        // [total_nodes][Hq] or null
   float* ws;
   int grid;  // CTAs of the main kernel
+  int twin;  // row tiles are pairs of M/2 rows; an odd last one is a single (kk_attn_tc.cu)
   // attention mass only
   const float* row_w;
   const int* row_lens;
@@ -51,19 +52,23 @@ struct AttnArgs {
 
 // How a call runs: which kernel, its row and token tiles, its grid.
 struct AttnPlan {
-  enum Kind { kSimt, kMma };
+  enum Kind { kSimt, kMma, kTc };
   Kind kind;
   int M, TK, grid;
 };
 // kk_attn_mma.cu (bf16; rows: query rows of a request and KV head, at most)
 AttnPlan attn_mma_plan(const KCache& kc, int rows);
 cudaError_t launch_attn_mma(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s);
+// kk_attn_tc.cu (bf16, D 64 or 128, both caches of layouts it suits)
+bool attn_tc_suits(const KCache& kc);
+AttnPlan attn_tc_plan();
+cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t s);
 
 struct AttnReq {
   int node0, n;      // first node, nodes
   int off, T;        // table start, cached tokens
   int ctx;           // token slots to visit: T, or block_size * selected blocks
-  int mt;            // row tiles
+  int mt, odd;       // row tiles; the last one is a single of M/2 rows
   int tiles_c, tiles;  // token tiles: cached, all (at least 1 when there are nodes)
 };
 
@@ -98,6 +103,7 @@ __device__ __forceinline__ AttnReq load_req(const AttnArgs& a, int r, int M, int
   }
   q.ctx = (int)ctx;
   q.mt = (q.n * a.G + M - 1) / M;
+  q.odd = a.twin && q.n > 0 && q.n * a.G - (q.mt - 1) * M <= M / 2;
   q.tiles_c = (int)((ctx + TK - 1) / TK);
   q.tiles = q.tiles_c + (a.dk ? (q.n + TK - 1) / TK : 0);
   if (q.tiles == 0) q.tiles = 1;
@@ -109,7 +115,34 @@ __device__ __forceinline__ AttnReq load_req(const AttnArgs& a, int r, int M, int
   return q;
 }
 __device__ __forceinline__ long long req_units(const AttnArgs& a, const AttnReq& q) {
-  return (long long)a.kc.H * q.mt * q.tiles;
+  return (long long)a.kc.H * ((long long)(q.mt - q.odd) * q.tiles + q.odd * ((q.tiles + 1) / 2));
+}
+
+// An item: KV head, row tile, whether it is a single, its first unit inside
+// the request and its number of units (a single's unit is two token tiles);
+// [t0, t1): the units of a range that starts inside it.
+struct ItemAt {
+  int h, mt, units, t0, t1;
+  bool single;
+  long long start;
+};
+__device__ __forceinline__ ItemAt item_of(const AttnReq& q, int h, int mt) {
+  ItemAt x;
+  const int pairs = q.mt - q.odd, half = (q.tiles + 1) / 2;
+  x.h = h;
+  x.mt = mt;
+  x.single = mt >= pairs;
+  x.units = x.single ? half : q.tiles;
+  x.start = h * ((long long)pairs * q.tiles + q.odd * half) + (long long)mt * q.tiles;
+  x.t0 = x.t1 = 0;
+  return x;
+}
+__device__ __forceinline__ ItemAt item_at(const AttnReq& q, long long local) {
+  const long long per = (long long)(q.mt - q.odd) * q.tiles + q.odd * ((q.tiles + 1) / 2);
+  const int h = (int)(local / per);
+  ItemAt x = item_of(q, h, min((int)((local - h * per) / q.tiles), q.mt - 1));
+  x.t0 = (int)(local - x.start);
+  return x;
 }
 
 // Element offset (without head and layer) of token slot v of a request in the
@@ -204,6 +237,19 @@ __device__ __forceinline__ float* partial_slot(const AttnArgs& a, int cta, int w
 __device__ __forceinline__ float row_inv(float l) { return l > 0.f || l != l ? 1.f / l : 0.f; }
 __device__ __forceinline__ float row_lse(float m, float l) {
   return l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// 2^x; results below the normal range are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two floats as bf16, each rounded once to nearest.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 template <typename T>

@@ -46,12 +46,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // Byte offset of 16-byte piece c of row `row` in a tile of D-element rows:
 // pieces are exchanged within 128 bytes so that eight rows' pieces of one
 // column fall into different banks.
@@ -251,13 +245,13 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
           mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
           const float ref = mx == -INFINITY ? 0.f : mx;
-          al[mr][hf] = exp2f(m_run[mr][hf] - ref);
+          al[mr][hf] = ex2(m_run[mr][hf] - ref);
           rise |= mx > m_run[mr][hf];
           m_run[mr][hf] = mx;
           float sum = 0.f;
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
-            const float p0 = exp2f(s[mr][nt][hf * 2] - ref), p1 = exp2f(s[mr][nt][hf * 2 + 1] - ref);
+            const float p0 = ex2(s[mr][nt][hf * 2] - ref), p1 = ex2(s[mr][nt][hf * 2 + 1] - ref);
             sum += p0 + p1;
             pa[mr][nt * 2 + hf] = pack_bf16(p0, p1);  // the weights' one rounding: bf16 feeds the product
           }
@@ -341,7 +335,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int x = 0; x < kWarps; ++x) {
-        const float f = exp2f(jm[x * M + m] - ref);
+        const float f = ex2(jm[x * M + m] - ref);
         const float4 y = *reinterpret_cast<const float4*>(join + (x * M + m) * D + d);
         l += jl[x * M + m] * f;
         acc.x += y.x * f;
