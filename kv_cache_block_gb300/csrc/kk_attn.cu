@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const AttnArgs 
 #pragma unroll
         for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
         const float m_new = fmaxf(m_run[i], mx), ref = m_new == -INFINITY ? 0.f : m_new;
-        const float p = exp2f(s[i] - ref), al = exp2f(m_run[i] - ref);
+        const float p = ex2(s[i] - ref), al = ex2(m_run[i] - ref);
         m_run[i] = m_new;
         l_run[i] = l_run[i] * al + p;  // this lane's share of the sum
 #pragma unroll
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const AttnArgs 
       const float ref = mm == -INFINITY ? 0.f : mm;
       float l = 0.f, acc = 0.f;
       for (int x = 0; x < 4; ++x) {
-        const float al = exp2f(s_m[x][m] - ref);
+        const float al = ex2(s_m[x][m] - ref);
         l += s_l[x][m] * al;
         acc += s_o[x][m][d] * al;
       }
@@ -197,30 +197,17 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const AttnArgs 
   }
 }
 
-// Block (item, row chunk): rows of one item's partial results, added up.
-// Whole items were written by the main kernel. `wpr` of the eight warps share a
-// row (more when few items are cut into many parts): each group of lanes that
-// spans a row's D values adds every n-th part in CTA order, and the groups'
-// sums are joined in order, so the result does not depend on timing.
-constexpr int kCombineThreads = 256;
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const AttnArgs a, int M, int TK, int mt_max,
-                                                                       int wpr) {
-  constexpr int L = D / 4 < 32 ? D / 4 : 32;  // lanes of a row
-  constexpr int V = D / (4 * L);              // float4 of a lane
-  constexpr int NG = kCombineThreads / L;     // lane groups of the block
-  __shared__ long long s_sum[2][kCombineThreads / 32];
-  __shared__ __align__(16) float s_acc[NG][D];
-  __shared__ float s_m[NG], s_l[NG];
-  const int tid = threadIdx.x;
-  const int mt = blockIdx.x % mt_max, h = (blockIdx.x / mt_max) % a.kc.H, r = blockIdx.x / (mt_max * a.kc.H);
-  const int rpb = kCombineThreads / 32 / wpr;  // rows of a block
-  const AttnReq rq = load_req(a, r, M, TK, false);
-  const int row0 = mt * M + blockIdx.y * rpb;
-  if (mt >= rq.mt || blockIdx.y * rpb >= M || row0 >= rq.n * a.G) return;
+// The CTAs [c0, c0 + n) whose partial results make up an item (n = 0: nothing
+// to add up, or no rows from `row` of the tile on), and c0's slot.
+struct Cut {
+  int c0, n, first, halves, node0, rows;
+};
+template <int NT>
+__device__ __forceinline__ Cut find_cut(const AttnArgs& a, int r, int h, int mt, int row, int M, int TK, int tid) {
+  __shared__ long long s_sum[2][NT / 32];
+  __shared__ Cut s_cut;
   long long before = 0, all = 0;
-  for (int i = tid; i < a.bt.R; i += kCombineThreads) {
+  for (int i = tid; i < a.bt.R; i += NT) {
     const long long n = req_units(a, load_req(a, i, M, TK, false));
     all += n;
     if (i < r) before += n;
@@ -235,21 +222,57 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const Att
     s_sum[1][tid >> 5] = all;
   }
   __syncthreads();
-  before = all = 0;
-  for (int x = 0; x < kCombineThreads / 32; ++x) {
-    before += s_sum[0][x];
-    all += s_sum[1][x];
+  if (tid == 0) {  // one thread divides for the block
+    before = all = 0;
+    for (int x = 0; x < NT / 32; ++x) {
+      before += s_sum[0][x];
+      all += s_sum[1][x];
+    }
+    const AttnReq rq = load_req(a, r, M, TK, false);
+    Cut c = {};
+    if (mt < rq.mt && mt * M + row < rq.n * a.G) {
+      const int G = (int)min((long long)a.grid, all);
+      const ItemAt it = item_of(rq, h, mt);
+      const long long lo = before + it.start, hi = lo + it.units - 1;
+      c.c0 = (int)(((lo + 1) * G - 1) / all);
+      c.n = (int)(((hi + 1) * G - 1) / all) - c.c0 + 1;
+      c.first = (long long)c.c0 * all / G == lo ? 0 : 1;  // c0's slot: its first item, or its last
+      c.halves = it.single ? 2 : 1;  // a single's streams leave a part each, M/2 rows apart
+      if (c.n == 1 && !it.single) c.n = 0;
+      c.node0 = rq.node0;
+      c.rows = rq.n * a.G;
+    }
+    s_cut = c;
   }
-  const int G = (int)min((long long)a.grid, all);
-  const ItemAt it = item_of(rq, h, mt);
-  const long long lo = before + it.start, hi = lo + it.units - 1;
-  const int c0 = (int)(((lo + 1) * G - 1) / all), c1 = (int)(((hi + 1) * G - 1) / all);
-  if (c0 == c1 && !it.single) return;
-  const int halves = it.single ? 2 : 1;  // a single's streams leave a part each, M/2 rows apart
-  const int first = (long long)c0 * all / G == lo ? 0 : 1;  // c0's slot: its first item, or its last
-  const int grp = tid / L, ln = tid % L, gpr = NG / rpb;    // lane groups of a row
-  const int row = row0 + grp / gpr, gi = grp % gpr;
-  const bool real = row < rq.n * a.G;
+  __syncthreads();
+  return s_cut;
+}
+
+// Block (item, row chunk): rows of one item's partial results, added up.
+// Whole items were written by the main kernel. `wpr` of the eight warps share a
+// row (more when few items are cut into many parts): each group of lanes that
+// spans a row's D values adds every n-th part in CTA order, and the groups'
+// sums are joined in order, so the result does not depend on timing.
+constexpr int kCombineThreads = 256;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const AttnArgs a, int M, int TK, int mt_max,
+                                                                       int wpr) {
+  constexpr int L = D / 4 < 32 ? D / 4 : 32;  // lanes of a row
+  constexpr int V = D / (4 * L);              // float4 of a lane
+  constexpr int NG = kCombineThreads / L;     // lane groups of the block
+  __shared__ __align__(16) float s_acc[NG][D];
+  __shared__ float s_m[NG], s_l[NG];
+  const int tid = threadIdx.x;
+  const int mt = blockIdx.x % mt_max, h = (blockIdx.x / mt_max) % a.kc.H, r = blockIdx.x / (mt_max * a.kc.H);
+  const int rpb = kCombineThreads / 32 / wpr;  // rows of a block
+  if (blockIdx.y * rpb >= M) return;
+  const Cut cut = find_cut<kCombineThreads>(a, r, h, mt, blockIdx.y * rpb, M, TK, tid);
+  if (cut.n == 0) return;
+  const int parts = cut.n;
+  const int grp = tid / L, ln = tid % L, gpr = NG / rpb;  // lane groups of a row
+  const int row = mt * M + blockIdx.y * rpb + grp / gpr, gi = grp % gpr;
+  const bool real = row < cut.rows;
   const int m = real ? row - mt * M : 0;
   pdl_wait();
   float mm = -INFINITY, l = 0.f;
@@ -257,17 +280,16 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const Att
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = gi; i < (c1 - c0 + 1) * halves; i += gpr) {
-    const int c = c0 + i / halves, pr = m + (i % halves) * (M / 2);
-    const float* part = partial_slot(a, c, c == c0 ? first : 0, M, D);
-    const float pm = part[M * D + pr], pl = part[M * D + M + pr];
+  for (int i = gi; i < parts; i += gpr) {
+    const float* part = partial_slot(a, cut.c0 + i, i == 0 ? cut.first : 0, M, D);
+    const float pm = part[M * D + m], pl = part[M * D + M + m];
     const float m2 = fmaxf(mm, pm), ref = m2 == -INFINITY ? 0.f : m2;
-    const float f = exp2f(mm - ref), al = exp2f(pm - ref);
+    const float f = ex2(mm - ref), al = ex2(pm - ref);
     l = l * f + pl * al;
     mm = m2;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const float4 x = *reinterpret_cast<const float4*>(part + (size_t)pr * D + (e * L + ln) * 4);
+      const float4 x = *reinterpret_cast<const float4*>(part + m * D + (e * L + ln) * 4);
       acc[e].x = acc[e].x * f + x.x * al;
       acc[e].y = acc[e].y * f + x.y * al;
       acc[e].z = acc[e].z * f + x.z * al;
@@ -289,7 +311,7 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const Att
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int x = 0; x < gpr; ++x) {
-      const float al = exp2f(s_m[grp + x] - ref);
+      const float al = ex2(s_m[grp + x] - ref);
       l += s_l[grp + x] * al;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
@@ -303,7 +325,7 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const Att
   }
   if (!real) return;
   const float inv = row_inv(l);
-  const long long at = (long long)(rq.node0 + row / a.G) * a.Hq + h * a.G + row % a.G;
+  const long long at = (long long)(cut.node0 + row / a.G) * a.Hq + h * a.G + row % a.G;
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     const long long d = at * D + (e * L + ln) * 4;
@@ -315,6 +337,77 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const Att
   if (ln == 0 && a.lse) a.lse[at] = row_lse(mm, l);
 }
 
+// The same for the tensor-memory kernel's slots, [D/4][256 rows][4]: a lane is a
+// row, a warp takes 16 of its values, and every load and store is whole sectors.
+template <int D>
+__global__ void __launch_bounds__(D * 2) attn_combine_tc_kernel(const AttnArgs a, int TK, int mt_max) {
+  constexpr int M = 256, NT = D * 2;
+  const int tid = threadIdx.x, ln = tid & 31, w = tid >> 5;
+  const int mt = blockIdx.x % mt_max, h = (blockIdx.x / mt_max) % a.kc.H, r = blockIdx.x / (mt_max * a.kc.H);
+  const Cut cut = find_cut<NT>(a, r, h, mt, blockIdx.y * 32, M, TK, tid);
+  if (cut.n == 0 || (cut.halves == 2 && blockIdx.y >= 4)) return;
+  const int m = blockIdx.y * 32 + ln, row = mt * M + m;
+  if (row >= cut.rows) return;
+  pdl_wait();
+  float mm = -INFINITY, l = 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int i = 0; i < cut.n * cut.halves; ++i) {
+    const int c = cut.halves == 2 ? i >> 1 : i, pr = cut.halves == 2 ? m + (i & 1) * (M / 2) : m;
+    const float* part = partial_slot(a, cut.c0 + c, c == 0 ? cut.first : 0, M, D);
+    const float pm = part[M * D + pr], pl = part[M * D + M + pr];
+    const float m2 = fmaxf(mm, pm), ref = m2 == -INFINITY ? 0.f : m2;
+    const float f = ex2(mm - ref), al = ex2(pm - ref);
+    l = l * f + pl * al;
+    mm = m2;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float4 x = reinterpret_cast<const float4*>(part)[(w * 4 + e) * M + pr];
+      acc[e].x = acc[e].x * f + x.x * al;
+      acc[e].y = acc[e].y * f + x.y * al;
+      acc[e].z = acc[e].z * f + x.z * al;
+      acc[e].w = acc[e].w * f + x.w * al;
+    }
+  }
+  const float inv = row_inv(l);
+  const long long at = (long long)(cut.node0 + row / a.G) * a.Hq + h * a.G + row % a.G;
+  uint32_t y[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    y[e * 2] = pack_bf16(acc[e].x * inv, acc[e].y * inv);
+    y[e * 2 + 1] = pack_bf16(acc[e].z * inv, acc[e].w * inv);
+  }
+  uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + w * 16);
+  out[0] = make_uint4(y[0], y[1], y[2], y[3]);
+  out[1] = make_uint4(y[4], y[5], y[6], y[7]);
+  if (w == 0 && a.lse) a.lse[at] = row_lse(mm, l);
+}
+
+// Launches a combine kernel so that it may start while the main kernel ends.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*k)(P...), dim3 grid, int threads, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+template <int D>
+cudaError_t combine_tc(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
+  const int rows = a.max_nodes * a.G, mt_max = (rows + pl.M - 1) / pl.M;
+  return launch_dependent(attn_combine_tc_kernel<D>,
+                          dim3((unsigned)(a.bt.R * a.kc.H * mt_max), (unsigned)((std::min(pl.M, rows) + 31) / 32)), D * 2,
+                          s, a, pl.TK, mt_max);
+}
+
 template <typename T, int D>
 cudaError_t combine_t(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
   const int M = pl.M;
@@ -324,16 +417,8 @@ cudaError_t combine_t(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
   int wpr = 1;
   while (wpr < 8 && pl.grid / items > 4 * wpr) wpr *= 2;
   const int rows = min(M, a.max_nodes * a.G), rpb = kCombineThreads / 32 / wpr;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)items, (unsigned)((rows + rpb - 1) / rpb));
-  cfg.blockDim = dim3(kCombineThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, D>, a, M, pl.TK, mt_max, wpr);
+  return launch_dependent(attn_combine_kernel<T, D>, dim3((unsigned)items, (unsigned)((rows + rpb - 1) / rpb)),
+                          kCombineThreads, s, a, M, pl.TK, mt_max, wpr);
 }
 
 template <int D>
@@ -382,6 +467,7 @@ cudaError_t launch_tree_attn(AttnArgs a, cudaStream_t s) {
     }
   }
   if (e != cudaSuccess) return e;
+  if (pl.kind == AttnPlan::kTc) return a.kc.D == 64 ? combine_tc<64>(a, pl, s) : combine_tc<128>(a, pl, s);
   switch (a.kc.D) {
     case 32: return bf ? combine_t<bf16_t, 32>(a, pl, s) : combine_t<float, 32>(a, pl, s);
     case 64: return bf ? combine_t<bf16_t, 64>(a, pl, s) : combine_t<float, 64>(a, pl, s);

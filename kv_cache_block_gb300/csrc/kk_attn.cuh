@@ -87,7 +87,7 @@ __device__ __forceinline__ AttnReq load_req(const AttnArgs& a, int r, int M, int
   q.off = a.bt.offsets[r];
   const int nb = a.bt.offsets[r + 1] - q.off;
   q.T = a.bt.seq_lens[r];
-  if (q.T < 0 || nb < 0 || nb > a.bt.max_blocks || nb != (int)(((long long)q.T + a.kc.bs - 1) / a.kc.bs)) {
+  if (q.T < 0 || nb < 0 || nb > a.bt.max_blocks || nb != (int)(((unsigned)q.T + (unsigned)a.kc.bs - 1u) / (unsigned)a.kc.bs)) {
     ok = false;
     q.T = 0;
   }
@@ -104,7 +104,7 @@ __device__ __forceinline__ AttnReq load_req(const AttnArgs& a, int r, int M, int
   q.ctx = (int)ctx;
   q.mt = (q.n * a.G + M - 1) / M;
   q.odd = a.twin && q.n > 0 && q.n * a.G - (q.mt - 1) * M <= M / 2;
-  q.tiles_c = (int)((ctx + TK - 1) / TK);
+  q.tiles_c = (int)(((unsigned)q.ctx + (unsigned)TK - 1u) / (unsigned)TK);
   q.tiles = q.tiles_c + (a.dk ? (q.n + TK - 1) / TK : 0);
   if (q.tiles == 0) q.tiles = 1;
   if (a.mass_out) {  // attention mass: the unit is a token tile of one KV head, whatever its rows
@@ -237,6 +237,17 @@ __device__ __forceinline__ float* partial_slot(const AttnArgs& a, int cta, int w
 __device__ __forceinline__ float row_inv(float l) { return l > 0.f || l != l ? 1.f / l : 0.f; }
 __device__ __forceinline__ float row_lse(float m, float l) {
   return l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// 16-byte asynchronous copies; one that is not `real` reads nothing and writes zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // 2^x; results below the normal range are 0.

@@ -2,17 +2,18 @@
 // a piece of a prompt): bound by the tensor cores and the exponentials.
 //
 // One CTA per SM with two streams, A and B, each a 128-row tile with its own
-// scores S (128 TMEM columns) and accumulator O (D columns). Warps 0-3 are
-// A's softmax, warps 4-7 B's (a thread owns a row), warp 8 issues every MMA
-// (tcgen05), warps 9-11 load. While one stream's softmax runs, the tensor cores
-// work for the other:
+// accumulator O (D columns of TMEM) and two score buffers S of 64 tokens. Warps
+// 0-3 are A's softmax, warps 4-7 B's (a thread owns a row), warp 8 issues every
+// MMA (tcgen05), warps 9-11 load:
 //   S_x = Q_x K^T    both operands in shared memory
 //   P_x = exp2(S_x * c - m_x)  written over S_x as bf16, the A operand
 //   O_x += P_x V     P from TMEM, V from shared memory as it lies (MN-major)
-// MMAs of one thread run in order, so S_x of the next tile may follow P_x V at
-// once. The maximum a row's weights are taken against moves only when the true
-// one has risen past it by 2^8: until then the weights stay below 2^8, which
-// costs bf16 nothing, and O need not be rescaled.
+// MMAs of one thread run in order, so the scores two steps on follow P_x V into
+// its buffer at once, and the softmax of the next step finds its scores ready:
+// with one 128-token buffer a stream it waited for P V and Q K^T each time
+// (199 us against TODO us on the 64-node tree). The maximum a row's weights are taken against
+// moves only when the true one has risen past it by 2^8: until then the weights
+// stay below 2^8, which costs bf16 nothing, and O need not be rescaled.
 //
 // An item is a pair of row tiles (both streams take every token tile) or, for
 // the last tile of an odd number, a single one (the streams take alternate
@@ -44,7 +45,8 @@ constexpr int kTmemCols = 512;
 constexpr float kRise = 8.f;
 
 // Notes on a tile for the softmax warps: which places hold a token, the drafted
-// tile it is (-1: cached tokens), and whether a drafted Value is not finite.
+// tile it is (-1: cached tokens), and, once its Values are there, whether one
+// of a draft's is not finite.
 struct TileNote {
   uint32_t live[4];
   int draft;
@@ -63,7 +65,8 @@ struct Cfg {
 struct Bars {
   uint64_t q_full, q_empty;
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t s_full[2][2], p_full[2][2];  // [stream][buffer]
+  uint64_t pv_done[2], o_full[2], o_empty[2];
   uint64_t note[kMeta];
   uint64_t drain;
 };
@@ -71,7 +74,8 @@ struct Bars {
 // Waits for a barrier's phase; gives up (false) past the limit or when another
 // role has given up, and tells the others.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const AttnArgs& a, volatile int* stop) {
-  if (mbar_try_wait(bar, parity)) return true;
+  for (int i = 0; i < 16; ++i)  // the timer is slow to read
+    if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {
     if (*stop) return false;
@@ -137,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* s_v = s_k + ST * C::kTile;
   __shared__ Bars b;
   __shared__ TileNote s_note[kMeta];
+  __shared__ const char* s_row[kTK];  // a copied tile's rows (null: nothing there)
   __shared__ long long s_place[kThreads / 32 + 4];
   __shared__ uint32_t s_tmem;
   __shared__ int s_stop;
@@ -144,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
   if (tid == 0) {
-    mbar_init(&b.q_full, 1);
+    mbar_init(&b.q_full, 8);
     mbar_init(&b.q_empty, 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&b.k_full[i], 1);
@@ -153,8 +158,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&b.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&b.s_full[i], 1);
-      mbar_init(&b.p_full[i], 4);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(&b.s_full[i][j], 1);
+        mbar_init(&b.p_full[i][j], 4);
+      }
+      mbar_init(&b.pv_done[i], 1);
       mbar_init(&b.o_full[i], 1);
       mbar_init(&b.o_empty[i], 4);
     }
@@ -174,13 +182,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   int r = pl.r;
   long long base = pl.base;
 
-  // Registers: 168 a thread at launch; the softmax warps hold a row of scores.
-  // 2 * 208 + 88 = 3 * 168, so every request is met from what the others return.
-  if (warp < 8)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-  else
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-
   if (warp < 8) {
     // ---- softmax: stream x, row `row` of its tile -----------------------------
     const int x = warp >> 2, row = (warp & 3) * 32 + lane;
@@ -188,50 +189,79 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_at = tmem + lane_at + x * 128, o_at = tmem + lane_at + 256 + x * 128;
     // scale 0 still has to leave hidden places at -inf: the smallest normal number stands for it
     const float c = fmaxf(fabsf(a.scale_log2), FLT_MIN);
-    uint32_t seen = 0, notes = 0, items = 0;  // S tiles of this stream, tiles of the CTA, items
+    uint32_t seen = 0, notes = 0, nitem = 0, items = 0;  // score steps of this stream; tiles, items of the CTA; of the stream
     bool alive = true;
     for (long long u = pl.u0; u < pl.u1 && alive;) {
       const Work w = work_at(a, pl, u, &r, &base);
       const int sub = w.at.single ? 0 : x;  // row tile of the stream
-      const int steps = w.at.single ? (w.tiles + 1 - x) / 2 : w.tiles;
+      const int steps = 2 * (w.at.single ? (w.tiles + 1 - x) / 2 : w.tiles);
       const int rows = w.rows - sub * 128;
       const bool busy = (warp & 3) * 32 < rows;  // this warp has rows at all
       const int qrow = w.row0 + sub * 128 + row;
       const int node = min(qrow / a.G, w.rq.n - 1);
+      // The stream's queries, a row a thread (a single item's stream B reads A's).
+      // A negative scale turns their signs; rows that do not exist are zero.
+      if (nitem > 0) {
+        alive = __all_sync(kFull, wait(&b.q_empty, (nitem - 1) & 1, a, stop));
+        if (!alive) break;
+      }
+      if (!w.at.single || x == 0) {
+        const bool real = row < rows;
+        const uint16_t* qp = static_cast<const uint16_t*>(a.q);
+        if (real) qp += (w.rq.node0 + qrow / a.G) * a.q_sn + (long long)(w.at.h * a.G + qrow % a.G) * a.q_sh;
+        const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+        for (int c0 = 0; c0 < D / 8; c0 += 8) {
+          uint4 y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            y[e] = real ? *reinterpret_cast<const uint4*>(qp + (c0 + e) * 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4*>(s_q + sub * C::kTile + (c0 / 8) * C::kChunk + row * 128 + ((e ^ (row & 7)) << 4)) =
+                make_uint4(y[e].x ^ flip, y[e].y ^ flip, y[e].z ^ flip, y[e].w ^ flip);
+        }
+        fence_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b.q_full);
+      ++nitem;
       float m_ref = -INFINITY, l = 0.f;  // in units of S
-      uint32_t odd = 0;
-      for (int i = 0; i < steps; ++i) {
-        const uint32_t no = notes + (w.at.single ? 2 * i + x : i);
+      uint32_t dtile = 0, dno[2] = {0, 0};  // drafted tiles taken, and their places in the ring of notes
+      for (int i = 0; i < steps; ++i, ++seen) {
+        const uint32_t no = notes + (w.at.single ? (i & ~1) + x : i >> 1);
         const TileNote* note = &s_note[no % kMeta];
-        alive = wait(&b.note[no % kMeta], (no / kMeta) & 1, a, stop) && wait(&b.s_full[x], seen & 1, a, stop);
-        ++seen;
+        const uint32_t buf = seen & 1, sp = s_at + buf * 64;
+        alive = wait(&b.note[no % kMeta], (no / kMeta) & 1, a, stop) &&
+                wait(&b.s_full[x][buf], (seen >> 1) & 1, a, stop);
         alive = __all_sync(kFull, alive);
         if (!alive) break;
         tc_fence_after();
         if (busy) {
-          uint32_t s[4][32];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) tmem_ld32(s_at + k * 32, s[k]);
-          uint32_t live[4] = {note->live[0], note->live[1], note->live[2], note->live[3]};
+          uint32_t s[2][32];
+          tmem_ld32(sp, s[0]);
+          tmem_ld32(sp + 32, s[1]);
+          uint32_t live[2] = {note->live[(i & 1) * 2], note->live[(i & 1) * 2 + 1]};
           const int draft = note->draft;
           if (draft >= 0) {
-            if (note->odd) odd |= 1u << draft;
+            dtile |= 1u << draft;
+            dno[draft & 1] = no % kMeta;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int j0 = draft * kTK + k * 32;
+            for (int k = 0; k < 2; ++k) {
+              const int word = draft * 4 + (i & 1) * 2 + k, j0 = word * 32;
               uint32_t see = 0xFFFFFFFFu;
               if (!a.mask)
                 see = node < j0 ? 0u : node - j0 >= 31 ? 0xFFFFFFFFu : (2u << (node - j0)) - 1u;
-              else if (draft * 4 + k < a.mask_words)
-                see = a.mask[(long long)(w.rq.node0 + node) * a.mask_words + draft * 4 + k];
+              else if (word < a.mask_words)
+                see = a.mask[(long long)(w.rq.node0 + node) * a.mask_words + word];
               live[k] &= see;
             }
           }
           tmem_wait_ld();
-          if ((live[0] & live[1] & live[2] & live[3]) != 0xFFFFFFFFu) {
+          if ((live[0] & live[1]) != 0xFFFFFFFFu) {
             // selected, whatever a hidden place holds
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (!((live[k] >> e) & 1u)) s[k][e] = 0xFF800000u;
@@ -239,9 +269,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float mx[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            mx[k] = __uint_as_float(s[k][0]);
+            mx[k] = __uint_as_float(s[k >> 1][(k & 1) * 16]);
 #pragma unroll
-            for (int e = 1; e < 32; ++e) mx[k] = fmaxf(mx[k], __uint_as_float(s[k][e]));
+            for (int e = 1; e < 16; ++e) mx[k] = fmaxf(mx[k], __uint_as_float(s[k >> 1][(k & 1) * 16 + e]));
           }
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           const bool first = i == 0;
@@ -254,7 +284,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               m_ref = m2;
               l *= al;
             }
-            if (!first) {  // S of this tile is complete, so is every product into O before it
+            if (!first) {
+              // every product into O so far (this stream's step before) has to be in
+              if (!wait(&b.pv_done[x], (seen - 1) & 1, a, stop)) al = 0.f;  // given up: the result is void
+              __syncwarp();
+              tc_fence_after();
 #pragma unroll 1
               for (int k = 0; k < D / 32; ++k) {
                 uint32_t o[32];
@@ -268,30 +302,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float mc = m_ref == -INFINITY ? 0.f : m_ref * c;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          uint32_t p[32];
 #pragma unroll
-          for (int k = 0; k < 4; k += 2) {
-            uint32_t p[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float p0 = ex2(__uint_as_float(s[k + e / 16][(2 * e) % 32]) * c - mc);
-              const float p1 = ex2(__uint_as_float(s[k + e / 16][(2 * e + 1) % 32]) * c - mc);
-              sum[e & 3] += p0 + p1;
-              p[e] = pack_bf16(p0, p1);  // the weights' one rounding
-            }
-            tmem_st32(s_at + k * 16, p);
+          for (int e = 0; e < 32; ++e) {
+            const float p0 = ex2(__uint_as_float(s[e / 16][(2 * e) % 32]) * c - mc);
+            const float p1 = ex2(__uint_as_float(s[e / 16][(2 * e + 1) % 32]) * c - mc);
+            sum[e & 3] += p0 + p1;
+            p[e] = pack_bf16(p0, p1);  // the weights' one rounding
           }
+          tmem_st32(sp, p);
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b.p_full[x]);
+        if (lane == 0) mbar_arrive(&b.p_full[x][buf]);
       }
       notes += w.tiles;
       // ---- the item's end: O and the row's maximum and sum
       if (alive && steps > 0) alive = __all_sync(kFull, wait(&b.o_full[x], items & 1, a, stop));
       if (!alive) break;
       tc_fence_after();
+      uint32_t odd = 0;
+      for (int d = 0; d < 2; ++d)
+        if ((dtile >> d) & 1u) odd |= s_note[dno[d]].odd ? 1u << d : 0u;
       const bool whole = !w.at.single && w.at.t0 == 0 && w.at.t1 == w.at.units;
       const bool mine = row < rows;
       const float inv = row_inv(l), ml2 = m_ref == -INFINITY ? -INFINITY : m_ref * c;
@@ -334,9 +368,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 out[e] = make_uint4(y[0], y[1], y[2], y[3]);
               }
             } else {
-              uint4* out = reinterpret_cast<uint4*>(part + (size_t)prow * D + k * 32);
+              // four values of every row lie together: a warp's stores are contiguous
+              uint4* out = reinterpret_cast<uint4*>(part) + k * 8 * 256 + prow;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) out[e] = make_uint4(o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
+              for (int e = 0; e < 8; ++e) out[e * 256] = make_uint4(o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
             }
           }
           __syncwarp();
@@ -359,223 +394,213 @@ __global__ void __launch_bounds__(kThreads, 1)
       u += w.at.t1 - w.at.t0;
     }
   } else if (warp == kMmaWarp) {
-    // ---- every MMA, by one thread ---------------------------------------------
-    if (lane == 0) {
-      constexpr uint32_t idqk = idesc_bf16_f32(128, 128), idpv = idesc_bf16_f32(128, D) | kIdescBMajorMN;
-      uint32_t kc = 0, vc = 0, nitem = 0, pc[2] = {0, 0}, oc[2] = {0, 0};
-      bool alive = true, any = false;
-      for (long long u = pl.u0; u < pl.u1 && alive;) {
-        const Work w = work_at(a, pl, u, &r, &base);
-        const bool single = w.at.single;
-        const int steps[2] = {single ? (w.tiles + 1) / 2 : w.tiles, single ? w.tiles / 2 : w.tiles};
-        alive = wait(&b.q_full, nitem & 1, a, stop);
-        if (!alive) break;
-        any = true;
-        // S_x of its next tile; K is let go behind its last reader
-        auto qk = [&](int x) {
-          const bool fresh = single || x == 0;
-          const uint32_t st = (fresh ? kc : kc - 1) % ST;
-          if (fresh) {
-            if (!wait(&b.k_full[st], (kc / ST) & 1, a, stop)) return false;
-            ++kc;
-          }
-          tc_fence_after();
-          const uint32_t q0 = smem_u32(s_q) + (single ? 0 : x) * C::kTile, k0 = smem_u32(s_k) + st * C::kTile;
+    // ---- every MMA: the warp stays together and one lane issues ----------------
+    constexpr uint32_t idqk = idesc_bf16_f32(128, 64), idpv = idesc_bf16_f32(128, D) | kIdescBMajorMN;
+    const uint64_t dq = desc_kmajor_sw128(smem_u32(s_q)), dk = desc_kmajor_sw128(smem_u32(s_k)),
+                   dv = desc_mnmajor_sw128(smem_u32(s_v), C::kChunk);
+    const uint32_t hi_k = (uint32_t)(dq >> 32), hi_v = (uint32_t)(dv >> 32);
+    const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+    uint32_t cnt = 0, nitem = 0, qs[2] = {0, 0}, ps[2] = {0, 0}, oc[2] = {0, 0};
+    bool alive = true;
+    for (long long u = pl.u0; u < pl.u1 && alive;) {
+      const Work w = work_at(a, pl, u, &r, &base);
+      const bool single = __shfl_sync(kFull, (int)w.at.single, 0);
+      const int tiles = __shfl_sync(kFull, w.tiles, 0);
+      const int steps[2] = {2 * (single ? (tiles + 1) / 2 : tiles), 2 * (single ? tiles / 2 : tiles)};
+      alive = __all_sync(kFull, wait(&b.q_full, nitem & 1, a, stop));
+      if (!alive) break;
+      // scores of step j of stream x (64 tokens); K is let go behind its last reader
+      auto qk = [&](int x, int j) {
+        const uint32_t no = cnt + (single ? (j & ~1) + x : j >> 1), st = no % ST;
+        const bool ok = (j & 1) || wait(&b.k_full[st], (no / ST) & 1, a, stop);
+        if (!__all_sync(kFull, ok)) return false;
+        tc_fence_after();
+        const uint32_t buf = qs[x]++ & 1, s_to = tm + x * 128 + buf * 64;
+        const uint32_t q0 = (uint32_t)dq + ((single ? 0 : x) * C::kTile >> 4);
+        const uint32_t k0 = (uint32_t)dk + ((st * C::kTile + (j & 1) * (C::kChunk / 2)) >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k / 4) * C::kChunk + (k % 4) * 32;
-            mma_bf16(tmem + x * 128, desc_kmajor_sw128(q0 + off), desc_kmajor_sw128(k0 + off), idqk, k > 0);
+            const uint32_t off = ((k / 4) * C::kChunk + (k % 4) * 32) >> 4;
+            mma_bf16_lo(s_to, q0 + off, k0 + off, hi_k, idqk, k > 0);
           }
-          mma_commit(&b.s_full[x]);
-          if (single || x == 1) mma_commit(&b.k_empty[st]);
-          return true;
-        };
-        auto pv = [&](int x, bool first) {
-          const bool fresh = single || x == 0;
-          const uint32_t st = (fresh ? vc : vc - 1) % ST;
-          if (!wait(&b.p_full[x], pc[x] & 1, a, stop)) return false;
-          ++pc[x];
-          if (fresh) {
-            if (!wait(&b.v_full[st], (vc / ST) & 1, a, stop)) return false;
-            ++vc;
-          }
-          // O is read out before the next item writes it
-          if (first && oc[x] > 0 && !wait(&b.o_empty[x], (oc[x] - 1) & 1, a, stop)) return false;
-          tc_fence_after();
-          const uint32_t v0 = smem_u32(s_v) + st * C::kTile;
-#pragma unroll
-          for (int k = 0; k < kTK / 16; ++k)
-            mma_bf16_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8, desc_mnmajor_sw128(v0 + k * 2048, C::kChunk), idpv,
-                        !(first && k == 0));
-          if (single || x == 1) mma_commit(&b.v_empty[st]);
-          return true;
-        };
-        for (int x = 0; x < 2 && alive; ++x)
-          if (steps[x] > 0) alive = qk(x);
-        for (int i = 0; i < steps[0] && alive; ++i) {
-          if (i == steps[0] - 1) mma_commit(&b.q_empty);  // every S of the item is on its way
-          for (int x = 0; x < 2 && alive; ++x) {
-            if (i >= steps[x]) continue;
-            alive = pv(x, i == 0);
-            if (!alive) break;
-            if (i + 1 < steps[x]) {
-              alive = qk(x);
-            } else {
-              mma_commit(&b.o_full[x]);
-              ++oc[x];
-            }
-          }
+          mma_commit(&b.s_full[x][buf]);
+          if ((j & 1) && (single || x == 1)) mma_commit(&b.k_empty[st]);
         }
-        ++nitem;
-        u += w.at.t1 - w.at.t0;
+        __syncwarp();
+        return true;
+      };
+      auto pv = [&](int x, int j) {
+        const uint32_t no = cnt + (single ? (j & ~1) + x : j >> 1), st = no % ST;
+        const uint32_t buf = ps[x] & 1, p_at = tm + x * 128 + buf * 64, o_to = tm + 256 + x * 128;
+        bool ok = wait(&b.p_full[x][buf], (ps[x] >> 1) & 1, a, stop);
+        ++ps[x];
+        if (!(j & 1)) ok = ok && wait(&b.v_full[st], (no / ST) & 1, a, stop);
+        // O is read out before the next item writes it
+        if (j == 0 && oc[x] > 0) ok = ok && wait(&b.o_empty[x], (oc[x] - 1) & 1, a, stop);
+        if (!__all_sync(kFull, ok)) return false;
+        tc_fence_after();
+        const uint32_t v0 = (uint32_t)dv + ((st * C::kTile + (j & 1) * (C::kChunk / 2)) >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_bf16_ts_lo(o_to, p_at + k * 8, v0 + (k * 2048 >> 4), hi_v, idpv, j > 0 || k > 0);
+          mma_commit(&b.pv_done[x]);
+          if ((j & 1) && (single || x == 1)) mma_commit(&b.v_empty[st]);
+          if (j + 1 == steps[x]) mma_commit(&b.o_full[x]);
+        }
+        __syncwarp();
+        return true;
+      };
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (alive && j < steps[x]) alive = qk(x, j);
+      for (int j = 0; j < steps[0] && alive; ++j) {
+        if (j == steps[0] - 2 && elect_one()) mma_commit(&b.q_empty);  // every score of the item is on its way
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (j >= steps[x] || !alive) continue;
+          alive = pv(x, j);
+          if (alive && j + 2 < steps[x]) alive = qk(x, j + 2);
+          if (j + 1 == steps[x]) ++oc[x];
+        }
       }
-      if (any) {  // nothing may be in flight when TMEM and shared memory go
-        mma_commit(&b.drain);
-        mbar_wait_bounded(&b.drain, 0, a.wait_ns);
-      }
+      cnt += tiles;
+      ++nitem;
+      u += w.at.t1 - w.at.t0;
     }
-    __syncwarp();
+    if (nitem > 0 || !alive) {  // nothing may be in flight when TMEM and shared memory go
+      if (elect_one()) mma_commit(&b.drain);
+      __syncwarp();
+      mbar_wait_bounded(&b.drain, 0, a.wait_ns);
+      __syncwarp();
+    }
   } else {
     // ---- loaders: three warps that stay in step (they leave together) ------------
     const int lt = tid - kLoadWarp * 32;
-    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale turns the queries' signs
     const int npiece = kTK / tb;                                  // page pieces of a tile
-    uint32_t cnt = 0, nitem = 0;
+    uint32_t cnt = 0, sent[2] = {0, 0};  // tiles of K and of V under way or done
     bool alive = true;
-    for (long long u = pl.u0; u < pl.u1;) {
-      const Work w = work_at(a, pl, u, &r, &base);
-      const int h = w.at.h, nsub = w.at.single ? 1 : 2;
-      if (alive && nitem > 0) alive = wait(&b.q_empty, (nitem - 1) & 1, a, stop);
-      alive = !named_sync_or(1, kLoaders, !alive);
-      if (!alive) break;
-      for (int i = lt; i < nsub * 128 * (D / 8); i += kLoaders) {
-        const int m = i / (D / 8), c8 = i % (D / 8), qrow = w.row0 + m;
-        uint4 y = make_uint4(0, 0, 0, 0);
-        if (m < w.rows) {
-          y = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (w.rq.node0 + qrow / a.G) * a.q_sn +
-                                              (long long)(h * a.G + qrow % a.G) * a.q_sh + c8 * 8);
-          y.x ^= flip;
-          y.y ^= flip;
-          y.z ^= flip;
-          y.w ^= flip;
-        }
-        *reinterpret_cast<uint4*>(s_q + (m >> 7) * C::kTile + (c8 >> 3) * C::kChunk + (m & 127) * 128 +
-                                  (((c8 & 7) ^ (m & 7)) << 4)) = y;
+    // K (or V) of tile i of the item into its stage; false when all three warps give up
+    auto load = [&](const Work& w, int i, bool val) -> bool {
+      const int h = w.at.h, t = w.first + i;
+      const uint32_t no = cnt + i, st = no % ST;
+      TileNote* note = &s_note[no % kMeta];
+      unsigned char* dst = (val ? s_v : s_k) + st * C::kTile;
+      uint64_t* bar = val ? &b.v_full[st] : &b.k_full[st];
+      const bool draft = t >= w.rq.tiles_c;
+      // a piece is a run of tb tokens in one page (tb divides the block size)
+      int page = 0, tok = 0;
+      bool full = true;
+      if (!draft && lane < npiece) {
+        TokenAt at;
+        const int v = t * kTK + lane * tb;
+        full = token_at(a, w.r, w.rq, v + tb - 1, false, &at) && token_at(a, w.r, w.rq, v, false, &at);
+        page = at.page;
+        tok = at.tok;
       }
-      fence_async_smem();
-      named_sync(1, kLoaders);
-      if (lt == 0) mbar_arrive(&b.q_full);
-      ++nitem;
-      for (int i = 0; i < w.tiles; ++i, ++cnt) {
-        const int t = w.first + i;
-        const uint32_t st = cnt % ST, ph = ((cnt / ST) & 1) ^ 1;
-        TileNote* note = &s_note[cnt % kMeta];
-        const bool draft = t >= w.rq.tiles_c;
-        // a piece is a run of tb tokens in one page (tb divides the block size)
-        int page = 0, tok = 0;
-        bool full = true;
-        if (!draft && lane < npiece) {
-          TokenAt at;
-          const int v = t * kTK + lane * tb;
-          full = token_at(a, w.r, w.rq, v + tb - 1, false, &at) && token_at(a, w.r, w.rq, v, false, &at);
-          page = at.page;
-          tok = at.tok;
-        }
-        full = __all_sync(kFull, full) && !draft;
-        alive = alive && wait(&b.k_empty[st], ph, a, stop);
-        alive = !named_sync_or(1, kLoaders, !alive);
-        if (!alive) break;
-        if (full) {
-          if (warp == kLoadWarp) {
-            if (lane == 0) {
+      full = __all_sync(kFull, full) && !draft;
+      alive = alive && wait(val ? &b.v_empty[st] : &b.k_empty[st], ((no / ST) & 1) ^ 1, a, stop);
+      alive = !named_sync_or(1, kLoaders, !alive);
+      if (!alive) return false;
+      ++sent[val];
+      if (full) {
+        if (warp == kLoadWarp) {
+          if (lane == 0) {
+            if (!val) {
               note->live[0] = note->live[1] = note->live[2] = note->live[3] = 0xFFFFFFFFu;
               note->draft = -1;
-              note->odd = 0;
-              mbar_arrive(&b.note[cnt % kMeta]);
-              mbar_arrive_expect_tx(&b.k_full[st], C::kTile);
+              mbar_arrive(&b.note[no % kMeta]);
             }
-            __syncwarp();
-            if (lane < npiece) {
-#pragma unroll
-              for (int c = 0; c < NC; ++c)
-                tma_load_4d(s_k + st * C::kTile + c * C::kChunk + lane * tb * 128, &tmk, c * 64, tok, h, page,
-                            &b.k_full[st]);
-            }
-            alive = __all_sync(kFull, wait(&b.v_empty[st], ph, a, stop));
-            if (alive) {
-              if (lane == 0) mbar_arrive_expect_tx(&b.v_full[st], C::kTile);
-              __syncwarp();
-              if (lane < npiece) {
-#pragma unroll
-                for (int c = 0; c < NC; ++c)
-                  tma_load_4d(s_v + st * C::kTile + c * C::kChunk + lane * tb * 128, &tmv, c * 64, tok, h, page,
-                              &b.v_full[st]);
-              }
-            }
+            mbar_arrive_expect_tx(bar, C::kTile);
           }
-          continue;
+          __syncwarp();
+          if (lane < npiece) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              tma_load_4d(dst + c * C::kChunk + lane * tb * 128, val ? &tmv : &tmk, c * 64, tok, h, page, bar);
+          }
         }
-        // copied by the 96 threads
-        alive = wait(&b.v_empty[st], ph, a, stop);
-        alive = !named_sync_or(1, kLoaders, !alive);
-        if (!alive) break;
-        bool hit = false;
+        return true;
+      }
+      // copied by the 96 threads
+      for (int m = lt; m < kTK; m += kLoaders) {
+        const char* p = nullptr;
+        const int n = (t - w.rq.tiles_c) * kTK + m;
+        TokenAt at;
+        if (!draft && token_at(a, w.r, w.rq, t * kTK + m, true, &at)) {
+          const KCache& kc = val ? a.vc : a.kc;
+          p = static_cast<const char*>(kc.base) +
+              (a.layer * kc.sL + at.page * kc.sP + h * kc.sH + at.tok * kc.sT) * 2;
+        } else if (draft && a.dk && n < w.rq.n) {
+          p = val ? static_cast<const char*>(a.dv) + ((w.rq.node0 + n) * a.dv_sn + h * a.dv_sh) * 2
+                  : static_cast<const char*>(a.dk) + ((w.rq.node0 + n) * a.dk_sn + h * a.dk_sh) * 2;
+        }
+        s_row[m] = p;
+      }
+      named_sync(1, kLoaders);
+      auto piece_at = [&](int j) {
+        const int m = j / (D / 8), c8 = j % (D / 8);
+        return dst + (c8 >> 3) * C::kChunk + m * 128 + (((c8 & 7) ^ (m & 7)) << 4);
+      };
+      for (int j = lt; j < kTK * (D / 8); j += kLoaders) {
+        const char* p = s_row[j / (D / 8)];
+        cp_async16(smem_u32(piece_at(j)), p ? p + (j % (D / 8)) * 16 : static_cast<const char*>(a.q), p != nullptr);
+      }
+      cp_wait_all();
+      bool hit = false;
+      if (draft && val)  // what is not finite is added back at the end, to the nodes that see it
         for (int j = lt; j < kTK * (D / 8); j += kLoaders) {
-          const int m = j / (D / 8), c8 = j % (D / 8);
-          uint4 ky = make_uint4(0, 0, 0, 0), vy = ky;
-          if (!draft) {
-            TokenAt at;
-            if (token_at(a, w.r, w.rq, t * kTK + m, false, &at)) {
-              ky = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.kc.base) + a.layer * a.kc.sL +
-                                                   at.page * a.kc.sP + h * a.kc.sH + at.tok * a.kc.sT + c8 * 8);
-              vy = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.vc.base) + a.layer * a.vc.sL +
-                                                   at.page * a.vc.sP + h * a.vc.sH + at.tok * a.vc.sT + c8 * 8);
-            }
-          } else {
-            const int n = (t - w.rq.tiles_c) * kTK + m;
-            if (a.dk && n < w.rq.n) {
-              ky = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dk) + (w.rq.node0 + n) * a.dk_sn +
-                                                   h * a.dk_sh + c8 * 8);
-              vy = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dv) + (w.rq.node0 + n) * a.dv_sn +
-                                                   h * a.dv_sh + c8 * 8);
-              hit |= drop_nonfinite(&vy);  // added back to the nodes that see it at the end
-            }
+          uint4 y = *reinterpret_cast<uint4*>(piece_at(j));
+          if (drop_nonfinite(&y)) {
+            *reinterpret_cast<uint4*>(piece_at(j)) = y;
+            hit = true;
           }
-          const uint32_t off = st * C::kTile + (c8 >> 3) * C::kChunk + m * 128 + (((c8 & 7) ^ (m & 7)) << 4);
-          *reinterpret_cast<uint4*>(s_k + off) = ky;
-          *reinterpret_cast<uint4*>(s_v + off) = vy;
         }
-        fence_async_smem();
-        hit = named_sync_or(1, kLoaders, hit);
-        if (warp == kLoadWarp) {
-          uint32_t live[4];
+      fence_async_smem();
+      hit = named_sync_or(1, kLoaders, hit);
+      if (warp == kLoadWarp) {
+        uint32_t live[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            TokenAt at;
-            const int n = (t - w.rq.tiles_c) * kTK + k * 32 + lane;
-            const bool ok = draft ? a.dk && n < w.rq.n : token_at(a, w.r, w.rq, t * kTK + k * 32 + lane, true, &at);
-            live[k] = __ballot_sync(kFull, ok);
-          }
-          if (lane == 0) {
+        for (int k = 0; k < 4; ++k) live[k] = __ballot_sync(kFull, s_row[k * 32 + lane] != nullptr);
+        if (lane == 0) {
+          if (val) {
+            note->odd = hit;
+          } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) note->live[k] = live[k];
             note->draft = draft ? t - w.rq.tiles_c : -1;
-            note->odd = hit;
-            mbar_arrive(&b.note[cnt % kMeta]);
-            mbar_arrive(&b.k_full[st]);
-            mbar_arrive(&b.v_full[st]);
+            mbar_arrive(&b.note[no % kMeta]);
           }
-          __syncwarp();
+          mbar_arrive(bar);
         }
+        __syncwarp();
       }
+      return true;
+    };
+    for (long long u = pl.u0; u < pl.u1;) {
+      const Work w = work_at(a, pl, u, &r, &base);
+      // K of a tile goes out ahead of V of the tile before: with two stages the
+      // scores of both streams run a tile ahead of their products with V.
+      bool left = false;
+      for (int i = 0; i <= w.tiles && !left; ++i) {
+        if (i < w.tiles) left = !load(w, i, false);
+        if (!left && i > 0) left = !load(w, i - 1, true);
+      }
+      if (left) break;
+      cnt += w.tiles;
       u += w.at.t1 - w.at.t0;
     }
     // copies in flight end before the CTA does (on the ordinary way they were all waited for)
-    if (*stop && warp == kLoadWarp && lane == 0)
-      for (uint32_t i = cnt > ST ? cnt - ST : 0; i <= cnt; ++i) {
+    if (*stop && warp == kLoadWarp && lane == 0) {
+      for (uint32_t i = sent[0] > ST ? sent[0] - ST : 0; i < sent[0]; ++i)
         mbar_wait_bounded(&b.k_full[i % ST], (i / ST) & 1, a.wait_ns);
+      for (uint32_t i = sent[1] > ST ? sent[1] - ST : 0; i < sent[1]; ++i)
         mbar_wait_bounded(&b.v_full[i % ST], (i / ST) & 1, a.wait_ns);
-      }
+    }
     __syncwarp();
   }
   tc_fence_before();
