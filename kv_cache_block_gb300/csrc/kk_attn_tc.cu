@@ -3,8 +3,8 @@
 //
 // One CTA per SM with two streams, A and B, each a 128-row tile with its own
 // accumulator O (D columns of TMEM) and two score buffers S of 64 tokens. Warps
-// 0-3 are A's softmax, warps 4-7 B's (a thread owns a row), warp 8 issues every
-// MMA (tcgen05), warps 9-11 load:
+// 0-3 are A's softmax, warps 4-7 B's (a thread owns a row), warp 8 issues A's
+// MMAs (tcgen05) and warp 9 B's, warps 10-11 load:
 //   S_x = Q_x K^T    both operands in shared memory
 //   P_x = exp2(S_x * c - m_x)  written over S_x as bf16, the A operand
 //   O_x += P_x V     P from TMEM, V from shared memory as it lies (MN-major)
@@ -38,7 +38,7 @@ namespace kk {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kLoaders = 96;
+constexpr int kMmaWarp = 8, kLoadWarp = 10, kLoaders = 64;
 constexpr int kTK = 128;
 constexpr int kMeta = 8;  // ring of per-tile notes from the loaders to the softmax warps
 constexpr int kTmemCols = 512;
@@ -73,19 +73,23 @@ struct Bars {
 
 // Waits for a barrier's phase; gives up (false) past the limit or when another
 // role has given up, and tells the others.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const AttnArgs& a, volatile int* stop) {
-  for (int i = 0; i < 16; ++i)  // the timer is slow to read
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, unsigned long long limit, int* err,
+                                       volatile int* stop) {
+  for (int i = 0; i < 64; ++i)  // the timer is slow to read
     if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {
     if (*stop) return false;
-    if (globaltimer_ns() - t0 > a.wait_ns) {
+    if (globaltimer_ns() - t0 > limit) {
       *stop = 1;
-      flag_error(a.err, kErrTimeout);
+      flag_error(err, kErrTimeout);
       return false;
     }
   }
   return true;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const AttnArgs& a, volatile int* stop) {
+  return mbar_try_wait(bar, parity) || wait_long(bar, parity, a.wait_ns, a.err, stop);
 }
 
 // An item's place in a CTA's range.
@@ -150,12 +154,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   if (tid == 0) {
     mbar_init(&b.q_full, 8);
-    mbar_init(&b.q_empty, 1);
+    mbar_init(&b.q_empty, 2);  // both streams
     for (int i = 0; i < 4; ++i) {
       mbar_init(&b.k_full[i], 1);
-      mbar_init(&b.k_empty[i], 1);
+      mbar_init(&b.k_empty[i], 2);  // both streams, or a single item's one stream twice
       mbar_init(&b.v_full[i], 1);
-      mbar_init(&b.v_empty[i], 1);
+      mbar_init(&b.v_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       for (int j = 0; j < 2; ++j) {
@@ -167,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&b.o_empty[i], 4);
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(&b.note[i], 1);
-    mbar_init(&b.drain, 1);
+    mbar_init(&b.drain, 2);
     s_stop = 0;
     fence_mbar_init();
   }
@@ -393,98 +397,97 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       u += w.at.t1 - w.at.t0;
     }
-  } else if (warp == kMmaWarp) {
-    // ---- every MMA: the warp stays together and one lane issues ----------------
+  } else if (warp < kLoadWarp) {
+    // ---- MMAs of stream x: the warp stays together and one lane issues ---------
+    // (one warp for both streams left the tensor cores idle half the time: waits,
+    // commits and the issue itself take longer than 12 products of this size)
     constexpr uint32_t idqk = idesc_bf16_f32(128, 64), idpv = idesc_bf16_f32(128, D) | kIdescBMajorMN;
+    const int x = __shfl_sync(kFull, warp - kMmaWarp, 0);
     const uint64_t dq = desc_kmajor_sw128(smem_u32(s_q)), dk = desc_kmajor_sw128(smem_u32(s_k)),
                    dv = desc_mnmajor_sw128(smem_u32(s_v), C::kChunk);
     const uint32_t hi_k = (uint32_t)(dq >> 32), hi_v = (uint32_t)(dv >> 32);
     const uint32_t tm = __shfl_sync(kFull, tmem, 0);
-    uint32_t cnt = 0, nitem = 0, qs[2] = {0, 0}, ps[2] = {0, 0}, oc[2] = {0, 0};
+    const uint32_t s_of = tm + x * 128, o_to = tm + 256 + x * 128;
+    uint32_t cnt = 0, nitem = 0, qs = 0, ps = 0, oc = 0;
     bool alive = true;
     for (long long u = pl.u0; u < pl.u1 && alive;) {
       const Work w = work_at(a, pl, u, &r, &base);
       const bool single = __shfl_sync(kFull, (int)w.at.single, 0);
       const int tiles = __shfl_sync(kFull, w.tiles, 0);
-      const int steps[2] = {2 * (single ? (tiles + 1) / 2 : tiles), 2 * (single ? tiles / 2 : tiles)};
+      const int steps = 2 * (single ? (tiles + 1 - x) / 2 : tiles);
+      const uint32_t q0 = (uint32_t)dq + ((single ? 0 : x) * C::kTile >> 4);
       alive = __all_sync(kFull, wait(&b.q_full, nitem & 1, a, stop));
       if (!alive) break;
-      // scores of step j of stream x (64 tokens); K is let go behind its last reader
-      auto qk = [&](int x, int j) {
+      // scores of step j (64 tokens); K is let go behind the tile's second half
+      auto qk = [&](int j) {
         const uint32_t no = cnt + (single ? (j & ~1) + x : j >> 1), st = no % ST;
         const bool ok = (j & 1) || wait(&b.k_full[st], (no / ST) & 1, a, stop);
         if (!__all_sync(kFull, ok)) return false;
         tc_fence_after();
-        const uint32_t buf = qs[x]++ & 1, s_to = tm + x * 128 + buf * 64;
-        const uint32_t q0 = (uint32_t)dq + ((single ? 0 : x) * C::kTile >> 4);
+        const uint32_t buf = qs++ & 1;
         const uint32_t k0 = (uint32_t)dk + ((st * C::kTile + (j & 1) * (C::kChunk / 2)) >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t off = ((k / 4) * C::kChunk + (k % 4) * 32) >> 4;
-            mma_bf16_lo(s_to, q0 + off, k0 + off, hi_k, idqk, k > 0);
+            mma_bf16_lo(s_of + buf * 64, q0 + off, k0 + off, hi_k, idqk, k > 0);
           }
           mma_commit(&b.s_full[x][buf]);
-          if ((j & 1) && (single || x == 1)) mma_commit(&b.k_empty[st]);
+          if (j & 1) {
+            mma_commit(&b.k_empty[st]);
+            if (single) mma_commit(&b.k_empty[st]);
+          }
         }
         __syncwarp();
         return true;
       };
-      auto pv = [&](int x, int j) {
+      auto pv = [&](int j) {
         const uint32_t no = cnt + (single ? (j & ~1) + x : j >> 1), st = no % ST;
-        const uint32_t buf = ps[x] & 1, p_at = tm + x * 128 + buf * 64, o_to = tm + 256 + x * 128;
-        bool ok = wait(&b.p_full[x][buf], (ps[x] >> 1) & 1, a, stop);
-        ++ps[x];
-        if (!(j & 1)) ok = ok && wait(&b.v_full[st], (no / ST) & 1, a, stop);
+        const uint32_t buf = ps & 1;
+        bool ok = (j & 1) || wait(&b.v_full[st], (no / ST) & 1, a, stop);
         // O is read out before the next item writes it
-        if (j == 0 && oc[x] > 0) ok = ok && wait(&b.o_empty[x], (oc[x] - 1) & 1, a, stop);
+        if (j == 0 && oc > 0) ok = ok && wait(&b.o_empty[x], (oc - 1) & 1, a, stop);
+        ok = ok && wait(&b.p_full[x][buf], (ps >> 1) & 1, a, stop);
+        ++ps;
         if (!__all_sync(kFull, ok)) return false;
         tc_fence_after();
         const uint32_t v0 = (uint32_t)dv + ((st * C::kTile + (j & 1) * (C::kChunk / 2)) >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_bf16_ts_lo(o_to, p_at + k * 8, v0 + (k * 2048 >> 4), hi_v, idpv, j > 0 || k > 0);
+            mma_bf16_ts_lo(o_to, s_of + buf * 64 + k * 8, v0 + (k * 2048 >> 4), hi_v, idpv, j > 0 || k > 0);
           mma_commit(&b.pv_done[x]);
-          if ((j & 1) && (single || x == 1)) mma_commit(&b.v_empty[st]);
-          if (j + 1 == steps[x]) mma_commit(&b.o_full[x]);
+          if (j & 1) {
+            mma_commit(&b.v_empty[st]);
+            if (single) mma_commit(&b.v_empty[st]);
+          }
+          if (j + 1 == steps) mma_commit(&b.o_full[x]);
         }
         __syncwarp();
         return true;
       };
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (alive && j < steps[x]) alive = qk(x, j);
-      for (int j = 0; j < steps[0] && alive; ++j) {
-        if (j == steps[0] - 2 && elect_one()) mma_commit(&b.q_empty);  // every score of the item is on its way
-        __syncwarp();
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (j >= steps[x] || !alive) continue;
-          alive = pv(x, j);
-          if (alive && j + 2 < steps[x]) alive = qk(x, j + 2);
-          if (j + 1 == steps[x]) ++oc[x];
-        }
-      }
+      if (steps > 0) alive = qk(0) && qk(1);
+      for (int j = 0; j < steps && alive; ++j) alive = pv(j) && (j + 2 >= steps || qk(j + 2));
+      // every score of the item is in, or on its way
+      if (elect_one()) mma_commit(&b.q_empty);
+      __syncwarp();
+      oc += steps > 0;
       cnt += tiles;
       ++nitem;
       u += w.at.t1 - w.at.t0;
     }
-    if (nitem > 0 || !alive) {  // nothing may be in flight when TMEM and shared memory go
-      if (elect_one()) mma_commit(&b.drain);
-      __syncwarp();
-      mbar_wait_bounded(&b.drain, 0, a.wait_ns);
-      __syncwarp();
-    }
+    // nothing may be in flight when TMEM and shared memory go
+    if (elect_one()) mma_commit(&b.drain);
+    __syncwarp();
+    mbar_wait_bounded(&b.drain, 0, a.wait_ns);
+    __syncwarp();
   } else {
-    // ---- loaders: three warps that stay in step (they leave together) ------------
+    // ---- loaders: two warps that stay in step (they leave together) --------------
     const int lt = tid - kLoadWarp * 32;
     const int npiece = kTK / tb;                                  // page pieces of a tile
     uint32_t cnt = 0, sent[2] = {0, 0};  // tiles of K and of V under way or done
     bool alive = true;
-    // K (or V) of tile i of the item into its stage; false when all three warps give up
+    // K (or V) of tile i of the item into its stage; false when both warps give up
     auto load = [&](const Work& w, int i, bool val) -> bool {
       const int h = w.at.h, t = w.first + i;
       const uint32_t no = cnt + i, st = no % ST;
@@ -526,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return true;
       }
-      // copied by the 96 threads
+      // copied by the 64 threads
       for (int m = lt; m < kTK; m += kLoaders) {
         const char* p = nullptr;
         const int n = (t - w.rq.tiles_c) * kTK + m;
