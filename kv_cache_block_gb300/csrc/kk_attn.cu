@@ -238,7 +238,7 @@ __device__ __forceinline__ Cut find_cut(const AttnArgs& a, int r, int h, int mt,
       c.n = (int)(((hi + 1) * G - 1) / all) - c.c0 + 1;
       c.first = (long long)c.c0 * all / G == lo ? 0 : 1;  // c0's slot: its first item, or its last
       c.halves = it.single ? 2 : 1;  // a single's streams leave a part each, M/2 rows apart
-      if (c.n == 1 && !it.single) c.n = 0;
+      if (c.n == 1) c.n = 0;
       c.node0 = rq.node0;
       c.rows = rq.n * a.G;
     }
@@ -349,26 +349,29 @@ __global__ void __launch_bounds__(D * 2) attn_combine_tc_kernel(const AttnArgs a
   const int m = blockIdx.y * 32 + ln, row = mt * M + m;
   if (row >= cut.rows) return;
   pdl_wait();
+  const int parts = cut.n * cut.halves, sh = cut.halves - 1;
+  auto slot = [&](int i) { return partial_slot(a, cut.c0 + (i >> sh), i >> sh ? 0 : cut.first, M, D); };
+  auto at_row = [&](int i) { return m + (i & sh) * (M / 2); };
   float mm = -INFINITY, l = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < parts; ++i) mm = fmaxf(mm, slot(i)[M * D + at_row(i)]);
+  const float ref = mm == -INFINITY ? 0.f : mm;
   float4 acc[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int i = 0; i < cut.n * cut.halves; ++i) {
-    const int c = cut.halves == 2 ? i >> 1 : i, pr = cut.halves == 2 ? m + (i & 1) * (M / 2) : m;
-    const float* part = partial_slot(a, cut.c0 + c, c == 0 ? cut.first : 0, M, D);
-    const float pm = part[M * D + pr], pl = part[M * D + M + pr];
-    const float m2 = fmaxf(mm, pm), ref = m2 == -INFINITY ? 0.f : m2;
-    const float f = ex2(mm - ref), al = ex2(pm - ref);
-    l = l * f + pl * al;
-    mm = m2;
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) {
+    const float* part = slot(i);
+    const int pr = at_row(i);
+    const float al = ex2(part[M * D + pr] - ref);
+    l += part[M * D + M + pr] * al;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float4 x = reinterpret_cast<const float4*>(part)[(w * 4 + e) * M + pr];
-      acc[e].x = acc[e].x * f + x.x * al;
-      acc[e].y = acc[e].y * f + x.y * al;
-      acc[e].z = acc[e].z * f + x.z * al;
-      acc[e].w = acc[e].w * f + x.w * al;
+      acc[e].x += x.x * al;
+      acc[e].y += x.y * al;
+      acc[e].z += x.z * al;
+      acc[e].w += x.w * al;
     }
   }
   const float inv = row_inv(l);
@@ -438,7 +441,9 @@ AttnPlan plan(const KCache& kc, const KCache& vc, int max_nodes, int G) {
   return attn_mma_plan(kc, rows);
 }
 
-size_t plan_bytes(const AttnPlan& pl, int D) { return (size_t)pl.grid * 2 * pl.M * (D + 2) * sizeof(float); }
+size_t plan_bytes(const AttnPlan& pl, int D) {
+  return (size_t)pl.grid * (pl.kind == AttnPlan::kTc ? 3 : 2) * pl.M * (D + 2) * sizeof(float);
+}
 
 }  // namespace
 

@@ -226,10 +226,10 @@ __device__ __forceinline__ AttnPlace find_place(const AttnArgs& a, int cta, int 
   return p;
 }
 
-// Partial results: slot s (two per CTA) holds M*D accumulators, then M running
-// maxima (log2 domain) and M sums.
+// Partial results: a slot (two per CTA, and a third where row tiles come in
+// pairs) holds M*D accumulators, then M running maxima (log2 domain) and M sums.
 __device__ __forceinline__ float* partial_slot(const AttnArgs& a, int cta, int which, int M, int D) {
-  return a.ws + (size_t)(2 * cta + which) * M * (D + 2);
+  return a.ws + (size_t)((a.twin ? 3 : 2) * cta + which) * M * (D + 2);
 }
 
 // 1 / sum and lse of a row with running maximum m (log2 domain) and sum l; a

@@ -4,27 +4,28 @@
 // One CTA per SM with two streams, A and B, each a 128-row tile with its own
 // accumulator O (D columns of TMEM) and two score buffers S of 64 tokens. Warps
 // 0-3 are A's softmax, warps 4-7 B's (a thread owns a row), warp 8 issues A's
-// MMAs (tcgen05) and warp 9 B's, warps 10-11 load:
+// MMAs (tcgen05) and warp 9 B's, warp 10 loads:
 //   S_x = Q_x K^T    both operands in shared memory
 //   P_x = exp2(S_x * c - m_x)  written over S_x as bf16, the A operand
 //   O_x += P_x V     P from TMEM, V from shared memory as it lies (MN-major)
 // MMAs of one thread run in order, so the scores two steps on follow P_x V into
-// its buffer at once, and the softmax of the next step finds its scores ready:
-// with one 128-token buffer a stream it waited for P V and Q K^T each time
-// (199 us against TODO us on the 64-node tree). The maximum a row's weights are taken against
-// moves only when the true one has risen past it by 2^8: until then the weights
-// stay below 2^8, which costs bf16 nothing, and O need not be rescaled.
+// its buffer at once, and the softmax of the next step finds its scores ready.
+// The maximum a row's weights are taken against moves only when the true one has
+// risen past it by 2^8: until then the weights stay below 2^8, which costs bf16
+// nothing, and O need not be rescaled.
 //
-// An item is a pair of row tiles (both streams take every token tile) or, for
-// the last tile of an odd number, a single one (the streams take alternate
-// token tiles and leave two partial results): either way a unit of work is two
-// tile products, and both streams are busy.
+// An item is a pair of row tiles (both streams take every token) or, for the
+// last tile of an odd number, a single one (A takes the first 64 tokens of every
+// 128-token tile, B the others, and they leave two partial results): either way
+// both streams are busy, every tile is read by both, and a unit of work (one
+// tile of a pair, two of a single) is four steps of 64 tokens.
 //
 // Full tiles of tokens come by TMA (one box per page piece and 64 dims, 128-byte
-// swizzle). Tiles with a place that holds no token (the end of a request, a
-// partial selected block, a bad page) and tiles of drafted nodes are copied by
-// the loader warps, zeros for what is not there: a weight of zero must not meet
-// what such a place holds.
+// swizzle), K of a tile ahead of V of the tile before; where the pages lie is
+// looked up a tile ahead. Tiles with a place that holds no token (the end of a
+// request, a partial selected block, a bad page) and tiles of drafted nodes are
+// copied by the loader's lanes, zeros for what is not there: a weight of zero
+// must not meet what such a place holds.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -38,28 +39,27 @@ namespace kk {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kMmaWarp = 8, kLoadWarp = 10, kLoaders = 64;
+constexpr int kMmaWarp = 8, kLoadWarp = 10;
 constexpr int kTK = 128;
-constexpr int kMeta = 8;  // ring of per-tile notes from the loaders to the softmax warps
+constexpr int kMeta = 8;  // ring of per-tile notes from the loader to the softmax warps
 constexpr int kTmemCols = 512;
 constexpr float kRise = 8.f;
 
-// Notes on a tile for the softmax warps: which places hold a token, the drafted
-// tile it is (-1: cached tokens), and, once its Values are there, whether one
-// of a draft's is not finite.
+// Notes on a tile for the softmax warps: which places hold a token, and the
+// drafted tile it is (-1: cached tokens).
 struct TileNote {
   uint32_t live[4];
   int draft;
-  int odd;
 };
 
 template <int D>
 struct Cfg {
   static constexpr int NC = D / 64;           // 64-dim chunks
-  static constexpr int ST = D == 64 ? 4 : 2;  // stages of K and of V
-  static constexpr int kChunk = 128 * 128;    // bytes of a chunk of 128 rows
-  static constexpr int kTile = NC * kChunk;   // bytes of 128 rows
-  static constexpr int kSmem = 2 * kTile + 2 * ST * kTile + 1024;
+  static constexpr int KS = D == 64 ? 4 : 3;  // stages of K
+  static constexpr int VS = D == 64 ? 4 : 2;  // stages of V
+  static constexpr int kChunk = 128 * 128;    // bytes of 64 dims of 128 rows
+  static constexpr int kTile = NC * kChunk;
+  static constexpr int kSmem = (2 + KS + VS) * kTile + 1024;
 };
 
 struct Bars {
@@ -67,29 +67,33 @@ struct Bars {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t s_full[2][2], p_full[2][2];  // [stream][buffer]
   uint64_t pv_done[2], o_full[2], o_empty[2];
+  uint64_t hand_full, hand_empty;  // stream B's part of a single item for stream A
   uint64_t note[kMeta];
   uint64_t drain;
 };
 
-// Waits for a barrier's phase; gives up (false) past the limit or when another
-// role has given up, and tells the others.
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, unsigned long long limit, int* err,
-                                       volatile int* stop) {
-  for (int i = 0; i < 64; ++i)  // the timer is slow to read
-    if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (*stop) return false;
-    if (globaltimer_ns() - t0 > limit) {
-      *stop = 1;
-      flag_error(err, kErrTimeout);
+// Waits for a barrier's phase with the whole warp; gives up (false) past the
+// limit or when another role has given up, and tells the others. All lanes leave
+// the loop at once: what the warp does next takes its addresses from uniform
+// registers and must not be reached by some lanes before the others.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const AttnArgs& a, volatile int* stop) {
+  uint32_t n = 0;
+  uint64_t t0 = 0;
+  while (!__all_sync(kFull, mbar_try_wait(bar, parity))) {
+    if ((++n & 63u) != 0) continue;  // the timer is slow to read
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    const bool late = now - t0 > a.wait_ns;
+    if (__any_sync(kFull, late || *stop)) {
+      if (late) {
+        *stop = 1;
+        flag_error(a.err, kErrTimeout);
+      }
+      __syncwarp();
       return false;
     }
   }
   return true;
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const AttnArgs& a, volatile int* stop) {
-  return mbar_try_wait(bar, parity) || wait_long(bar, parity, a.wait_ns, a.err, stop);
 }
 
 // An item's place in a CTA's range.
@@ -136,28 +140,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const AttnArgs a,
                    const int tb) {
   using C = Cfg<D>;
-  constexpr int NC = C::NC, ST = C::ST;
+  constexpr int NC = C::NC, KS = C::KS, VS = C::VS;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* s_q = smem;
   unsigned char* s_k = s_q + 2 * C::kTile;
-  unsigned char* s_v = s_k + ST * C::kTile;
+  unsigned char* s_v = s_k + KS * C::kTile;
   __shared__ Bars b;
   __shared__ TileNote s_note[kMeta];
-  __shared__ const char* s_row[kTK];  // a copied tile's rows (null: nothing there)
+  __shared__ int s_odd[kMeta];  // a drafted tile has a Value that is not finite
   __shared__ long long s_place[kThreads / 32 + 4];
   __shared__ uint32_t s_tmem;
   __shared__ int s_stop;
   volatile int* stop = &s_stop;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   pdl_launch_dependents();
   if (tid == 0) {
     mbar_init(&b.q_full, 8);
     mbar_init(&b.q_empty, 2);  // both streams
     for (int i = 0; i < 4; ++i) {
       mbar_init(&b.k_full[i], 1);
-      mbar_init(&b.k_empty[i], 2);  // both streams, or a single item's one stream twice
+      mbar_init(&b.k_empty[i], 2);  // both streams
       mbar_init(&b.v_full[i], 1);
       mbar_init(&b.v_empty[i], 2);
     }
@@ -170,6 +174,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&b.o_full[i], 1);
       mbar_init(&b.o_empty[i], 4);
     }
+    mbar_init(&b.hand_full, 4);
+    mbar_init(&b.hand_empty, 4);
     for (int i = 0; i < kMeta; ++i) mbar_init(&b.note[i], 1);
     mbar_init(&b.drain, 2);
     s_stop = 0;
@@ -182,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   const AttnPlace pl = find_place<kThreads>(a, blockIdx.x, 256, kTK, s_place, tid);  // holds block barriers
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(kFull, s_tmem, 0);
   int r = pl.r;
   long long base = pl.base;
 
@@ -193,23 +199,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_at = tmem + lane_at + x * 128, o_at = tmem + lane_at + 256 + x * 128;
     // scale 0 still has to leave hidden places at -inf: the smallest normal number stands for it
     const float c = fmaxf(fabsf(a.scale_log2), FLT_MIN);
-    uint32_t seen = 0, notes = 0, nitem = 0, items = 0;  // score steps of this stream; tiles, items of the CTA; of the stream
+    uint32_t seen = 0, notes = 0, items = 0, hands = 0;  // steps, tiles, items; singles handed over
     bool alive = true;
     for (long long u = pl.u0; u < pl.u1 && alive;) {
       const Work w = work_at(a, pl, u, &r, &base);
-      const int sub = w.at.single ? 0 : x;  // row tile of the stream
-      const int steps = 2 * (w.at.single ? (w.tiles + 1 - x) / 2 : w.tiles);
-      const int rows = w.rows - sub * 128;
+      const bool single = __shfl_sync(kFull, (int)w.at.single, 0);
+      const int tiles = __shfl_sync(kFull, w.tiles, 0);
+      const int sub = single ? 0 : x;  // row tile of the stream
+      const int steps = single ? tiles : 2 * tiles;
+      const int rows = __shfl_sync(kFull, w.rows, 0) - sub * 128;
       const bool busy = (warp & 3) * 32 < rows;  // this warp has rows at all
       const int qrow = w.row0 + sub * 128 + row;
       const int node = min(qrow / a.G, w.rq.n - 1);
       // The stream's queries, a row a thread (a single item's stream B reads A's).
       // A negative scale turns their signs; rows that do not exist are zero.
-      if (nitem > 0) {
-        alive = __all_sync(kFull, wait(&b.q_empty, (nitem - 1) & 1, a, stop));
+      if (items > 0) {
+        alive = wait(&b.q_empty, (items - 1) & 1, a, stop);
         if (!alive) break;
       }
-      if (!w.at.single || x == 0) {
+      if (!single || x == 0) {
         const bool real = row < rows;
         const uint16_t* qp = static_cast<const uint16_t*>(a.q);
         if (real) qp += (w.rq.node0 + qrow / a.G) * a.q_sn + (long long)(w.at.h * a.G + qrow % a.G) * a.q_sh;
@@ -222,37 +230,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             y[e] = real ? *reinterpret_cast<const uint4*>(qp + (c0 + e) * 8) : make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<uint4*>(s_q + sub * C::kTile + (c0 / 8) * C::kChunk + row * 128 + ((e ^ (row & 7)) << 4)) =
+            *reinterpret_cast<uint4*>(s_q + sub * C::kTile + (c0 / 8) * C::kChunk + row * 128 +
+                                      ((e ^ (row & 7)) << 4)) =
                 make_uint4(y[e].x ^ flip, y[e].y ^ flip, y[e].z ^ flip, y[e].w ^ flip);
         }
         fence_async_smem();
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&b.q_full);
-      ++nitem;
+      __syncwarp();
       float m_ref = -INFINITY, l = 0.f;  // in units of S
-      uint32_t dtile = 0, dno[2] = {0, 0};  // drafted tiles taken, and their places in the ring of notes
+      uint32_t dtile = 0, dfirst = 0;    // drafted tiles taken, and the place of the first among the notes
       for (int i = 0; i < steps; ++i, ++seen) {
-        const uint32_t no = notes + (w.at.single ? (i & ~1) + x : i >> 1);
+        const uint32_t no = notes + (single ? i : i >> 1);
+        const int half = single ? x : i & 1;  // 64 tokens of the tile
         const TileNote* note = &s_note[no % kMeta];
         const uint32_t buf = seen & 1, sp = s_at + buf * 64;
         alive = wait(&b.note[no % kMeta], (no / kMeta) & 1, a, stop) &&
                 wait(&b.s_full[x][buf], (seen >> 1) & 1, a, stop);
-        alive = __all_sync(kFull, alive);
         if (!alive) break;
         tc_fence_after();
         if (busy) {
           uint32_t s[2][32];
           tmem_ld32(sp, s[0]);
           tmem_ld32(sp + 32, s[1]);
-          uint32_t live[2] = {note->live[(i & 1) * 2], note->live[(i & 1) * 2 + 1]};
+          uint32_t live[2] = {note->live[half * 2], note->live[half * 2 + 1]};
           const int draft = note->draft;
           if (draft >= 0) {
             dtile |= 1u << draft;
-            dno[draft & 1] = no % kMeta;
+            dfirst = no - draft;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const int word = draft * 4 + (i & 1) * 2 + k, j0 = word * 32;
+              const int word = draft * 4 + half * 2 + k, j0 = word * 32;
               uint32_t see = 0xFFFFFFFFu;
               if (!a.mask)
                 see = node < j0 ? 0u : node - j0 >= 31 ? 0xFFFFFFFFu : (2u << (node - j0)) - 1u;
@@ -261,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               live[k] &= see;
             }
           }
+          __syncwarp();
           tmem_wait_ld();
           if ((live[0] & live[1]) != 0xFFFFFFFFu) {
             // selected, whatever a hidden place holds
@@ -270,6 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 32; ++e)
                 if (!((live[k] >> e) & 1u)) s[k][e] = 0xFF800000u;
           }
+          __syncwarp();
           float mx[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -288,10 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               m_ref = m2;
               l *= al;
             }
+            __syncwarp();
             if (!first) {
               // every product into O so far (this stream's step before) has to be in
               if (!wait(&b.pv_done[x], (seen - 1) & 1, a, stop)) al = 0.f;  // given up: the result is void
-              __syncwarp();
               tc_fence_after();
 #pragma unroll 1
               for (int k = 0; k < D / 32; ++k) {
@@ -321,36 +332,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b.p_full[x][buf]);
+        __syncwarp();
       }
-      notes += w.tiles;
+      notes += tiles;
       // ---- the item's end: O and the row's maximum and sum
-      if (alive && steps > 0) alive = __all_sync(kFull, wait(&b.o_full[x], items & 1, a, stop));
+      if (alive) alive = wait(&b.o_full[x], items & 1, a, stop);
       if (!alive) break;
       tc_fence_after();
       uint32_t odd = 0;
-      for (int d = 0; d < 2; ++d)
-        if ((dtile >> d) & 1u) odd |= s_note[dno[d]].odd ? 1u << d : 0u;
-      const bool whole = !w.at.single && w.at.t0 == 0 && w.at.t1 == w.at.units;
+      for (int d = 0; d < kMaxNodes / kTK; ++d)
+        if ((dtile >> d) & 1u) odd |= s_odd[(dfirst + d) % kMeta] ? 1u << d : 0u;
+      // An item that is this CTA's alone is written out here; of a single one,
+      // stream B first hands its part to stream A through the CTA's third slot.
+      const bool whole = w.at.t0 == 0 && w.at.t1 == w.at.units;
+      const bool give = whole && single && x == 1, take = whole && single && x == 0;
+      if (give && hands > 0) alive = wait(&b.hand_empty, (hands - 1) & 1, a, stop);
+      if (take) alive = wait(&b.hand_full, hands & 1, a, stop);
+      if (!alive) break;
       const bool mine = row < rows;
-      const float inv = row_inv(l), ml2 = m_ref == -INFINITY ? -INFINITY : m_ref * c;
       const int prow = x * 128 + row;  // row of the partial slot (both streams of a single item leave one)
-      float* part = partial_slot(a, blockIdx.x, u == pl.u0 ? 0 : 1, 256, D);
+      float* part = partial_slot(a, blockIdx.x, whole ? 2 : u == pl.u0 ? 0 : 1, 256, D);
       const long long at = (long long)(w.rq.node0 + qrow / a.G) * a.Hq + w.at.h * a.G + qrow % a.G;
+      float m2 = m_ref == -INFINITY ? -INFINITY : m_ref * c;
+      float fa = 1.f, fb = 0.f;  // factors of this stream's and (take) the other's part
+      if (take && mine) {
+        const float mb = part[256 * D + 128 + row], lb = part[256 * D + 256 + 128 + row];
+        const float mm = fmaxf(m2, mb), ref = mm == -INFINITY ? 0.f : mm;
+        fa = ex2(m2 - ref);
+        fb = ex2(mb - ref);
+        l = l * fa + lb * fb;
+        m2 = mm;
+      }
+      const float inv = row_inv(l);
+      __syncwarp();
       if (busy) {
 #pragma unroll 1
         for (int k = 0; k < D / 32; ++k) {
           uint32_t o[32];
-          if (steps > 0) {
-            tmem_ld32(o_at + k * 32, o);
-            tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0;
-          }
+          tmem_ld32(o_at + k * 32, o);
+          tmem_wait_ld();
           if (mine) {
             if (odd) {  // drafted Values that are not finite, for the nodes that see them
               for (int j = 0; j < w.rq.n; ++j) {
-                if (!((odd >> (j >> 7)) & 1u) || !sees(a, w.rq, node, j)) continue;
+                if (!((odd >> (j / kTK)) & 1u) || !sees(a, w.rq, node, j)) continue;
                 const uint16_t* v = static_cast<const uint16_t*>(a.dv) + (w.rq.node0 + j) * a.dv_sn + w.at.h * a.dv_sh;
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
@@ -360,7 +384,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
-            if (whole) {
+            if (take) {
+              const float4* other = reinterpret_cast<const float4*>(part) + k * 8 * 256 + 128 + row;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 y = other[e * 256];
+                o[e * 4] = __float_as_uint(__uint_as_float(o[e * 4]) * fa + y.x * fb);
+                o[e * 4 + 1] = __float_as_uint(__uint_as_float(o[e * 4 + 1]) * fa + y.y * fb);
+                o[e * 4 + 2] = __float_as_uint(__uint_as_float(o[e * 4 + 2]) * fa + y.z * fb);
+                o[e * 4 + 3] = __float_as_uint(__uint_as_float(o[e * 4 + 3]) * fa + y.w * fb);
+              }
+            }
+            if (whole && !give) {
               uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + k * 32);
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -381,20 +416,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         if (mine) {
-          if (whole) {
-            if (a.lse) a.lse[at] = row_lse(ml2, l);
+          if (whole && !give) {
+            if (a.lse) a.lse[at] = row_lse(m2, l);
           } else {
-            part[256 * D + prow] = ml2;
+            part[256 * D + prow] = m2;
             part[256 * D + 256 + prow] = l;
           }
         }
       }
-      if (steps > 0) {
-        ++items;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&b.o_empty[x]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&b.o_empty[x]);
+        if (give) mbar_arrive(&b.hand_full);
+        if (take) mbar_arrive(&b.hand_empty);
       }
+      __syncwarp();
+      ++items;
+      hands += give || take;
       u += w.at.t1 - w.at.t0;
     }
   } else if (warp < kLoadWarp) {
@@ -402,30 +441,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (one warp for both streams left the tensor cores idle half the time: waits,
     // commits and the issue itself take longer than 12 products of this size)
     constexpr uint32_t idqk = idesc_bf16_f32(128, 64), idpv = idesc_bf16_f32(128, D) | kIdescBMajorMN;
-    const int x = __shfl_sync(kFull, warp - kMmaWarp, 0);
+    const int x = warp - kMmaWarp;
     const uint64_t dq = desc_kmajor_sw128(smem_u32(s_q)), dk = desc_kmajor_sw128(smem_u32(s_k)),
                    dv = desc_mnmajor_sw128(smem_u32(s_v), C::kChunk);
     const uint32_t hi_k = (uint32_t)(dq >> 32), hi_v = (uint32_t)(dv >> 32);
-    const uint32_t tm = __shfl_sync(kFull, tmem, 0);
-    const uint32_t s_of = tm + x * 128, o_to = tm + 256 + x * 128;
-    uint32_t cnt = 0, nitem = 0, qs = 0, ps = 0, oc = 0;
+    const uint32_t s_of = tmem + x * 128, o_to = tmem + 256 + x * 128;
+    uint32_t cnt = 0, items = 0, qs = 0, ps = 0;  // tiles and items before; steps
     bool alive = true;
     for (long long u = pl.u0; u < pl.u1 && alive;) {
       const Work w = work_at(a, pl, u, &r, &base);
       const bool single = __shfl_sync(kFull, (int)w.at.single, 0);
       const int tiles = __shfl_sync(kFull, w.tiles, 0);
-      const int steps = 2 * (single ? (tiles + 1 - x) / 2 : tiles);
+      const int steps = single ? tiles : 2 * tiles;
       const uint32_t q0 = (uint32_t)dq + ((single ? 0 : x) * C::kTile >> 4);
-      alive = __all_sync(kFull, wait(&b.q_full, nitem & 1, a, stop));
+      alive = wait(&b.q_full, items & 1, a, stop);
       if (!alive) break;
-      // scores of step j (64 tokens); K is let go behind the tile's second half
+      // scores of step j, 64 tokens; a tile is let go behind its last step
       auto qk = [&](int j) {
-        const uint32_t no = cnt + (single ? (j & ~1) + x : j >> 1), st = no % ST;
-        const bool ok = (j & 1) || wait(&b.k_full[st], (no / ST) & 1, a, stop);
-        if (!__all_sync(kFull, ok)) return false;
+        const uint32_t no = cnt + (single ? j : j >> 1), st = no % KS;
+        const int half = single ? x : j & 1;
+        if ((single || !half) && !wait(&b.k_full[st], (no / KS) & 1, a, stop)) return false;
         tc_fence_after();
         const uint32_t buf = qs++ & 1;
-        const uint32_t k0 = (uint32_t)dk + ((st * C::kTile + (j & 1) * (C::kChunk / 2)) >> 4);
+        const uint32_t k0 = (uint32_t)dk + ((st * C::kTile + half * (C::kChunk / 2)) >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
@@ -433,47 +471,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_bf16_lo(s_of + buf * 64, q0 + off, k0 + off, hi_k, idqk, k > 0);
           }
           mma_commit(&b.s_full[x][buf]);
-          if (j & 1) {
-            mma_commit(&b.k_empty[st]);
-            if (single) mma_commit(&b.k_empty[st]);
-          }
+          if (single || half) mma_commit(&b.k_empty[st]);
         }
         __syncwarp();
         return true;
       };
       auto pv = [&](int j) {
-        const uint32_t no = cnt + (single ? (j & ~1) + x : j >> 1), st = no % ST;
+        const uint32_t no = cnt + (single ? j : j >> 1), st = no % VS;
+        const int half = single ? x : j & 1;
         const uint32_t buf = ps & 1;
-        bool ok = (j & 1) || wait(&b.v_full[st], (no / ST) & 1, a, stop);
+        if ((single || !half) && !wait(&b.v_full[st], (no / VS) & 1, a, stop)) return false;
         // O is read out before the next item writes it
-        if (j == 0 && oc > 0) ok = ok && wait(&b.o_empty[x], (oc - 1) & 1, a, stop);
-        ok = ok && wait(&b.p_full[x][buf], (ps >> 1) & 1, a, stop);
+        if (j == 0 && items > 0 && !wait(&b.o_empty[x], (items - 1) & 1, a, stop)) return false;
+        if (!wait(&b.p_full[x][buf], (ps >> 1) & 1, a, stop)) return false;
         ++ps;
-        if (!__all_sync(kFull, ok)) return false;
         tc_fence_after();
-        const uint32_t v0 = (uint32_t)dv + ((st * C::kTile + (j & 1) * (C::kChunk / 2)) >> 4);
+        const uint32_t v0 = (uint32_t)dv + ((st * C::kTile + half * (C::kChunk / 2)) >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_bf16_ts_lo(o_to, s_of + buf * 64 + k * 8, v0 + (k * 2048 >> 4), hi_v, idpv, j > 0 || k > 0);
           mma_commit(&b.pv_done[x]);
-          if (j & 1) {
-            mma_commit(&b.v_empty[st]);
-            if (single) mma_commit(&b.v_empty[st]);
-          }
+          if (single || half) mma_commit(&b.v_empty[st]);
           if (j + 1 == steps) mma_commit(&b.o_full[x]);
         }
         __syncwarp();
         return true;
       };
-      if (steps > 0) alive = qk(0) && qk(1);
+      alive = qk(0) && (steps < 2 || qk(1));
       for (int j = 0; j < steps && alive; ++j) alive = pv(j) && (j + 2 >= steps || qk(j + 2));
       // every score of the item is in, or on its way
       if (elect_one()) mma_commit(&b.q_empty);
       __syncwarp();
-      oc += steps > 0;
       cnt += tiles;
-      ++nitem;
+      ++items;
       u += w.at.t1 - w.at.t0;
     }
     // nothing may be in flight when TMEM and shared memory go
@@ -481,128 +512,129 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     mbar_wait_bounded(&b.drain, 0, a.wait_ns);
     __syncwarp();
-  } else {
-    // ---- loaders: two warps that stay in step (they leave together) --------------
-    const int lt = tid - kLoadWarp * 32;
-    const int npiece = kTK / tb;                                  // page pieces of a tile
-    uint32_t cnt = 0, sent[2] = {0, 0};  // tiles of K and of V under way or done
+  } else if (warp == kLoadWarp) {
+    // ---- loader: the warp stays together and one lane issues the copies ------------
+    const int npiece = kTK / tb;  // page pieces of a tile
+    uint32_t cnt = 0, sent[2] = {0, 0};  // tiles of the items before; tiles of K and V sent
     bool alive = true;
-    // K (or V) of tile i of the item into its stage; false when both warps give up
-    auto load = [&](const Work& w, int i, bool val) -> bool {
-      const int h = w.at.h, t = w.first + i;
-      const uint32_t no = cnt + i, st = no % ST;
-      TileNote* note = &s_note[no % kMeta];
-      unsigned char* dst = (val ? s_v : s_k) + st * C::kTile;
-      uint64_t* bar = val ? &b.v_full[st] : &b.k_full[st];
-      const bool draft = t >= w.rq.tiles_c;
-      // a piece is a run of tb tokens in one page (tb divides the block size)
-      int page = 0, tok = 0;
-      bool full = true;
-      if (!draft && lane < npiece) {
+    // Where a tile's pieces lie: a piece is a run of tb tokens in one page (tb
+    // divides the block size).
+    struct Piece {
+      int page, tok;
+      bool full;
+    };
+    auto look = [&](const Work& w, int i) {
+      Piece x{0, 0, true};
+      const int t = w.first + i;
+      if (i >= w.tiles || t >= w.rq.tiles_c) {
+        x.full = false;
+      } else if (lane < npiece) {
         TokenAt at;
         const int v = t * kTK + lane * tb;
-        full = token_at(a, w.r, w.rq, v + tb - 1, false, &at) && token_at(a, w.r, w.rq, v, false, &at);
-        page = at.page;
-        tok = at.tok;
+        x.full = token_at(a, w.r, w.rq, v + tb - 1, false, &at) && token_at(a, w.r, w.rq, v, false, &at);
+        x.page = at.page;
+        x.tok = at.tok;
       }
-      full = __all_sync(kFull, full) && !draft;
-      alive = alive && wait(val ? &b.v_empty[st] : &b.k_empty[st], ((no / ST) & 1) ^ 1, a, stop);
-      alive = !named_sync_or(1, kLoaders, !alive);
-      if (!alive) return false;
-      ++sent[val];
-      if (full) {
-        if (warp == kLoadWarp) {
-          if (lane == 0) {
-            if (!val) {
-              note->live[0] = note->live[1] = note->live[2] = note->live[3] = 0xFFFFFFFFu;
-              note->draft = -1;
-              mbar_arrive(&b.note[no % kMeta]);
-            }
-            mbar_arrive_expect_tx(bar, C::kTile);
+      __syncwarp();
+      return x;
+    };
+    // K (or V) of tile i of the item into its stage
+    auto load = [&](const Work& w, int i, const Piece& pc, const bool val) {
+      const int h = __shfl_sync(kFull, w.at.h, 0), t = w.first + i;
+      const uint32_t no = cnt + i, ns = val ? VS : KS, st = no % ns;
+      TileNote* note = &s_note[no % kMeta];
+      uint64_t *noted = &b.note[no % kMeta], *bar = val ? &b.v_full[st] : &b.k_full[st];
+      unsigned char* dst = (val ? s_v : s_k) + st * C::kTile;
+      if (!wait(val ? &b.v_empty[st] : &b.k_empty[st], ((no / ns) & 1) ^ 1, a, stop)) return false;
+      sent[val] = no + 1;
+      if (__all_sync(kFull, pc.full)) {
+        if (elect_one()) {
+          if (!val) {
+            note->live[0] = note->live[1] = note->live[2] = note->live[3] = 0xFFFFFFFFu;
+            note->draft = -1;
+            mbar_arrive(noted);
           }
-          __syncwarp();
-          if (lane < npiece) {
+          mbar_arrive_expect_tx(bar, C::kTile);
+        }
+        __syncwarp();
+        for (int k = 0; k < npiece; ++k) {
+          const int page = __shfl_sync(kFull, pc.page, k), tok = __shfl_sync(kFull, pc.tok, k);
+          if (elect_one()) {
 #pragma unroll
             for (int c = 0; c < NC; ++c)
-              tma_load_4d(dst + c * C::kChunk + lane * tb * 128, val ? &tmv : &tmk, c * 64, tok, h, page, bar);
+              tma_load_4d(dst + c * C::kChunk + k * tb * 128, val ? &tmv : &tmk, c * 64, tok, h, page, bar);
           }
+          __syncwarp();
         }
         return true;
       }
-      // copied by the 64 threads
-      for (int m = lt; m < kTK; m += kLoaders) {
+      // copied, a row a lane at a time
+      const bool draft = t >= w.rq.tiles_c;
+      bool hit = false;
+      uint32_t live[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int m = k * 32 + lane, n = (t - w.rq.tiles_c) * kTK + m;
         const char* p = nullptr;
-        const int n = (t - w.rq.tiles_c) * kTK + m;
         TokenAt at;
         if (!draft && token_at(a, w.r, w.rq, t * kTK + m, true, &at)) {
           const KCache& kc = val ? a.vc : a.kc;
-          p = static_cast<const char*>(kc.base) +
-              (a.layer * kc.sL + at.page * kc.sP + h * kc.sH + at.tok * kc.sT) * 2;
+          p = static_cast<const char*>(kc.base) + (a.layer * kc.sL + at.page * kc.sP + h * kc.sH + at.tok * kc.sT) * 2;
         } else if (draft && a.dk && n < w.rq.n) {
           p = val ? static_cast<const char*>(a.dv) + ((w.rq.node0 + n) * a.dv_sn + h * a.dv_sh) * 2
                   : static_cast<const char*>(a.dk) + ((w.rq.node0 + n) * a.dk_sn + h * a.dk_sh) * 2;
         }
-        s_row[m] = p;
-      }
-      named_sync(1, kLoaders);
-      auto piece_at = [&](int j) {
-        const int m = j / (D / 8), c8 = j % (D / 8);
-        return dst + (c8 >> 3) * C::kChunk + m * 128 + (((c8 & 7) ^ (m & 7)) << 4);
-      };
-      for (int j = lt; j < kTK * (D / 8); j += kLoaders) {
-        const char* p = s_row[j / (D / 8)];
-        cp_async16(smem_u32(piece_at(j)), p ? p + (j % (D / 8)) * 16 : static_cast<const char*>(a.q), p != nullptr);
-      }
-      cp_wait_all();
-      bool hit = false;
-      if (draft && val)  // what is not finite is added back at the end, to the nodes that see it
-        for (int j = lt; j < kTK * (D / 8); j += kLoaders) {
-          uint4 y = *reinterpret_cast<uint4*>(piece_at(j));
-          if (drop_nonfinite(&y)) {
-            *reinterpret_cast<uint4*>(piece_at(j)) = y;
-            hit = true;
+        live[k] = __ballot_sync(kFull, p != nullptr);
+#pragma unroll
+        for (int j0 = 0; j0 < D / 8; j0 += 8) {
+          uint4 y[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            y[j] = p ? *reinterpret_cast<const uint4*>(p + (j0 + j) * 16) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            // a draft's Value that is not finite is added back at the end, to the nodes that see it
+            if (draft && val) hit |= drop_nonfinite(&y[j]);
+            *reinterpret_cast<uint4*>(dst + m * 128 + (j0 / 8) * C::kChunk + ((j ^ (m & 7)) << 4)) = y[j];
           }
         }
+      }
       fence_async_smem();
-      hit = named_sync_or(1, kLoaders, hit);
-      if (warp == kLoadWarp) {
-        uint32_t live[4];
+      hit = __any_sync(kFull, hit);
+      if (lane == 0) {
+        if (val) {
+          s_odd[no % kMeta] = hit;
+        } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) live[k] = __ballot_sync(kFull, s_row[k * 32 + lane] != nullptr);
-        if (lane == 0) {
-          if (val) {
-            note->odd = hit;
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) note->live[k] = live[k];
-            note->draft = draft ? t - w.rq.tiles_c : -1;
-            mbar_arrive(&b.note[no % kMeta]);
-          }
-          mbar_arrive(bar);
+          for (int k = 0; k < 4; ++k) note->live[k] = live[k];
+          note->draft = draft ? t - w.rq.tiles_c : -1;
+          mbar_arrive(noted);
         }
-        __syncwarp();
+        mbar_arrive(bar);
       }
+      __syncwarp();
       return true;
     };
-    for (long long u = pl.u0; u < pl.u1;) {
+    for (long long u = pl.u0; u < pl.u1 && alive;) {
       const Work w = work_at(a, pl, u, &r, &base);
-      // K of a tile goes out ahead of V of the tile before: with two stages the
-      // scores of both streams run a tile ahead of their products with V.
-      bool left = false;
-      for (int i = 0; i <= w.tiles && !left; ++i) {
-        if (i < w.tiles) left = !load(w, i, false);
-        if (!left && i > 0) left = !load(w, i - 1, true);
+      const int tiles = __shfl_sync(kFull, w.tiles, 0);
+      Piece last = look(w, 0), cur = last, next = look(w, 1);
+      for (int i = 0; i <= tiles && alive; ++i) {  // K of tile i, V of the tile before
+        if (i < tiles) alive = load(w, i, cur, false);
+        if (i > 0 && alive) alive = load(w, i - 1, last, true);
+        last = cur;
+        cur = next;
+        next = look(w, i + 2);
       }
-      if (left) break;
-      cnt += w.tiles;
+      cnt += tiles;
       u += w.at.t1 - w.at.t0;
     }
     // copies in flight end before the CTA does (on the ordinary way they were all waited for)
-    if (*stop && warp == kLoadWarp && lane == 0) {
-      for (uint32_t i = sent[0] > ST ? sent[0] - ST : 0; i < sent[0]; ++i)
-        mbar_wait_bounded(&b.k_full[i % ST], (i / ST) & 1, a.wait_ns);
-      for (uint32_t i = sent[1] > ST ? sent[1] - ST : 0; i < sent[1]; ++i)
-        mbar_wait_bounded(&b.v_full[i % ST], (i / ST) & 1, a.wait_ns);
+    if (*stop && lane == 0) {
+      for (uint32_t i = sent[0] > KS ? sent[0] - KS : 0; i < sent[0]; ++i)
+        mbar_wait_bounded(&b.k_full[i % KS], (i / KS) & 1, a.wait_ns);
+      for (uint32_t i = sent[1] > VS ? sent[1] - VS : 0; i < sent[1]; ++i)
+        mbar_wait_bounded(&b.v_full[i % VS], (i / VS) & 1, a.wait_ns);
     }
     __syncwarp();
   }

@@ -207,6 +207,16 @@ def test_many_requests(cuda):
     _check(*_run(pc, 0, [1] * 700, 2, scale=-0.3))
 
 
+@pytest.mark.parametrize("D,lo,hi", [(64, 8, 8), (128, 7, 30)])
+def test_many_short_trees(cuda, D, lo, hi):
+    """Several whole items of each kind (one row tile, two, three) in every CTA's share."""
+    rng = np.random.default_rng(D)
+    lens = [int(x) for x in rng.integers(0, 150, 170)]
+    counts = [int(x) for x in rng.integers(lo, hi + 1, 170)]
+    pc = Paged(lens, H=3 if hi == 8 else 1, D=D, bs=16, L=1, seed=5)
+    _check(*_run(pc, 0, counts, 5 if hi == 8 else 10, draft=True))
+
+
 @pytest.mark.parametrize("counts", [[1, 1], [30, 64]])
 def test_streams_graphs_and_repeats(cuda, counts):
     """Same bits on another stream, again, and replayed from a graph."""
