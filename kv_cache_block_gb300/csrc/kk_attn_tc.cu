@@ -568,9 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return true;
       }
-      // copied, a row a lane at a time
+      // copied, a row a lane, all copies in flight at once
       const bool draft = t >= w.rq.tiles_c;
-      bool hit = false;
       uint32_t live[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -584,18 +583,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           p = val ? static_cast<const char*>(a.dv) + ((w.rq.node0 + n) * a.dv_sn + h * a.dv_sh) * 2
                   : static_cast<const char*>(a.dk) + ((w.rq.node0 + n) * a.dk_sn + h * a.dk_sh) * 2;
         }
-        live[k] = __ballot_sync(kFull, p != nullptr);
+        const bool real = p != nullptr;
+        live[k] = __ballot_sync(kFull, real);
+        if (!real) p = static_cast<const char*>(a.q);
+        const uint32_t to = smem_u32(dst) + m * 128;
 #pragma unroll
-        for (int j0 = 0; j0 < D / 8; j0 += 8) {
-          uint4 y[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            y[j] = p ? *reinterpret_cast<const uint4*>(p + (j0 + j) * 16) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            // a draft's Value that is not finite is added back at the end, to the nodes that see it
-            if (draft && val) hit |= drop_nonfinite(&y[j]);
-            *reinterpret_cast<uint4*>(dst + m * 128 + (j0 / 8) * C::kChunk + ((j ^ (m & 7)) << 4)) = y[j];
+        for (int j = 0; j < D / 8; ++j)
+          cp_async16(to + (j / 8) * C::kChunk + (((j & 7) ^ (m & 7)) << 4), p + (real ? j * 16 : 0), real);
+      }
+      cp_wait_all();
+      bool hit = false;
+      if (draft && val) {
+        // a draft's Value that is not finite is added back at the end, to the nodes that see it
+#pragma unroll 1
+        for (int k = 0; k < 4 * (D / 8); ++k) {
+          uint4* y = reinterpret_cast<uint4*>(dst + ((k & 3) * 32 + lane) * 128 + (k / 32) * C::kChunk +
+                                              ((k >> 2 & 7) << 4));
+          uint4 z = *y;
+          if (drop_nonfinite(&z)) {
+            *y = z;
+            hit = true;
           }
         }
       }
