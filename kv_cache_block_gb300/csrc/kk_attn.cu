@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const AttnArgs 
       ++r;
       continue;
     }
-    const int item = (int)((u - base) / rq.tiles);
+    const int item = (int)udiv(u - base, rq.tiles);
     const int t0 = (int)((u - base) - (long long)item * rq.tiles);
     const int t1 = (int)min((long long)rq.tiles, t0 + (pl.u1 - u));
     const int h = item / rq.mt, row0 = (item - h * rq.mt) * M;
@@ -231,12 +231,12 @@ __device__ __forceinline__ Cut find_cut(const AttnArgs& a, int r, int h, int mt,
     const AttnReq rq = load_req(a, r, M, TK, false);
     Cut c = {};
     if (mt < rq.mt && mt * M + row < rq.n * a.G) {
-      const int G = (int)min((long long)a.grid, all);
+      const Split sp = make_split(all, a.grid);
       const ItemAt it = item_of(rq, h, mt);
-      const long long lo = before + it.start, hi = lo + it.units - 1;
-      c.c0 = (int)(((lo + 1) * G - 1) / all);
-      c.n = (int)(((hi + 1) * G - 1) / all) - c.c0 + 1;
-      c.first = (long long)c.c0 * all / G == lo ? 0 : 1;  // c0's slot: its first item, or its last
+      const long long lo = before + it.start;
+      c.c0 = split_owner(sp, lo);
+      c.n = split_owner(sp, lo + it.units - 1) - c.c0 + 1;
+      c.first = split_start(sp, c.c0) == lo ? 0 : 1;  // c0's slot: its first item, or its last
       c.halves = it.single ? 2 : 1;  // a single's streams leave a part each, M/2 rows apart
       if (c.n == 1) c.n = 0;
       c.node0 = rq.node0;

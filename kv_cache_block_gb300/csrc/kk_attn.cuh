@@ -4,8 +4,9 @@
 // row i*G + g; rows are taken in tiles of M. An item is (r, h, row tile); its
 // tokens are cut into tiles of TK: those of the cached tokens first, then those
 // of the drafted nodes. Each (item, tile) is one unit of work, numbered request
-// by request, and CTA c of the grid takes the units [c*total/G, (c+1)*total/G):
-// the SMs stay level whatever the lengths are, without any work list from the
+// by request, and every CTA of G (the grid, or fewer when there are fewer units)
+// takes total / G of them in order, the first total % G CTAs one more: the SMs
+// stay level whatever the lengths are, without any work list from the
 // host. An item inside one CTA's range is written out by that CTA; an item
 // that ranges cut leaves one partial result per CTA (running maximum, sum and
 // accumulator) in the workspace, at most two per CTA (its first and its last
@@ -118,6 +119,29 @@ __device__ __forceinline__ long long req_units(const AttnArgs& a, const AttnReq&
   return (long long)a.kc.H * ((long long)(q.mt - q.odd) * q.tiles + q.odd * ((q.tiles + 1) / 2));
 }
 
+// a / b of non-negative numbers; in 32 bits, a tenth of the time, where they fit.
+__device__ __forceinline__ long long udiv(long long a, long long b) {
+  if (((unsigned long long)a | (unsigned long long)b) >> 32) return a / b;
+  return (long long)((unsigned)a / (unsigned)b);
+}
+// The CTAs' ranges over `total` units.
+struct Split {
+  long long q;  // units of a CTA, and one more in the first `rem` CTAs
+  int rem, G;
+};
+__device__ __forceinline__ Split make_split(long long total, int grid) {
+  Split s;
+  s.G = (int)min((long long)grid, total);
+  s.q = s.G > 0 ? udiv(total, s.G) : 0;
+  s.rem = (int)(total - s.q * s.G);
+  return s;
+}
+__device__ __forceinline__ long long split_start(const Split& s, int c) { return c * s.q + min(c, s.rem); }
+__device__ __forceinline__ int split_owner(const Split& s, long long u) {
+  const long long big = (s.q + 1) * s.rem;
+  return (int)(u < big ? udiv(u, s.q + 1) : s.rem + udiv(u - big, s.q));
+}
+
 // An item: KV head, row tile, whether it is a single, its first unit inside
 // the request and its number of units (a single's unit is two token tiles);
 // [t0, t1): the units of a range that starts inside it.
@@ -139,8 +163,8 @@ __device__ __forceinline__ ItemAt item_of(const AttnReq& q, int h, int mt) {
 }
 __device__ __forceinline__ ItemAt item_at(const AttnReq& q, long long local) {
   const long long per = (long long)(q.mt - q.odd) * q.tiles + q.odd * ((q.tiles + 1) / 2);
-  const int h = (int)(local / per);
-  ItemAt x = item_of(q, h, min((int)((local - h * per) / q.tiles), q.mt - 1));
+  const int h = (int)udiv(local, per);
+  ItemAt x = item_of(q, h, min((int)udiv(local - h * per, q.tiles), q.mt - 1));
   x.t0 = (int)(local - x.start);
   return x;
 }
@@ -205,9 +229,9 @@ __device__ __forceinline__ AttnPlace find_place(const AttnArgs& a, int cta, int 
   }
   long long lo = before + incl - mine;
   AttnPlace p;
-  const int G = (int)min((long long)a.grid, total);
-  p.u0 = cta < G ? (long long)cta * total / G : total;
-  p.u1 = cta < G ? (long long)(cta + 1) * total / G : total;
+  const Split sp = make_split(total, a.grid);
+  p.u0 = cta < sp.G ? split_start(sp, cta) : total;
+  p.u1 = cta < sp.G ? split_start(sp, cta + 1) : total;
   long long* found = sh + NT / 32;
   if (p.u0 < p.u1 && lo <= p.u0 && p.u0 < lo + mine) {
     int r = r0;

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
       ++r;
       continue;
     }
-    const int item = (int)((u - base) / rq.tiles);
+    const int item = (int)udiv(u - base, rq.tiles);
     const int t0 = (int)((u - base) - (long long)item * rq.tiles);
     const int t1 = (int)min((long long)rq.tiles, t0 + (pl.u1 - u));
     const int h = item / rq.mt, row0 = (item - h * rq.mt) * M;

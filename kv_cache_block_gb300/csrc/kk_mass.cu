@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const AttnArgs a) {
       ++r;
       continue;
     }
-    const int h = (int)((u - base) / rq.tiles), t = (int)((u - base) % rq.tiles);
+    const int h = (int)udiv(u - base, rq.tiles), t = (int)(u - base - (long long)h * rq.tiles);
     const int v = t * kTK + tid;
     TokenAt at;
     const bool ok = token_at(a, r, rq, v, true, &at);
