@@ -41,10 +41,9 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const AttnArgs 
       ++r;
       continue;
     }
-    const int item = (int)udiv(u - base, rq.tiles);
-    const int t0 = (int)((u - base) - (long long)item * rq.tiles);
-    const int t1 = (int)min((long long)rq.tiles, t0 + (pl.u1 - u));
-    const int h = item / rq.mt, row0 = (item - h * rq.mt) * M;
+    ItemAt it = item_at(rq, u - base);
+    it.t1 = (int)min((long long)rq.tiles, it.t0 + (pl.u1 - u));
+    const int t0 = it.t0, t1 = it.t1, h = it.h, row0 = it.mt * M;
     const int rows = min(M, rq.n * a.G - row0);
     for (int i = tid; i < M * D; i += kSimtThreads) {
       const int m = i / D, d = i - m * D, row = row0 + m;
@@ -198,9 +197,11 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const AttnArgs 
 }
 
 // The CTAs [c0, c0 + n) whose partial results make up an item (n = 0: nothing
-// to add up, or no rows from `row` of the tile on), and c0's slot.
+// to add up, or no rows from `row` of the tile on), and c0's slot: worked out
+// again from the sizes while the main kernel still runs, so that nothing but
+// the parts is read after it.
 struct Cut {
-  int c0, n, first, halves, node0, rows;
+  int c0, n, first, node0, rows;
 };
 template <int NT>
 __device__ __forceinline__ Cut find_cut(const AttnArgs& a, int r, int h, int mt, int row, int M, int TK, int tid) {
@@ -237,7 +238,6 @@ __device__ __forceinline__ Cut find_cut(const AttnArgs& a, int r, int h, int mt,
       c.c0 = split_owner(sp, lo);
       c.n = split_owner(sp, lo + it.units - 1) - c.c0 + 1;
       c.first = split_start(sp, c.c0) == lo ? 0 : 1;  // c0's slot: its first item, or its last
-      c.halves = it.single ? 2 : 1;  // a single's streams leave a part each, M/2 rows apart
       if (c.n == 1) c.n = 0;
       c.node0 = rq.node0;
       c.rows = rq.n * a.G;
@@ -268,8 +268,8 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const Att
   const int rpb = kCombineThreads / 32 / wpr;  // rows of a block
   if (blockIdx.y * rpb >= M) return;
   const Cut cut = find_cut<kCombineThreads>(a, r, h, mt, blockIdx.y * rpb, M, TK, tid);
-  if (cut.n == 0) return;
   const int parts = cut.n;
+  if (parts == 0) return;
   const int grp = tid / L, ln = tid % L, gpr = NG / rpb;  // lane groups of a row
   const int row = mt * M + blockIdx.y * rpb + grp / gpr, gi = grp % gpr;
   const bool real = row < cut.rows;
@@ -338,54 +338,69 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const Att
 }
 
 // The same for the tensor-memory kernel's slots, [D/4][256 rows][4]: a lane is a
-// row, a warp takes 16 of its values, and every load and store is whole sectors.
+// row, a warp takes 8 of its values, and every load and store is whole sectors.
+// Blocks of 32 rows x 32 values and eight parts in flight a thread: with a row's
+// 128 values in one block and four in flight, 18 parts took 11 us of latency.
+constexpr int kTcCombineThreads = 128;
+
 template <int D>
-__global__ void __launch_bounds__(D * 2) attn_combine_tc_kernel(const AttnArgs a, int TK, int mt_max) {
-  constexpr int M = 256, NT = D * 2;
+__global__ void __launch_bounds__(kTcCombineThreads) attn_combine_tc_kernel(const AttnArgs a, int TK, int mt_max) {
+  constexpr int M = 256, U = 8;
   const int tid = threadIdx.x, ln = tid & 31, w = tid >> 5;
   const int mt = blockIdx.x % mt_max, h = (blockIdx.x / mt_max) % a.kc.H, r = blockIdx.x / (mt_max * a.kc.H);
-  const Cut cut = find_cut<NT>(a, r, h, mt, blockIdx.y * 32, M, TK, tid);
-  if (cut.n == 0 || (cut.halves == 2 && blockIdx.y >= 4)) return;
-  const int m = blockIdx.y * 32 + ln, row = mt * M + m;
-  if (row >= cut.rows) return;
+  const AttnReq rq = load_req(a, r, M, TK, false);
+  const int m = blockIdx.y * 32 + ln, row = mt * M + m, v4 = (blockIdx.z * 4 + w) * 2;  // first float4 of the row
+  if (mt >= rq.mt || row >= rq.n * a.G) return;
   pdl_wait();
-  const int parts = cut.n * cut.halves, sh = cut.halves - 1;
-  auto slot = [&](int i) { return partial_slot(a, cut.c0 + (i >> sh), i >> sh ? 0 : cut.first, M, D); };
+  const int4 cut = a.cuts[blockIdx.x];
+  if (cut.z == cut.x) return;
+  // a single's streams leave a part each, M/2 rows apart
+  const int sh = mt >= rq.mt - rq.odd, parts = (cut.z - cut.x + 1) << sh;
+  auto slot = [&](int i) { return partial_slot(a, cut.x + (i >> sh), i >> sh ? 0 : cut.y, M, D); };
   auto at_row = [&](int i) { return m + (i & sh) * (M / 2); };
   float mm = -INFINITY, l = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < parts; ++i) mm = fmaxf(mm, slot(i)[M * D + at_row(i)]);
-  const float ref = mm == -INFINITY ? 0.f : mm;
-  float4 acc[4];
+  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int b = 0; b < parts; b += U) {
+    float pm[U], pl[U];
+    float4 x[U][2];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = 0; i < parts; ++i) {
-    const float* part = slot(i);
-    const int pr = at_row(i);
-    const float al = ex2(part[M * D + pr] - ref);
-    l += part[M * D + M + pr] * al;
+    for (int i = 0; i < U; ++i) {
+      const bool on = b + i < parts;
+      const float* part = slot(on ? b + i : b);
+      const int pr = at_row(on ? b + i : b);
+      pm[i] = on ? part[M * D + pr] : -INFINITY;
+      pl[i] = part[M * D + M + pr];
+      x[i][0] = reinterpret_cast<const float4*>(part)[v4 * M + pr];
+      x[i][1] = reinterpret_cast<const float4*>(part)[(v4 + 1) * M + pr];
+    }
+    float m2 = mm;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float4 x = reinterpret_cast<const float4*>(part)[(w * 4 + e) * M + pr];
-      acc[e].x += x.x * al;
-      acc[e].y += x.y * al;
-      acc[e].z += x.z * al;
-      acc[e].w += x.w * al;
+    for (int i = 0; i < U; ++i) m2 = fmaxf(m2, pm[i]);
+    const float ref = m2 == -INFINITY ? 0.f : m2, f = ex2(mm - ref);
+    mm = m2;
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) acc[e] = make_float4(acc[e].x * f, acc[e].y * f, acc[e].z * f, acc[e].w * f);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (b + i >= parts) break;
+      const float al = ex2(pm[i] - ref);
+      l += pl[i] * al;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        acc[e].x += x[i][e].x * al;
+        acc[e].y += x[i][e].y * al;
+        acc[e].z += x[i][e].z * al;
+        acc[e].w += x[i][e].w * al;
+      }
     }
   }
   const float inv = row_inv(l);
-  const long long at = (long long)(cut.node0 + row / a.G) * a.Hq + h * a.G + row % a.G;
-  uint32_t y[8];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    y[e * 2] = pack_bf16(acc[e].x * inv, acc[e].y * inv);
-    y[e * 2 + 1] = pack_bf16(acc[e].z * inv, acc[e].w * inv);
-  }
-  uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + w * 16);
-  out[0] = make_uint4(y[0], y[1], y[2], y[3]);
-  out[1] = make_uint4(y[4], y[5], y[6], y[7]);
-  if (w == 0 && a.lse) a.lse[at] = row_lse(mm, l);
+  const long long at = (long long)(rq.node0 + row / a.G) * a.Hq + h * a.G + row % a.G;
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + v4 * 4) =
+      make_uint4(pack_bf16(acc[0].x * inv, acc[0].y * inv), pack_bf16(acc[0].z * inv, acc[0].w * inv),
+                 pack_bf16(acc[1].x * inv, acc[1].y * inv), pack_bf16(acc[1].z * inv, acc[1].w * inv));
+  if (v4 == 0 && a.lse) a.lse[at] = row_lse(mm, l);
 }
 
 // Launches a combine kernel so that it may start while the main kernel ends.
@@ -405,16 +420,17 @@ cudaError_t launch_dependent(void (*k)(P...), dim3 grid, int threads, cudaStream
 
 template <int D>
 cudaError_t combine_tc(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
-  const int rows = a.max_nodes * a.G, mt_max = (rows + pl.M - 1) / pl.M;
-  return launch_dependent(attn_combine_tc_kernel<D>,
-                          dim3((unsigned)(a.bt.R * a.kc.H * mt_max), (unsigned)((std::min(pl.M, rows) + 31) / 32)), D * 2,
-                          s, a, pl.TK, mt_max);
+  const int rows = a.max_nodes * a.G, mt_max = a.mt_max;
+  return launch_dependent(
+      attn_combine_tc_kernel<D>,
+      dim3((unsigned)(a.bt.R * a.kc.H * mt_max), (unsigned)((std::min(pl.M, rows) + 31) / 32), (unsigned)(D / 32)),
+      kTcCombineThreads, s, a, pl.TK, mt_max);
 }
 
 template <typename T, int D>
 cudaError_t combine_t(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
   const int M = pl.M;
-  const int mt_max = (int)(((long long)a.max_nodes * a.G + M - 1) / M);
+  const int mt_max = a.mt_max;
   const long long items = (long long)a.bt.R * a.kc.H * mt_max;
   // warps of a row: about four parts each when every CTA works on few items
   int wpr = 1;
@@ -445,19 +461,30 @@ size_t plan_bytes(const AttnPlan& pl, int D) {
   return (size_t)pl.grid * (pl.kind == AttnPlan::kTc ? 3 : 2) * pl.M * (D + 2) * sizeof(float);
 }
 
+// The notes on the items, in front of the partial results.
+size_t cut_bytes(const AttnPlan& pl, int R, int H, int rows) {
+  if (pl.kind != AttnPlan::kTc) return 0;
+  return ((size_t)R * H * ((rows + pl.M - 1) / pl.M) * sizeof(int4) + 255) & ~size_t(255);
+}
+
 }  // namespace
 
-size_t attn_workspace_bytes(const KCache& kc, int max_nodes, int G) {
+size_t attn_workspace_bytes(const KCache& kc, int R, int max_nodes, int G) {
   // enough for either kernel: which one runs also depends on the V cache's strides
-  size_t n = plan_bytes(plan(kc, kc, max_nodes, G), kc.D);
-  if (kc.dtype == 1) n = std::max(n, plan_bytes(attn_mma_plan(kc, max_nodes * G), kc.D));
-  return n;
+  const int rows = max_nodes * G;
+  auto size = [&](const AttnPlan& pl) { return cut_bytes(pl, R, kc.H, rows) + plan_bytes(pl, kc.D); };
+  const size_t n = size(plan(kc, kc, max_nodes, G));
+  return kc.dtype == 1 ? std::max(n, size(attn_mma_plan(kc, rows))) : n;
 }
 
 cudaError_t launch_tree_attn(AttnArgs a, cudaStream_t s) {
   const AttnPlan pl = plan(a.kc, a.vc, a.max_nodes, a.G);
   a.grid = pl.grid;
   a.twin = pl.kind == AttnPlan::kTc;
+  const int rows = a.max_nodes * a.G;
+  a.mt_max = (rows + pl.M - 1) / pl.M;
+  a.cuts = reinterpret_cast<int4*>(a.ws);
+  a.ws = reinterpret_cast<float*>(reinterpret_cast<char*>(a.ws) + cut_bytes(pl, a.bt.R, a.kc.H, rows));
   const bool bf = a.kc.dtype == 1;
   cudaError_t e = cudaErrorNotSupported;
   if (pl.kind == AttnPlan::kTc) {

@@ -37,6 +37,8 @@ struct AttnArgs {
   float scale_log2;  // scale * log2(e)
   void* out;         // [total_nodes][Hq][D]
   float* lse;        // [total_nodes][Hq] or null
+  int4* cuts;        // [R * H * mt_max]: the CTAs that share an item (see note_cut; twin only)
+  int mt_max;        // row tiles of a request, at most
   float* ws;
   int grid;  // CTAs of the main kernel
   int twin;  // row tiles are pairs of M/2 rows; an odd last one is a single (kk_attn_tc.cu)
@@ -254,6 +256,18 @@ __device__ __forceinline__ AttnPlace find_place(const AttnArgs& a, int cta, int 
 // pairs) holds M*D accumulators, then M running maxima (log2 domain) and M sums.
 __device__ __forceinline__ float* partial_slot(const AttnArgs& a, int cta, int which, int M, int D) {
   return a.ws + (size_t)((a.twin ? 3 : 2) * cta + which) * M * (D + 2);
+}
+
+// For the tensor-memory kernel's combine: the CTA that holds an item's first unit notes itself
+// and its slot (0 where the item starts its range), the one that holds the last
+// unit notes itself: (first CTA, its slot, last CTA).
+__device__ __forceinline__ void note_cut(const AttnArgs& a, int cta, int r, const ItemAt& it, bool starts) {
+  int* c = reinterpret_cast<int*>(a.cuts + ((long long)r * a.kc.H + it.h) * a.mt_max + it.mt);
+  if (it.t0 == 0) {
+    c[0] = cta;
+    c[1] = starts ? 0 : 1;
+  }
+  if (it.t1 == it.units) c[2] = cta;
 }
 
 // 1 / sum and lse of a row with running maximum m (log2 domain) and sum l; a

@@ -72,7 +72,8 @@ size_t kk_tree_attn_workspace_bytes(const kk_kcache_desc* kc, const kk_block_tab
     return 0;
   kk::KCache c = {};
   if (kk::check_kcache_desc(kc, &c) != KK_OK) return 0;
-  return kk::attn_workspace_bytes(c, max_nodes, num_q_heads / c.H);
+  if (bt->num_requests < 0 || bt->num_requests > 65535) return 0;
+  return kk::attn_workspace_bytes(c, bt->num_requests, max_nodes, num_q_heads / c.H);
 }
 
 kk_status kk_tree_attn(const kk_kcache_desc* kc, const kk_kcache_desc* vc, const kk_block_table* bt, int32_t layer,
@@ -109,7 +110,7 @@ kk_status kk_tree_attn(const kk_kcache_desc* kc, const kk_kcache_desc* vc, const
   if (!out) return KK_ERR_INVALID;
   if (!aligned(out, 16) || !aligned(lse, 4)) return KK_ERR_UNSUPPORTED;
   if ((long long)a.bt.R * a.kc.H * a.max_nodes * a.G > 0x7FFFFFFFll) return KK_ERR_UNSUPPORTED;
-  if (!workspace || workspace_bytes < kk::attn_workspace_bytes(a.kc, a.max_nodes, a.G)) return KK_ERR_INVALID;
+  if (!workspace || workspace_bytes < kk::attn_workspace_bytes(a.kc, a.bt.R, a.max_nodes, a.G)) return KK_ERR_INVALID;
   if (!aligned(workspace, 256)) return KK_ERR_UNSUPPORTED;
   a.out = out;
   a.lse = lse;

@@ -121,10 +121,9 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
       ++r;
       continue;
     }
-    const int item = (int)udiv(u - base, rq.tiles);
-    const int t0 = (int)((u - base) - (long long)item * rq.tiles);
-    const int t1 = (int)min((long long)rq.tiles, t0 + (pl.u1 - u));
-    const int h = item / rq.mt, row0 = (item - h * rq.mt) * M;
+    ItemAt it = item_at(rq, u - base);
+    it.t1 = (int)min((long long)rq.tiles, it.t0 + (pl.u1 - u));
+    const int t0 = it.t0, t1 = it.t1, h = it.h, row0 = it.mt * M;
     const int rows = min(M, rq.n * a.G - row0);
     // the first tiles' copies go out before the queries are read
     Tok nx = find_token<D>(a, r, rq, h, t0, w, lane);

@@ -205,6 +205,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Work w = work_at(a, pl, u, &r, &base);
       const bool single = __shfl_sync(kFull, (int)w.at.single, 0);
       const int tiles = __shfl_sync(kFull, w.tiles, 0);
+      if (tid == 0) note_cut(a, blockIdx.x, r, w.at, u == pl.u0);
+      __syncwarp();
       const int sub = single ? 0 : x;  // row tile of the stream
       const int steps = single ? tiles : 2 * tiles;
       const int rows = __shfl_sync(kFull, w.rows, 0) - sub * 128;

@@ -198,9 +198,9 @@ unsigned long long wait_limit_ns();
 long long take_skip_box();
 
 // kk_attn.cu: attention of drafted nodes over the paged cache (AttnArgs:
-// kk_attn.cuh). The workspace holds two partial results per CTA of the grid.
+// kk_attn.cuh). The workspace holds the partial results of the grid's CTAs.
 struct AttnArgs;
-size_t attn_workspace_bytes(const KCache& kc, int max_nodes, int G);
+size_t attn_workspace_bytes(const KCache& kc, int R, int max_nodes, int G);
 cudaError_t launch_tree_attn(AttnArgs a, cudaStream_t s);
 // kk_mass.cu: the attention weight every cached token received
 cudaError_t launch_attn_mass(const AttnArgs& a, cudaStream_t s);
