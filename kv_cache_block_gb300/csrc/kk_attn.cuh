@@ -67,6 +67,10 @@ bool attn_tc_suits(const KCache& kc);
 AttnPlan attn_tc_plan();
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t s);
 
+// kk_mass_tc.cu (bf16, D 64, 128 or 256, a layout it suits)
+bool mass_tc_suits(const KCache& kc);
+cudaError_t launch_mass_tc(const AttnArgs& a, cudaStream_t s);
+
 struct AttnReq {
   int node0, n;      // first node, nodes
   int off, T;        // table start, cached tokens

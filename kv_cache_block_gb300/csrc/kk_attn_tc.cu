@@ -27,13 +27,12 @@
 // copied by the loader's lanes, zeros for what is not there: a weight of zero
 // must not meet what such a place holds.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include <cfloat>
 
 #include "kk_attn.cuh"
 #include "kk_pdl.cuh"
-#include "kk_tcgen05.cuh"
+#include "kk_tiles.cuh"
 
 namespace kk {
 namespace {
@@ -71,30 +70,6 @@ struct Bars {
   uint64_t note[kMeta];
   uint64_t drain;
 };
-
-// Waits for a barrier's phase with the whole warp; gives up (false) past the
-// limit or when another role has given up, and tells the others. All lanes leave
-// the loop at once: what the warp does next takes its addresses from uniform
-// registers and must not be reached by some lanes before the others.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const AttnArgs& a, volatile int* stop) {
-  uint32_t n = 0;
-  uint64_t t0 = 0;
-  while (!__all_sync(kFull, mbar_try_wait(bar, parity))) {
-    if ((++n & 63u) != 0) continue;  // the timer is slow to read
-    const uint64_t now = globaltimer_ns();
-    if (t0 == 0) t0 = now;
-    const bool late = now - t0 > a.wait_ns;
-    if (__any_sync(kFull, late || *stop)) {
-      if (late) {
-        *stop = 1;
-        flag_error(a.err, kErrTimeout);
-      }
-      __syncwarp();
-      return false;
-    }
-  }
-  return true;
-}
 
 // An item's place in a CTA's range.
 struct Work {
@@ -216,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The stream's queries, a row a thread (a single item's stream B reads A's).
       // A negative scale turns their signs; rows that do not exist are zero.
       if (items > 0) {
-        alive = wait(&b.q_empty, (items - 1) & 1, a, stop);
+        alive = warp_wait(&b.q_empty, (items - 1) & 1, a, stop);
         if (!alive) break;
       }
       if (!single || x == 0) {
@@ -248,8 +223,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int half = single ? x : i & 1;  // 64 tokens of the tile
         const TileNote* note = &s_note[no % kMeta];
         const uint32_t buf = seen & 1, sp = s_at + buf * 64;
-        alive = wait(&b.note[no % kMeta], (no / kMeta) & 1, a, stop) &&
-                wait(&b.s_full[x][buf], (seen >> 1) & 1, a, stop);
+        alive = warp_wait(&b.note[no % kMeta], (no / kMeta) & 1, a, stop) &&
+                warp_wait(&b.s_full[x][buf], (seen >> 1) & 1, a, stop);
         if (!alive) break;
         tc_fence_after();
         if (busy) {
@@ -304,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (!first) {
               // every product into O so far (this stream's step before) has to be in
-              if (!wait(&b.pv_done[x], (seen - 1) & 1, a, stop)) al = 0.f;  // given up: the result is void
+              if (!warp_wait(&b.pv_done[x], (seen - 1) & 1, a, stop)) al = 0.f;  // given up: the result is void
               tc_fence_after();
 #pragma unroll 1
               for (int k = 0; k < D / 32; ++k) {
@@ -338,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       notes += tiles;
       // ---- the item's end: O and the row's maximum and sum
-      if (alive) alive = wait(&b.o_full[x], items & 1, a, stop);
+      if (alive) alive = warp_wait(&b.o_full[x], items & 1, a, stop);
       if (!alive) break;
       tc_fence_after();
       uint32_t odd = 0;
@@ -348,8 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // stream B first hands its part to stream A through the CTA's third slot.
       const bool whole = w.at.t0 == 0 && w.at.t1 == w.at.units;
       const bool give = whole && single && x == 1, take = whole && single && x == 0;
-      if (give && hands > 0) alive = wait(&b.hand_empty, (hands - 1) & 1, a, stop);
-      if (take) alive = wait(&b.hand_full, hands & 1, a, stop);
+      if (give && hands > 0) alive = warp_wait(&b.hand_empty, (hands - 1) & 1, a, stop);
+      if (take) alive = warp_wait(&b.hand_full, hands & 1, a, stop);
       if (!alive) break;
       const bool mine = row < rows;
       const int prow = x * 128 + row;  // row of the partial slot (both streams of a single item leave one)
@@ -456,13 +431,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tiles = __shfl_sync(kFull, w.tiles, 0);
       const int steps = single ? tiles : 2 * tiles;
       const uint32_t q0 = (uint32_t)dq + ((single ? 0 : x) * C::kTile >> 4);
-      alive = wait(&b.q_full, items & 1, a, stop);
+      alive = warp_wait(&b.q_full, items & 1, a, stop);
       if (!alive) break;
       // scores of step j, 64 tokens; a tile is let go behind its last step
       auto qk = [&](int j) {
         const uint32_t no = cnt + (single ? j : j >> 1), st = no % KS;
         const int half = single ? x : j & 1;
-        if ((single || !half) && !wait(&b.k_full[st], (no / KS) & 1, a, stop)) return false;
+        if ((single || !half) && !warp_wait(&b.k_full[st], (no / KS) & 1, a, stop)) return false;
         tc_fence_after();
         const uint32_t buf = qs++ & 1;
         const uint32_t k0 = (uint32_t)dk + ((st * C::kTile + half * (C::kChunk / 2)) >> 4);
@@ -482,10 +457,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t no = cnt + (single ? j : j >> 1), st = no % VS;
         const int half = single ? x : j & 1;
         const uint32_t buf = ps & 1;
-        if ((single || !half) && !wait(&b.v_full[st], (no / VS) & 1, a, stop)) return false;
+        if ((single || !half) && !warp_wait(&b.v_full[st], (no / VS) & 1, a, stop)) return false;
         // O is read out before the next item writes it
-        if (j == 0 && items > 0 && !wait(&b.o_empty[x], (items - 1) & 1, a, stop)) return false;
-        if (!wait(&b.p_full[x][buf], (ps >> 1) & 1, a, stop)) return false;
+        if (j == 0 && items > 0 && !warp_wait(&b.o_empty[x], (items - 1) & 1, a, stop)) return false;
+        if (!warp_wait(&b.p_full[x][buf], (ps >> 1) & 1, a, stop)) return false;
         ++ps;
         tc_fence_after();
         const uint32_t v0 = (uint32_t)dv + ((st * C::kTile + half * (C::kChunk / 2)) >> 4);
@@ -547,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       TileNote* note = &s_note[no % kMeta];
       uint64_t *noted = &b.note[no % kMeta], *bar = val ? &b.v_full[st] : &b.k_full[st];
       unsigned char* dst = (val ? s_v : s_k) + st * C::kTile;
-      if (!wait(val ? &b.v_empty[st] : &b.k_empty[st], ((no / ns) & 1) ^ 1, a, stop)) return false;
+      if (!warp_wait(val ? &b.v_empty[st] : &b.k_empty[st], ((no / ns) & 1) ^ 1, a, stop)) return false;
       sent[val] = no + 1;
       if (__all_sync(kFull, pc.full)) {
         if (elect_one()) {
@@ -655,38 +630,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// 4-D map of one layer: 64 dims x `tb` tokens of a (token, head, page) cache.
-bool encode_map(const KCache& kc, int layer, int tb, CUtensorMap* tm) {
-  auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
-  if (!encode) return false;
-  const long long ext[3] = {kc.bs, kc.H, kc.num_pages}, st[3] = {kc.sT * 2, kc.sH * 2, kc.sP * 2};
-  cuuint64_t dims[4] = {(cuuint64_t)kc.D, 0, 0, 0}, strides[3];
-  for (int i = 0; i < 3; ++i) {
-    dims[i + 1] = (cuuint64_t)ext[i];
-    strides[i] = ext[i] == 1 ? (cuuint64_t)kc.D * 2 : (cuuint64_t)st[i];
-  }
-  const cuuint32_t box[4] = {64, (cuuint32_t)tb, 1, 1}, es[4] = {1, 1, 1, 1};
-  void* at = const_cast<uint16_t*>(static_cast<const uint16_t*>(kc.base) + layer * kc.sL);
-  return encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, at, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int piece(int bs) {  // tokens of a TMA box: the largest divisor of both the block and the tile
-  int a = bs, b = kTK;
-  while (b) {
-    const int t = a % b;
-    a = b;
-    b = t;
-  }
-  return a;
-}
-
 template <int D>
 cudaError_t go(const AttnArgs& a, cudaStream_t s) {
   CUtensorMap tk, tv;
-  const int tb = piece(a.kc.bs);
-  if (!encode_map(a.kc, a.layer, tb, &tk) || !encode_map(a.vc, a.layer, tb, &tv)) return cudaErrorNotSupported;
+  const int tb = tile_piece(a.kc.bs, kTK);
+  if (!encode_tile_map(a.kc, a.layer, tb, &tk) || !encode_tile_map(a.vc, a.layer, tb, &tv)) return cudaErrorNotSupported;
   const cudaError_t e =
       cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
@@ -696,13 +644,7 @@ cudaError_t go(const AttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-bool attn_tc_suits(const KCache& kc) {
-  if (kc.dtype != 1 || (kc.D != 64 && kc.D != 128) || kc.bs % 8 != 0) return false;
-  const long long ext[3] = {kc.bs, kc.H, kc.num_pages}, st[3] = {kc.sT, kc.sH, kc.sP};
-  for (int i = 0; i < 3; ++i)
-    if (ext[i] > 1 && (st[i] < 8 || st[i] * 2 >= (1ll << 40))) return false;
-  return true;
-}
+bool attn_tc_suits(const KCache& kc) { return (kc.D == 64 || kc.D == 128) && tile_layout_suits(kc); }
 
 AttnPlan attn_tc_plan() { return AttnPlan{AttnPlan::kTc, 256, kTK, sm_count()}; }
 

@@ -111,6 +111,7 @@ cudaError_t simt_t(AttnArgs a, cudaStream_t s) {
 
 cudaError_t launch_attn_mass(const AttnArgs& a, cudaStream_t s) {
   const bool bf = a.kc.dtype == 1;
+  if (mass_tc_suits(a.kc)) return launch_mass_tc(a, s);
   switch (a.kc.D) {
     case 32: return bf ? simt_t<bf16_t, 32>(a, s) : simt_t<float, 32>(a, s);
     case 64: return bf ? simt_t<bf16_t, 64>(a, s) : simt_t<float, 64>(a, s);
