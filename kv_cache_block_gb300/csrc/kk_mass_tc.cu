@@ -14,6 +14,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kk_tiles.cuh"
 
@@ -27,10 +28,11 @@ constexpr int kTK = 128;
 constexpr int kCols = 128;  // rows of a job
 constexpr int kMaxRows = 1024;
 constexpr int kStagesMax = 8;
-constexpr int kSmemMax = 227 * 1024 - 1024 - 16 * 1024;  // next to the row list and the barriers
+constexpr int kSmemMax = 227 * 1024 - 1024 - 20 * 1024;  // next to the row list and the barriers
 
-struct RowInfo {
+struct __align__(16) RowInfo {
   float b, w;  // -lse in the log2 domain, weight
+  int len;     // tokens the row sees
 };
 
 struct Bars {
@@ -53,11 +55,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* s_k = smem;
   unsigned char* s_q = s_k + NS * kTile;  // [64-dim chunk][rows_pad][128 bytes], 128-byte swizzle
   __shared__ Bars b;
-  __shared__ __align__(16) RowInfo s_row[kMaxRows];
-  __shared__ int s_len[kMaxRows];
+  __shared__ RowInfo s_row[kMaxRows + 32];  // rows up to a whole group of 32 see nothing
   __shared__ long long s_place[kThreads / 32 + 4];
   __shared__ int s_cnt[kEpi / 32];
-  __shared__ int s_rows, s_minlen;  // rows of the item that count; the least tokens one of them sees
+  __shared__ int s_rows;  // rows of the item that count
   __shared__ uint32_t s_tmem;
   __shared__ int s_stop;
   volatile int* stop = &s_stop;
@@ -117,17 +118,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++items;
       alive = !named_sync_or(1, kEpi, !alive);
       if (!alive) break;
-      if (tid == 0) s_minlen = 0x7FFFFFFF;
       const int r0 = min(row_begin, rq.n * a.G), r1 = min(row_end, rq.n * a.G);
-      int have = 0;
-      for (int x0 = r0; x0 < r1; x0 += kEpi) {  // list the rows that count, in order
-        const int x = x0 + tid, node = rq.node0 + x / a.G;
-        float w = 0.f, l = -INFINITY;
+      constexpr int NX = kMaxRows / kEpi;  // rows a thread looks at
+      float rw[NX], rl[NX];
+      int rn[NX], len[NX];
+#pragma unroll
+      for (int y = 0; y < NX; ++y) {
+        const int x = r0 + y * kEpi + tid;
+        rw[y] = 0.f;
         if (x < r1) {
-          w = a.row_w ? a.row_w[node] : 1.f;
-          l = a.lse[(long long)node * a.Hq + h * a.G + x % a.G];
+          rn[y] = rq.node0 + x / a.G;
+          rw[y] = a.row_w ? a.row_w[rn[y]] : 1.f;
+          rl[y] = a.lse[(long long)rn[y] * a.Hq + h * a.G + x % a.G];
+          len[y] = a.row_lens ? a.row_lens[rn[y]] : rq.T;
         }
-        const bool on = x < r1 && w != 0.f && l != -INFINITY;
+      }
+      int have = 0;
+#pragma unroll
+      for (int y = 0; y < NX; ++y) {  // list the rows that count, in order
+        if (r0 + y * kEpi >= r1) break;
+        const bool on = rw[y] != 0.f && rl[y] != -INFINITY;
         const uint32_t m = __ballot_sync(kFull, on);
         if (lane == 0) s_cnt[warp] = __popc(m);
         named_sync(1, kEpi);
@@ -137,12 +147,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           all += s_cnt[k];
         }
         if (on) {
-          const int i = before + __popc(m & ((1u << lane) - 1u));
-          const int len = a.row_lens ? a.row_lens[node] : rq.T;
-          s_row[i] = RowInfo{-l * 1.44269504088896341f, w};
-          s_len[i] = len;
-          atomicMin(&s_minlen, len);
-          const uint16_t* q = static_cast<const uint16_t*>(a.q) + node * a.q_sn + (long long)(h * a.G + x % a.G) * a.q_sh;
+          const int i = before + __popc(m & ((1u << lane) - 1u)), x = r0 + y * kEpi + tid;
+          s_row[i] = RowInfo{-rl[y] * 1.44269504088896341f, rw[y], len[y]};
+          const uint16_t* q =
+              static_cast<const uint16_t*>(a.q) + rn[y] * a.q_sn + (long long)(h * a.G + x % a.G) * a.q_sh;
 #pragma unroll
           for (int c = 0; c < D / 8; ++c)
             cp_async16(smem_u32(s_q) + (c / 8) * rows_pad * 128 + i * 128 + (((c & 7) ^ (i & 7)) << 4), q + c * 8, true);
@@ -150,28 +158,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         have = all;
         named_sync(1, kEpi);
       }
+      if (tid < 32) s_row[have + tid] = RowInfo{0.f, 0.f, 0};
       if (tid == 0) s_rows = have;
       cp_wait_all();
       fence_async_smem();
       named_sync(1, kEpi);
       if (lane == 0) mbar_arrive(&b.q_full);
       __syncwarp();
-      const int n = __shfl_sync(kFull, s_rows, 0), minlen = __shfl_sync(kFull, s_minlen, 0);
+      const int n = __shfl_sync(kFull, s_rows, 0);
       const int nch = (n + kCols - 1) / kCols;
       const int old = a.old_lens ? a.old_lens[r] : rq.T;
+      // A tile's token is looked up two tiles ahead and what it had is read one
+      // tile ahead: two dependent loads that would else wait behind every tile.
+      auto find = [&](int t) {  // the token's weight, or -1
+        TokenAt tk;
+        long long x = -1;
+        if (t < at.t1 && token_at(a, r, rq, t * kTK + row, true, &tk))
+          x = (((long long)a.layer * a.kc.num_pages + tk.page) * a.kc.H + h) * a.kc.bs + tk.tok;
+        __syncwarp();
+        return x;
+      };
+      auto had = [&](int t, long long x) {
+        float y = 0.f;
+        // a later pass over more rows adds to what the first one wrote
+        if (x >= 0 && row_begin > 0)
+          y = a.mass_out[x];
+        else if (x >= 0 && a.mass_in && t * kTK + row < old)
+          y = a.decay * a.mass_in[x];
+        __syncwarp();
+        return y;
+      };
+      long long x1 = find(at.t0 + g), x2 = find(at.t0 + g + 2);
+      float had1 = had(at.t0 + g, x1);
       for (int t = at.t0 + g; t < at.t1 && alive; t += 2) {
         const int v = t * kTK + row;
-        TokenAt tk;
-        const bool ok = token_at(a, r, rq, v, true, &tk);
-        const long long x = (((long long)a.layer * a.kc.num_pages + tk.page) * a.kc.H + h) * a.kc.bs + tk.tok;
-        // a later pass over more rows adds to what the first one wrote
-        float had = 0.f;
-        if (ok && row_begin > 0)
-          had = a.mass_out[x];
-        else if (ok && a.mass_in && v < old)
-          had = a.decay * a.mass_in[x];
-        __syncwarp();
-        const bool cut = (t + 1) * kTK > minlen;  // some row does not see all of the tile
+        const long long x = x1;
+        const float before = had1;
+        had1 = had(t + 2, x2);
+        x1 = x2;
+        x2 = find(t + 4);
         float acc = 0.f;
         for (int c = 0; c < nch; ++c, ++jobs) {
           const uint32_t buf = g + 2 * (jobs & 1);
@@ -179,37 +204,48 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!alive) break;
           tc_fence_after();
           const int cols = min(kCols, n - c * kCols);
-#pragma unroll 1
-          for (int k = 0; k < cols; k += 32) {
-            uint32_t s[32];
-            tmem_ld32(tmem + lane_at + buf * kCols + k, s);
+          const uint32_t at_col = tmem + lane_at + buf * kCols;
+          const RowInfo* ri = s_row + c * kCols;
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+          // One small loop for whole, ragged and causal tiles alike: a row's length
+          // is tested for every token. The exponentials bound it (16 a clock and SM),
+          // the test hides behind them; a second copy of the loop without it cost
+          // more in fetched code than it saved.
+          auto sum = [&](auto count, const uint32_t* s, int k) {
+#pragma unroll
+            for (int e = 0; e < decltype(count)::value; ++e) {
+              const RowInfo y = ri[k + e];
+              const float p = ex2(__uint_as_float(s[e]) * a.scale_log2 + y.b);
+              part[e & 3] += y.w * (v < y.len ? p : 0.f);  // selected: a hidden place may hold anything
+            }
+          };
+          if (cols <= 8) {
+            uint32_t s0[8];
+            tmem_ld8(at_col, s0);
             tmem_wait_ld();
-            const int j0 = c * kCols + k;
-            float part[4] = {0.f, 0.f, 0.f, 0.f};
-            if (!cut && k + 32 <= cols) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const float4 y = *reinterpret_cast<const float4*>(&s_row[j0 + e]);
-                part[e & 3] += y.y * ex2(__uint_as_float(s[e]) * a.scale_log2 + y.x);
-                part[(e & 3) + 1] += y.w * ex2(__uint_as_float(s[e + 1]) * a.scale_log2 + y.z);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const int j = min(j0 + e, n - 1);
-                const RowInfo y = s_row[j];
-                const float p = y.w * ex2(__uint_as_float(s[e]) * a.scale_log2 + y.b);
-                part[e & 3] += (k + e < cols && v < s_len[j]) ? p : 0.f;  // selected, not multiplied
+            sum(std::integral_constant<int, 8>{}, s0, 0);
+          } else {
+            uint32_t s0[32], s1[32];
+            tmem_ld32(at_col, s0);
+#pragma unroll 1
+            for (int k = 0; k < cols; k += 64) {  // the next columns come while these are summed
+              tmem_wait_ld();
+              if (k + 32 < cols) tmem_ld32(at_col + k + 32, s1);
+              sum(std::integral_constant<int, 32>{}, s0, k);
+              if (k + 32 < cols) {
+                tmem_wait_ld();
+                if (k + 64 < cols) tmem_ld32(at_col + k + 64, s0);
+                sum(std::integral_constant<int, 32>{}, s1, k + 32);
               }
             }
-            acc += (part[0] + part[1]) + (part[2] + part[3]);
           }
+          acc += (part[0] + part[1]) + (part[2] + part[3]);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&b.s_empty[buf]);
           __syncwarp();
         }
-        if (ok && alive) a.mass_out[x] = had + acc;
+        if (x >= 0 && alive) a.mass_out[x] = before + acc;
         __syncwarp();
       }
       u += at.t1 - at.t0;
