@@ -11,7 +11,11 @@ namespace {
 
 // ---- selection -------------------------------------------------------------
 constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+// Weights of a row kept in shared memory (next to the histogram); longer rows
+// are read again for each of the five passes.
+constexpr int kMaxCached = 48 * 1024;
 
 // Order of a weight as an unsigned integer (larger: heavier): -0 as +0, NaN 0.
 __device__ __forceinline__ uint32_t mass_key(float m) {
@@ -20,19 +24,22 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
 
 // One CTA per (request, layer, head). The key of the (keep - sinks - recent)-th
 // heaviest token of the middle is found digit by digit (11, 11 and 10 bits)
-// from histograms in shared memory; then one ordered pass writes the tokens
-// above it and the first of those equal to it.
+// from histograms in shared memory; then every warp counts the tokens of its
+// share above it and equal to it, and, knowing the counts before its own, writes
+// its kept tokens in order.
+template <bool kCached>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(KCache kc, Table bt, const float* mass, int sinks,
                                                                    int recent, int keep, int* kept, int* new_lens,
                                                                    int* err) {
+  extern __shared__ uint32_t s_key[];  // cached: the middle's keys
   __shared__ uint32_t s_hist[kBins];
-  __shared__ uint32_t s_scan[kSelThreads / 32];
+  __shared__ uint32_t s_scan[kSelWarps], s_eq[kSelWarps];
   __shared__ uint32_t s_digit, s_left;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int h = blockIdx.x % kc.H, l = (blockIdx.x / kc.H) % kc.L, r = blockIdx.x / (kc.H * kc.L);
-  const int off = bt.offsets[r], nb = bt.offsets[r + 1] - off;
+  const int off = bt.offsets[r], nb = bt.offsets[r + 1] - off, bs = kc.bs;
   int T = bt.seq_lens[r];
-  if (T < 0 || nb < 0 || nb > bt.max_blocks || nb != (int)(((long long)T + kc.bs - 1) / kc.bs)) {
+  if (T < 0 || nb < 0 || nb > bt.max_blocks || nb != (int)(((unsigned)T + (unsigned)bs - 1u) / (unsigned)bs)) {
     if (tid == 0) flag_error(err, kErrBadIndex);
     T = 0;
   }
@@ -49,14 +56,35 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(KCache kc, Ta
   for (int i = tid; i < sinks; i += kSelThreads) out[i] = i;
   for (int i = tid; i < recent; i += kSelThreads) out[keep - recent + i] = T - recent + i;
   if (want == 0) return;
-  const float* mbase = mass + ((long long)l * kc.num_pages * kc.H + h) * kc.bs;
-  auto key_at = [&](int t) -> uint32_t {
-    const int b = t / kc.bs, page = bt.pages[off + b];
+  const float* mbase = mass + ((long long)l * kc.num_pages * kc.H + h) * bs;
+  const long long page_stride = (long long)kc.H * bs;
+  auto weight_of = [&](int b, int o) -> uint32_t {
+    const int page = bt.pages[off + b];
     if (page < 0 || page >= kc.num_pages) {
       flag_error(err, kErrBadIndex);
       return 0u;
     }
-    return mass_key(mbase[(long long)page * kc.H * kc.bs + (t - b * kc.bs)]);
+    return mass_key(mbase[page * page_stride + o]);
+  };
+  if (kCached) {
+    // A thread keeps its place in the block and steps whole blocks: one division
+    // in all, and four blocks' loads in flight.
+    const int per = bs < kSelThreads ? kSelThreads / bs : 1;  // blocks a turn
+    const int b0 = bs < kSelThreads ? tid / bs : 0, o0 = bs < kSelThreads ? tid - b0 * bs : tid;
+    if (b0 < per)
+      for (int o = o0; o < bs; o += kSelThreads) {
+#pragma unroll 4
+        for (int b = m0 / bs + b0; b < nb; b += per) {
+          const int t = b * bs + o;
+          if (t >= m0 && t < m1) s_key[t - m0] = weight_of(b, o);
+        }
+      }
+    __syncthreads();
+  }
+  auto key_at = [&](int t) -> uint32_t {
+    if (kCached) return s_key[t - m0];
+    const int b = t / bs;
+    return weight_of(b, t - b * bs);
   };
   uint32_t prefix = 0, left = want;
   int shift = 32;
@@ -67,6 +95,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(KCache kc, Ta
     shift -= bits;
     for (int i = tid; i < bins; i += kSelThreads) s_hist[i] = 0;
     __syncthreads();
+#pragma unroll 4
     for (int t = m0 + tid; t < m1; t += kSelThreads) {
       const uint32_t k = key_at(t);
       if (pass == 0 || (k >> up) == prefix) atomicAdd(&s_hist[(k >> shift) & (bins - 1)], 1u);
@@ -104,36 +133,41 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(KCache kc, Ta
     __syncthreads();
   }
   // `prefix` is the threshold key; the first `left` tokens equal to it stay
-  uint32_t done = (uint32_t)sinks, eq_done = 0;
-  for (int t0 = m0; t0 < m1; t0 += kSelThreads) {
-    const int t = t0 + tid;
-    const uint32_t k = t < m1 ? key_at(t) : 0u;
-    const bool gt = t < m1 && k > prefix, eq = t < m1 && k == prefix;
-    const uint32_t bg = __ballot_sync(kFull, gt), be = __ballot_sync(kFull, eq), lt = (1u << lane) - 1u;
-    if (lane == 0) s_scan[w] = (uint32_t)__popc(bg) | ((uint32_t)__popc(be) << 16);
-    __syncthreads();
-    uint32_t g = 0, e = 0, gs = 0, es = 0;
-    for (int x = 0; x < kSelThreads / 32; ++x) {
-      const uint32_t y = s_scan[x];
-      if (x < w) {
-        g += y & 0xFFFFu;
-        e += y >> 16;
-      }
-      gs += y & 0xFFFFu;
-      es += y >> 16;
-    }
-    const uint32_t my_g = g + __popc(bg & lt), my_e = eq_done + e + __popc(be & lt);
-    const uint32_t e_before = min(my_e, left) - min(eq_done, left);  // equal ones kept earlier in this pass
-    if (gt || (eq && my_e < left)) out[done + my_g + e_before] = t;
-    done += gs + min(eq_done + es, left) - min(eq_done, left);
-    eq_done += es;
-    __syncthreads();
+  const int seg = ((m1 - m0 + kSelWarps * 32 - 1) / (kSelWarps * 32)) * 32;  // a warp's share
+  const int t0 = min(m1, m0 + w * seg), t1 = min(m1, t0 + seg);
+  uint32_t gt = 0, eq = 0;
+#pragma unroll 4
+  for (int t = t0 + lane; t < t1; t += 32) {
+    const uint32_t k = key_at(t);
+    gt += k > prefix;
+    eq += k == prefix;
+  }
+  gt = __reduce_add_sync(kFull, gt);
+  eq = __reduce_add_sync(kFull, eq);
+  if (lane == 0) {
+    s_scan[w] = gt;
+    s_eq[w] = eq;
+  }
+  __syncthreads();
+  uint32_t g_done = 0, e_done = 0;  // tokens above and equal before this warp's
+  for (int x = 0; x < w; ++x) {
+    g_done += s_scan[x];
+    e_done += s_eq[x];
+  }
+  const uint32_t lt = (1u << lane) - 1u;
+  for (int b = t0; b < t1; b += 32) {
+    const int t = b + lane;
+    const uint32_t k = t < t1 ? key_at(t) : 0u;
+    const bool above = t < t1 && k > prefix, same = t < t1 && k == prefix;
+    const uint32_t bg = __ballot_sync(kFull, above), be = __ballot_sync(kFull, same);
+    const uint32_t my_e = e_done + __popc(be & lt);
+    if (above || (same && my_e < left)) out[sinks + g_done + __popc(bg & lt) + min(my_e, left)] = t;
+    g_done += __popc(bg);
+    e_done += __popc(be);
   }
 }
 
 // ---- move --------------------------------------------------------------------
-constexpr int kMoveThreads = 256;
-
 struct MoveArgs {
   KCache kc, vc;
   Table bt;
@@ -142,103 +176,209 @@ struct MoveArgs {
   const float* mass_in;
   float* mass_out;
   const int* dst_pages;  // [R][dst_blocks], or null: the request's own pages
-  int row16;             // 16-byte pieces of a row
   int* err;
 };
 
-// One CTA per (request, layer, head). Slots are taken in chunks; a chunk is
-// read whole before any of it is written, and since kept[i] >= i its writes
-// never reach a source of a later chunk: the move is safe in place.
-__global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const MoveArgs a) {
+// The sizes of the row of kept tokens that block x moves.
+struct MoveRow {
+  int h, l, r, off, T, n;
+  bool ok;
+};
+__device__ __forceinline__ MoveRow move_row(const MoveArgs& a, int x, bool report) {
+  MoveRow m;
+  m.h = x % a.kc.H;
+  m.l = (x / a.kc.H) % a.kc.L;
+  m.r = x / (a.kc.H * a.kc.L);
+  m.off = a.bt.offsets[m.r];
+  const int nb = a.bt.offsets[m.r + 1] - m.off;
+  m.T = a.bt.seq_lens[m.r];
+  m.ok = !(m.T < 0 || nb < 0 || nb > a.bt.max_blocks ||
+           nb != (int)(((unsigned)m.T + (unsigned)a.kc.bs - 1u) / (unsigned)a.kc.bs));
+  if (!m.ok && report) flag_error(a.err, kErrBadIndex);
+  m.n = m.ok ? min(m.T, a.keep) : 0;
+  return m;
+}
+// Where slot i of the row comes from and goes to.
+struct Move {
+  int sp, st, dp, dt;
+  bool ok;
+};
+__device__ __forceinline__ Move move_at(const MoveArgs& a, const MoveRow& m, const int* kept, int i) {
+  Move x{0, 0, 0, 0, false};
+  if (i >= m.n) return x;
+  const int t = kept[i], bs = a.kc.bs;
+  if (t < 0 || t >= m.T) {
+    flag_error(a.err, kErrBadIndex);
+    return x;
+  }
+  const int sb = t / bs, db = i / bs;
+  x.st = t - sb * bs;
+  x.dt = i - db * bs;
+  x.sp = a.bt.pages[m.off + sb];
+  x.dp = a.dst_pages ? a.dst_pages[(long long)m.r * a.dst_blocks + db] : a.bt.pages[m.off + db];
+  if (x.sp < 0 || x.sp >= a.kc.num_pages || x.dp < 0 || x.dp >= a.kc.num_pages) {
+    flag_error(a.err, kErrBadIndex);
+    return x;
+  }
+  x.ok = true;
+  return x;
+}
+__device__ __forceinline__ long long row_at(const KCache& c, const MoveRow& m, int page, int tok, int es) {
+  return (m.l * c.sL + page * c.sP + m.h * c.sH + tok * c.sT) * es;
+}
+__device__ __forceinline__ uint4 ld16_once(const char* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+constexpr int kMoveThreads = 256;
+
+// To other pages: a warp moves kRows kept tokens. Each lane finds one token's
+// places; then P lanes copy a token's row of P 16-byte pieces, the rows' loads
+// all in flight before the first store.
+template <int P>
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs a) {
+  constexpr int RI = 32 / P;           // rows of one instruction
+  constexpr int kRows = 8 * RI < 32 ? 8 * RI : 32;
+  constexpr int U = kRows / RI;        // loads in flight, for K and for V each
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, sub = lane / P, c = lane % P * 16;
+  const MoveRow m = move_row(a, blockIdx.x, blockIdx.y == 0 && threadIdx.x == 0);
+  const int i0 = (blockIdx.y * (kMoveThreads / 32) + w) * kRows;
+  if (i0 >= m.n) return;
+  const int es = a.kc.dtype == 1 ? 2 : 4;
+  const Move mv = lane < kRows ? move_at(a, m, a.kept + (long long)blockIdx.x * a.keep, i0 + lane) : Move{0, 0, 0, 0, false};
+  const uint32_t ok = __ballot_sync(kFull, mv.ok);
+  const bool has_v = a.vc.base != nullptr;
+  const long long ks = row_at(a.kc, m, mv.sp, mv.st, es), kd = row_at(a.kc, m, mv.dp, mv.dt, es);
+  const long long vs = row_at(a.vc, m, mv.sp, mv.st, es), vd = row_at(a.vc, m, mv.dp, mv.dt, es);
+  const long long mi = ((long long)m.l * a.kc.num_pages * a.kc.H + m.h) * a.kc.bs;
+  const long long mp = (long long)a.kc.H * a.kc.bs;
+  float wt = 0.f;
+  if (a.mass_in && mv.ok) wt = a.mass_in[mi + mv.sp * mp + mv.st];
+  const char* kb = static_cast<const char*>(a.kc.base);
+  const char* vb = static_cast<const char*>(a.vc.base);
+  uint4 kx[U], vx[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int row = u * RI + sub;
+    const long long s = __shfl_sync(kFull, ks, row), v = __shfl_sync(kFull, vs, row);
+    const bool on = (ok >> row) & 1u;
+    kx[u] = vx[u] = make_uint4(0, 0, 0, 0);
+    if (on) kx[u] = ld16_once(kb + s + c);
+    if (on && has_v) vx[u] = ld16_once(vb + v + c);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int row = u * RI + sub;
+    const long long d = __shfl_sync(kFull, kd, row), v = __shfl_sync(kFull, vd, row);
+    if ((ok >> row) & 1u) {
+      *reinterpret_cast<uint4*>(const_cast<char*>(kb) + d + c) = kx[u];
+      if (has_v) *reinterpret_cast<uint4*>(const_cast<char*>(vb) + v + c) = vx[u];
+    }
+  }
+  if (a.mass_in && mv.ok) a.mass_out[mi + mv.dp * mp + mv.dt] = wt;
+}
+
+// In place: a cluster per (request, layer, head) takes the slots in chunks. A
+// chunk is read whole, by all its CTAs, before any of it is written, and since
+// kept[i] >= i its writes never reach a source of a later chunk.
+__global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const MoveArgs a, int P) {
   constexpr int U = 4;
   const int tid = threadIdx.x;
-  const int H = a.kc.H, bs = a.kc.bs;
-  const int h = blockIdx.x % H, l = (blockIdx.x / H) % a.kc.L, r = blockIdx.x / (H * a.kc.L);
-  const int off = a.bt.offsets[r], nb = a.bt.offsets[r + 1] - off, T = a.bt.seq_lens[r];
-  if (T < 0 || nb < 0 || nb > a.bt.max_blocks || nb != (int)(((long long)T + bs - 1) / bs)) {
-    if (tid == 0) flag_error(a.err, kErrBadIndex);
-    return;
-  }
-  const int n = min(T, a.keep), es = a.kc.dtype == 1 ? 2 : 4;
-  const int* kept = a.kept + (long long)blockIdx.x * a.keep;
-  const int* dst = a.dst_pages ? a.dst_pages + (long long)r * a.dst_blocks : a.bt.pages + off;
-  const int* src = a.bt.pages + off;
-  auto place = [&](int i, int* sp, int* st, int* dp, int* dt) -> bool {
-    const int t = kept[i];
-    if (t < 0 || t >= T) {
-      flag_error(a.err, kErrBadIndex);
-      return false;
-    }
-    *sp = src[t / bs];
-    *st = t % bs;
-    *dp = dst[i / bs];
-    *dt = i % bs;
-    if (*sp < 0 || *sp >= a.kc.num_pages || *dp < 0 || *dp >= a.kc.num_pages) {
-      flag_error(a.err, kErrBadIndex);
-      return false;
-    }
-    return true;
-  };
-  const int per = kMoveThreads / a.row16 * U;  // rows of a chunk
-  const int piece = tid % a.row16, sub = tid / a.row16;
-  for (int c = 0; c < n; c += per) {
+  const int C = (int)cluster_size(), rank = (int)cluster_rank();
+  const int x = blockIdx.x / C;
+  const MoveRow m = move_row(a, x, rank == 0 && tid == 0);
+  const int es = a.kc.dtype == 1 ? 2 : 4;
+  const int* kept = a.kept + (long long)x * a.keep;
+  const int rows = kMoveThreads / P, per = rows * U * C;  // rows of a turn, of a chunk
+  const int c = tid % P * 16, sub = tid / P;
+  const char* kb = static_cast<const char*>(a.kc.base);
+  const char* vb = static_cast<const char*>(a.vc.base);
+  const long long mi = ((long long)m.l * a.kc.num_pages * a.kc.H + m.h) * a.kc.bs;
+  const long long mp = (long long)a.kc.H * a.kc.bs;
+  for (int b = 0; b < m.n; b += per) {
     uint4 kx[U], vx[U];
-    long long kd[U], vd[U];
+    Move mv[U];
+    float wt[U];
 #pragma unroll
-    for (int x = 0; x < U; ++x) {
-      const int i = c + x * (kMoveThreads / a.row16) + sub;
-      int sp, st, dp, dt;
-      kd[x] = -1;
-      if (i < min(n, c + per) && place(i, &sp, &st, &dp, &dt)) {
-        kx[x] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.kc.base) +
-                                                (l * a.kc.sL + sp * a.kc.sP + h * a.kc.sH + st * a.kc.sT) * es +
-                                                piece * 16);
-        kd[x] = (l * a.kc.sL + dp * a.kc.sP + h * a.kc.sH + dt * a.kc.sT) * es + piece * 16;
-        if (a.vc.base) {
-          vx[x] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.vc.base) +
-                                                  (l * a.vc.sL + sp * a.vc.sP + h * a.vc.sH + st * a.vc.sT) * es +
-                                                  piece * 16);
-          vd[x] = (l * a.vc.sL + dp * a.vc.sP + h * a.vc.sH + dt * a.vc.sT) * es + piece * 16;
-        }
+    for (int u = 0; u < U; ++u) {
+      mv[u] = move_at(a, m, kept, b + (u * C + rank) * rows + sub);
+      kx[u] = vx[u] = make_uint4(0, 0, 0, 0);
+      wt[u] = 0.f;
+      if (mv[u].ok) {
+        kx[u] = ld16_once(kb + row_at(a.kc, m, mv[u].sp, mv[u].st, es) + c);
+        if (vb) vx[u] = ld16_once(vb + row_at(a.vc, m, mv[u].sp, mv[u].st, es) + c);
+        if (a.mass_in && c == 0) wt[u] = a.mass_in[mi + mv[u].sp * mp + mv[u].st];
       }
     }
-    __syncthreads();
+    cluster_arrive_release();  // every lane's loads have landed: their values are used below
+    cluster_wait_acquire();
 #pragma unroll
-    for (int x = 0; x < U; ++x)
-      if (kd[x] >= 0) {
-        *reinterpret_cast<uint4*>(const_cast<char*>(static_cast<const char*>(a.kc.base)) + kd[x]) = kx[x];
-        if (a.vc.base)
-          *reinterpret_cast<uint4*>(const_cast<char*>(static_cast<const char*>(a.vc.base)) + vd[x]) = vx[x];
+    for (int u = 0; u < U; ++u)
+      if (mv[u].ok) {
+        *reinterpret_cast<uint4*>(const_cast<char*>(kb) + row_at(a.kc, m, mv[u].dp, mv[u].dt, es) + c) = kx[u];
+        if (vb) *reinterpret_cast<uint4*>(const_cast<char*>(vb) + row_at(a.vc, m, mv[u].dp, mv[u].dt, es) + c) = vx[u];
+        if (a.mass_in && c == 0) a.mass_out[mi + mv[u].dp * mp + mv[u].dt] = wt[u];
       }
   }
-  if (!a.mass_in) return;
-  const long long mrow = ((long long)l * a.kc.num_pages * H + h) * bs;
-  for (int c = 0; c < n; c += kMoveThreads) {
-    const int i = c + tid;
-    int sp, st, dp, dt;
-    const bool ok = i < n && place(i, &sp, &st, &dp, &dt);
-    const float m = ok ? a.mass_in[mrow + (long long)sp * H * bs + st] : 0.f;
-    __syncthreads();
-    if (ok) a.mass_out[mrow + (long long)dp * H * bs + dt] = m;
-  }
+}
+
+template <int P>
+cudaError_t move_t(const MoveArgs& a, int items, cudaStream_t s) {
+  constexpr int kRows = 8 * (32 / P) < 32 ? 8 * (32 / P) : 32;
+  const int per = kMoveThreads / 32 * kRows;
+  evict_move_kernel<P><<<dim3((unsigned)items, (unsigned)((a.keep + per - 1) / per)), kMoveThreads, 0, s>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_evict_select(const KCache& kc, const Table& bt, const float* mass, int sinks, int recent, int keep,
                                 int* kept, int* new_lens, int* err, cudaStream_t s) {
-  evict_select_kernel<<<bt.R * kc.L * kc.H, kSelThreads, 0, s>>>(kc, bt, mass, sinks, recent, keep, kept, new_lens,
-                                                                 err);
+  const int grid = bt.R * kc.L * kc.H;
+  const long long most = (long long)bt.max_blocks * kc.bs;  // tokens of a request
+  if (most <= kMaxCached) {
+    const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kMaxCached * 4);
+    if (e != cudaSuccess) return e;
+    evict_select_kernel<true><<<grid, kSelThreads, (size_t)most * 4, s>>>(kc, bt, mass, sinks, recent, keep, kept,
+                                                                         new_lens, err);
+  } else {
+    evict_select_kernel<false><<<grid, kSelThreads, 0, s>>>(kc, bt, mass, sinks, recent, keep, kept, new_lens, err);
+  }
   return cudaGetLastError();
 }
 
 cudaError_t launch_evict_compact(const KCache& kc, const KCache& vc, const Table& bt, const int* kept, int keep,
                                  const float* mass_in, float* mass_out, const int* dst_pages, int* err,
                                  cudaStream_t s) {
-  const MoveArgs a{kc, vc, bt, kept, keep, (keep + kc.bs - 1) / kc.bs, mass_in, mass_out, dst_pages,
-                   kc.D * (kc.dtype == 1 ? 2 : 4) / 16, err};
-  evict_compact_kernel<<<bt.R * kc.L * kc.H, kMoveThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  const MoveArgs a{kc, vc, bt, kept, keep, (keep + kc.bs - 1) / kc.bs, mass_in, mass_out, dst_pages, err};
+  const int items = bt.R * kc.L * kc.H, P = kc.D * (kc.dtype == 1 ? 2 : 4) / 16;  // 16-byte pieces of a row
+  if (dst_pages) switch (P) {
+      case 4: return move_t<4>(a, items, s);
+      case 8: return move_t<8>(a, items, s);
+      case 16: return move_t<16>(a, items, s);
+      case 32: return move_t<32>(a, items, s);
+      default: return cudaErrorNotSupported;
+    }
+  // CTAs of a cluster: enough to fill the SMs when there are few rows of tokens
+  int C = 1;
+  while (C < 8 && (long long)items * C < 4ll * sm_count()) C *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items * C));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)C;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_compact_kernel, a, P);
 }
 
 }  // namespace kk
