@@ -4,6 +4,8 @@
 //    to the lower index, NaN below everything);
 //  * evict_compact_kernel: their Keys, Values and weights moved to slots
 //    0 .. keep-1 of the request's pages, or of new ones.
+#include <cmath>
+
 #include "kk_device.cuh"
 
 namespace kk {
@@ -28,7 +30,7 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
 // share above it and equal to it, and, knowing the counts before its own, writes
 // its kept tokens in order.
 template <bool kCached>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(KCache kc, Table bt, const float* mass, int sinks,
+__global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(KCache kc, Table bt, const float* mass, int sinks,
                                                                    int recent, int keep, int* kept, int* new_lens,
                                                                    int* err) {
   extern __shared__ uint32_t s_key[];  // cached: the middle's keys
@@ -68,17 +70,33 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(KCache kc, Ta
   };
   if (kCached) {
     // A thread keeps its place in the block and steps whole blocks: one division
-    // in all, and four blocks' loads in flight.
+    // in all. Eight pages are read, then eight weights, so that the two dependent
+    // loads cost two latencies a round.
+    constexpr int U = 8;
     const int per = bs < kSelThreads ? kSelThreads / bs : 1;  // blocks a turn
     const int b0 = bs < kSelThreads ? tid / bs : 0, o0 = bs < kSelThreads ? tid - b0 * bs : tid;
+    bool bad = false;
     if (b0 < per)
-      for (int o = o0; o < bs; o += kSelThreads) {
-#pragma unroll 4
-        for (int b = m0 / bs + b0; b < nb; b += per) {
-          const int t = b * bs + o;
-          if (t >= m0 && t < m1) s_key[t - m0] = weight_of(b, o);
+      for (int o = o0; o < bs; o += kSelThreads)
+        for (int b = m0 / bs + b0; b < nb; b += per * U) {
+          int page[U];
+          float wt[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) page[u] = b + u * per < nb ? bt.pages[off + b + u * per] : 0;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int t = (b + u * per) * bs + o;
+            const bool in = b + u * per < nb && t >= m0 && t < m1, good = page[u] >= 0 && page[u] < kc.num_pages;
+            bad |= in && !good;
+            wt[u] = in && good ? mbase[page[u] * page_stride + o] : NAN;  // a bad page ranks last
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int t = (b + u * per) * bs + o;
+            if (b + u * per < nb && t >= m0 && t < m1) s_key[t - m0] = mass_key(wt[u]);
+          }
         }
-      }
+    if (bad) flag_error(err, kErrBadIndex);
     __syncthreads();
   }
   auto key_at = [&](int t) -> uint32_t {
