@@ -3,9 +3,9 @@
 // over the cached tokens (or those of the selected blocks, "Key-Key Semantic
 // Affinity" page §5.2 step 4: only they are loaded) and the drafted nodes a
 // node may see. One pass over the tokens with a running maximum and sum per
-// row; the work division is kk_attn.cuh's.
-//  * attn_simt_kernel: float32 caches, on the CUDA cores;
-//  * attn_combine_kernel: adds up the parts of the items that were cut.
+// row; the work division is kk_attn.cuh's. The main kernels are in kk_attn_f32.cu
+// (float32 caches), kk_attn_mma.cu (bf16, few rows) and kk_attn_tc.cu (bf16, many
+// rows); this file chooses one and adds up the parts of the items that were cut.
 #include <algorithm>
 
 #include "kk_attn.cuh"
@@ -13,188 +13,6 @@
 
 namespace kk {
 namespace {
-
-constexpr int kSimtThreads = 128;
-constexpr int kSimtM = 8;     // query rows per item
-constexpr int kSimtTK = 128;  // tokens per unit: 32 per warp
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const AttnArgs a) {
-  constexpr int EPV = Vec16<T>::kElems;
-  constexpr int ES = elem_bytes<T>();
-  constexpr int M = kSimtM, DL = D / 32;
-  __shared__ __align__(16) float s_q[M][D];
-  __shared__ __align__(16) float s_p[4][32][M];
-  __shared__ __align__(16) float s_o[4][M][D];
-  __shared__ float s_m[4][M], s_l[4][M];
-  __shared__ long long s_place[kSimtThreads / 32 + 4];
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-  pdl_launch_dependents();
-  const AttnPlace pl = find_place<kSimtThreads>(a, blockIdx.x, M, kSimtTK, s_place, tid);
-  int r = pl.r;
-  long long base = pl.base;
-  for (long long u = pl.u0; u < pl.u1;) {
-    const AttnReq rq = load_req(a, r, M, kSimtTK, false);
-    const long long units = req_units(a, rq);
-    if (u >= base + units) {
-      base += units;
-      ++r;
-      continue;
-    }
-    ItemAt it = item_at(rq, u - base);
-    it.t1 = (int)min((long long)rq.tiles, it.t0 + (pl.u1 - u));
-    const int t0 = it.t0, t1 = it.t1, h = it.h, row0 = it.mt * M;
-    const int rows = min(M, rq.n * a.G - row0);
-    for (int i = tid; i < M * D; i += kSimtThreads) {
-      const int m = i / D, d = i - m * D, row = row0 + m;
-      float x = 0.f;
-      if (m < rows) {
-        const long long at = (rq.node0 + row / a.G) * a.q_sn + (long long)(h * a.G + row % a.G) * a.q_sh + d;
-        x = ES == 4 ? static_cast<const float*>(a.q)[at]
-                    : __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.q)[at] << 16);
-      }
-      s_q[m][d] = x;
-    }
-    __syncthreads();
-    float m_run[M], l_run[M], o[M][DL];
-#pragma unroll
-    for (int i = 0; i < M; ++i) {
-      m_run[i] = -INFINITY;
-      l_run[i] = 0.f;
-#pragma unroll
-      for (int e = 0; e < DL; ++e) o[i][e] = 0.f;
-    }
-    for (int t = t0; t < t1; ++t) {
-      const bool draft = t >= rq.tiles_c;
-      const char *kp = nullptr, *vp = nullptr;
-      bool ok;
-      uint32_t vis = (1u << M) - 1u;  // rows that may see this lane's token
-      if (!draft) {
-        TokenAt at;
-        ok = token_at(a, r, rq, t * kSimtTK + tid, true, &at);
-        kp = static_cast<const char*>(a.kc.base) +
-             (a.layer * a.kc.sL + at.page * a.kc.sP + h * a.kc.sH + at.tok * a.kc.sT) * ES;
-        vp = static_cast<const char*>(a.vc.base) +
-             (a.layer * a.vc.sL + at.page * a.vc.sP + h * a.vc.sH + at.tok * a.vc.sT) * ES;
-      } else {
-        const int j = (t - rq.tiles_c) * kSimtTK + tid;
-        ok = a.dk && j < rq.n;
-        if (ok) {
-          kp = static_cast<const char*>(a.dk) + ((rq.node0 + j) * a.dk_sn + h * a.dk_sh) * ES;
-          vp = static_cast<const char*>(a.dv) + ((rq.node0 + j) * a.dv_sn + h * a.dv_sh) * ES;
-          vis = 0;
-          for (int i = 0; i < rows; ++i) vis |= sees(a, rq, (row0 + i) / a.G, j) ? 1u << i : 0u;
-        }
-      }
-      float s[M];
-#pragma unroll
-      for (int i = 0; i < M; ++i) s[i] = 0.f;
-      if (ok) {
-#pragma unroll 4
-        for (int c = 0; c < D / EPV; ++c) {
-          float k[EPV];
-          Vec16<T>::unpack(*reinterpret_cast<const uint4*>(kp + c * 16), k);
-#pragma unroll
-          for (int i = 0; i < M; ++i)
-#pragma unroll
-            for (int e = 0; e < EPV; e += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(&s_q[i][c * EPV + e]);
-              s[i] += k[e] * x.x;
-              s[i] += k[e + 1] * x.y;
-              s[i] += k[e + 2] * x.z;
-              s[i] += k[e + 3] * x.w;
-            }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < M; ++i) {
-        // selected, not added: what a hidden place holds (NaN, infinity) never enters
-        s[i] = (ok && ((vis >> i) & 1u)) ? s[i] * a.scale_log2 : -INFINITY;
-        float mx = s[i];
-#pragma unroll
-        for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
-        const float m_new = fmaxf(m_run[i], mx), ref = m_new == -INFINITY ? 0.f : m_new;
-        const float p = ex2(s[i] - ref), al = ex2(m_run[i] - ref);
-        m_run[i] = m_new;
-        l_run[i] = l_run[i] * al + p;  // this lane's share of the sum
-#pragma unroll
-        for (int e = 0; e < DL; ++e) o[i][e] *= al;
-        s_p[w][lane][i] = p;
-      }
-      __syncwarp();
-      const uint32_t live = __ballot_sync(kFull, ok);
-      for (uint32_t left = live; left; left &= left - 1) {
-        const int k = __ffs(left) - 1;
-        const char* v = reinterpret_cast<const char*>(__shfl_sync(kFull, (unsigned long long)vp, k));
-        float x[DL];
-#pragma unroll
-        for (int e = 0; e < DL; ++e)
-          x[e] = ES == 4 ? reinterpret_cast<const float*>(v)[lane * DL + e]
-                         : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(v)[lane * DL + e] << 16);
-        float pr[M];
-#pragma unroll
-        for (int i = 0; i < M; i += 4)
-          *reinterpret_cast<float4*>(&pr[i]) = *reinterpret_cast<const float4*>(&s_p[w][k][i]);
-        if (!draft) {
-#pragma unroll
-          for (int i = 0; i < M; ++i)
-#pragma unroll
-            for (int e = 0; e < DL; ++e) o[i][e] += pr[i] * x[e];
-        } else {  // a node hidden from some rows may hold anything
-          const uint32_t vk = __shfl_sync(kFull, vis, k);
-#pragma unroll
-          for (int i = 0; i < M; ++i)
-            if ((vk >> i) & 1u)
-#pragma unroll
-              for (int e = 0; e < DL; ++e) o[i][e] += pr[i] * x[e];
-        }
-      }
-      __syncwarp();
-    }
-    // the four warps' shares of the item
-#pragma unroll
-    for (int i = 0; i < M; ++i) {
-      float l = l_run[i];
-#pragma unroll
-      for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(kFull, l, x);
-      if (lane == 0) {
-        s_m[w][i] = m_run[i];
-        s_l[w][i] = l;
-      }
-#pragma unroll
-      for (int e = 0; e < DL; ++e) s_o[w][i][lane * DL + e] = o[i][e];
-    }
-    __syncthreads();
-    const bool whole = t0 == 0 && t1 == rq.tiles;
-    float* part = partial_slot(a, blockIdx.x, u == pl.u0 ? 0 : 1, M, D);
-    for (int i = tid; i < rows * D; i += kSimtThreads) {
-      const int m = i / D, d = i - m * D;
-      float mm = s_m[0][m];
-      for (int x = 1; x < 4; ++x) mm = fmaxf(mm, s_m[x][m]);
-      const float ref = mm == -INFINITY ? 0.f : mm;
-      float l = 0.f, acc = 0.f;
-      for (int x = 0; x < 4; ++x) {
-        const float al = ex2(s_m[x][m] - ref);
-        l += s_l[x][m] * al;
-        acc += s_o[x][m][d] * al;
-      }
-      if (whole) {
-        const int row = row0 + m;
-        const long long at = (long long)(rq.node0 + row / a.G) * a.Hq + h * a.G + row % a.G;
-        store_elem<T>(a.out, at * D + d, acc * row_inv(l));
-        if (d == 0 && a.lse) a.lse[at] = row_lse(mm, l);
-      } else {
-        part[i] = acc;
-        if (d == 0) {
-          part[M * D + m] = mm;
-          part[M * D + M + m] = l;
-        }
-      }
-    }
-    __syncthreads();
-    u += t1 - t0;
-  }
-}
 
 // The CTAs [c0, c0 + n) whose partial results make up an item (n = 0: nothing
 // to add up, or no rows from `row` of the tile on), and c0's slot: worked out
@@ -440,19 +258,13 @@ cudaError_t combine_t(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
                           kCombineThreads, s, a, M, pl.TK, mt_max, wpr);
 }
 
-template <int D>
-cudaError_t simt_t(const AttnArgs& a, cudaStream_t s) {
-  attn_simt_kernel<float, D><<<a.grid, kSimtThreads, 0, s>>>(a);
-  return cudaGetLastError();
-}
-
 // Rows per KV head from which the tensor-memory kernel is taken (where the
 // caches' layouts suit it).
 constexpr int kTcRows = 33;
 
 AttnPlan plan(const KCache& kc, const KCache& vc, int max_nodes, int G) {
   const int rows = max_nodes * G;
-  if (kc.dtype != 1) return AttnPlan{AttnPlan::kSimt, kSimtM, kSimtTK, sm_count() * 4};
+  if (kc.dtype != 1) return attn_f32_plan(kc, rows);
   if (rows >= kTcRows && attn_tc_suits(kc) && attn_tc_suits(vc)) return attn_tc_plan();
   return attn_mma_plan(kc, rows);
 }
@@ -492,11 +304,7 @@ cudaError_t launch_tree_attn(AttnArgs a, cudaStream_t s) {
   } else if (pl.kind == AttnPlan::kMma) {
     e = launch_attn_mma(a, pl, s);
   } else {
-    switch (a.kc.D) {
-      case 32: e = simt_t<32>(a, s); break;
-      case 64: e = simt_t<64>(a, s); break;
-      case 128: e = simt_t<128>(a, s); break;
-    }
+    e = launch_attn_f32(a, pl, s);
   }
   if (e != cudaSuccess) return e;
   if (pl.kind == AttnPlan::kTc) return a.kc.D == 64 ? combine_tc<64>(a, pl, s) : combine_tc<128>(a, pl, s);

@@ -55,13 +55,16 @@ struct AttnArgs {
 
 // How a call runs: which kernel, its row and token tiles, its grid.
 struct AttnPlan {
-  enum Kind { kSimt, kMma, kTc };
+  enum Kind { kF32, kMma, kTc };
   Kind kind;
   int M, TK, grid;
 };
 // kk_attn_mma.cu (bf16; rows: query rows of a request and KV head, at most)
 AttnPlan attn_mma_plan(const KCache& kc, int rows);
 cudaError_t launch_attn_mma(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s);
+// kk_attn_f32.cu (float32)
+AttnPlan attn_f32_plan(const KCache& kc, int rows);
+cudaError_t launch_attn_f32(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s);
 // kk_attn_tc.cu (bf16, D 64 or 128, both caches of layouts it suits)
 bool attn_tc_suits(const KCache& kc);
 AttnPlan attn_tc_plan();

@@ -8,16 +8,14 @@
 // matrix instructions, and keeps its own running maximum, sum and accumulator:
 // no barrier between warps until the item ends, so loads never wait for a
 // neighbour. Two CTAs of three stages hold 128 KB in flight per SM at D = 128.
-#include "kk_attn.cuh"
+#include "kk_attn_ring.cuh"
 #include "kk_pdl.cuh"
 
 namespace kk {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kTok = 16;  // tokens of a warp's share of a tile
-constexpr int kTK = kWarps * kTok;
+constexpr int kWarps = kRingWarps, kThreads = kWarps * 32;
+constexpr int kTok = kRingTok, kTK = kRingTK;
 constexpr int kStages = 3;
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -44,36 +42,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 template <int D>
 __device__ __forceinline__ uint32_t swz(int row, int c) {
   return D >= 64 ? row * D * 2 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
-}
-
-// A lane's token of the tile the warp loads next.
-struct Tok {
-  const char *k, *v;
-  bool ok;
-};
-
-template <int D>
-__device__ __forceinline__ Tok find_token(const AttnArgs& a, int r, const AttnReq& rq, int h, int t, int w, int lane) {
-  Tok x;
-  const int l = lane & 15;
-  if (t < rq.tiles_c) {
-    TokenAt at;
-    x.ok = token_at(a, r, rq, t * kTK + w * kTok + l, true, &at);
-    x.k = static_cast<const char*>(a.kc.base) +
-          (a.layer * a.kc.sL + at.page * a.kc.sP + h * a.kc.sH + at.tok * a.kc.sT) * 2;
-    x.v = static_cast<const char*>(a.vc.base) +
-          (a.layer * a.vc.sL + at.page * a.vc.sP + h * a.vc.sH + at.tok * a.vc.sT) * 2;
-  } else {
-    const int j = (t - rq.tiles_c) * kTK + w * kTok + l;
-    x.ok = a.dk && t < rq.tiles && j < rq.n;
-    x.k = static_cast<const char*>(x.ok ? a.dk : a.q);
-    x.v = x.k;
-    if (x.ok) {
-      x.k += ((long long)(rq.node0 + j) * a.dk_sn + h * a.dk_sh) * 2;
-      x.v = static_cast<const char*>(a.dv) + ((long long)(rq.node0 + j) * a.dv_sn + h * a.dv_sh) * 2;
-    }
-  }
-  return x;
 }
 
 template <int D>
@@ -126,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
     const int t0 = it.t0, t1 = it.t1, h = it.h, row0 = it.mt * M;
     const int rows = min(M, rq.n * a.G - row0);
     // the first tiles' copies go out before the queries are read
-    Tok nx = find_token<D>(a, r, rq, h, t0, w, lane);
+    Tok nx = find_token<2>(a, r, rq, h, t0, w, lane);
 #pragma unroll
     for (int st = 0; st < kStages - 1; ++st) {
       const bool on = t0 + st < t1;
@@ -134,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
       cp_commit();
       const uint32_t ok = __ballot_sync(kFull, on && nx.ok) & 0xFFFFu;
       if (lane == 0) s_ok[w][st] = ok;
-      nx = find_token<D>(a, r, rq, h, min(t0 + st + 1, t1 - 1), w, lane);
+      nx = find_token<2>(a, r, rq, h, min(t0 + st + 1, t1 - 1), w, lane);
     }
     for (int i = tid; i < M * (D / 8); i += kThreads) {
       const int m = i / (D / 8), c = i - m * (D / 8), row = row0 + m;
@@ -167,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
         cp_commit();
         const uint32_t ok = __ballot_sync(kFull, on && nx.ok) & 0xFFFFu;
         if (lane == 0) s_ok[w][fs] = ok;
-        nx = find_token<D>(a, r, rq, h, min(t + kStages, t1 - 1), w, lane);
+        nx = find_token<2>(a, r, rq, h, min(t + kStages, t1 - 1), w, lane);
       }
       const uint32_t kst = ring + st * kStage, vst = kst + kTok * D * 2;
       const uint32_t live = s_ok[w][st];

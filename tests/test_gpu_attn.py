@@ -170,10 +170,10 @@ def test_hidden_drafts_may_hold_anything(cuda, dtype, n, bad):
         assert torch.isnan(out[3].float()).all()
 
 
-@pytest.mark.parametrize("counts", [[1, 1], [11, 40]])
-def test_infinite_keys(cuda, counts):
+@pytest.mark.parametrize("dtype,counts", [("bf16", [1, 1]), ("bf16", [11, 40]), ("f32", [1, 1]), ("f32", [11, 40])])
+def test_infinite_keys(cuda, dtype, counts):
     """A token whose score is -inf takes no part; rows that all tokens leave at -inf are empty."""
-    pc = Paged([40, 20], H=1, D=64, bs=16, seed=2)
+    pc = Paged([40, 20], H=1, D=64, bs=16, dtype=dtype, seed=2)
     pc.k[:] = torch.nan_to_num(pc.k.float(), nan=0.0).abs().to(pc.tdt)
     for t in (3, 17, 39):
         pc.k[0, int(pc.pages[t // 16]), 0, t % 16, 5] = -math.inf
@@ -189,7 +189,7 @@ def test_infinite_keys(cuda, counts):
                     _gpu(q), 0.1, out, lse, workspace=_workspace(kk, pc, max(counts), 4))
     a = no[1]
     keep = [t for t in range(40) if t not in (3, 17, 39)]
-    small = Paged([len(keep)], H=1, D=64, bs=16, seed=2)
+    small = Paged([len(keep)], H=1, D=64, bs=16, dtype=dtype, seed=2)
     for i, t in enumerate(keep):
         for x, y in ((small.k, pc.k), (small.v, pc.v)):
             x[0, int(small.pages[i // 16]), 0, i % 16] = y[0, int(pc.pages[t // 16]), 0, t % 16]
