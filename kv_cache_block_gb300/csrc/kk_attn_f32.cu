@@ -6,7 +6,9 @@
 // rows shared it and a tile waited for uncoalesced rows.
 //
 // The structure is kk_attn_mma.cu's (a ring of 16-byte asynchronous copies per
-// warp, no barrier between warps until an item ends), with m16n8k8 instructions.
+// warp, no barrier between warps until an item ends), with m16n8k8 instructions
+// and 8 tokens a warp: four warps of 16 tokens left each scheduler one warp and
+// its chain of dependent products.
 // Which of eight contracted positions holds which dim (or token) does not matter
 // as long as both operands agree: it is chosen so that a lane reads 16 bytes of
 // a row at once, and so that the scores' registers are the next product's.
@@ -16,8 +18,8 @@
 namespace kk {
 namespace {
 
-constexpr int kWarps = kRingWarps, kThreads = kWarps * 32;
-constexpr int kTok = kRingTok, kTK = kRingTK;
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kTK = kRingTK, kTok = kTK / kWarps;  // tokens of a warp's share: one 8-column product
 constexpr int kStages = 3;
 
 // x's leading 11 bits as tf32, rounded to nearest.
@@ -41,14 +43,6 @@ __device__ __forceinline__ void mma1688(float (&d)[4], const uint32_t (&a)[4], u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// d += a b with both operands in halves.
-__device__ __forceinline__ void mma3(float (&d)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], const Halves& b0,
-                                     const Halves& b1) {
-  mma1688(d, al, b0.hi, b1.hi);
-  mma1688(d, ah, b0.lo, b1.lo);
-  mma1688(d, ah, b0.hi, b1.hi);
-}
-
 // Byte offset of 16-byte piece c of row `row`: pieces are exchanged so that the
 // rows 2q, 2q+1 (scores) and the rows of one parity (weights) that eight lanes
 // read together fall into different banks.
@@ -110,15 +104,15 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
     const int t0 = it.t0, t1 = it.t1, h = it.h, row0 = it.mt * M;
     const int rows = min(M, rq.n * a.G - row0);
     // the first tiles' copies go out before the queries are read
-    Tok nx = find_token<4>(a, r, rq, h, t0, w, lane);
+    Tok nx = find_token<4, kTok>(a, r, rq, h, t0, w, lane);
 #pragma unroll
     for (int st = 0; st < kStages - 1; ++st) {
       const bool on = t0 + st < t1;
       if (on) load_tokens<D>(smem_u32(ring) + st * kStage, nx, lane);
       cp_commit();
-      const uint32_t ok = __ballot_sync(kFull, on && nx.ok) & 0xFFFFu;
+      const uint32_t ok = __ballot_sync(kFull, on && nx.ok) & 0xFFu;
       if (lane == 0) s_ok[w][st] = ok;
-      nx = find_token<4>(a, r, rq, h, min(t0 + st + 1, t1 - 1), w, lane);
+      nx = find_token<4, kTok>(a, r, rq, h, min(t0 + st + 1, t1 - 1), w, lane);
     }
     for (int i = tid; i < M * (D / 4); i += kThreads) {
       const int m = i / (D / 4), c = i - m * (D / 4), row = row0 + m;
@@ -152,9 +146,9 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
         const bool on = t + kStages - 1 < t1;
         if (on) load_tokens<D>(smem_u32(ring) + fs * kStage, nx, lane);
         cp_commit();
-        const uint32_t ok = __ballot_sync(kFull, on && nx.ok) & 0xFFFFu;
+        const uint32_t ok = __ballot_sync(kFull, on && nx.ok) & 0xFFu;
         if (lane == 0) s_ok[w][fs] = ok;
-        nx = find_token<4>(a, r, rq, h, min(t + kStages, t1 - 1), w, lane);
+        nx = find_token<4, kTok>(a, r, rq, h, min(t + kStages, t1 - 1), w, lane);
       }
       unsigned char* kst = ring + st * kStage;
       unsigned char* vst = kst + kTok * D * 4;
@@ -176,23 +170,20 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
         }
         odd = __any_sync(kFull, odd);
       }
-      // scores of 16 tokens
-      float s[MR][2][4];
+      // scores of 8 tokens; the three kinds of product in sums of their own while
+      // registers allow, three chains instead of one
+      constexpr int NCH = MR <= 2 ? 3 : 1;
+      float s[MR][4], c3[NCH][MR][4];
 #pragma unroll
-      for (int mr = 0; mr < MR; ++mr)
+      for (int x = 0; x < NCH; ++x)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[mr][0][e] = s[mr][1][e] = 0.f;
+        for (int mr = 0; mr < MR; ++mr)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c3[x][mr][e] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        Halves b[2][4];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const float4 x = f4(kst + swz<D>(nt * 8 + g, ks * 4 + q4));
-          b[nt][0] = split(x.x);
-          b[nt][1] = split(x.y);
-          b[nt][2] = split(x.z);
-          b[nt][3] = split(x.w);
-        }
+        const float4 kx = f4(kst + swz<D>(g, ks * 4 + q4));
+        const Halves b[4] = {split(kx.x), split(kx.y), split(kx.z), split(kx.w)};
 #pragma unroll
         for (int mr = 0; mr < MR; ++mr) {
           const float4 h0 = f4(qh + swz<D>(mr * 16 + g, ks * 4 + q4)), h1 = f4(qh + swz<D>(mr * 16 + 8 + g, ks * 4 + q4));
@@ -202,31 +193,38 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
           const uint32_t al[2][4] = {{tf32_of(l0.x), tf32_of(l1.x), tf32_of(l0.y), tf32_of(l1.y)},
                                      {tf32_of(l0.z), tf32_of(l1.z), tf32_of(l0.w), tf32_of(l1.w)}};
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) mma3(s[mr][nt], ah[x], al[x], b[nt][2 * x], b[nt][2 * x + 1]);
+          for (int x = 0; x < 2; ++x) {
+            mma1688(c3[0][mr], al[x], b[2 * x].hi, b[2 * x + 1].hi);
+            mma1688(c3[NCH / 2][mr], ah[x], b[2 * x].lo, b[2 * x + 1].lo);
+            mma1688(c3[NCH - 1][mr], ah[x], b[2 * x].hi, b[2 * x + 1].hi);
+          }
         }
       }
+#pragma unroll
+      for (int mr = 0; mr < MR; ++mr)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          s[mr][e] = NCH == 1 ? c3[0][mr][e] : (c3[0][mr][e] + c3[NCH / 2][mr][e]) + c3[NCH - 1][mr][e];
       // An infinite Key has no low half (infinity less itself): its scores, NaN
       // here, are formed again from the whole values.
       bool nan = false;
 #pragma unroll
       for (int mr = 0; mr < MR; ++mr)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) nan |= s[mr][0][e] != s[mr][0][e] || s[mr][1][e] != s[mr][1][e];
+        for (int e = 0; e < 4; ++e) nan |= s[mr][e] != s[mr][e];
       if (__any_sync(kFull, nan)) {
 #pragma unroll
         for (int mr = 0; mr < MR; ++mr)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int m = mr * 16 + (e & 2 ? 8 : 0) + g, k = (e >> 2) * 8 + q4 * 2 + (e & 1);
+          for (int e = 0; e < 4; ++e) {
+            const int m = mr * 16 + (e & 2 ? 8 : 0) + g, k = q4 * 2 + (e & 1);
             float sum = 0.f;
 #pragma unroll 1
             for (int c = 0; c < D / 4; ++c) {
               const float4 y = f4(kst + swz<D>(k, c)), x = f4(qh + swz<D>(m, c)), z = f4(ql + swz<D>(m, c));
               sum += (x.x + z.x) * y.x + (x.y + z.y) * y.y + (x.z + z.z) * y.z + (x.w + z.w) * y.w;
             }
-            s[mr][e >> 2][e & 3] = sum;
+            s[mr][e] = sum;
           }
       }
       bool rise = false;
@@ -237,35 +235,27 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
         for (int hf = 0; hf < 2; ++hf) {
           float mx = m_run[mr][hf];
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int k = nt * 8 + q4 * 2 + e;
-              float& x = s[mr][nt][hf * 2 + e];
-              bool see = (live >> k) & 1;
-              if (draft && see) {
-                const int row = row0 + mr * 16 + hf * 8 + g;
-                see = row < rq.n * a.G && sees(a, rq, row / a.G, j0 + k);
-              }
-              x = see ? x * a.scale_log2 : -INFINITY;  // selected, whatever a hidden place holds
-              mx = fmaxf(mx, x);
+          for (int e = 0; e < 2; ++e) {
+            const int k = q4 * 2 + e;
+            float& x = s[mr][hf * 2 + e];
+            bool see = (live >> k) & 1;
+            if (draft && see) {
+              const int row = row0 + mr * 16 + hf * 8 + g;
+              see = row < rq.n * a.G && sees(a, rq, row / a.G, j0 + k);
             }
+            x = see ? x * a.scale_log2 : -INFINITY;  // selected, whatever a hidden place holds
+            mx = fmaxf(mx, x);
+          }
           mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
           const float ref = mx == -INFINITY ? 0.f : mx;
           al[mr][hf] = ex2(m_run[mr][hf] - ref);
           rise |= mx > m_run[mr][hf];
           m_run[mr][hf] = mx;
-          float sum = 0.f;
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float& x = s[mr][nt][hf * 2 + e];
-              x = ex2(x - ref);
-              sum += x;
-            }
-          l_run[mr][hf] = l_run[mr][hf] * al[mr][hf] + sum;
+          const float p0 = ex2(s[mr][hf * 2] - ref), p1 = ex2(s[mr][hf * 2 + 1] - ref);
+          s[mr][hf * 2] = p0;
+          s[mr][hf * 2 + 1] = p1;
+          l_run[mr][hf] = l_run[mr][hf] * al[mr][hf] + (p0 + p1);
         }
       if (__any_sync(kFull, rise)) {  // a maximum rarely rises after the first tiles
 #pragma unroll
@@ -279,28 +269,26 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
           }
       }
       // Position q4 of the contraction is token 2 q4, position q4 + 4 token 2 q4 + 1
+      uint32_t ph[MR][4], pw[MR][4];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        uint32_t ph[MR][4], pw[MR][4];
+      for (int mr = 0; mr < MR; ++mr) {
+        const Halves x0 = split(s[mr][0]), x1 = split(s[mr][2]), x2 = split(s[mr][1]), x3 = split(s[mr][3]);
+        ph[mr][0] = x0.hi, ph[mr][1] = x1.hi, ph[mr][2] = x2.hi, ph[mr][3] = x3.hi;
+        pw[mr][0] = x0.lo, pw[mr][1] = x1.lo, pw[mr][2] = x2.lo, pw[mr][3] = x3.lo;
+      }
 #pragma unroll
-        for (int mr = 0; mr < MR; ++mr) {
-          const Halves x0 = split(s[mr][nt][0]), x1 = split(s[mr][nt][2]), x2 = split(s[mr][nt][1]),
-                       x3 = split(s[mr][nt][3]);
-          ph[mr][0] = x0.hi, ph[mr][1] = x1.hi, ph[mr][2] = x2.hi, ph[mr][3] = x3.hi;
-          pw[mr][0] = x0.lo, pw[mr][1] = x1.lo, pw[mr][2] = x2.lo, pw[mr][3] = x3.lo;
-        }
+      for (int blk = 0; blk < D / 32; ++blk) {  // column n of product j is dim blk * 32 + 4 n + j
+        const float4 v0 = f4(vst + swz<D>(q4 * 2, blk * 8 + g)), v1 = f4(vst + swz<D>(q4 * 2 + 1, blk * 8 + g));
+        const Halves b0[4] = {split(v0.x), split(v0.y), split(v0.z), split(v0.w)};
+        const Halves b1[4] = {split(v1.x), split(v1.y), split(v1.z), split(v1.w)};
 #pragma unroll
-        for (int blk = 0; blk < D / 32; ++blk) {  // column n of product j is dim blk * 32 + 4 n + j
-          const float4 v0 = f4(vst + swz<D>(nt * 8 + q4 * 2, blk * 8 + g));
-          const float4 v1 = f4(vst + swz<D>(nt * 8 + q4 * 2 + 1, blk * 8 + g));
-          const float y0[4] = {v0.x, v0.y, v0.z, v0.w}, y1[4] = {v1.x, v1.y, v1.z, v1.w};
+        for (int k = 0; k < 3; ++k)  // each kind over all accumulators: no product waits for the one before
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const Halves b0 = split(y0[j]), b1 = split(y1[j]);
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int mr = 0; mr < MR; ++mr) mma3(o[mr][blk * 4 + j], ph[mr], pw[mr], b0, b1);
-          }
-        }
+            for (int mr = 0; mr < MR; ++mr)
+              mma1688(o[mr][blk * 4 + j], k == 0 ? pw[mr] : ph[mr], k == 1 ? b0[j].lo : b0[j].hi,
+                      k == 1 ? b1[j].lo : b1[j].hi);
       }
       if (odd) {  // drafts that are not finite, for the nodes that see them
         for (int k = 0; k < kTok && j0 + k < rq.n; ++k)

@@ -14,8 +14,8 @@
 namespace kk {
 namespace {
 
-constexpr int kWarps = kRingWarps, kThreads = kWarps * 32;
-constexpr int kTok = kRingTok, kTK = kRingTK;
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kTK = kRingTK, kTok = kTK / kWarps;  // tokens of a warp's share of a tile
 constexpr int kStages = 3;
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
     const int t0 = it.t0, t1 = it.t1, h = it.h, row0 = it.mt * M;
     const int rows = min(M, rq.n * a.G - row0);
     // the first tiles' copies go out before the queries are read
-    Tok nx = find_token<2>(a, r, rq, h, t0, w, lane);
+    Tok nx = find_token<2, kTok>(a, r, rq, h, t0, w, lane);
 #pragma unroll
     for (int st = 0; st < kStages - 1; ++st) {
       const bool on = t0 + st < t1;
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
       cp_commit();
       const uint32_t ok = __ballot_sync(kFull, on && nx.ok) & 0xFFFFu;
       if (lane == 0) s_ok[w][st] = ok;
-      nx = find_token<2>(a, r, rq, h, min(t0 + st + 1, t1 - 1), w, lane);
+      nx = find_token<2, kTok>(a, r, rq, h, min(t0 + st + 1, t1 - 1), w, lane);
     }
     for (int i = tid; i < M * (D / 8); i += kThreads) {
       const int m = i / (D / 8), c = i - m * (D / 8), row = row0 + m;
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
         cp_commit();
         const uint32_t ok = __ballot_sync(kFull, on && nx.ok) & 0xFFFFu;
         if (lane == 0) s_ok[w][fs] = ok;
-        nx = find_token<2>(a, r, rq, h, min(t + kStages, t1 - 1), w, lane);
+        nx = find_token<2, kTok>(a, r, rq, h, min(t + kStages, t1 - 1), w, lane);
       }
       const uint32_t kst = ring + st * kStage, vst = kst + kTok * D * 2;
       const uint32_t live = s_ok[w][st];
