@@ -151,6 +151,14 @@ __device__ __forceinline__ int split_owner(const Split& s, long long u) {
   return (int)(u < big ? udiv(u, s.q + 1) : s.rem + udiv(u - big, s.q));
 }
 
+// Units that a CTA has done before it comes to unit u, and those of its range.
+__device__ __forceinline__ int split_time(const Split& s, long long u, int* range) {
+  const long long big = (s.q + 1) * s.rem;
+  *range = (int)(u < big ? s.q + 1 : s.q);
+  const long long v = u < big ? u : u - big;
+  return (int)(v - udiv(v, *range) * *range);
+}
+
 // An item: KV head, row tile, whether it is a single, its first unit inside
 // the request and its number of units (a single's unit is two token tiles);
 // [t0, t1): the units of a range that starts inside it.
@@ -214,7 +222,7 @@ __device__ __forceinline__ bool token_at(const AttnArgs& a, int r, const AttnReq
 // range [u0, u1) of all units. Called by NT threads (a multiple of 32, at most
 // 1024); `sh` is NT/32 + 4 long longs of shared memory.
 struct AttnPlace {
-  long long u0, u1, base;
+  long long u0, u1, base, total;
   int r;
 };
 template <int NT>
@@ -238,6 +246,7 @@ __device__ __forceinline__ AttnPlace find_place(const AttnArgs& a, int cta, int 
   }
   long long lo = before + incl - mine;
   AttnPlace p;
+  p.total = total;
   const Split sp = make_split(total, a.grid);
   p.u0 = cta < sp.G ? split_start(sp, cta) : total;
   p.u1 = cta < sp.G ? split_start(sp, cta + 1) : total;

@@ -124,12 +124,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* s_v = s_k + KS * C::kTile;
   __shared__ Bars b;
   __shared__ TileNote s_note[kMeta];
-  __shared__ int s_odd[kMeta];  // a drafted tile has a Value that is not finite
+  __shared__ int s_odd[4][kMaxNodes / kTK];  // by item: a drafted tile has a Value that is not finite
   __shared__ long long s_place[kThreads / 32 + 4];
   __shared__ uint32_t s_tmem;
   __shared__ int s_stop;
   volatile int* stop = &s_stop;
-  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
+  const int tid = threadIdx.x, warp = uni(tid >> 5), lane = tid & 31;
   pdl_launch_dependents();
   if (tid == 0) {
     mbar_init(&b.q_full, 8);
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   const AttnPlace pl = find_place<kThreads>(a, blockIdx.x, 256, kTK, s_place, tid);  // holds block barriers
   tc_fence_after();
-  const uint32_t tmem = __shfl_sync(kFull, s_tmem, 0);
+  const uint32_t tmem = uni(s_tmem);
   int r = pl.r;
   long long base = pl.base;
 
@@ -178,13 +178,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool alive = true;
     for (long long u = pl.u0; u < pl.u1 && alive;) {
       const Work w = work_at(a, pl, u, &r, &base);
-      const bool single = __shfl_sync(kFull, (int)w.at.single, 0);
-      const int tiles = __shfl_sync(kFull, w.tiles, 0);
+      const bool single = uni((int)w.at.single);
+      const int tiles = uni(w.tiles);
       if (tid == 0) note_cut(a, blockIdx.x, r, w.at, u == pl.u0);
       __syncwarp();
       const int sub = single ? 0 : x;  // row tile of the stream
       const int steps = single ? tiles : 2 * tiles;
-      const int rows = __shfl_sync(kFull, w.rows, 0) - sub * 128;
+      const int rows = uni(w.rows) - sub * 128;
       const bool busy = (warp & 3) * 32 < rows;  // this warp has rows at all
       const int qrow = w.row0 + sub * 128 + row;
       const int node = min(qrow / a.G, w.rq.n - 1);
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&b.q_full);
       __syncwarp();
       float m_ref = -INFINITY, l = 0.f;  // in units of S
-      uint32_t dtile = 0, dfirst = 0;    // drafted tiles taken, and the place of the first among the notes
+      uint32_t dtile = 0;                // drafted tiles taken
       for (int i = 0; i < steps; ++i, ++seen) {
         const uint32_t no = notes + (single ? i : i >> 1);
         const int half = single ? x : i & 1;  // 64 tokens of the tile
@@ -235,7 +235,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int draft = note->draft;
           if (draft >= 0) {
             dtile |= 1u << draft;
-            dfirst = no - draft;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const int word = draft * 4 + half * 2 + k, j0 = word * 32;
@@ -318,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       uint32_t odd = 0;
       for (int d = 0; d < kMaxNodes / kTK; ++d)
-        if ((dtile >> d) & 1u) odd |= s_odd[(dfirst + d) % kMeta] ? 1u << d : 0u;
+        if ((dtile >> d) & 1u) odd |= s_odd[items & 3][d] ? 1u << d : 0u;
       // An item that is this CTA's alone is written out here; of a single one,
       // stream B first hands its part to stream A through the CTA's third slot.
       const bool whole = w.at.t0 == 0 && w.at.t1 == w.at.units;
@@ -427,8 +426,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool alive = true;
     for (long long u = pl.u0; u < pl.u1 && alive;) {
       const Work w = work_at(a, pl, u, &r, &base);
-      const bool single = __shfl_sync(kFull, (int)w.at.single, 0);
-      const int tiles = __shfl_sync(kFull, w.tiles, 0);
+      const bool single = uni((int)w.at.single);
+      const int tiles = uni(w.tiles);
+      cnt = uni(cnt);
+      items = uni(items);
+      qs = uni(qs);
+      ps = uni(ps);
       const int steps = single ? tiles : 2 * tiles;
       const uint32_t q0 = (uint32_t)dq + ((single ? 0 : x) * C::kTile >> 4);
       alive = warp_wait(&b.q_full, items & 1, a, stop);
@@ -492,39 +495,81 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kLoadWarp) {
     // ---- loader: the warp stays together and one lane issues the copies ------------
     const int npiece = kTK / tb;  // page pieces of a tile
-    uint32_t cnt = 0, sent[2] = {0, 0};  // tiles of the items before; tiles of K and V sent
+    uint32_t cnt = 0, items = 0, sent[2] = {0, 0};  // tiles and items before; tiles of K and V sent
+    const Split split = make_split(pl.total, a.grid);
     bool alive = true;
     // Where a tile's pieces lie: a piece is a run of tb tokens in one page (tb
     // divides the block size).
     struct Piece {
-      int page, tok;
-      bool full;
+      int page, tok, logical;
     };
+    // The order of an item's tiles. The first pair of row tiles goes through them
+    // in order; where the others stand in their CTA's time they take the tile that
+    // CTAs of the first pair have in hand then (a single, which does two tiles a
+    // unit, those of two CTAs): K and V come from DRAM once, and from L2 for the
+    // other row tiles (654 -> 384 MB would be the ideal on the 64-node tree).
+    int rot = 0, half = 0;  // rotation; tiles of the first of two runs (0: one run)
+    auto place = [&](const Work& w, long long u) {
+      const int units = w.at.single ? (w.tiles + 1) / 2 : w.tiles;
+      half = w.at.single ? units : 0;
+      rot = 0;
+      if (w.at.mt > 0) {
+        const long long ref = base + item_of(w.rq, w.at.h, 0).start + w.first;
+        int range;
+        const int d = (int)(u - pl.u0) - split_time(split, ref, &range);
+        rot = d < 0 ? d + range : d;
+        if (rot >= units || rot < 0) rot = 0;
+      }
+      rot = uni(rot);
+      half = uni(half);
+    };
+    auto tile_of = [&](const Work& w, int i) {
+      if (half == 0) {
+        const int x = i + rot;
+        return w.first + (x < w.tiles ? x : x - w.tiles);
+      }
+      // units j = rot, rot + 1, ...: tiles j and half + j; of an odd number, unit
+      // half - 1 has no second tile
+      if ((w.tiles & 1) && i > 2 * (half - 1 - rot)) ++i;
+      int j = (i >> 1) + rot;
+      if (j >= half) j -= half;
+      return w.first + (i & 1) * half + j;
+    };
+    // What the tables say of a tile's pieces, read a tile ahead and not looked at
+    // before the tile's turn, so that the loop does not wait for it.
     auto look = [&](const Work& w, int i) {
-      Piece x{0, 0, true};
-      const int t = w.first + i;
-      if (i >= w.tiles || t >= w.rq.tiles_c) {
-        x.full = false;
-      } else if (lane < npiece) {
-        TokenAt at;
-        const int v = t * kTK + lane * tb;
-        x.full = token_at(a, w.r, w.rq, v + tb - 1, false, &at) && token_at(a, w.r, w.rq, v, false, &at);
-        x.page = at.page;
-        x.tok = at.tok;
+      Piece x{-1, 0, 0};
+      const int t = tile_of(w, i), v = t * kTK + lane * tb;
+      if (i < w.tiles && t < w.rq.tiles_c && lane < npiece && v + tb <= w.rq.ctx) {
+        const int bk = (unsigned)v / (unsigned)a.kc.bs;
+        x.tok = v - bk * a.kc.bs;
+        if (a.sel_pages) {
+          const long long at = (long long)w.r * a.selK + bk;
+          x.logical = a.sel_logical[at];
+          x.page = a.sel_pages[at];
+        } else {
+          x.page = a.bt.pages[w.rq.off + bk];
+        }
       }
       __syncwarp();
       return x;
     };
+    // Whether all of the tile's pieces hold tokens only.
+    auto all_full = [&](const Work& w, const Piece& x) {
+      bool ok = x.page >= 0 && x.page < a.kc.num_pages;
+      if (a.sel_pages) ok = ok && x.logical >= 0 && (long long)x.logical * a.kc.bs + x.tok + tb <= w.rq.T;
+      return __all_sync(kFull, ok || lane >= npiece);
+    };
     // K (or V) of tile i of the item into its stage
     auto load = [&](const Work& w, int i, const Piece& pc, const bool val) {
-      const int h = __shfl_sync(kFull, w.at.h, 0), t = w.first + i;
+      const int h = uni(w.at.h), t = tile_of(w, i);
       const uint32_t no = cnt + i, ns = val ? VS : KS, st = no % ns;
       TileNote* note = &s_note[no % kMeta];
       uint64_t *noted = &b.note[no % kMeta], *bar = val ? &b.v_full[st] : &b.k_full[st];
       unsigned char* dst = (val ? s_v : s_k) + st * C::kTile;
       if (!warp_wait(val ? &b.v_empty[st] : &b.k_empty[st], ((no / ns) & 1) ^ 1, a, stop)) return false;
       sent[val] = no + 1;
-      if (__all_sync(kFull, pc.full)) {
+      if (t < w.rq.tiles_c && all_full(w, pc)) {
         if (elect_one()) {
           if (!val) {
             note->live[0] = note->live[1] = note->live[2] = note->live[3] = 0xFFFFFFFFu;
@@ -587,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       hit = __any_sync(kFull, hit);
       if (lane == 0) {
         if (val) {
-          s_odd[no % kMeta] = hit;
+          if (draft) s_odd[items & 3][t - w.rq.tiles_c] = hit;
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k) note->live[k] = live[k];
@@ -601,7 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (long long u = pl.u0; u < pl.u1 && alive;) {
       const Work w = work_at(a, pl, u, &r, &base);
-      const int tiles = __shfl_sync(kFull, w.tiles, 0);
+      const int tiles = uni(w.tiles);
+      place(w, u);
       Piece last = look(w, 0), cur = last, next = look(w, 1);
       for (int i = 0; i <= tiles && alive; ++i) {  // K of tile i, V of the tile before
         if (i < tiles) alive = load(w, i, cur, false);
@@ -611,6 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         next = look(w, i + 2);
       }
       cnt += tiles;
+      ++items;
       u += w.at.t1 - w.at.t0;
     }
     // copies in flight end before the CTA does (on the ordinary way they were all waited for)

@@ -9,6 +9,12 @@
 
 namespace kk {
 
+// A value all lanes hold, as one the compiler knows to be uniform (the warp-wide
+// reduction's result lives in a uniform register, a shuffle's does not): what
+// issues copies and MMAs takes its operands from there.
+__device__ __forceinline__ uint32_t uni(uint32_t x) { return __reduce_or_sync(kFull, x); }
+__device__ __forceinline__ int uni(int x) { return (int)__reduce_or_sync(kFull, (unsigned)x); }
+
 // Waits for a barrier's phase with the whole warp; gives up (false) past the
 // limit or when another role has given up, and tells the others. All lanes leave
 // the loop at once: what the warp does next takes its addresses from uniform
