@@ -289,3 +289,16 @@ def test_bad_device_data_is_reported(cuda):
                             sel=kk.Selection(pg, lg2, cnt), workspace=ws)
             assert kk.kk_device_error() == kk.KK_ERR_BAD_INDEX
             check(out[no[2]:], ref[0][no[2]:], ref[2][no[2]:], "out of the sound request")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("nodes", [2, 8, 24, 40])
+def test_scores_that_keep_rising(cuda, D, nodes):
+    """Scores that grow by far more than the lazy maximum's slack, in the middle and in the last tile."""
+    for T in (64, 128, 400, 1024):
+        pc = Paged([T], H=1, D=D, bs=16, L=1, seed=T)
+        pc.k = pc.k.float()
+        for t in range(T):
+            pc.k[0, int(pc.pages[t // 16]), 0, t % 16] *= 0.2 + 6.0 * (t / T) ** 2
+        pc.k = pc.k.to(pc.tdt)
+        _check(*_run(pc, 0, [nodes], 7))
