@@ -163,9 +163,17 @@ def _ptr(t, dtype=None, name="tensor"):
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it: 0.1 us a call
+# instead of 2.9 on the GB300 host, where a short call's kernels take 5-10 us.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _check(fn: str, status: int):
