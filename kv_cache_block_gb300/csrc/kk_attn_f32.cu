@@ -52,6 +52,20 @@ __device__ __forceinline__ uint32_t swz(int row, int c) {
   return row * D * 4 + ((c ^ f) << 4);
 }
 
+// q_m . k_t from the whole values.
+template <int D>
+__device__ __noinline__ float whole_dot(const unsigned char* qh, const unsigned char* ql, const unsigned char* k, int m,
+                                        int t) {
+  auto f4 = [](const unsigned char* p) { return *reinterpret_cast<const float4*>(p); };
+  float sum = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < D / 4; ++c) {
+    const float4 y = f4(k + swz<D>(t, c)), x = f4(qh + swz<D>(m, c)), z = f4(ql + swz<D>(m, c));
+    sum += (x.x + z.x) * y.x + (x.y + z.y) * y.y + (x.z + z.z) * y.z + (x.w + z.w) * y.w;
+  }
+  return sum;
+}
+
 template <int D>
 __device__ __forceinline__ void load_tokens(uint32_t stage, const Tok& x, int lane) {
   constexpr int CH = D / 4, RI = 32 / CH;  // pieces of a row, rows per instruction
@@ -180,7 +194,9 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
         for (int mr = 0; mr < MR; ++mr)
 #pragma unroll
           for (int e = 0; e < 4; ++e) c3[x][mr][e] = 0.f;
-#pragma unroll
+      // for many rows a loop whose code is fetched once (unrolled, instruction fetch
+      // bound the short calls); one row tile needs the overlap of its few products
+#pragma unroll(MR == 1 ? KS : 1)
       for (int ks = 0; ks < KS; ++ks) {
         const float4 kx = f4(kst + swz<D>(g, ks * 4 + q4));
         const Halves b[4] = {split(kx.x), split(kx.y), split(kx.z), split(kx.w)};
@@ -218,13 +234,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int m = mr * 16 + (e & 2 ? 8 : 0) + g, k = q4 * 2 + (e & 1);
-            float sum = 0.f;
-#pragma unroll 1
-            for (int c = 0; c < D / 4; ++c) {
-              const float4 y = f4(kst + swz<D>(k, c)), x = f4(qh + swz<D>(m, c)), z = f4(ql + swz<D>(m, c));
-              sum += (x.x + z.x) * y.x + (x.y + z.y) * y.y + (x.z + z.z) * y.z + (x.w + z.w) * y.w;
-            }
-            s[mr][e] = sum;
+            s[mr][e] = whole_dot<D>(qh, ql, kst, m, k);
           }
       }
       bool rise = false;

@@ -28,14 +28,15 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
 // heaviest token of the middle is found digit by digit (11, 11 and 10 bits)
 // from histograms in shared memory; then every warp counts the tokens of its
 // share above it and equal to it, and, knowing the counts before its own, writes
-// its kept tokens in order.
-template <bool kCached>
-__global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(KCache kc, Table bt, const float* mass, int sinks,
-                                                                   int recent, int keep, int* kept, int* new_lens,
-                                                                   int* err) {
-  extern __shared__ uint32_t s_key[];  // cached: the middle's keys
+// its kept tokens in order. Bound by instructions, so keys are taken four at a
+// time (and read four at a time where the weights lie so, kVec = 4).
+template <bool kCached, int kVec>
+__global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(KCache kc, Table bt, const float* mass,
+                                                                      int sinks, int recent, int keep, int* kept,
+                                                                      int* new_lens, int* err) {
+  extern __shared__ __align__(16) uint32_t s_key[];  // cached: the keys of the request's tokens
   __shared__ uint32_t s_hist[kBins];
-  __shared__ uint32_t s_scan[kSelWarps], s_eq[kSelWarps];
+  __shared__ uint32_t s_scan[kSelWarps];
   __shared__ uint32_t s_digit, s_left;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int h = blockIdx.x % kc.H, l = (blockIdx.x / kc.H) % kc.L, r = blockIdx.x / (kc.H * kc.L);
@@ -60,50 +61,91 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(KCache kc,
   if (want == 0) return;
   const float* mbase = mass + ((long long)l * kc.num_pages * kc.H + h) * bs;
   const long long page_stride = (long long)kc.H * bs;
-  auto weight_of = [&](int b, int o) -> uint32_t {
-    const int page = bt.pages[off + b];
-    if (page < 0 || page >= kc.num_pages) {
-      flag_error(err, kErrBadIndex);
-      return 0u;
-    }
-    return mass_key(mbase[page * page_stride + o]);
-  };
   if (kCached) {
     // A thread keeps its place in the block and steps whole blocks: one division
-    // in all. Eight pages are read, then eight weights, so that the two dependent
-    // loads cost two latencies a round.
-    constexpr int U = 8;
-    const int per = bs < kSelThreads ? kSelThreads / bs : 1;  // blocks a turn
-    const int b0 = bs < kSelThreads ? tid / bs : 0, o0 = bs < kSelThreads ? tid - b0 * bs : tid;
+    // in all. U pages are read, then U weights, so that the two dependent loads
+    // cost two latencies a round.
+    constexpr int U = kVec == 4 ? 4 : 8;
+    const int row = bs / kVec;                                  // pieces of a block
+    const int per = row < kSelThreads ? kSelThreads / row : 1;  // blocks a turn
+    const int b0 = row < kSelThreads ? tid / row : 0, o0 = row < kSelThreads ? tid - b0 * row : tid;
     bool bad = false;
     if (b0 < per)
-      for (int o = o0; o < bs; o += kSelThreads)
+      for (int o = o0; o < row; o += kSelThreads)
         for (int b = m0 / bs + b0; b < nb; b += per * U) {
           int page[U];
-          float wt[U];
+          float wt[U][kVec];
 #pragma unroll
           for (int u = 0; u < U; ++u) page[u] = b + u * per < nb ? bt.pages[off + b + u * per] : 0;
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            const int t = (b + u * per) * bs + o;
-            const bool in = b + u * per < nb && t >= m0 && t < m1, good = page[u] >= 0 && page[u] < kc.num_pages;
-            bad |= in && !good;
-            wt[u] = in && good ? mbase[page[u] * page_stride + o] : NAN;  // a bad page ranks last
+            const bool good = page[u] >= 0 && page[u] < kc.num_pages;
+            bad |= !good;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) wt[u][e] = NAN;  // a bad page ranks last
+            if (b + u * per < nb && good) {
+              // past the last token a page may hold anything: its keys are not looked at
+              const float* p = mbase + page[u] * page_stride + o * kVec;
+              if constexpr (kVec == 4) {
+                const float4 x = *reinterpret_cast<const float4*>(p);
+                wt[u][0] = x.x;
+                wt[u][1] = x.y;
+                wt[u][2] = x.z;
+                wt[u][3] = x.w;
+              } else {
+                wt[u][0] = *p;
+              }
+            }
           }
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            const int t = (b + u * per) * bs + o;
-            if (b + u * per < nb && t >= m0 && t < m1) s_key[t - m0] = mass_key(wt[u]);
+            if (b + u * per >= nb) break;
+            uint32_t* to = s_key + (b + u * per) * bs + o * kVec;
+            if constexpr (kVec == 4)
+              *reinterpret_cast<uint4*>(to) =
+                  make_uint4(mass_key(wt[u][0]), mass_key(wt[u][1]), mass_key(wt[u][2]), mass_key(wt[u][3]));
+            else
+              *to = mass_key(wt[u][0]);
           }
         }
     if (bad) flag_error(err, kErrBadIndex);
     __syncthreads();
   }
-  auto key_at = [&](int t) -> uint32_t {
-    if (kCached) return s_key[t - m0];
-    const int b = t / bs;
-    return weight_of(b, t - b * bs);
+  // Keys of tokens 4 v .. 4 v + 3, and which of them are of the middle.
+  struct Four {
+    uint32_t k[4];
+    uint32_t in;
   };
+  auto four = [&](int v) {
+    Four f;
+    const int t = v * 4;
+    f.in = 0xFu;
+    if (t < m0 || t + 3 >= m1) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (t + e < m0 || t + e >= m1) f.in &= ~(1u << e);
+    }
+    if (kCached) {
+      const uint4 x = *reinterpret_cast<const uint4*>(s_key + t);
+      f.k[0] = x.x;
+      f.k[1] = x.y;
+      f.k[2] = x.z;
+      f.k[3] = x.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f.k[e] = 0;
+        if (!((f.in >> e) & 1u)) continue;
+        const int b = (t + e) / bs, page = bt.pages[off + b];
+        if (page < 0 || page >= kc.num_pages)
+          flag_error(err, kErrBadIndex);
+        else
+          f.k[e] = mass_key(mbase[page * page_stride + (t + e - b * bs)]);
+      }
+    }
+    return f;
+  };
+  const int v0 = m0 / 4, v1 = (m1 + 3) / 4;
   uint32_t prefix = 0, left = want;
   int shift = 32;
 #pragma unroll 1
@@ -113,10 +155,12 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(KCache kc,
     shift -= bits;
     for (int i = tid; i < bins; i += kSelThreads) s_hist[i] = 0;
     __syncthreads();
-#pragma unroll 4
-    for (int t = m0 + tid; t < m1; t += kSelThreads) {
-      const uint32_t k = key_at(t);
-      if (pass == 0 || (k >> up) == prefix) atomicAdd(&s_hist[(k >> shift) & (bins - 1)], 1u);
+    for (int v = v0 + tid; v < v1; v += kSelThreads) {
+      const Four f = four(v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (((f.in >> e) & 1u) && (pass == 0 || (f.k[e] >> up) == prefix))
+          atomicAdd(&s_hist[(f.k[e] >> shift) & (bins - 1)], 1u);
     }
     __syncthreads();
     // from the top bin down: the bin in which the `left`-th key lies
@@ -150,38 +194,50 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(KCache kc,
     left = s_left;
     __syncthreads();
   }
-  // `prefix` is the threshold key; the first `left` tokens equal to it stay
-  const int seg = ((m1 - m0 + kSelWarps * 32 - 1) / (kSelWarps * 32)) * 32;  // a warp's share
-  const int t0 = min(m1, m0 + w * seg), t1 = min(m1, t0 + seg);
-  uint32_t gt = 0, eq = 0;
-#pragma unroll 4
-  for (int t = t0 + lane; t < t1; t += 32) {
-    const uint32_t k = key_at(t);
-    gt += k > prefix;
-    eq += k == prefix;
-  }
-  gt = __reduce_add_sync(kFull, gt);
-  eq = __reduce_add_sync(kFull, eq);
-  if (lane == 0) {
-    s_scan[w] = gt;
-    s_eq[w] = eq;
-  }
+  // `prefix` is the threshold key; the first `left` tokens equal to it stay. Counts
+  // are kept as (above, equal) halves of 64 bits.
+  const int seg = ((v1 - v0 + kSelWarps * 32 - 1) / (kSelWarps * 32)) * 32;  // a warp's share
+  const int a0 = min(v1, v0 + w * seg), a1 = min(v1, a0 + seg);
+  __shared__ unsigned long long s_before[kSelWarps];
+  auto count = [&](const Four& f) {
+    unsigned long long c = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if ((f.in >> e) & 1u) c += f.k[e] > prefix ? 1ull : f.k[e] == prefix ? 1ull << 32 : 0ull;
+    return c;
+  };
+  unsigned long long mine = 0;
+  for (int v = a0 + lane; v < a1; v += 32) mine += count(four(v));
+  const uint32_t gt = __reduce_add_sync(kFull, (uint32_t)mine), eq = __reduce_add_sync(kFull, (uint32_t)(mine >> 32));
+  if (lane == 0) s_before[w] = ((unsigned long long)eq << 32) | gt;
   __syncthreads();
-  uint32_t g_done = 0, e_done = 0;  // tokens above and equal before this warp's
-  for (int x = 0; x < w; ++x) {
-    g_done += s_scan[x];
-    e_done += s_eq[x];
-  }
-  const uint32_t lt = (1u << lane) - 1u;
-  for (int b = t0; b < t1; b += 32) {
-    const int t = b + lane;
-    const uint32_t k = t < t1 ? key_at(t) : 0u;
-    const bool above = t < t1 && k > prefix, same = t < t1 && k == prefix;
-    const uint32_t bg = __ballot_sync(kFull, above), be = __ballot_sync(kFull, same);
-    const uint32_t my_e = e_done + __popc(be & lt);
-    if (above || (same && my_e < left)) out[sinks + g_done + __popc(bg & lt) + min(my_e, left)] = t;
-    g_done += __popc(bg);
-    e_done += __popc(be);
+  unsigned long long done = 0;  // above and equal before this warp's
+  for (int x = 0; x < w; ++x) done += s_before[x];
+  for (int b = a0; b < a1; b += 32) {
+    const int v = b + lane;
+    Four f;
+    f.in = 0;
+    if (v < a1) f = four(v);
+    const unsigned long long c = count(f);
+    // a lane holds 4 at most, a warp 128: both counts in one word for the scan
+    const uint32_t both = (uint32_t)c | (uint32_t)(c >> 32) << 16;
+    uint32_t incl = both;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const uint32_t all = __shfl_sync(kFull, incl, 31), ex = incl - both;
+    uint32_t g = (uint32_t)done + (ex & 0xFFFFu), q = (uint32_t)(done >> 32) + (ex >> 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (!((f.in >> e) & 1u)) continue;
+      const bool above = f.k[e] > prefix, same = f.k[e] == prefix;
+      if (above || (same && q < left)) out[sinks + g + min(q, left)] = v * 4 + e;
+      g += above;
+      q += same;
+    }
+    done += ((unsigned long long)(all >> 16) << 32) + (all & 0xFFFFu);
   }
 }
 
@@ -360,13 +416,15 @@ cudaError_t launch_evict_select(const KCache& kc, const Table& bt, const float* 
   const int grid = bt.R * kc.L * kc.H;
   const long long most = (long long)bt.max_blocks * kc.bs;  // tokens of a request
   if (most <= kMaxCached) {
-    const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kMaxCached * 4);
+    const bool vec = kc.bs % 4 == 0 && reinterpret_cast<uintptr_t>(mass) % 16 == 0;
+    const auto k = vec ? evict_select_kernel<true, 4> : evict_select_kernel<true, 1>;
+    const size_t smem = ((size_t)most + 3) / 4 * 16;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxCached * 4);
     if (e != cudaSuccess) return e;
-    evict_select_kernel<true><<<grid, kSelThreads, (size_t)most * 4, s>>>(kc, bt, mass, sinks, recent, keep, kept,
-                                                                         new_lens, err);
+    k<<<grid, kSelThreads, smem, s>>>(kc, bt, mass, sinks, recent, keep, kept, new_lens, err);
   } else {
-    evict_select_kernel<false><<<grid, kSelThreads, 0, s>>>(kc, bt, mass, sinks, recent, keep, kept, new_lens, err);
+    evict_select_kernel<false, 1>
+        <<<grid, kSelThreads, 0, s>>>(kc, bt, mass, sinks, recent, keep, kept, new_lens, err);
   }
   return cudaGetLastError();
 }

@@ -120,6 +120,9 @@ def _masses(kind, shape, g):
     (1, [50], 3, 5, 8),  # nothing but the first and the last
     (16, [5000], 1, 1, 4900),
     (16, [70], 0, 0, 1),
+    (12, [1001], 2, 3, 100),
+    (640, [1900, 20], 5, 6, 777),  # blocks of more tokens than a CTA has threads
+    (16, [60000], 3, 70, 20000),  # rows too long to be held
 ])
 def test_select(cuda, kind, bs, lens, sinks, recent, keep):
     from kv_cache_block_gb300 import kk
