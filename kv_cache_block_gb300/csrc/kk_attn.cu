@@ -157,68 +157,96 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const Att
 
 // The same for the tensor-memory kernel's slots, [D/4][256 rows][4]: a lane is a
 // row, a warp takes 8 of its values, and every load and store is whole sectors.
-// Blocks of 32 rows x 32 values and eight parts in flight a thread: with a row's
-// 128 values in one block and four in flight, 18 parts took 11 us of latency.
+// A block has 32 rows x 32 values and, where few items are cut into many parts,
+// `groups` of four warps that take every groups-th part and are joined in order.
+// Eight parts are in flight a thread: with a row's 128 values in one block and
+// four in flight, 18 parts took 11 us of latency.
 constexpr int kTcCombineThreads = 128;
 
-template <int D>
-__global__ void __launch_bounds__(kTcCombineThreads) attn_combine_tc_kernel(const AttnArgs a, int TK, int mt_max) {
+struct RowPart {  // a running result: eight values of one row
+  float m, l;
+  float4 acc[2];
+};
+
+template <int D, int groups>
+__global__ void __launch_bounds__(kTcCombineThreads * groups)
+    attn_combine_tc_kernel(const AttnArgs a, int TK, int mt_max) {
   constexpr int M = 256, U = 8;
-  const int tid = threadIdx.x, ln = tid & 31, w = tid >> 5;
+  __shared__ RowPart s_part[groups > 1 ? groups - 1 : 1][kTcCombineThreads];
+  const int tid = threadIdx.x % kTcCombineThreads, ln = tid & 31, w = tid >> 5;
+  const int grp = threadIdx.x / kTcCombineThreads;
   const int mt = blockIdx.x % mt_max, h = (blockIdx.x / mt_max) % a.kc.H, r = blockIdx.x / (mt_max * a.kc.H);
   const AttnReq rq = load_req(a, r, M, TK, false);
   const int m = blockIdx.y * 32 + ln, row = mt * M + m, v4 = (blockIdx.z * 4 + w) * 2;  // first float4 of the row
-  if (mt >= rq.mt || row >= rq.n * a.G) return;
+  const bool real = mt < rq.mt && row < rq.n * a.G;
   pdl_wait();
   const int4 cut = a.cuts[blockIdx.x];
-  if (cut.z == cut.x) return;
+  if (mt >= rq.mt || cut.z == cut.x) return;  // the block as one: no such item, or one written whole
   // a single's streams leave a part each, M/2 rows apart
-  const int sh = mt >= rq.mt - rq.odd, parts = (cut.z - cut.x + 1) << sh;
+  const int sh = mt >= rq.mt - rq.odd, parts = real ? (cut.z - cut.x + 1) << sh : 0;
   auto slot = [&](int i) { return partial_slot(a, cut.x + (i >> sh), i >> sh ? 0 : cut.y, M, D); };
   auto at_row = [&](int i) { return m + (i & sh) * (M / 2); };
-  float mm = -INFINITY, l = 0.f;
-  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int b = 0; b < parts; b += U) {
+  RowPart s = {-INFINITY, 0.f, {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)}};
+  auto add = [&](float al, float l, const float4 (&x)[2]) {
+    s.l += l * al;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      s.acc[e].x += x[e].x * al;
+      s.acc[e].y += x[e].y * al;
+      s.acc[e].z += x[e].z * al;
+      s.acc[e].w += x[e].w * al;
+    }
+  };
+  auto raise = [&](float m2) {  // the running results in terms of the maximum m2; the factor's reference
+    const float ref = m2 == -INFINITY ? 0.f : m2, f = ex2(s.m - ref);
+    s.m = m2;
+    s.l *= f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      s.acc[e] = make_float4(s.acc[e].x * f, s.acc[e].y * f, s.acc[e].z * f, s.acc[e].w * f);
+    return ref;
+  };
+  for (int b = grp; b < parts; b += U * groups) {
     float pm[U], pl[U];
     float4 x[U][2];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const bool on = b + i < parts;
-      const float* part = slot(on ? b + i : b);
-      const int pr = at_row(on ? b + i : b);
+      const int p = b + i * groups;
+      const bool on = p < parts;
+      const float* part = slot(on ? p : b);
+      const int pr = at_row(on ? p : b);
       pm[i] = on ? part[M * D + pr] : -INFINITY;
       pl[i] = part[M * D + M + pr];
       x[i][0] = reinterpret_cast<const float4*>(part)[v4 * M + pr];
       x[i][1] = reinterpret_cast<const float4*>(part)[(v4 + 1) * M + pr];
     }
-    float m2 = mm;
+    float m2 = s.m;
 #pragma unroll
     for (int i = 0; i < U; ++i) m2 = fmaxf(m2, pm[i]);
-    const float ref = m2 == -INFINITY ? 0.f : m2, f = ex2(mm - ref);
-    mm = m2;
-    l *= f;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) acc[e] = make_float4(acc[e].x * f, acc[e].y * f, acc[e].z * f, acc[e].w * f);
+    const float ref = raise(m2);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      if (b + i >= parts) break;
-      const float al = ex2(pm[i] - ref);
-      l += pl[i] * al;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        acc[e].x += x[i][e].x * al;
-        acc[e].y += x[i][e].y * al;
-        acc[e].z += x[i][e].z * al;
-        acc[e].w += x[i][e].w * al;
-      }
+      if (b + i * groups >= parts) break;
+      add(ex2(pm[i] - ref), pl[i], x[i]);
     }
   }
-  const float inv = row_inv(l);
+  if constexpr (groups > 1) {
+    if (grp) s_part[grp - 1][tid] = s;
+    __syncthreads();
+    if (grp) return;
+    for (int g = 1; g < groups; ++g) {
+      const RowPart o = s_part[g - 1][tid];
+      const float ref = raise(fmaxf(s.m, o.m));
+      add(ex2(o.m - ref), o.l, o.acc);
+    }
+  }
+  if (!real) return;
+  const float inv = row_inv(s.l);
   const long long at = (long long)(rq.node0 + row / a.G) * a.Hq + h * a.G + row % a.G;
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + v4 * 4) =
-      make_uint4(pack_bf16(acc[0].x * inv, acc[0].y * inv), pack_bf16(acc[0].z * inv, acc[0].w * inv),
-                 pack_bf16(acc[1].x * inv, acc[1].y * inv), pack_bf16(acc[1].z * inv, acc[1].w * inv));
-  if (v4 == 0 && a.lse) a.lse[at] = row_lse(mm, l);
+      make_uint4(pack_bf16(s.acc[0].x * inv, s.acc[0].y * inv), pack_bf16(s.acc[0].z * inv, s.acc[0].w * inv),
+                 pack_bf16(s.acc[1].x * inv, s.acc[1].y * inv), pack_bf16(s.acc[1].z * inv, s.acc[1].w * inv));
+  if (v4 == 0 && a.lse) a.lse[at] = row_lse(s.m, s.l);
 }
 
 // Launches a combine kernel so that it may start while the main kernel ends.
@@ -239,10 +267,19 @@ cudaError_t launch_dependent(void (*k)(P...), dim3 grid, int threads, cudaStream
 template <int D>
 cudaError_t combine_tc(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
   const int rows = a.max_nodes * a.G, mt_max = a.mt_max;
-  return launch_dependent(
-      attn_combine_tc_kernel<D>,
-      dim3((unsigned)(a.bt.R * a.kc.H * mt_max), (unsigned)((std::min(pl.M, rows) + 31) / 32), (unsigned)(D / 32)),
-      kTcCombineThreads, s, a, pl.TK, mt_max);
+  const long long items = (long long)a.bt.R * a.kc.H * mt_max;
+  const dim3 grid((unsigned)items, (unsigned)((std::min(pl.M, rows) + 31) / 32), (unsigned)(D / 32));
+  // groups: about eight parts each (a single item leaves two a CTA) while the SMs hold every block. One request
+  // of 32768 tokens: 62 -> 39 us (35 rows), 61 -> 49 (252 rows); where blocks of more groups would wait for room,
+  // 8 x 2048 tokens and 252 rows, they took 47 us instead of 41.
+  const long long blocks = (long long)grid.x * grid.y * grid.z;
+  int groups = 1;
+  while (groups < 4 && pl.grid * 2 / items > 8 * groups && blocks * groups * 2 <= 4 * sm_count())
+    groups *= 2;
+  auto go = [&](auto k) { return launch_dependent(k, grid, kTcCombineThreads * groups, s, a, pl.TK, mt_max); };
+  return groups == 1   ? go(attn_combine_tc_kernel<D, 1>)
+         : groups == 2 ? go(attn_combine_tc_kernel<D, 2>)
+                       : go(attn_combine_tc_kernel<D, 4>);
 }
 
 template <typename T, int D>
@@ -258,15 +295,31 @@ cudaError_t combine_t(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
                           kCombineThreads, s, a, M, pl.TK, mt_max, wpr);
 }
 
-// Rows per KV head from which the tensor-memory kernel is taken (where the
-// caches' layouts suit it).
-constexpr int kTcRows = 33;
+// When the tensor-memory kernel is taken, where the caches' layouts suit it: for
+// more rows than one tile of 16, once (cached tokens of all requests and KV
+// heads) x (tiles of 32 rows) pass 24 K. It starts and ends slower than the mma
+// kernel, which reads the tokens again for every 32 rows and multiplies at a
+// fraction of its rate. Measured at D = 128 and groups of 7 (mma / tensor
+// memory, us): 4 K tokens x 1 17.0 / 23.1, 4 K x 3 18.8 / 23.1, 16 K x 1 18.9 /
+// 22.9, 16 K x 2 24.8 / 22.9, 32 K x 1 26.8 / 24.8, 4 K x 8 28.8 / 26.7, 32 K x 3
+// 37.2 / 26.9, 1 M x 1 162.8 / 103.8, 1 M x 2 299 / 105; at D = 64 16 K x 1 16.9 /
+// 18.8 and 16 K x 2 24.8 / 19.2. One tile of 16 rows: 1 M tokens 97.0 / 96.5 and
+// 131 K 26.9 / 31.5 (D = 64: 57.4 / 65.8 and 20.7 / 28.9).
+constexpr int kTcRows = 17;
+constexpr long long kTcWork = 24 << 10;
 
-AttnPlan plan(const KCache& kc, const KCache& vc, int max_nodes, int G) {
+AttnPlan plan(const KCache& kc, const KCache& vc, int max_nodes, int G, long long tokens) {
   const int rows = max_nodes * G;
   if (kc.dtype != 1) return attn_f32_plan(kc, rows);
-  if (rows >= kTcRows && attn_tc_suits(kc) && attn_tc_suits(vc)) return attn_tc_plan();
+  if (rows >= kTcRows && tokens * ((rows + 31) / 32) >= kTcWork && attn_tc_suits(kc) && attn_tc_suits(vc))
+    return attn_tc_plan();
   return attn_mma_plan(kc, rows);
+}
+
+// Cached tokens of every request and KV head that a call reads, at most.
+long long most_tokens(const AttnArgs& a) {
+  const long long blocks = a.sel_pages ? std::min(a.selK, a.bt.max_blocks) : a.bt.max_blocks;
+  return blocks * a.kc.bs * a.bt.R * a.kc.H;
 }
 
 size_t plan_bytes(const AttnPlan& pl, int D) {
@@ -282,15 +335,16 @@ size_t cut_bytes(const AttnPlan& pl, int R, int H, int rows) {
 }  // namespace
 
 size_t attn_workspace_bytes(const KCache& kc, int R, int max_nodes, int G) {
-  // enough for either kernel: which one runs also depends on the V cache's strides
+  // enough for either kernel: which one runs also depends on the V cache's strides and the tokens
   const int rows = max_nodes * G;
   auto size = [&](const AttnPlan& pl) { return cut_bytes(pl, R, kc.H, rows) + plan_bytes(pl, kc.D); };
-  const size_t n = size(plan(kc, kc, max_nodes, G));
-  return kc.dtype == 1 ? std::max(n, size(attn_mma_plan(kc, rows))) : n;
+  if (kc.dtype != 1) return size(attn_f32_plan(kc, rows));
+  const size_t n = size(attn_mma_plan(kc, rows));
+  return attn_tc_suits(kc) ? std::max(n, size(attn_tc_plan())) : n;
 }
 
 cudaError_t launch_tree_attn(AttnArgs a, cudaStream_t s) {
-  const AttnPlan pl = plan(a.kc, a.vc, a.max_nodes, a.G);
+  const AttnPlan pl = plan(a.kc, a.vc, a.max_nodes, a.G, most_tokens(a));
   a.grid = pl.grid;
   a.twin = pl.kind == AttnPlan::kTc;
   const int rows = a.max_nodes * a.G;

@@ -15,6 +15,8 @@ BF16 = torch.finfo(torch.bfloat16).eps / 2
 class Paged:
     """K and V of `lens` tokens in shuffled pages; every slot that holds no token is NaN."""
 
+    bound = 0  # a looser host bound of the tables' lengths: which kernel reads a cache depends on it
+
     def __init__(self, lens, H=2, D=64, bs=16, L=2, dtype="bf16", layout="LPHTD", extra=3, seed=0, fill=math.nan):
         g = torch.Generator().manual_seed(seed)
         self.lens, self.H, self.D, self.bs, self.L, self.dtype = list(lens), H, D, bs, L, dtype
@@ -57,7 +59,7 @@ class Paged:
         desc = lambda x: kk.kcache_desc(x, code, self.L, self.H, self.D, self.bs, self.P, x.stride()[:4])  # noqa: E731
         self.kd, self.vd = desc(self.gk), desc(self.gv)
         i32 = lambda a: torch.as_tensor(a, dtype=torch.int32).cuda()  # noqa: E731
-        self.bt = kk.BlockTable(i32(self.pages), i32(self.off), i32(self.lens), max(self.nb) if self.nb else 0)
+        self.bt = kk.BlockTable(i32(self.pages), i32(self.off), i32(self.lens), max([*self.nb, self.bound]))
         return self
 
     @staticmethod

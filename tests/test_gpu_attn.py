@@ -12,6 +12,12 @@ from tests.attn_ref import Paged, attn_ref, check, words
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True, params=[0, 1 << 16], ids=["tight", "loose"])
+def table_bound(request, monkeypatch):
+    """Short lengths under a tight and a loose bound: every variant at every size."""
+    monkeypatch.setattr(Paged, "bound", request.param)
+
+
 def _nodes(counts, Hq, D, dt, H, seed, fused=True):
     """Offsets, queries and drafted K and V (views of one fused tensor, or separate dense ones)."""
     g = torch.Generator().manual_seed(seed)
@@ -53,7 +59,7 @@ def _run(pc, layer, counts, G, draft=False, see=None, sel=None, seed=5, scale=No
                    _gpu(dk) if draft else None, _gpu(dv) if draft else None)
     gsel = None
     if sel is not None:
-        K = max(max(len(s) for s in sel), 1) + 1
+        K = max(max(len(s) for s in sel), 1, min(Paged.bound, 2000)) + 1
         lg = torch.full((len(sel), K), -1, dtype=torch.int32)
         pg = lg.clone()
         for r, s in enumerate(sel):
@@ -268,18 +274,21 @@ def test_bad_device_data_is_reported(cuda):
         for page in (-1, pc.P):
             pages = pc.bt.pages.clone()
             pages[int(pc.off[0]) + 2] = page
-            go(kk.BlockTable(pages, pc.bt.offsets, pc.bt.seq_lens, max(pc.nb)), kk.Tree(mx, offs))
+            go(kk.BlockTable(pages, pc.bt.offsets, pc.bt.seq_lens, pc.bt.c.max_blocks), kk.Tree(mx, offs))
         lens = pc.bt.seq_lens.clone()
         lens[1] = 200
-        go(kk.BlockTable(pc.bt.pages, pc.bt.offsets, lens, max(pc.nb)), kk.Tree(mx, offs))
+        go(kk.BlockTable(pc.bt.pages, pc.bt.offsets, lens, pc.bt.c.max_blocks), kk.Tree(mx, offs))
         short = offs.clone()
         short[1] = no[-1] + 3
         out = torch.full(q.shape, 5.0, dtype=q.dtype, device="cuda")
         kk.kk_tree_attn(pc.kd, pc.vd, pc.bt, 0, kk.Tree(mx, short), q, 0.125, out, workspace=ws)
         assert kk.kk_device_error() == kk.KK_ERR_BAD_INDEX
         check(out[no[2]:], ref[0][no[2]:], ref[2][no[2]:], "out of the sound request")
-        lg = torch.arange(4, dtype=torch.int32).repeat(3, 1).cuda()
-        pg = torch.stack([pc.bt.pages[int(pc.off[r]):int(pc.off[r]) + 4] for r in range(3)]).contiguous()
+        K = max(4, min(Paged.bound, 2000))
+        lg, pg = (torch.full((3, K), -1, dtype=torch.int32, device="cuda") for _ in range(2))
+        for r in range(3):
+            lg[r, :4] = torch.arange(4)
+            pg[r, :4] = pc.bt.pages[int(pc.off[r]):int(pc.off[r]) + 4]
         for r, what in ((0, 99), (1, -7)):
             lg2 = lg.clone()
             lg2[r, 1] = what
