@@ -295,25 +295,28 @@ cudaError_t combine_t(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
                           kCombineThreads, s, a, M, pl.TK, mt_max, wpr);
 }
 
-// When the tensor-memory kernel is taken, where the caches' layouts suit it: for
-// more rows than one tile of 16, once (cached tokens of all requests and KV
-// heads) x (tiles of 32 rows) pass 24 K. It starts and ends slower than the mma
-// kernel, which reads the tokens again for every 32 rows and multiplies at a
-// fraction of its rate. Measured at D = 128 and groups of 7 (mma / tensor
-// memory, us): 4 K tokens x 1 17.0 / 23.1, 4 K x 3 18.8 / 23.1, 16 K x 1 18.9 /
-// 22.9, 16 K x 2 24.8 / 22.9, 32 K x 1 26.8 / 24.8, 4 K x 8 28.8 / 26.7, 32 K x 3
-// 37.2 / 26.9, 1 M x 1 162.8 / 103.8, 1 M x 2 299 / 105; at D = 64 16 K x 1 16.9 /
-// 18.8 and 16 K x 2 24.8 / 19.2. One tile of 16 rows: 1 M tokens 97.0 / 96.5 and
-// 131 K 26.9 / 31.5 (D = 64: 57.4 / 65.8 and 20.7 / 28.9).
-constexpr int kTcRows = 17;
-constexpr long long kTcWork = 24 << 10;
+// When the tensor-memory kernel is taken, where the caches' layouts suit it: it
+// starts and ends slower than the mma kernel (23 against 15 us for 4 K cached
+// tokens of all requests and KV heads), which reads the tokens once for every 16
+// rows; so once tokens x (tiles of 16 rows - 1) pass 72 K. Measured with groups
+// of 7 (mma / tensor memory, us), D = 128: 4 K x 5 20.7 / 23.1, 16 K x 1 20.5 /
+// 22.9, 16 K x 3 24.8 / 23.7, 64 K x 1 28.7 / 31.0, 16 K x 5 26.9 / 24.9, 64 K x 3
+// 37.4 / 33.0, 64 K x 5 46.9 / 37.2; D = 64: 64 K x 1 20.7 / 24.9, 16 K x 5 20.7 /
+// 18.8, 64 K x 3 26.9 / 25.8, 64 K x 5 32.5 / 26.9. One tile of 16 rows: 1 M tokens
+// 97.0 / 96.5 and 131 K 26.9 / 31.5 (D = 64: 57.4 / 65.8 and 20.7 / 28.9).
+constexpr long long kTcWork = 72 << 10;
+// From where the mma kernel's tiles have 32 rows (layouts that do not suit the
+// other kernel): 512 K tokens of 128 dims and 28, 63, 91 rows 90 / 153 / 215 us
+// against 100 / 176 / 252 with 16, but 64 K tokens 31 / 41 / 51 against 29 / 37 / 47;
+// 1 M of 32 dims and 28, 63 rows 66 / 123 against 77 / 138. Never for 64 dims (512 K:
+// 80 / 130 / 173 against 60 / 101 / 139).
+constexpr long long kWideTokens = 256 << 10;
 
 AttnPlan plan(const KCache& kc, const KCache& vc, int max_nodes, int G, long long tokens) {
   const int rows = max_nodes * G;
   if (kc.dtype != 1) return attn_f32_plan(kc, rows);
-  if (rows >= kTcRows && tokens * ((rows + 31) / 32) >= kTcWork && attn_tc_suits(kc) && attn_tc_suits(vc))
-    return attn_tc_plan();
-  return attn_mma_plan(kc, rows);
+  if (tokens * ((rows - 1) / 16) >= kTcWork && attn_tc_suits(kc) && attn_tc_suits(vc)) return attn_tc_plan();
+  return attn_mma_plan(kc, rows > 16 && tokens >= kWideTokens);
 }
 
 // Cached tokens of every request and KV head that a call reads, at most.
@@ -335,11 +338,11 @@ size_t cut_bytes(const AttnPlan& pl, int R, int H, int rows) {
 }  // namespace
 
 size_t attn_workspace_bytes(const KCache& kc, int R, int max_nodes, int G) {
-  // enough for either kernel: which one runs also depends on the V cache's strides and the tokens
+  // enough for any: which one runs also depends on the V cache's strides and the tokens
   const int rows = max_nodes * G;
   auto size = [&](const AttnPlan& pl) { return cut_bytes(pl, R, kc.H, rows) + plan_bytes(pl, kc.D); };
   if (kc.dtype != 1) return size(attn_f32_plan(kc, rows));
-  const size_t n = size(attn_mma_plan(kc, rows));
+  const size_t n = std::max(size(attn_mma_plan(kc, false)), size(attn_mma_plan(kc, true)));
   return attn_tc_suits(kc) ? std::max(n, size(attn_tc_plan())) : n;
 }
 

@@ -59,10 +59,10 @@ struct AttnPlan {
   Kind kind;
   int M, TK, grid;
 };
-// kk_attn_mma.cu (bf16; rows: query rows of a request and KV head, at most)
-AttnPlan attn_mma_plan(const KCache& kc, int rows);
+// kk_attn_mma.cu (bf16; wide: 32 rows a tile instead of 16 where D is 32 or 128)
+AttnPlan attn_mma_plan(const KCache& kc, bool wide);
 cudaError_t launch_attn_mma(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s);
-// kk_attn_f32.cu (float32)
+// kk_attn_f32.cu (float32; rows: query rows of a request and KV head, at most)
 AttnPlan attn_f32_plan(const KCache& kc, int rows);
 cudaError_t launch_attn_f32(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s);
 // kk_attn_tc.cu (bf16, D 64 or 128, both caches of layouts it suits)

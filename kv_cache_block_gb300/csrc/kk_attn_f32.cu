@@ -2,7 +2,7 @@
 // into two tf32 numbers, x = hi + lo up to 2^-22 |x|, and a product is hi hi' +
 // hi lo' + lo hi' (the dropped lo lo' is below 2^-22 of it), summed in float32.
 // That keeps the products of float32 inputs within a few roundings of float32
-// while M = 16 to 64 query rows share one read of K and V; on the CUDA cores 8
+// while M = 16 or 32 query rows share one read of K and V; on the CUDA cores 8
 // rows shared it and a tile waited for uncoalesced rows.
 //
 // The structure is kk_attn_mma.cu's (a ring of 16-byte asynchronous copies per
@@ -402,25 +402,23 @@ AttnPlan plan_t() {
   const int per = 227 * 1024 / (f32_smem<D, MR>() + 1024 + 256);
   return AttnPlan{AttnPlan::kF32, MR * 16, kTK, sm_count() * (per < 1 ? 1 : per > 4 ? 4 : per)};
 }
-template <int D>
-AttnPlan plan_d(int rows) {
-  // as many rows as a read of K and V can serve (registers: 64 rows of 64 dims)
-  if (rows <= 16) return plan_t<D, 1>();
-  return rows <= 32 || D == 128 ? plan_t<D, 2>() : plan_t<D, D == 128 ? 2 : 4>();
-}
 
 }  // namespace
 
+// 16 rows a tile, 32 where rows of 128 dims make the reads dear. Groups of 7, us
+// at 32 / 16 rows: D = 128, 8 x 8192 tokens and 28, 56, 280 rows 87 / 94, 146 / 167,
+// 555 / 670 (2 x 4096: 28.9 / 26.9, 37.1 / 35.9, 92.5 / 103); D = 64 64 / 52, 105 / 88,
+// 386 / 340 (64 rows: 89 at 56, 363 at 280): the more CTAs of an SM hide more.
 AttnPlan attn_f32_plan(const KCache& kc, int rows) {
-  return kc.D == 32 ? plan_d<32>(rows) : kc.D == 64 ? plan_d<64>(rows) : plan_d<128>(rows);
+  if (kc.D == 128) return rows <= 16 ? plan_t<128, 1>() : plan_t<128, 2>();
+  return kc.D == 32 ? plan_t<32, 1>() : plan_t<64, 1>();
 }
 
 cudaError_t launch_attn_f32(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
-  const int mr = pl.M / 16;
   switch (a.kc.D) {
-    case 32: return mr == 1 ? go<32, 1>(a, s) : mr == 2 ? go<32, 2>(a, s) : go<32, 4>(a, s);
-    case 64: return mr == 1 ? go<64, 1>(a, s) : mr == 2 ? go<64, 2>(a, s) : go<64, 4>(a, s);
-    case 128: return mr == 1 ? go<128, 1>(a, s) : go<128, 2>(a, s);
+    case 32: return go<32, 1>(a, s);
+    case 64: return go<64, 1>(a, s);
+    case 128: return pl.M == 16 ? go<128, 1>(a, s) : go<128, 2>(a, s);
   }
   return cudaErrorNotSupported;
 }

@@ -333,30 +333,28 @@ cudaError_t go(const AttnArgs& a, cudaStream_t s) {
 }
 
 template <int D>
-AttnPlan plan_d(int rows) {
-  // one 16-row tile for a decode token's group; else 32 rows share a read of K
-  // and V (registers: the accumulator of 32 rows of 256 does not fit)
-  const bool two = rows > 16 && D < 256;
-  const int smem = two ? mma_smem<D, D < 256 ? 2 : 1>() : mma_smem<D, 1>();
+AttnPlan plan_d(bool wide) {
+  const bool two = wide && (D == 32 || D == 128);  // registers: the accumulator of 32 rows of 256 does not fit
+  const int smem = two ? mma_smem<D, D == 32 || D == 128 ? 2 : 1>() : mma_smem<D, 1>();
   const int per = 227 * 1024 / (smem + 1024 + 256);
   return AttnPlan{AttnPlan::kMma, two ? 32 : 16, kTK, sm_count() * (per < 1 ? 1 : per > 4 ? 4 : per)};
 }
 
 }  // namespace
 
-AttnPlan attn_mma_plan(const KCache& kc, int rows) {
+AttnPlan attn_mma_plan(const KCache& kc, bool wide) {
   switch (kc.D) {
-    case 32: return plan_d<32>(rows);
-    case 64: return plan_d<64>(rows);
-    case 128: return plan_d<128>(rows);
-    default: return plan_d<256>(rows);
+    case 32: return plan_d<32>(wide);
+    case 64: return plan_d<64>(wide);
+    case 128: return plan_d<128>(wide);
+    default: return plan_d<256>(wide);
   }
 }
 
 cudaError_t launch_attn_mma(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
   switch (a.kc.D) {
     case 32: return pl.M == 16 ? go<32, 1>(a, s) : go<32, 2>(a, s);
-    case 64: return pl.M == 16 ? go<64, 1>(a, s) : go<64, 2>(a, s);
+    case 64: return go<64, 1>(a, s);
     case 128: return pl.M == 16 ? go<128, 1>(a, s) : go<128, 2>(a, s);
     case 256: return go<256, 1>(a, s);
   }
