@@ -540,10 +540,12 @@ typedef struct kk_selection {
  * gets 0 and -inf. Tokens past seq_lens[r] and drafted nodes a node does not
  * see take no part, whatever those places hold. Sums and the softmax are
  * float32; on bf16 caches the weights are rounded to bf16 before they multiply
- * the Values. num_q_heads is a multiple of num_kv_heads; scale is finite.
+ * the Values; on float32 caches products are sums of three products of tf32
+ * halves, within 2^-21 of float32's. num_q_heads is a multiple of num_kv_heads; scale is finite.
  * workspace: device, 256-byte aligned, of kk_tree_attn_workspace_bytes(); no
  * initial contents; calls that may run at once need separate ones. The same
- * call gives the same bits.
+ * call gives the same bits (bt->max_blocks included: how the work is divided
+ * depends on it, and a bound far above the real tables costs time).
  */
 size_t kk_tree_attn_workspace_bytes(const kk_kcache_desc* kc, const kk_block_table* bt, int32_t max_nodes,
                                     int32_t num_q_heads);

@@ -2,8 +2,12 @@
 //  * evict_select_kernel: the first `sinks` tokens, the last `recent` ones and
 //    the heaviest of the rest, `keep` in all, in ascending order (equal weights
 //    to the lower index, NaN below everything);
-//  * evict_compact_kernel: their Keys, Values and weights moved to slots
-//    0 .. keep-1 of the request's pages, or of new ones.
+//  * evict_move_kernel, evict_compact_kernel: their Keys, Values and weights
+//    moved to slots 0 .. keep-1 of new pages, or of the request's own.
+// Measured, 896 rows of 8192 bf16 tokens of 128 dims cut to 2048: the selection 43
+// us (29 MB read once: bound by instructions, 78 % of the issue slots, and by equal
+// weights meeting in one bin of a histogram), the move to new pages 287 us (1.87
+// GB, 6.6 TB/s), in place 378.
 #include <cmath>
 
 #include "kk_device.cuh"
