@@ -78,6 +78,26 @@ def test_mass_of_empty_and_rejected_rows(cuda):
         assert kk.kk_device_error() == 0
 
 
+@pytest.mark.parametrize("dtype,D,bs", [("f32", 32, 16), ("f32", 64, 16), ("f32", 128, 64), ("bf16", 32, 16),
+                                        ("bf16", 128, 12), ("bf16", 256, 12), ("bf16", 64, 16), ("bf16", 128, 128)])
+def test_mass_of_many_tokens(cuda, dtype, D, bs):
+    """Several tiles in every CTA's share, of one item and of the next; more rows than are held at a time."""
+    from kv_cache_block_gb300 import kk
+
+    lens, counts, G, H = [40000, 17, 25003], [1, 2, 20], 2, 4
+    pc = Paged(lens, H=H, D=D, bs=bs, dtype=dtype, L=1, seed=D + bs).to_gpu()
+    no, q = _queries(counts, H * G, D, pc.tdt, 3)
+    g = torch.Generator().manual_seed(2)
+    lse = 8 + torch.rand(q.shape[:2], generator=g)
+    mass = torch.rand((1, pc.P, H, bs), generator=g)
+    out = mass.cuda()
+    kk.kk_attn_mass(pc.kd, pc.bt, 0, kk.Tree(20, torch.as_tensor(no, dtype=torch.int32).cuda()), q.cuda(), 0.1,
+                    lse.cuda(), out, out, decay=0.5)
+    assert kk.kk_device_error() == 0
+    ref, tol = mass_ref(pc, 0, no, q, 0.1, G, lse, mass, decay=0.5)
+    check(out, ref, tol, "mass")
+
+
 def test_mass_bad_page(cuda):
     from kv_cache_block_gb300 import kk
 
