@@ -109,6 +109,20 @@ def test_long_rows_are_split_and_joined(cuda, dtype, H, G, lens):
     _check(*_run(pc, 0, [5] * len(lens), G, draft=True))
 
 
+@pytest.mark.parametrize("dtype,D,G,lens,counts", [
+    ("bf16", 128, 7, [70000, 3, 41001], [1, 1, 2]),
+    ("bf16", 256, 2, [50000, 31001], [1, 9]),
+    ("bf16", 32, 9, [50000, 41001], [1, 2]),
+    ("bf16", 64, 8, [60000, 41001], [9, 33]),  # the last of one row tile, or of three
+    ("bf16", 128, 4, [60000, 31001], [2, 30]),
+    ("f32", 64, 3, [50000, 31001], [1, 7]),
+    ("f32", 128, 5, [50000, 31001], [1, 5]),
+])
+def test_many_tiles_of_every_cta(cuda, dtype, D, G, lens, counts):
+    pc = Paged(lens, H=1, D=D, bs=16, dtype=dtype, L=1, seed=D + G)
+    _check(*_run(pc, 0, counts, G, draft=True))
+
+
 def _tree(n, rng, empty=False):
     see = np.zeros((n, n), dtype=bool)
     for j in range(n):
