@@ -342,8 +342,10 @@ size_t attn_workspace_bytes(const KCache& kc, int R, int max_nodes, int G) {
   const int rows = max_nodes * G;
   auto size = [&](const AttnPlan& pl) { return cut_bytes(pl, R, kc.H, rows) + plan_bytes(pl, kc.D); };
   if (kc.dtype != 1) return size(attn_f32_plan(kc, rows));
-  const size_t n = std::max(size(attn_mma_plan(kc, false)), size(attn_mma_plan(kc, true)));
-  return attn_tc_suits(kc) ? std::max(n, size(attn_tc_plan())) : n;
+  const size_t n = size(attn_mma_plan(kc, false));
+  if (rows <= 16) return n;
+  const size_t m = std::max(n, size(attn_mma_plan(kc, true)));
+  return attn_tc_suits(kc) ? std::max(m, size(attn_tc_plan())) : m;
 }
 
 cudaError_t launch_tree_attn(AttnArgs a, cudaStream_t s) {
