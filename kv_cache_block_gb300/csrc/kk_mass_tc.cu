@@ -13,10 +13,11 @@
 // own lane, which stores nothing.
 //
 // Measured, D = 128, groups of 7: one node, 8 requests of up to 32768 tokens (195
-// MB) 41.5 us, 4.7 TB/s (a fifth of it starts and ends the call); 64 causal nodes,
-// 2 x 16384 tokens (9.7 GF, 38 M exponentials) 36.5 us: an exponential costs its
-// thread about eight other instructions (a scale, a bound, a weight, a sum), so
-// the epilogue groups bind, not the tensor cores (16 %).
+// MB) 42.4 us, 4.6 TB/s, about 13 of it before and after the stream of tiles (four
+// times the tokens run at 6.3 TB/s); up to 64 causal nodes, 2 x 16384 tokens (9.7 GF,
+// 38 M exponentials) 35 us, half of it start and end too: 2 x 65536 tokens and 64
+// nodes take 99 us, 610 TF/s, two thirds of what 16 exponentials a clock and SM
+// allow. Twice the epilogue warps, which halved a tile's rows, were slower (39 us).
 #include <cuda.h>
 
 #include <algorithm>
@@ -36,9 +37,9 @@ constexpr int kMaxRows = 1024;
 constexpr int kStagesMax = 8;
 constexpr int kSmemMax = 227 * 1024 - 1024 - 20 * 1024;  // next to the row list and the barriers
 
-struct __align__(16) RowInfo {
-  float b, w;  // -lse in the log2 domain, weight
-  int len;     // tokens the row sees
+struct __align__(8) RowInfo {
+  float w;  // weight
+  int len;  // tokens the row sees
 };
 
 struct Bars {
@@ -61,7 +62,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* s_k = smem;
   unsigned char* s_q = s_k + NS * kTile;  // [64-dim chunk][rows_pad][128 bytes], 128-byte swizzle
   __shared__ Bars b;
-  __shared__ RowInfo s_row[kMaxRows + 32];  // rows up to a whole group of 32 see nothing
+  // Rows up to a whole group of 32 see nothing.
+  __shared__ __align__(16) float s_b[kMaxRows + 32];  // -lse in the log2 domain
+  __shared__ __align__(16) RowInfo s_row[kMaxRows + 32];
+  __shared__ int s_least;  // tokens that every row sees, with a weight of 1 (0 where there is another)
   __shared__ long long s_place[kThreads / 32 + 4];
   __shared__ int s_cnt[kEpi / 32];
   __shared__ int s_rows;  // rows of the item that count
@@ -124,6 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++items;
       alive = !named_sync_or(1, kEpi, !alive);
       if (!alive) break;
+      if (tid == 0) s_least = 0x7fffffff;
       const int r0 = min(row_begin, rq.n * a.G), r1 = min(row_end, rq.n * a.G);
       constexpr int NX = kMaxRows / kEpi;  // rows a thread looks at
       float rw[NX], rl[NX];
@@ -154,7 +159,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (on) {
           const int i = before + __popc(m & ((1u << lane) - 1u)), x = r0 + y * kEpi + tid;
-          s_row[i] = RowInfo{-rl[y] * 1.44269504088896341f, rw[y], len[y]};
+          s_b[i] = -rl[y] * 1.44269504088896341f;
+          s_row[i] = RowInfo{rw[y], len[y]};
+          atomicMin(&s_least, rw[y] == 1.f ? len[y] : 0);
           const uint16_t* q =
               static_cast<const uint16_t*>(a.q) + rn[y] * a.q_sn + (long long)(h * a.G + x % a.G) * a.q_sh;
 #pragma unroll
@@ -164,7 +171,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         have = all;
         named_sync(1, kEpi);
       }
-      if (tid < 32) s_row[have + tid] = RowInfo{0.f, 0.f, 0};
+      if (tid < 32) {
+        s_b[have + tid] = 0.f;
+        s_row[have + tid] = RowInfo{0.f, 0};
+      }
       if (tid == 0) s_rows = have;
       cp_wait_all();
       fence_async_smem();
@@ -174,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = __shfl_sync(kFull, s_rows, 0);
       const int nch = (n + kCols - 1) / kCols;
       const int old = a.old_lens ? a.old_lens[r] : rq.T;
+      const int least = __shfl_sync(kFull, s_least, 0);
       // A tile's token is looked up two tiles ahead and what it had is read one
       // tile ahead: two dependent loads that would else wait behind every tile.
       auto find = [&](int t) {  // the token's weight, or -1
@@ -211,18 +222,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const int cols = min(kCols, n - c * kCols);
           const uint32_t at_col = tmem + lane_at + buf * kCols;
+          const float4* rb = reinterpret_cast<const float4*>(s_b + c * kCols);
           const RowInfo* ri = s_row + c * kCols;
           float part[4] = {0.f, 0.f, 0.f, 0.f};
-          // One small loop for whole, ragged and causal tiles alike: a row's length
-          // is tested for every token. The exponentials bound it (16 a clock and SM),
-          // the test hides behind them; a second copy of the loop without it cost
-          // more in fetched code than it saved.
+          // What a row's values cost to read bounds this: shared memory gives a
+          // clock's worth of a warp 4 bytes a lane, whoever shares them. So where
+          // every row sees the whole tile with weight 1, only its lse is read.
           auto sum = [&](auto count, const uint32_t* s, int k) {
+            constexpr int N = decltype(count)::value;
+            if (N > 8 && (t + 1) * kTK <= least && k + N <= cols) {
 #pragma unroll
-            for (int e = 0; e < decltype(count)::value; ++e) {
-              const RowInfo y = ri[k + e];
-              const float p = ex2(__uint_as_float(s[e]) * a.scale_log2 + y.b);
-              part[e & 3] += y.w * (v < y.len ? p : 0.f);  // selected: a hidden place may hold anything
+              for (int e = 0; e < N; e += 4) {
+                const float4 y = rb[(k + e) / 4];
+                part[0] += ex2(__uint_as_float(s[e]) * a.scale_log2 + y.x);
+                part[1] += ex2(__uint_as_float(s[e + 1]) * a.scale_log2 + y.y);
+                part[2] += ex2(__uint_as_float(s[e + 2]) * a.scale_log2 + y.z);
+                part[3] += ex2(__uint_as_float(s[e + 3]) * a.scale_log2 + y.w);
+              }
+              return;
+            }
+#pragma unroll
+            for (int e = 0; e < N; e += 4) {
+              const float4 b4 = rb[(k + e) / 4];
+              const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const RowInfo y = ri[k + e + j];
+                const float p = ex2(__uint_as_float(s[e + j]) * a.scale_log2 + bb[j]);
+                part[j] += y.w * (v < y.len ? p : 0.f);  // selected: a hidden place may hold anything
+              }
             }
           };
           if (cols <= 8) {
