@@ -4,7 +4,7 @@
 //    to the lower index, NaN below everything);
 //  * evict_move_kernel, evict_compact_kernel: their Keys, Values and weights
 //    moved to slots 0 .. keep-1 of new pages, or of the request's own.
-// Measured, 896 rows of 8192 bf16 tokens of 128 dims cut to 2048: the selection 43
+// Measured, 896 rows of 8192 bf16 tokens of 128 dims cut to 2048: the selection 41
 // us (29 MB read once: bound by instructions, 78 % of the issue slots, and by equal
 // weights meeting in one bin of a histogram), the move to new pages 287 us (1.87
 // GB, 6.6 TB/s), in place 378.
@@ -16,8 +16,6 @@ namespace kk {
 namespace {
 
 // ---- selection -------------------------------------------------------------
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 // Weights of a row kept in shared memory (next to the histogram); longer rows
 // are read again for each of the five passes.
@@ -28,19 +26,19 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
   return m != m ? 0u : f32_to_ordered(m + 0.f);
 }
 
-// One CTA per (request, layer, head). The key of the (keep - sinks - recent)-th
+// One CTA of NT threads per (request, layer, head). The key of the (keep - sinks - recent)-th
 // heaviest token of the middle is found digit by digit (11, 11 and 10 bits)
 // from histograms in shared memory; then every warp counts the tokens of its
 // share above it and equal to it, and, knowing the counts before its own, writes
 // its kept tokens in order. Bound by instructions, so keys are taken four at a
 // time (and read four at a time where the weights lie so, kVec = 4).
-template <bool kCached, int kVec>
-__global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(KCache kc, Table bt, const float* mass,
+template <int NT, bool kCached, int kVec>
+__global__ void __launch_bounds__(NT, 1536 / NT) evict_select_kernel(KCache kc, Table bt, const float* mass,
                                                                       int sinks, int recent, int keep, int* kept,
                                                                       int* new_lens, int* err) {
   extern __shared__ __align__(16) uint32_t s_key[];  // cached: the keys of the request's tokens
-  __shared__ uint32_t s_hist[kBins];
-  __shared__ uint32_t s_scan[kSelWarps];
+  __shared__ __align__(16) uint32_t s_hist[kBins];
+  __shared__ uint32_t s_scan[NT / 32];
   __shared__ uint32_t s_digit, s_left;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int h = blockIdx.x % kc.H, l = (blockIdx.x / kc.H) % kc.L, r = blockIdx.x / (kc.H * kc.L);
@@ -53,15 +51,15 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(KCache kc,
   int* out = kept + (long long)blockIdx.x * keep;
   const int n = min(T, keep);
   if (tid == 0 && l == 0 && h == 0 && new_lens) new_lens[r] = n;
-  for (int i = n + tid; i < keep; i += kSelThreads) out[i] = -1;
+  for (int i = n + tid; i < keep; i += NT) out[i] = -1;
   if (T <= keep) {
-    for (int i = tid; i < n; i += kSelThreads) out[i] = i;
+    for (int i = tid; i < n; i += NT) out[i] = i;
     return;
   }
   const int m0 = sinks, m1 = T - recent;  // the middle [m0, m1)
   const uint32_t want = (uint32_t)(keep - sinks - recent);
-  for (int i = tid; i < sinks; i += kSelThreads) out[i] = i;
-  for (int i = tid; i < recent; i += kSelThreads) out[keep - recent + i] = T - recent + i;
+  for (int i = tid; i < sinks; i += NT) out[i] = i;
+  for (int i = tid; i < recent; i += NT) out[keep - recent + i] = T - recent + i;
   if (want == 0) return;
   const float* mbase = mass + ((long long)l * kc.num_pages * kc.H + h) * bs;
   const long long page_stride = (long long)kc.H * bs;
@@ -71,11 +69,11 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(KCache kc,
     // cost two latencies a round.
     constexpr int U = kVec == 4 ? 4 : 8;
     const int row = bs / kVec;                                  // pieces of a block
-    const int per = row < kSelThreads ? kSelThreads / row : 1;  // blocks a turn
-    const int b0 = row < kSelThreads ? tid / row : 0, o0 = row < kSelThreads ? tid - b0 * row : tid;
+    const int per = row < NT ? NT / row : 1;  // blocks a turn
+    const int b0 = row < NT ? tid / row : 0, o0 = row < NT ? tid - b0 * row : tid;
     bool bad = false;
     if (b0 < per)
-      for (int o = o0; o < row; o += kSelThreads)
+      for (int o = o0; o < row; o += NT)
         for (int b = m0 / bs + b0; b < nb; b += per * U) {
           int page[U];
           float wt[U][kVec];
@@ -157,9 +155,9 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(KCache kc,
     const int bits = pass == 2 ? 10 : 11, bins = 1 << bits;
     const int up = shift;
     shift -= bits;
-    for (int i = tid; i < bins; i += kSelThreads) s_hist[i] = 0;
+    for (int i = tid; i < bins; i += NT) s_hist[i] = 0;
     __syncthreads();
-    for (int v = v0 + tid; v < v1; v += kSelThreads) {
+    for (int v = v0 + tid; v < v1; v += NT) {
       const Four f = four(v);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -168,12 +166,19 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(KCache kc,
     }
     __syncthreads();
     // from the top bin down: the bin in which the `left`-th key lies
-    constexpr int PER = kBins / kSelThreads;
-    const int per = bins / kSelThreads;
+    constexpr int PER = kBins / NT;  // a multiple of 4
     uint32_t c[PER], sum = 0;
+    const int low = bins - (tid + 1) * PER;  // the thread's bins, low + PER - 1 .. low
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (i < per) sum += c[i] = s_hist[bins - 1 - (tid * per + i)];
+    for (int i = 0; i < PER; i += 4) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (low >= 0) x = *reinterpret_cast<const uint4*>(&s_hist[low + PER - 4 - i]);
+      c[i] = x.w;
+      c[i + 1] = x.z;
+      c[i + 2] = x.y;
+      c[i + 3] = x.x;
+      sum += (x.x + x.y) + (x.z + x.w);
+    }
     uint32_t incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -186,9 +191,8 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(KCache kc,
     for (int x = 0; x < w; ++x) before += s_scan[x];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      if (i >= per) break;
       if (before < left && left <= before + c[i]) {
-        s_digit = (uint32_t)(bins - 1 - (tid * per + i));
+        s_digit = (uint32_t)(low + PER - 1 - i);
         s_left = left - before;
       }
       before += c[i];
@@ -200,9 +204,9 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(KCache kc,
   }
   // `prefix` is the threshold key; the first `left` tokens equal to it stay. Counts
   // are kept as (above, equal) halves of 64 bits.
-  const int seg = ((v1 - v0 + kSelWarps * 32 - 1) / (kSelWarps * 32)) * 32;  // a warp's share
+  const int seg = ((v1 - v0 + NT - 1) / NT) * 32;  // a warp's share
   const int a0 = min(v1, v0 + w * seg), a1 = min(v1, a0 + seg);
-  __shared__ unsigned long long s_before[kSelWarps];
+  __shared__ unsigned long long s_before[NT / 32];
   auto count = [&](const Four& f) {
     unsigned long long c = 0;
 #pragma unroll
@@ -422,14 +426,19 @@ cudaError_t launch_evict_select(const KCache& kc, const Table& bt, const float* 
   // 896 rows of 8192 tokens, us: kept in shared memory 44 (one key at a time 50), read again 105
   if (most <= kMaxCached) {
     const bool vec = kc.bs % 4 == 0 && reinterpret_cast<uintptr_t>(mass) % 16 == 0;
-    const auto k = vec ? evict_select_kernel<true, 4> : evict_select_kernel<true, 1>;
+    // Four warps a row where the steps between barriers are short, or where rows queue for an SM. 128 / 512
+    // threads, us: 7168 rows of 512 tokens 53 / 117, 896 of 512 12.5 / 18.7, 192 of 512 8.4 / 10.5, 896 of 4096 25 /
+    // 29, of 8192 50 / 41, 192 of 2048 12.5 / 10.5, 48 of 4096 15.6 / 10.4.
+    const int nt = most <= 1024 || (most <= 4096 && grid > 3 * sm_count()) ? 128 : 512;
+    const auto k = nt == 128 ? vec ? evict_select_kernel<128, true, 4> : evict_select_kernel<128, true, 1>
+                   : vec     ? evict_select_kernel<512, true, 4>
+                             : evict_select_kernel<512, true, 1>;
     const size_t smem = ((size_t)most + 3) / 4 * 16;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxCached * 4);
     if (e != cudaSuccess) return e;
-    k<<<grid, kSelThreads, smem, s>>>(kc, bt, mass, sinks, recent, keep, kept, new_lens, err);
+    k<<<grid, nt, smem, s>>>(kc, bt, mass, sinks, recent, keep, kept, new_lens, err);
   } else {
-    evict_select_kernel<false, 1>
-        <<<grid, kSelThreads, 0, s>>>(kc, bt, mass, sinks, recent, keep, kept, new_lens, err);
+    evict_select_kernel<512, false, 1><<<grid, 512, 0, s>>>(kc, bt, mass, sinks, recent, keep, kept, new_lens, err);
   }
   return cudaGetLastError();
 }
