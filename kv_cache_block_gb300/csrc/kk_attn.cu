@@ -287,7 +287,8 @@ cudaError_t combine_t(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
   const int M = pl.M;
   const int mt_max = a.mt_max;
   const long long items = (long long)a.bt.R * a.kc.H * mt_max;
-  // warps of a row: about four parts each when every CTA works on few items
+  // warps of a row: about four parts each when every CTA works on few items (one warp always: a million tokens
+  // 379 us instead of 346, 8 x 32768 77 instead of 73, one of 1031 14.8 instead of 12.6; 32 selections the same)
   int wpr = 1;
   while (wpr < 8 && pl.grid / items > 4 * wpr) wpr *= 2;
   const int rows = min(M, a.max_nodes * a.G), rpb = kCombineThreads / 32 / wpr;
