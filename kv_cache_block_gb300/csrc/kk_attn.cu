@@ -84,15 +84,17 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const Att
   const int tid = threadIdx.x;
   const int mt = blockIdx.x % mt_max, h = (blockIdx.x / mt_max) % a.kc.H, r = blockIdx.x / (mt_max * a.kc.H);
   const int rpb = kCombineThreads / 32 / wpr;  // rows of a block
-  if (blockIdx.y * rpb >= M) return;
   const Cut cut = find_cut<kCombineThreads>(a, r, h, mt, blockIdx.y * rpb, M, TK, tid);
+  // Every block waits, those with nothing to join too: what the stream or a graph
+  // runs next is ordered behind this kernel alone, and without a cut item nothing
+  // else here would keep it from ending before the main kernel does.
+  pdl_wait();
   const int parts = cut.n;
   if (parts == 0) return;
   const int grp = tid / L, ln = tid % L, gpr = NG / rpb;  // lane groups of a row
   const int row = mt * M + blockIdx.y * rpb + grp / gpr, gi = grp % gpr;
   const bool real = row < cut.rows;
   const int m = real ? row - mt * M : 0;
-  pdl_wait();
   float mm = -INFINITY, l = 0.f;
   float4 acc[V];
 #pragma unroll

@@ -1,0 +1,66 @@
+"""What a stream or a graph runs behind an attention call sees all of it, also
+when no item was cut and the join has nothing to add up: one 64-token tile an
+item, so the calls behind it are held back by the join's wait alone."""
+import numpy as np
+import pytest
+import torch
+
+from tests.attn_ref import Paged
+
+pytestmark = pytest.mark.gpu
+
+R, H, G, D, BS, K = 1500, 2, 7, 64, 16, 4
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_calls_behind_uncut_items(cuda, dtype):
+    """A graph: the table of one choice of blocks, attention over it, its weights, a copy of its result, then
+    the next choice's table into the same place. Every replay gives what separate, synchronised calls give."""
+    from kv_cache_block_gb300 import kk
+
+    rng = np.random.default_rng(3)
+    lens = [int(x) for x in rng.integers(BS * K, 300, R)]
+    pc = Paged(lens, H=H, D=D, bs=BS, L=1, dtype=dtype, seed=4, fill=0.0).to_gpu()
+    blocks = lambda start: torch.tensor([[start(t) + j for j in range(K)] for t in lens],  # noqa: E731
+                                        dtype=torch.int32).cuda()
+    first, last = blocks(lambda t: 0), blocks(lambda t: t // BS - K)
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn((R, H * G, D), generator=g).to(pc.tdt).cuda()
+    i32 = lambda *shape: torch.full(shape, -1, dtype=torch.int32, device="cuda")  # noqa: E731
+    pages, logical, count = i32(R, K), i32(R, K), i32(R)
+    sel = kk.Selection(pages, logical, count)
+    out, seen = torch.zeros_like(q), torch.zeros_like(q)
+    lse = torch.zeros((R, H * G), device="cuda")
+    mass = torch.zeros((1, pc.P, H, BS), device="cuda")
+    ws = torch.empty(kk.kk_tree_attn_workspace_bytes(pc.kd, pc.bt, 1, H * G), dtype=torch.uint8, device="cuda")
+    tree = kk.Tree(1)
+
+    def step(wait):
+        kk.kk_compact_table(first, pc.bt, pages, logical, count)
+        wait()
+        out.zero_()
+        lse.fill_(1e30)
+        wait()
+        kk.kk_tree_attn(pc.kd, pc.vd, pc.bt, 0, tree, q, 0.1, out, lse, sel=sel, workspace=ws)
+        wait()
+        kk.kk_compact_table(last, pc.bt, pages, logical, count)  # launched as a dependent of what is before it
+        wait()
+        seen.copy_(out)
+        kk.kk_attn_mass(pc.kd, pc.bt, 0, tree, q, 0.1, lse, None, mass)
+        wait()
+
+    step(torch.cuda.synchronize)
+    want, want_mass, want_lse = seen.clone(), mass.clone(), lse.clone()
+    assert torch.isfinite(want).all() and torch.isfinite(want_lse).all() and kk.kk_device_error() == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(lambda: None)
+    for _ in range(200):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(seen, want) and torch.equal(lse, want_lse) and torch.equal(mass, want_mass)
+    for _ in range(200):  # and as the stream orders them
+        step(lambda: None)
+        torch.cuda.synchronize()
+        assert torch.equal(seen, want) and torch.equal(lse, want_lse) and torch.equal(mass, want_mass)
+    assert kk.kk_device_error() == 0
