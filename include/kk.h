@@ -102,9 +102,13 @@ typedef struct kk_block_table {
  *   `box` of its first CTA (counted from 0 in that CTA's issue order), so the
  *   wait for that box runs out; -1 cancels. The request is used up by that
  *   launch. KK_ERR_INVALID for box < -1.
+ * kk_debug_skip_tile_copy: the same for tile `tile` of the Keys that the first
+ *   CTA of the next launch of a tensor-core kernel of kk_attn_mass loads.
+ *   KK_ERR_INVALID for tile < -1.
  */
 kk_status kk_debug_set_wait_limit(uint64_t ns);
 kk_status kk_debug_skip_pool_copy(int64_t box);
+kk_status kk_debug_skip_tile_copy(int64_t tile);
 
 /* Name of a status code (static string). */
 const char* kk_status_str(kk_status s);

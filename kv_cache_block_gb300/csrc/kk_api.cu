@@ -31,10 +31,11 @@ int* error_word() {
 
 kk_status from_cuda(cudaError_t e) { return e == cudaSuccess ? KK_OK : KK_ERR_CUDA; }
 
-// Limit of every bounded wait, and the one-shot request to leave a pool copy
-// out (failure-detection tests), both set by the diagnostic calls below.
+// Limit of every bounded wait, and the one-shot requests to leave a copy out
+// (failure-detection tests), set by the diagnostic calls below.
 std::atomic<unsigned long long> g_wait_ns{kk::kDefaultWaitNs};
 std::atomic<long long> g_skip_box{-1};
+std::atomic<long long> g_skip_tile{-1};
 
 bool dim_supported(int dtype, int D) {
   if (D != 32 && D != 64 && D != 128 && D != 256) return false;
@@ -110,6 +111,12 @@ kk_status kk_debug_set_wait_limit(uint64_t ns) {
 kk_status kk_debug_skip_pool_copy(int64_t box) {
   if (box < -1) return KK_ERR_INVALID;
   g_skip_box = (long long)box;
+  return KK_OK;
+}
+
+kk_status kk_debug_skip_tile_copy(int64_t tile) {
+  if (tile < -1) return KK_ERR_INVALID;
+  g_skip_tile = (long long)tile;
   return KK_OK;
 }
 
@@ -633,5 +640,6 @@ int* device_error_word() { return error_word(); }
 unsigned long long wait_limit_ns() { return g_wait_ns.load(); }
 
 long long take_skip_box() { return g_skip_box.exchange(-1); }
+long long take_skip_tile() { return g_skip_tile.exchange(-1); }
 
 }  // namespace kk

@@ -50,6 +50,7 @@ struct AttnArgs {
   const float* mass_in;
   float* mass_out;
   unsigned long long wait_ns;
+  long long skip_tile;  // failure-detection tests: CTA 0 leaves this Key tile uncopied (-1: none)
   int* err;
 };
 

@@ -670,8 +670,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++items;
       u += w.at.t1 - w.at.t0;
     }
-    // copies in flight end before the CTA does (on the ordinary way they were all waited for)
-    if (*stop && lane == 0) {
+    // Copies in flight end before the CTA does. All of them were waited for unless
+    // another role gives up, which it may do after this one has sent its last.
+    if (lane == 0) {
       for (uint32_t i = sent[0] > KS ? sent[0] - KS : 0; i < sent[0]; ++i)
         mbar_wait_bounded(&b.k_full[i % KS], (i / KS) & 1, a.wait_ns);
       for (uint32_t i = sent[1] > VS ? sent[1] - VS : 0; i < sent[1]; ++i)

@@ -193,9 +193,11 @@ int* device_error_word();
 // kk_api.cu: the limit of every bounded wait (kDefaultWaitNs unless a
 // diagnostic call set another), and a one-shot request, for failure-detection
 // tests, that the next persistent pool launch leave TMA box `box` of its first
-// CTA uncopied (-1: none; taking it clears it).
+// CTA uncopied (-1: none; taking it clears it); the same for a Key tile of the
+// tensor-core kernels over a paged cache.
 unsigned long long wait_limit_ns();
 long long take_skip_box();
+long long take_skip_tile();
 
 // kk_attn.cu: attention of drafted nodes over the paged cache (AttnArgs:
 // kk_attn.cuh). The workspace holds the partial results of the grid's CTAs.

@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---- loader ----------------------------------------------------------------------
     const int npiece = kTK / tb;  // page pieces of a tile
+    const long long skip = blockIdx.x == 0 ? a.skip_tile : -1;
     uint32_t cnt = 0, sent = 0;
     bool alive = true;
     for (long long u = pl.u0; u < pl.u1 && alive;) {
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t pieces = __ballot_sync(kFull, on);
         if (elect_one()) mbar_arrive_expect_tx(&b.k_full[st], __popc(pieces) * tb * D * 2);
         __syncwarp();
-        for (int k = 0; k < npiece; ++k) {
+        for (int k = no == skip ? npiece : 0; k < npiece; ++k) {
           const int page = __shfl_sync(kFull, cur.page, k), tok = __shfl_sync(kFull, cur.tok, k);
           if (((pieces >> k) & 1u) && elect_one()) {
 #pragma unroll
@@ -386,8 +387,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       cnt += tiles;
       u += at.t1 - at.t0;
     }
-    // copies in flight end before the CTA does (on the ordinary way they were all waited for)
-    if (*stop && lane == 0)
+    // Copies in flight end before the CTA does. All of them were waited for unless
+    // another role gives up, which it may do after this one has sent its last.
+    if (lane == 0)
       for (uint32_t i = sent > (uint32_t)NS ? sent - NS : 0; i < sent; ++i)
         mbar_wait_bounded(&b.k_full[i % NS], (i / NS) & 1, a.wait_ns);
     __syncwarp();
@@ -421,6 +423,7 @@ cudaError_t go(AttnArgs a, cudaStream_t s) {
     const int pad = (std::min(rows - b, max_rows<D>()) + 15) & ~15;
     const int ns = std::min(kStagesMax, (kSmemMax - pad * D * 2) / (128 * D * 2));
     const int smem = ns * 128 * D * 2 + pad * D * 2 + 1024;
+    a.skip_tile = take_skip_tile();
     k<<<a.grid, kThreads, smem, s>>>(tk, a, tb, b, b + max_rows<D>(), pad, ns);
     e = cudaGetLastError();
   }

@@ -88,6 +88,7 @@ def _load():
         "kk_status_str": (ctypes.c_char_p, [ctypes.c_int]),
         "kk_debug_set_wait_limit": (ctypes.c_int, [ctypes.c_uint64]),
         "kk_debug_skip_pool_copy": (ctypes.c_int, [I64]),
+        "kk_debug_skip_tile_copy": (ctypes.c_int, [I64]),
         "kk_device_error": (ctypes.c_int, [P, ctypes.POINTER(I32)]),
         "kk_pool_blocks": (ctypes.c_int, [KC, P, P, I32, P, I32, P, P, P]),
         "kk_head_variance_workspace_bytes": (SZ, [KC, I32, I32]),
@@ -133,7 +134,8 @@ _lib = _load()
 
 #: the C entry points declared in include/kk.h
 EXPORTS = (
-    "kk_status_str", "kk_device_error", "kk_debug_set_wait_limit", "kk_debug_skip_pool_copy", "kk_pool_blocks", "kk_head_variance_workspace_bytes",
+    "kk_status_str", "kk_device_error", "kk_debug_set_wait_limit", "kk_debug_skip_pool_copy", "kk_debug_skip_tile_copy",
+    "kk_pool_blocks", "kk_head_variance_workspace_bytes",
     "kk_head_variance", "kk_pool_blocks_weighted", "kk_pool_blocks_weighted_static", "kk_anchor", "kk_score", "kk_topk",
     "kk_score_topk", "kk_select_step", "kk_score_topk_stable", "kk_select_step_stable",
     "kk_compact_table", "kk_append_tokens", "kk_anchor_ring_fill", "kk_select_step_workspace_bytes",
@@ -331,6 +333,11 @@ def kk_debug_set_wait_limit(ns: int):
 def kk_debug_skip_pool_copy(box: int):
     """The next persistent pool launch leaves TMA box ``box`` of its first CTA uncopied (-1 cancels)."""
     _check("kk_debug_skip_pool_copy", _lib.kk_debug_skip_pool_copy(int(box)))
+
+
+def kk_debug_skip_tile_copy(tile: int):
+    """The next launch of a tensor-core mass kernel leaves Key tile ``tile`` of its first CTA uncopied (-1 cancels)."""
+    _check("kk_debug_skip_tile_copy", _lib.kk_debug_skip_tile_copy(int(tile)))
 
 
 def kk_device_error(stream=None) -> int:
