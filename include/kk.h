@@ -103,7 +103,9 @@ typedef struct kk_block_table {
  *   wait for that box runs out; -1 cancels. The request is used up by that
  *   launch. KK_ERR_INVALID for box < -1.
  * kk_debug_skip_tile_copy: the same for tile `tile` of the Keys that the first
- *   CTA of the next launch of a tensor-core kernel of kk_attn_mass loads.
+ *   CTA of the next launch of a tensor-core kernel (kk_tree_attn on many rows,
+ *   kk_attn_mass) loads by TMA: its wait expects one copy of 16 bytes more than
+ *   is issued.
  *   KK_ERR_INVALID for tile < -1.
  */
 kk_status kk_debug_set_wait_limit(uint64_t ns);

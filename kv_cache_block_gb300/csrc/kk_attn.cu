@@ -183,7 +183,11 @@ __global__ void __launch_bounds__(kTcCombineThreads * groups)
   const bool real = mt < rq.mt && row < rq.n * a.G;
   pdl_wait();
   const int4 cut = a.cuts[blockIdx.x];
-  if (mt >= rq.mt || cut.z == cut.x) return;  // the block as one: no such item, or one written whole
+  // the block as one: no such item, or one written whole
+  if (mt >= rq.mt || cut.z == cut.x) return;
+  // A CTA that gave up a wait leaves the notes of its last items unwritten, and the
+  // workspace held anything before: what is no possible note is not followed.
+  if (cut.x < 0 || cut.z < cut.x || cut.z >= a.grid || (cut.y & ~1)) return;
   // a single's streams leave a part each, M/2 rows apart
   const int sh = mt >= rq.mt - rq.odd, parts = real ? (cut.z - cut.x + 1) << sh : 0;
   auto slot = [&](int i) { return partial_slot(a, cut.x + (i >> sh), i >> sh ? 0 : cut.y, M, D); };

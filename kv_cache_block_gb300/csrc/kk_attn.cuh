@@ -50,7 +50,7 @@ struct AttnArgs {
   const float* mass_in;
   float* mass_out;
   unsigned long long wait_ns;
-  long long skip_tile;  // failure-detection tests: CTA 0 leaves this Key tile uncopied (-1: none)
+  long long skip_tile;  // failure-detection tests: CTA 0 waits for 16 bytes more than this Key tile has (-1: none)
   int* err;
 };
 

@@ -506,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int npiece = kTK / tb;  // page pieces of a tile
     uint32_t cnt = 0, items = 0, sent[2] = {0, 0};  // tiles and items before; tiles of K and V sent
     const Split split = make_split(pl.total, a.grid);
+    const uint32_t skip = blockIdx.x == 0 ? (uint32_t)a.skip_tile : ~0u;
     bool alive = true;
     // Where a tile's pieces lie: a piece is a run of tb tokens in one page (tb
     // divides the block size).
@@ -586,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             note->draft = -1;
             mbar_arrive(noted);
           }
-          mbar_arrive_expect_tx(bar, C::kTile);
+          mbar_arrive_expect_tx(bar, C::kTile + (!val && no == skip ? 16 : 0));
         }
         __syncwarp();
         for (int k = 0; k < npiece; ++k) {
@@ -689,13 +690,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D>
-cudaError_t go(const AttnArgs& a, cudaStream_t s) {
+cudaError_t go(AttnArgs a, cudaStream_t s) {
   CUtensorMap tk, tv;
   const int tb = tile_piece(a.kc.bs, kTK);
   if (!encode_tile_map(a.kc, a.layer, tb, &tk) || !encode_tile_map(a.vc, a.layer, tb, &tv)) return cudaErrorNotSupported;
   const cudaError_t e =
       cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
+  a.skip_tile = take_skip_tile();
   attn_tc_kernel<D><<<a.grid, kThreads, Cfg<D>::kSmem, s>>>(tk, tv, a, tb);
   return cudaGetLastError();
 }

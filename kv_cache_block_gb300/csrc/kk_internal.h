@@ -194,7 +194,8 @@ int* device_error_word();
 // diagnostic call set another), and a one-shot request, for failure-detection
 // tests, that the next persistent pool launch leave TMA box `box` of its first
 // CTA uncopied (-1: none; taking it clears it); the same for a Key tile of the
-// tensor-core kernels over a paged cache.
+// tensor-core kernels over a paged cache, whose wait expects 16 bytes that no
+// copy brings (a branch around the copies cost the loader 4 % of a tree's time).
 unsigned long long wait_limit_ns();
 long long take_skip_box();
 long long take_skip_tile();

@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---- loader ----------------------------------------------------------------------
     const int npiece = kTK / tb;  // page pieces of a tile
-    const long long skip = blockIdx.x == 0 ? a.skip_tile : -1;
+    const uint32_t skip = blockIdx.x == 0 ? (uint32_t)a.skip_tile : ~0u;
     uint32_t cnt = 0, sent = 0;
     bool alive = true;
     for (long long u = pl.u0; u < pl.u1 && alive;) {
@@ -370,9 +370,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!alive) break;
         sent = no + 1;
         const uint32_t pieces = __ballot_sync(kFull, on);
-        if (elect_one()) mbar_arrive_expect_tx(&b.k_full[st], __popc(pieces) * tb * D * 2);
+        if (elect_one()) mbar_arrive_expect_tx(&b.k_full[st], __popc(pieces) * tb * D * 2 + (no == skip ? 16 : 0));
         __syncwarp();
-        for (int k = no == skip ? npiece : 0; k < npiece; ++k) {
+        for (int k = 0; k < npiece; ++k) {
           const int page = __shfl_sync(kFull, cur.page, k), tok = __shfl_sync(kFull, cur.tok, k);
           if (((pieces >> k) & 1u) && elect_one()) {
 #pragma unroll

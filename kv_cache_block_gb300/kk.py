@@ -336,7 +336,8 @@ def kk_debug_skip_pool_copy(box: int):
 
 
 def kk_debug_skip_tile_copy(tile: int):
-    """The next launch of a tensor-core mass kernel leaves Key tile ``tile`` of its first CTA uncopied (-1 cancels)."""
+    """The next launch of a tensor-core attention or mass kernel is one copy of Key tile ``tile`` short in
+    its first CTA (-1 cancels)."""
     _check("kk_debug_skip_tile_copy", _lib.kk_debug_skip_tile_copy(int(tile)))
 
 
