@@ -50,6 +50,10 @@ constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kLoadWarp = 10;
 constexpr int kTK = 128;
 constexpr int kMeta = 8;  // ring of per-tile notes from the loader to the softmax warps
+// Ring of per-item notes of drafted Values, more than the stages of V: with items of
+// one tile, V of the item VS items on needs only this item's last product, which is also
+// what lets its notes be read; V of the one after that waits for the read (o_empty).
+constexpr int kOdd = 8;
 constexpr int kTmemCols = 512;
 constexpr float kRise = 8.f;
 
@@ -133,7 +137,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* s_v = s_k + KS * C::kTile;
   __shared__ Bars b;
   __shared__ TileNote s_note[kMeta];
-  __shared__ int s_odd[4][kMaxNodes / kTK];  // by item: a drafted tile has a Value that is not finite
+  static_assert(kOdd > VS + 1);
+  __shared__ int s_odd[kOdd][kMaxNodes / kTK];  // by item: a drafted tile has a Value that is not finite
   __shared__ long long s_place[kThreads / 32 + 4];
   __shared__ uint32_t s_tmem;
   __shared__ int s_stop;
@@ -326,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       uint32_t odd = 0;
       for (int d = 0; d < kMaxNodes / kTK; ++d)
-        if ((dtile >> d) & 1u) odd |= s_odd[items & 3][d] ? 1u << d : 0u;
+        if ((dtile >> d) & 1u) odd |= s_odd[items % kOdd][d] ? 1u << d : 0u;
       // An item that is this CTA's alone is written out here; of a single one,
       // stream B first hands its part to stream A through the CTA's third slot.
       const bool whole = w.at.t0 == 0 && w.at.t1 == w.at.units;
@@ -643,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       hit = __any_sync(kFull, hit);
       if (lane == 0) {
         if (val) {
-          if (draft) s_odd[items & 3][t - w.rq.tiles_c] = hit;
+          if (draft) s_odd[items % kOdd][t - w.rq.tiles_c] = hit;
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k) note->live[k] = live[k];

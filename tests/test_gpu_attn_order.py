@@ -64,3 +64,33 @@ def test_calls_behind_uncut_items(cuda, dtype):
         torch.cuda.synchronize()
         assert torch.equal(seen, want) and torch.equal(lse, want_lse) and torch.equal(mass, want_mass)
     assert kk.kk_device_error() == 0
+
+
+@pytest.mark.parametrize("D,nodes,G", [(64, 19, 7), (64, 36, 7), (128, 19, 7)])
+def test_drafts_alone_and_not_finite(cuda, D, nodes, G):
+    """Many requests of drafts without cached tokens (but the first), one tile each, so that the loader runs several items
+    ahead: a Value that is not finite reaches the nodes of its own request that see it and no others."""
+    from kv_cache_block_gb300 import kk
+
+    n, H = 1200, 2
+    pc = Paged([1] + [0] * (n - 1), H=H, D=D, bs=BS, L=1, seed=1)
+    pc.bound = 64  # a loose bound of the tables' lengths: many rows on the tensor cores
+    pc.to_gpu()
+    g = torch.Generator().manual_seed(D + nodes)
+    x = torch.randn((n * nodes, H * G + 2 * H, D), generator=g).bfloat16()
+    q, k, v = x[:, :H * G], x[:, H * G:H * G + H], x[:, H * G + H:]
+    bad = torch.rand(n, generator=g) < 0.3
+    at = torch.arange(n) * nodes + nodes - 1  # the last node, which only it sees (causal)
+    v[at[bad], :, 5] = float("inf")
+    x = x.cuda()
+    q, k, v = x[:, :H * G], x[:, H * G:H * G + H], x[:, H * G + H:]
+    out = torch.empty((n * nodes, H * G, D), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(kk.kk_tree_attn_workspace_bytes(pc.kd, pc.bt, nodes, H * G), dtype=torch.uint8, device="cuda")
+    for _ in range(20):
+        out.zero_()
+        kk.kk_tree_attn(pc.kd, pc.vd, pc.bt, 0, kk.Tree(nodes, None, None, k, v), q, 0.1, out, workspace=ws)
+        inf = torch.isinf(out)
+        want = torch.zeros_like(inf)
+        want[at[bad].cuda(), :, 5] = True
+        assert torch.equal(inf, want) and not torch.isnan(out).any()
+    assert kk.kk_device_error() == 0
