@@ -362,8 +362,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(o_at + k * 32, o);
           tmem_wait_ld();
           if (mine) {
-            if (odd) {  // drafted Values that are not finite, for the nodes that see them
+            // Drafted Values that are not finite, for the nodes that see them; of a single
+            // item each stream's own half, since the other's may weigh nothing in the join.
+            if (odd) {
               for (int j = 0; j < w.rq.n; ++j) {
+                if (single && (j / 64 & 1) != x) continue;
                 if (!((odd >> (j / kTK)) & 1u) || !sees(a, w.rq, node, j)) continue;
                 const uint16_t* v = static_cast<const uint16_t*>(a.dv) + (w.rq.node0 + j) * a.dv_sn + w.at.h * a.dv_sh;
 #pragma unroll

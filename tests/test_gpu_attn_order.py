@@ -94,3 +94,36 @@ def test_drafts_alone_and_not_finite(cuda, D, nodes, G):
         want[at[bad].cuda(), :, 5] = True
         assert torch.equal(inf, want) and not torch.isnan(out).any()
     assert kk.kk_device_error() == 0
+
+
+@pytest.mark.parametrize("D,nodes,G,lens", [
+    (64, 16, 7, [1] + [0] * 1199),  # single row tiles: drafts alone, a whole item a request
+    (64, 100, 1, [1] + [0] * 1199),
+    (128, 18, 7, [513] * 300),  # whole items of several tiles
+    (128, 18, 7, [60000, 3]),  # cut items
+    (128, 16, 16, [30000, 40]),  # a pair of row tiles, cut
+])
+def test_infinite_drafts_are_infinite(cuda, D, nodes, G, lens):
+    """An infinite drafted Value makes the nodes that see it infinite, not NaN, whichever part holds it."""
+    from kv_cache_block_gb300 import kk
+
+    n, H = len(lens), 2
+    pc = Paged(lens, H=H, D=D, bs=BS, L=1, seed=1)
+    pc.bound = 64
+    pc.to_gpu()
+    g = torch.Generator().manual_seed(D + nodes)
+    x = torch.randn((n * nodes, H * G + 2 * H, D), generator=g).bfloat16()
+    first, last = torch.arange(n) * nodes + nodes // 2, torch.arange(n) * nodes + nodes - 1
+    x[first, H * G + H:, 5] = float("-inf")
+    x[last, H * G + H:, 9] = float("inf")
+    x = x.cuda()
+    q, k, v = x[:, :H * G], x[:, H * G:H * G + H], x[:, H * G + H:]
+    out = torch.zeros((n * nodes, H * G, D), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(kk.kk_tree_attn_workspace_bytes(pc.kd, pc.bt, nodes, H * G), dtype=torch.uint8, device="cuda")
+    kk.kk_tree_attn(pc.kd, pc.vd, pc.bt, 0, kk.Tree(nodes, None, None, k, v), q, 0.1, out, workspace=ws)
+    assert kk.kk_device_error() == 0
+    out = out.cpu().reshape(n, nodes, H * G, D)
+    assert torch.isneginf(out[:, nodes // 2:, :, 5]).all() and torch.isposinf(out[:, -1, :, 9]).all()
+    out[:, nodes // 2:, :, 5] = 0
+    out[:, -1, :, 9] = 0
+    assert torch.isfinite(out).all()
