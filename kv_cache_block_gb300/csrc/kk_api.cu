@@ -98,7 +98,15 @@ VarWorkspace carve(void* ws, int LH, int D, long long total_blocks) {
 
 namespace kk {
 kk_status check_kcache_desc(const kk_kcache_desc* kc, KCache* out) { return check_kcache(kc, out); }
-kk_status check_block_table(const kk_block_table* bt, Table* out) { return check_table(bt, true, out); }
+kk_status check_block_table(const kk_block_table* bt, Table* out) {
+  // no block in any table: the kernels of these calls read no page, so there need be none
+  if (bt && bt->max_blocks == 0 && !bt->pages) {
+    kk_block_table t = *bt;
+    t.pages = t.offsets;
+    return check_table(&t, true, out);
+  }
+  return check_table(bt, true, out);
+}
 }  // namespace kk
 
 extern "C" {

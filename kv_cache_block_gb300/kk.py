@@ -206,7 +206,7 @@ class BlockTable:
             _ptr(offsets, torch.int32, "offsets"),
             _ptr(seq_lens, torch.int32, "seq_lens") if seq_lens is not None else None,
             offsets.numel() - 1,
-            int(max_blocks),
+            int(max_blocks) if pages.numel() else 0,
         )
 
     @property

@@ -1,0 +1,31 @@
+"""Host checks of the attention, mass and eviction calls and of their binding
+beyond the plain refusals: no CUDA call is made (no GPU needed)."""
+import ctypes
+
+import pytest
+
+from tests.test_abi import _desc, _table
+from tests.test_attn_abi import _tree
+
+
+@pytest.fixture(scope="module")
+def kk():
+    from kv_cache_block_gb300 import kk as mod
+
+    return mod
+
+
+def test_tables_without_pages(kk):
+    """Pages may be missing where no table has a block, and only there."""
+    B, lib, d = ctypes.byref, kk._lib, _desc(kk)
+    none = kk.kk_block_table(None, 4096, 4096, 1, 0)
+    some = kk.kk_block_table(None, 4096, 4096, 1, 1)
+    assert lib.kk_tree_attn_workspace_bytes(B(d), B(none), 1, 14) > 0
+
+    def attn(t):  # no nodes: nothing is launched
+        return lib.kk_tree_attn(B(d), B(d), B(t), 0, None, B(_tree(kk, total_nodes=0)), None, 0, 0, 14, 0.1, None,
+                                None, None, 0, None)
+
+    assert attn(none) == kk.KK_OK and attn(some) == kk.KK_ERR_INVALID
+    assert attn(kk.kk_block_table(None, None, 4096, 1, 0)) == kk.KK_ERR_INVALID
+    assert attn(kk.kk_block_table(None, 4096, None, 1, 0)) == kk.KK_ERR_INVALID

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.attn_ref import Paged
+from tests.attn_ref import Paged, attn_ref, check
 
 pytestmark = pytest.mark.gpu
 
@@ -127,3 +127,31 @@ def test_infinite_drafts_are_infinite(cuda, D, nodes, G, lens):
     out[:, nodes // 2:, :, 5] = 0
     out[:, -1, :, 9] = 0
     assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_no_request_has_a_token_yet(cuda, dtype):
+    """Empty tables, whose tensor of pages has no address: drafts see one another, the rest has nothing to do."""
+    from kv_cache_block_gb300 import kk
+
+    pc = Paged([0, 0, 0], H=H, D=D, bs=BS, L=1, dtype=dtype).to_gpu()
+    assert pc.bt.pages.numel() == 0
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn((3 * 5, H * G + 2 * H, D), generator=g).to(pc.tdt)
+    parts = lambda y: (y[:, :H * G], y[:, H * G:H * G + H], y[:, H * G + H:])  # noqa: E731
+    (q, k, v), (qg, kg, vg) = parts(x), parts(x.cuda())
+    ws = torch.empty(kk.kk_tree_attn_workspace_bytes(pc.kd, pc.bt, 5, H * G), dtype=torch.uint8, device="cuda")
+    out, lse = torch.ones(q.shape, dtype=q.dtype, device="cuda"), torch.ones(q.shape[:2], device="cuda")
+    kk.kk_tree_attn(pc.kd, pc.vd, pc.bt, 0, kk.Tree(5, None, None, kg, vg), qg, 0.1, out, lse, workspace=ws)
+    ref = attn_ref(pc, 0, [0, 5, 10, 15], q, 0.1, G, k, v)
+    check(out, ref[0], ref[2], "out")
+    check(lse, ref[1], ref[3], "lse")
+    kk.kk_tree_attn(pc.kd, pc.vd, pc.bt, 0, kk.Tree(5), qg, 0.1, out, lse, workspace=ws)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    mass = torch.ones((1, pc.P, H, BS), device="cuda")
+    kk.kk_attn_mass(pc.kd, pc.bt, 0, kk.Tree(5), qg, 0.1, lse, mass, mass)
+    kept, new = torch.ones((3, 1, H, 7), dtype=torch.int32, device="cuda"), torch.ones(3, dtype=torch.int32, device="cuda")
+    kk.kk_evict_select(pc.kd, pc.bt, mass, 1, 1, kept, new)
+    kk.kk_evict_compact(pc.kd, pc.vd, pc.bt, kept, mass, mass)
+    assert (mass == 1).all() and (kept == -1).all() and (new == 0).all()
+    assert kk.kk_device_error() == 0
