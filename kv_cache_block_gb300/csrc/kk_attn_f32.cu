@@ -12,10 +12,10 @@
 // Which of eight contracted positions holds which dim (or token) does not matter
 // as long as both operands agree: it is chosen so that a lane reads 16 bytes of
 // a row at once, and so that the scores' registers are the next product's.
-// Measured, groups of 7, D = 64: one node, 8 x 8192 tokens and 2 heads (67 MB) 33
+// Measured, groups of 7, D = 64: one node, 8 x 8192 tokens and 2 heads (67 MB) 35
 // us; 8 nodes, 2 x 4096 tokens 26 us, of which the main kernel 22, half its issue
-// slots busy; on the CUDA cores 44 (8 nodes). 40 nodes, 8 x 8192: 28 TF/s of
-// products (84 of tf32 instructions'), bound by the issue of cuts and products.
+// slots busy; on the CUDA cores 44 (8 nodes). 40 nodes, 8 x 8192: 26 TF/s of
+// products (78 of tf32 instructions'), bound by the issue of cuts and products.
 #include "kk_attn_ring.cuh"
 #include "kk_pdl.cuh"
 
@@ -41,11 +41,18 @@ __device__ __forceinline__ Halves split(float x) {
   h.lo = tf32_of(x - __uint_as_float(h.hi));
   return h;
 }
+// Whether x has no two halves: what tf32 rounds to infinity, infinities, NaN.
+__device__ __forceinline__ bool no_halves(float x) { return (__float_as_uint(x) & 0x7FFFFFFFu) >= 0x7F7FF000u; }
 __device__ __forceinline__ void mma1688(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The first half of a query's value: what would round to infinity is cut off
+// instead, so that both halves together are the value, also for whole_dot.
+__device__ __forceinline__ float query_half(float x) {
+  return isfinite(x) && no_halves(x) ? __uint_as_float(__float_as_uint(x) & 0xFFFFE000u) : __uint_as_float(tf32_of(x));
 }
 // Byte offset of 16-byte piece c of row `row`: pieces are exchanged so that the
 // rows 2q, 2q+1 (scores) and the rows of one parity (weights) that eight lanes
@@ -138,10 +145,10 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
       if (m < rows)
         x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + (rq.node0 + row / a.G) * a.q_sn +
                                              (long long)(h * a.G + row % a.G) * a.q_sh + c * 4);
-      const float4 y = make_float4(__uint_as_float(tf32_of(x.x)), __uint_as_float(tf32_of(x.y)),
-                                   __uint_as_float(tf32_of(x.z)), __uint_as_float(tf32_of(x.w)));
+      const float4 y = make_float4(query_half(x.x), query_half(x.y), query_half(x.z), query_half(x.w));
       *reinterpret_cast<float4*>(qh + swz<D>(m, c)) = y;
-      *reinterpret_cast<float4*>(ql + swz<D>(m, c)) = make_float4(x.x - y.x, x.y - y.y, x.z - y.z, x.w - y.w);
+      *reinterpret_cast<float4*>(ql + swz<D>(m, c)) = make_float4(isinf(x.x) ? 0.f : x.x - y.x, isinf(x.y) ? 0.f : x.y - y.y,
+                                                                  isinf(x.z) ? 0.f : x.z - y.z, isinf(x.w) ? 0.f : x.w - y.w);
     }
     __syncthreads();
 
@@ -173,21 +180,6 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
       const uint32_t live = s_ok[w][st];
       const bool draft = t >= rq.tiles_c;
       const int j0 = (t - rq.tiles_c) * kTK + w * kTok;  // a drafted tile's first node
-      bool odd = false;
-      if (draft) {
-        // A drafted Value that is not finite must not meet the zero weights of
-        // the nodes that do not see it: it is taken out here and given to the
-        // nodes that do after the products.
-#pragma unroll 1
-        for (int i = lane; i < kTok * D; i += 32) {
-          uint32_t* x = reinterpret_cast<uint32_t*>(vst) + i;
-          if ((*x & 0x7F800000u) == 0x7F800000u) {
-            *x = 0;
-            odd = true;
-          }
-        }
-        odd = __any_sync(kFull, odd);
-      }
       // scores of 8 tokens; the three kinds of product in sums of their own while
       // registers allow, three chains instead of one
       constexpr int NCH = MR <= 2 ? 3 : 1;
@@ -225,8 +217,8 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           s[mr][e] = NCH == 1 ? c3[0][mr][e] : (c3[0][mr][e] + c3[NCH / 2][mr][e]) + c3[NCH - 1][mr][e];
-      // An infinite Key has no low half (infinity less itself): its scores, NaN
-      // here, are formed again from the whole values.
+      // A Key without halves (infinite, or rounded to infinity) and an infinite query
+      // leave NaN here: the scores are formed again from the whole values.
       bool nan = false;
 #pragma unroll
       for (int mr = 0; mr < MR; ++mr)
@@ -282,6 +274,45 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
             o[mr][n][3] *= al[mr][1];
           }
       }
+      // Values without halves (too large for tf32, infinite, NaN) are given to the rows
+      // that see them here, and 0 stands for them in the products. A NaN alone among
+      // cached tokens, which all rows see, goes the ordinary way. Looking for them
+      // costs 0 to 6 % (64 dims, 40 nodes 341 -> 363 us).
+      float top = 0.f;
+      bool bad = false;
+#pragma unroll
+      for (int blk = 0; blk < D / 32; ++blk)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float4 v = f4(vst + swz<D>(q4 * 2 + k, blk * 8 + g));
+          top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+          if (draft) bad |= v.x != v.x || v.y != v.y || v.z != v.z || v.w != v.w;
+        }
+      if (__any_sync(kFull, bad || no_halves(top))) {
+#pragma unroll 1
+        for (int k = 0; k < kTok; ++k) {
+          float* x = reinterpret_cast<float*>(vst + k * D * 4);  // the token's row, its pieces in their own order
+#pragma unroll
+          for (int mr = 0; mr < MR; ++mr)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const int row = row0 + mr * 16 + hf * 8 + g;
+              const float p = __shfl_sync(kFull, k & 1 ? s[mr][hf * 2 + 1] : s[mr][hf * 2], (lane & ~3) | k >> 1);
+              const bool sure = row < rq.n * a.G && (!draft || (j0 + k < rq.n && sees(a, rq, row / a.G, j0 + k)));
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float y = x[(swz<D>(k, n / 4 * 8 + q4 * 2 + e) - k * D * 4) / 4 + n % 4];
+                  if (sure && no_halves(y)) o[mr][n][hf * 2 + e] += isfinite(y) ? p * y : y;
+                }
+            }
+          __syncwarp();
+          for (int i = lane; i < D; i += 32)
+            if (no_halves(x[i])) x[i] = 0.f;
+        }
+        __syncwarp();
+      }
       // Position q4 of the contraction is token 2 q4, position q4 + 4 token 2 q4 + 1
       uint32_t ph[MR][4], pw[MR][4];
 #pragma unroll
@@ -303,24 +334,6 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
             for (int mr = 0; mr < MR; ++mr)
               mma1688(o[mr][blk * 4 + j], k == 0 ? pw[mr] : ph[mr], k == 1 ? b0[j].lo : b0[j].hi,
                       k == 1 ? b1[j].lo : b1[j].hi);
-      }
-      if (odd) {  // drafts that are not finite, for the nodes that see them
-        for (int k = 0; k < kTok && j0 + k < rq.n; ++k)
-#pragma unroll
-          for (int mr = 0; mr < MR; ++mr)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const int row = row0 + mr * 16 + hf * 8 + g;
-              if (row >= rq.n * a.G || !sees(a, rq, row / a.G, j0 + k)) continue;
-              const float* v = static_cast<const float*>(a.dv) + (rq.node0 + j0 + k) * a.dv_sn + h * a.dv_sh;
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const float x = v[n / 4 * 32 + (q4 * 2 + e) * 4 + n % 4];
-                  if ((__float_as_uint(x) & 0x7F800000u) == 0x7F800000u) o[mr][n][hf * 2 + e] += x;
-                }
-            }
       }
       __syncwarp();
       st = st == kStages - 1 ? 0 : st + 1;
