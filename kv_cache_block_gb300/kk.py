@@ -266,7 +266,8 @@ class Tree:
             self.c.v, self.c.v_stride_node, self.c.v_stride_head = _strided(v, "v")
 
     def bind(self, kc, q):
-        """The C struct for queries ``q`` [nodes][query heads][D]."""
+        """A C struct for queries ``q`` [nodes][query heads][D], this call's own: calls of other threads
+        may share the tree."""
         n = q.shape[0]
         for t, name in ((self.mask, "mask"), (self.k, "k"), (self.v, "v")):
             if t is not None and t.shape[0] < n:
@@ -276,8 +277,9 @@ class Tree:
                 _check_elems(kc, t, name)
                 if t.shape[1] != kc.num_kv_heads:
                     raise ValueError(f"{name} has {t.shape[1]} heads, the cache {kc.num_kv_heads}")
-        self.c.total_nodes = n
-        return ctypes.byref(self.c)
+        c = kk_tree.from_buffer_copy(self.c)
+        c.total_nodes = n
+        return ctypes.byref(c)
 
 
 class Selection:

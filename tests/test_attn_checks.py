@@ -29,3 +29,14 @@ def test_tables_without_pages(kk):
     assert attn(none) == kk.KK_OK and attn(some) == kk.KK_ERR_INVALID
     assert attn(kk.kk_block_table(None, None, 4096, 1, 0)) == kk.KK_ERR_INVALID
     assert attn(kk.kk_block_table(None, 4096, None, 1, 0)) == kk.KK_ERR_INVALID
+
+
+def test_a_tree_serves_several_calls_at_once(kk):
+    """Each call has a struct of its own: binding other queries does not change one that is under way."""
+    import torch
+
+    tree, desc = kk.Tree(4), _desc(kk)
+    first = tree.bind(desc, torch.zeros(8, 14, 128, dtype=torch.bfloat16))
+    second = tree.bind(desc, torch.zeros(400, 14, 128, dtype=torch.bfloat16))
+    assert first._obj.total_nodes == 8 and second._obj.total_nodes == 400
+    assert first._obj.max_nodes == second._obj.max_nodes == 4
