@@ -265,10 +265,12 @@ class Tree:
             self.c.k, self.c.k_stride_node, self.c.k_stride_head = _strided(k, "k")
             self.c.v, self.c.v_stride_node, self.c.v_stride_head = _strided(v, "v")
 
-    def bind(self, kc, q):
-        """A C struct for queries ``q`` [nodes][query heads][D], this call's own: calls of other threads
-        may share the tree."""
+    def bind(self, kc, q, bt):
+        """A C struct for queries ``q`` [nodes][query heads][D] of the requests of ``bt``, this call's own:
+        calls of other threads may share the tree."""
         n = q.shape[0]
+        if self.node_offsets is not None and self.node_offsets.numel() != bt.num_requests + 1:
+            raise ValueError(f"node_offsets must have {bt.num_requests + 1} elements")
         for t, name in ((self.mask, "mask"), (self.k, "k"), (self.v, "v")):
             if t is not None and t.shape[0] < n:
                 raise ValueError(f"{name} has fewer rows than q")
@@ -550,17 +552,18 @@ def kk_tree_attn(kc, vc, bt: BlockTable, layer: int, tree: Tree, q, scale: float
     """Attention of the nodes of ``tree`` over layer ``layer`` of the cache (``sel``: a :class:`Selection`
     of its blocks). ``q``: [nodes][query heads][D] (may be strided), ``out`` the same shape, contiguous."""
     _check_elems(kc, q, "q")
-    qp, qn, qh = _strided(q, "q")
     if out.shape != q.shape or out.element_size() != q.element_size():
         raise ValueError("out must have q's shape and type")
     if lse is not None and lse.numel() != q.shape[0] * q.shape[1]:
         raise ValueError("lse must be [nodes][query heads]")
     if sel is not None and sel.pages.shape[0] != bt.num_requests:
         raise ValueError("the selection has another number of requests than the table")
+    nodes = tree.bind(kc, q, bt)
+    qp, qn, qh = _strided(q, "q")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("kk_tree_attn", _lib.kk_tree_attn(
         ctypes.byref(kc), ctypes.byref(vc), ctypes.byref(bt.c), layer, None if sel is None else ctypes.byref(sel.c),
-        tree.bind(kc, q), qp, qn, qh, q.shape[1], float(scale), _ptr(out, name="out"),
+        nodes, qp, qn, qh, q.shape[1], float(scale), _ptr(out, name="out"),
         _ptr(lse, torch.float32, "lse"), _ptr(workspace, name="workspace"), ws_bytes, _stream(stream)))
 
 
@@ -575,13 +578,14 @@ def kk_attn_mass(kc, bt: BlockTable, layer: int, tree: Tree, q, scale: float, ls
                  row_lens=None, old_lens=None, decay: float = 1.0, stream=None):
     """Adds the weight every cached token received from the nodes to ``mass_in`` (may be ``mass_out``)."""
     _check_elems(kc, q, "q")
-    qp, qn, qh = _strided(q, "q")
     for t, name, n in ((lse, "lse", q.shape[0] * q.shape[1]), (row_w, "row_w", q.shape[0]),
                        (row_lens, "row_lens", q.shape[0]), (old_lens, "old_lens", bt.num_requests)):
         if t is not None and t.numel() != n:
             raise ValueError(f"{name} must have {n} elements")
+    nodes = tree.bind(kc, q, bt)
+    qp, qn, qh = _strided(q, "q")
     _check("kk_attn_mass", _lib.kk_attn_mass(
-        ctypes.byref(kc), ctypes.byref(bt.c), layer, tree.bind(kc, q), qp, qn, qh, q.shape[1], float(scale),
+        ctypes.byref(kc), ctypes.byref(bt.c), layer, nodes, qp, qn, qh, q.shape[1], float(scale),
         _ptr(lse, torch.float32, "lse"), _ptr(row_w, torch.float32, "row_w"),
         _ptr(row_lens, torch.int32, "row_lens"), _ptr(old_lens, torch.int32, "old_lens"), float(decay),
         _mass_ptr(kc, mass_in, "mass_in"), _mass_ptr(kc, mass_out, "mass_out"), _stream(stream)))
@@ -594,7 +598,9 @@ def _kept_ptr(kc, bt, kept):
 
 
 def kk_evict_select(kc, bt: BlockTable, mass, sinks: int, recent: int, kept, new_lens=None, stream=None):
-    """``kept``: int32 [R][layers][KV heads][keep]."""
+    """``kept``: int32 [R][layers][KV heads][keep]; ``new_lens``: int32 [R], not the table's own lengths."""
+    if new_lens is not None and new_lens.numel() != bt.num_requests:
+        raise ValueError(f"new_lens must have {bt.num_requests} elements")
     _check("kk_evict_select", _lib.kk_evict_select(
         ctypes.byref(kc), ctypes.byref(bt.c), _mass_ptr(kc, mass, "mass"), sinks, recent, kept.shape[-1],
         _kept_ptr(kc, bt, kept), _ptr(new_lens, torch.int32, "new_lens"), _stream(stream)))

@@ -1,6 +1,7 @@
 """Host checks of the attention, mass and eviction calls and of their binding
 beyond the plain refusals: no CUDA call is made (no GPU needed)."""
 import ctypes
+import types
 
 import pytest
 
@@ -35,8 +36,27 @@ def test_a_tree_serves_several_calls_at_once(kk):
     """Each call has a struct of its own: binding other queries does not change one that is under way."""
     import torch
 
-    tree, desc = kk.Tree(4), _desc(kk)
-    first = tree.bind(desc, torch.zeros(8, 14, 128, dtype=torch.bfloat16))
-    second = tree.bind(desc, torch.zeros(400, 14, 128, dtype=torch.bfloat16))
+    tree, desc, bt = kk.Tree(4), _desc(kk), types.SimpleNamespace(num_requests=2)
+    first = tree.bind(desc, torch.zeros(8, 14, 128, dtype=torch.bfloat16), bt)
+    second = tree.bind(desc, torch.zeros(400, 14, 128, dtype=torch.bfloat16), bt)
     assert first._obj.total_nodes == 8 and second._obj.total_nodes == 400
     assert first._obj.max_nodes == second._obj.max_nodes == 4
+
+
+def test_sizes_by_request(kk):
+    """What the kernels index by request has to be that long."""
+    import torch
+
+    desc, bt = _desc(kk), types.SimpleNamespace(num_requests=3, c=_table(kk, R=3))
+    q = torch.zeros(6, 14, 128, dtype=torch.bfloat16)
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
+    tree = kk.Tree(2)
+    for n in (3, 5):
+        tree.node_offsets = i32(n)
+        with pytest.raises(ValueError, match="node_offsets must have 4"):
+            kk.kk_tree_attn(desc, desc, bt, 0, tree, q, 0.1, torch.zeros_like(q))
+        with pytest.raises(ValueError, match="node_offsets must have 4"):
+            kk.kk_attn_mass(desc, bt, 0, tree, q, 0.1, torch.zeros(6, 14), None, torch.zeros(2, 8, 2, 16))
+    for n in (0, 2, 4):
+        with pytest.raises(ValueError, match="new_lens must have 3"):
+            kk.kk_evict_select(desc, bt, torch.zeros(2, 8, 2, 16), 0, 0, i32(3, 2, 2, 4), i32(n))
