@@ -552,8 +552,9 @@ def kk_tree_attn(kc, vc, bt: BlockTable, layer: int, tree: Tree, q, scale: float
     """Attention of the nodes of ``tree`` over layer ``layer`` of the cache (``sel``: a :class:`Selection`
     of its blocks). ``q``: [nodes][query heads][D] (may be strided), ``out`` the same shape, contiguous."""
     _check_elems(kc, q, "q")
-    if out.shape != q.shape or out.element_size() != q.element_size():
-        raise ValueError("out must have q's shape and type")
+    _check_elems(kc, out, "out")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
     if lse is not None and lse.numel() != q.shape[0] * q.shape[1]:
         raise ValueError("lse must be [nodes][query heads]")
     if sel is not None and sel.pages.shape[0] != bt.num_requests:

@@ -60,3 +60,19 @@ def test_sizes_by_request(kk):
     for n in (0, 2, 4):
         with pytest.raises(ValueError, match="new_lens must have 3"):
             kk.kk_evict_select(desc, bt, torch.zeros(2, 8, 2, 16), 0, 0, i32(3, 2, 2, 4), i32(n))
+
+
+def test_output_has_the_caches_type(kk):
+    """A float16 result is as wide as bf16, but its bits would be read as other numbers."""
+    import torch
+
+    desc, bt, tree = _desc(kk), types.SimpleNamespace(num_requests=3, c=_table(kk, R=3)), kk.Tree(2)
+    q = torch.zeros(6, 14, 128, dtype=torch.bfloat16)
+    for dt in (torch.float16, torch.float32, torch.uint16):
+        with pytest.raises(TypeError, match="out has dtype"):
+            kk.kk_tree_attn(desc, desc, bt, 0, tree, q, 0.1, torch.zeros(6, 14, 128, dtype=dt))
+    with pytest.raises(ValueError, match="out must have q's shape"):
+        kk.kk_tree_attn(desc, desc, bt, 0, tree, q, 0.1, torch.zeros(6, 7, 128, dtype=torch.bfloat16))
+    f32 = _desc(kk, dtype=kk.KK_F32)
+    with pytest.raises(TypeError, match="out has dtype"):
+        kk.kk_tree_attn(f32, f32, bt, 0, tree, q.float(), 0.1, torch.zeros(6, 14, 128, dtype=torch.int32))
