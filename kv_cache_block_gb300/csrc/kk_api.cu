@@ -99,6 +99,9 @@ VarWorkspace carve(void* ws, int LH, int D, long long total_blocks) {
 namespace kk {
 kk_status check_kcache_desc(const kk_kcache_desc* kc, KCache* out) { return check_kcache(kc, out); }
 kk_status check_block_table(const kk_block_table* bt, Table* out) {
+  if (bt && (reinterpret_cast<uintptr_t>(bt->pages) | reinterpret_cast<uintptr_t>(bt->offsets) |
+             reinterpret_cast<uintptr_t>(bt->seq_lens)) % 4)
+    return KK_ERR_UNSUPPORTED;
   // no block in any table: the kernels of these calls read no page, so there need be none
   if (bt && bt->max_blocks == 0 && !bt->pages) {
     kk_block_table t = *bt;

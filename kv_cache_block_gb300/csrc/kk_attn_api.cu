@@ -41,7 +41,7 @@ kk_status common_args(const kk_kcache_desc* kc, const kk_block_table* bt, int32_
     if (!q) return KK_ERR_INVALID;
     if (!rows_ok(q, q_sn, q_sh, es)) return KK_ERR_UNSUPPORTED;
   }
-  if ((long long)tree->max_nodes * Hq > (1 << 20)) return KK_ERR_UNSUPPORTED;
+  if ((long long)tree->max_nodes * Hq > (1 << 20) || !aligned(tree->node_offsets, 4)) return KK_ERR_UNSUPPORTED;
   a->layer = layer;
   a->node_off = tree->node_offsets;
   a->max_nodes = tree->max_nodes;
@@ -101,6 +101,7 @@ kk_status kk_tree_attn(const kk_kcache_desc* kc, const kk_kcache_desc* vc, const
   }
   if (sel) {
     if (!sel->pages || !sel->logical || !sel->count || sel->K < 1) return KK_ERR_INVALID;
+    if (!aligned(sel->pages, 4) || !aligned(sel->logical, 4) || !aligned(sel->count, 4)) return KK_ERR_UNSUPPORTED;
     a.sel_pages = sel->pages;
     a.sel_logical = sel->logical;
     a.sel_count = sel->count;
@@ -129,7 +130,9 @@ kk_status kk_attn_mass(const kk_kcache_desc* kc, const kk_block_table* bt, int32
   if (!std::isfinite(decay)) return KK_ERR_INVALID;
   if (a.bt.R == 0) return KK_OK;
   if (!mass_out || (a.total_nodes > 0 && !lse)) return KK_ERR_INVALID;
-  if (!aligned(mass_in, 4) || !aligned(mass_out, 4) || !aligned(lse, 4)) return KK_ERR_UNSUPPORTED;
+  if (!aligned(mass_in, 4) || !aligned(mass_out, 4) || !aligned(lse, 4) || !aligned(row_w, 4) ||
+      !aligned(row_lens, 4) || !aligned(old_lens, 4))
+    return KK_ERR_UNSUPPORTED;
   a.lse = const_cast<float*>(lse);
   a.row_w = row_w;
   a.row_lens = row_lens;
@@ -160,7 +163,7 @@ kk_status kk_evict_select(const kk_kcache_desc* kc, const kk_block_table* bt, co
   if (sinks < 0 || recent < 0 || (long long)sinks + recent > keep) return KK_ERR_INVALID;
   if (t.R == 0) return KK_OK;
   if (!mass || !kept) return KK_ERR_INVALID;
-  if (!aligned(mass, 4) || !aligned(kept, 4)) return KK_ERR_UNSUPPORTED;
+  if (!aligned(mass, 4) || !aligned(kept, 4) || !aligned(new_lens, 4)) return KK_ERR_UNSUPPORTED;
   int* err = kk::device_error_word();
   if (!err) return KK_ERR_CUDA;
   return done(kk::launch_evict_select(c, t, mass, sinks, recent, keep, kept, new_lens, err, stream));

@@ -76,3 +76,30 @@ def test_output_has_the_caches_type(kk):
     f32 = _desc(kk, dtype=kk.KK_F32)
     with pytest.raises(TypeError, match="out has dtype"):
         kk.kk_tree_attn(f32, f32, bt, 0, tree, q.float(), 0.1, torch.zeros(6, 14, 128, dtype=torch.int32))
+
+
+def test_arrays_off_their_boundaries(kk):
+    """An integer or float array off its 4-byte boundary would fault in the kernels: it is refused."""
+    B, lib, d, t, UNS = ctypes.byref, kk._lib, _desc(kk), _table(kk), kk.KK_ERR_UNSUPPORTED
+    n = lib.kk_tree_attn_workspace_bytes(B(d), B(t), 4, 14)
+
+    def attn(bt=t, tree=None, sel=None):
+        return lib.kk_tree_attn(B(d), B(d), B(bt), 0, None if sel is None else B(sel), B(tree or _tree(kk)), 4096, 1792,
+                                128, 14, 0.1, 4096, None, 4096, n, None)
+
+    assert attn(tree=_tree(kk, node_offsets=4098)) == UNS
+    for bad in ((4097, 4096, 4096), (4096, 4098, 4096), (4096, 4096, 4099)):
+        assert attn(sel=kk.kk_selection(*bad, 4)) == UNS
+        assert attn(bt=kk.kk_block_table(*bad, 1, 4)) == UNS
+
+    def mass(tree=None, w=None, lens=None, old=None, bt=t):
+        return lib.kk_attn_mass(B(d), B(bt), 0, B(tree or _tree(kk)), 4096, 1792, 128, 14, 0.1, 4096, w, lens, old, 1.0,
+                                None, 4096, None)
+
+    assert mass(tree=_tree(kk, node_offsets=4099)) == UNS and mass(w=4098) == UNS
+    assert mass(lens=4097) == UNS and mass(old=4098) == UNS
+    assert mass(bt=kk.kk_block_table(4098, 4096, 4096, 1, 4)) == UNS
+    assert lib.kk_evict_select(B(d), B(t), 4096, 1, 2, 4, 4096, 4098, None) == UNS
+    bad = kk.kk_block_table(4096, 4096, 4098, 1, 4)
+    assert lib.kk_evict_select(B(d), B(bad), 4096, 1, 2, 4, 4096, None, None) == UNS
+    assert lib.kk_evict_compact(B(d), None, B(bad), 4096, 4, None, None, None, None) == UNS
