@@ -591,7 +591,8 @@ kk_status kk_attn_mass(const kk_kcache_desc* kc, const kk_block_table* bt, int32
  * weight (mass as kk_attn_mass writes it; equal weights to the lower index,
  * -0 equals +0, NaN below everything). kept: device int32 [R][L][H][keep],
  * token indices in ascending order, -1 past min(keep, seq_lens[r]), which also
- * goes to new_lens[r] (nullable device int32 [R]). keep >= 1, sinks >= 0,
+ * goes to new_lens[r] (nullable device int32 [R], apart from bt->seq_lens:
+ * KK_ERR_INVALID). keep >= 1, sinks >= 0,
  * recent >= 0, sinks + recent <= keep. kc gives the sizes (its base is not
  * read).
  */

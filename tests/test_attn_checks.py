@@ -103,3 +103,11 @@ def test_arrays_off_their_boundaries(kk):
     bad = kk.kk_block_table(4096, 4096, 4098, 1, 4)
     assert lib.kk_evict_select(B(d), B(bad), 4096, 1, 2, 4, 4096, None, None) == UNS
     assert lib.kk_evict_compact(B(d), None, B(bad), 4096, 4, None, None, None, None) == UNS
+
+
+def test_new_lengths_apart_from_the_old(kk):
+    """Written over the table's own lengths, the new ones would be read as the old by other CTAs."""
+    B, lib, d = ctypes.byref, kk._lib, _desc(kk)
+    t = kk.kk_block_table(4096, 4096, 8192, 3, 4)
+    for new in (8192, 8192 - 8, 8192 + 8):
+        assert lib.kk_evict_select(B(d), B(t), 4096, 1, 2, 4, 4096, new, None) == kk.KK_ERR_INVALID
