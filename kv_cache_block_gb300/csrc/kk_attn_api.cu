@@ -164,10 +164,10 @@ kk_status kk_evict_select(const kk_kcache_desc* kc, const kk_block_table* bt, co
   if (sinks < 0 || recent < 0 || (long long)sinks + recent > keep) return KK_ERR_INVALID;
   if (t.R == 0) return KK_OK;
   if (!mass || !kept) return KK_ERR_INVALID;
+  if (!aligned(mass, 4) || !aligned(kept, 4) || !aligned(new_lens, 4)) return KK_ERR_UNSUPPORTED;
   // other CTAs of a request still read its length when the first one writes the new one
   const intptr_t apart = reinterpret_cast<intptr_t>(new_lens) - reinterpret_cast<intptr_t>(t.seq_lens);
   if (new_lens && std::llabs(apart) < 4ll * t.R) return KK_ERR_INVALID;
-  if (!aligned(mass, 4) || !aligned(kept, 4) || !aligned(new_lens, 4)) return KK_ERR_UNSUPPORTED;
   int* err = kk::device_error_word();
   if (!err) return KK_ERR_CUDA;
   return done(kk::launch_evict_select(c, t, mass, sinks, recent, keep, kept, new_lens, err, stream));
