@@ -498,7 +498,8 @@ kk_status kk_coarse_means(const float* vb, int32_t D, int32_t num_pages, const k
  * of the tokens that received least. Values are a second paged cache (vc)
  * with the K cache's type, sizes and page ids; its strides may differ. A table
  * of requests that all have no token yet (max_blocks 0) needs no pages. Arrays
- * of integers and floats lie on 4-byte boundaries (KK_ERR_UNSUPPORTED).
+ * of integers and floats lie on 4-byte boundaries (KK_ERR_UNSUPPORTED). A
+ * request has at most 2^31 - 65536 tokens, selected slots or tokens to keep.
  */
 
 /*

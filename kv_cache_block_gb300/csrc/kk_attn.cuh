@@ -98,7 +98,7 @@ __device__ __forceinline__ AttnReq load_req(const AttnArgs& a, int r, int M, int
   q.off = a.bt.offsets[r];
   const int nb = a.bt.offsets[r + 1] - q.off;
   q.T = a.bt.seq_lens[r];
-  if (q.T < 0 || nb < 0 || nb > a.bt.max_blocks || nb != (int)(((unsigned)q.T + (unsigned)a.kc.bs - 1u) / (unsigned)a.kc.bs)) {
+  if (q.T < 0 || q.T > kMaxTokens || nb < 0 || nb > a.bt.max_blocks || nb != (int)(((unsigned)q.T + (unsigned)a.kc.bs - 1u) / (unsigned)a.kc.bs)) {
     ok = false;
     q.T = 0;
   }
@@ -107,7 +107,7 @@ __device__ __forceinline__ AttnReq load_req(const AttnArgs& a, int r, int M, int
     const int c = a.sel_count[r];
     if (c < 0 || c > a.selK) ok = false;
     ctx = (c < 0 || c > a.selK || q.T == 0) ? 0 : (long long)c * a.kc.bs;
-    if (ctx > 0x7FFFFF00ll) {
+    if (ctx > kMaxTokens) {
       ok = false;
       ctx = 0;
     }

@@ -151,7 +151,7 @@ static kk_status evict_args(const kk_kcache_desc* kc, const kk_block_table* bt, 
   if (st != KK_OK) return st;
   if ((st = kk::check_block_table(bt, t)) != KK_OK) return st;
   if (keep < 1) return KK_ERR_INVALID;
-  if ((long long)t->R * c->L * c->H > 0x7FFFFFFFll) return KK_ERR_UNSUPPORTED;
+  if ((long long)t->R * c->L * c->H > 0x7FFFFFFFll || keep > kk::kMaxTokens) return KK_ERR_UNSUPPORTED;
   return KK_OK;
 }
 

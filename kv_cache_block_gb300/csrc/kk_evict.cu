@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(NT, 1536 / NT) evict_select_kernel(KCache kc, 
   const int h = blockIdx.x % kc.H, l = (blockIdx.x / kc.H) % kc.L, r = blockIdx.x / (kc.H * kc.L);
   const int off = bt.offsets[r], nb = bt.offsets[r + 1] - off, bs = kc.bs;
   int T = bt.seq_lens[r];
-  if (T < 0 || nb < 0 || nb > bt.max_blocks || nb != (int)(((unsigned)T + (unsigned)bs - 1u) / (unsigned)bs)) {
+  if (T < 0 || T > kMaxTokens || nb < 0 || nb > bt.max_blocks || nb != (int)(((unsigned)T + (unsigned)bs - 1u) / (unsigned)bs)) {
     if (tid == 0) flag_error(err, kErrBadIndex);
     T = 0;
   }
@@ -274,7 +274,7 @@ __device__ __forceinline__ MoveRow move_row(const MoveArgs& a, int x, bool repor
   m.off = a.bt.offsets[m.r];
   const int nb = a.bt.offsets[m.r + 1] - m.off;
   m.T = a.bt.seq_lens[m.r];
-  m.ok = !(m.T < 0 || nb < 0 || nb > a.bt.max_blocks ||
+  m.ok = !(m.T < 0 || m.T > kMaxTokens || nb < 0 || nb > a.bt.max_blocks ||
            nb != (int)(((unsigned)m.T + (unsigned)a.kc.bs - 1u) / (unsigned)a.kc.bs));
   if (!m.ok && report) flag_error(a.err, kErrBadIndex);
   m.n = m.ok ? min(m.T, a.keep) : 0;

@@ -209,6 +209,8 @@ cudaError_t launch_tree_attn(AttnArgs a, cudaStream_t s);
 cudaError_t launch_attn_mass(const AttnArgs& a, cudaStream_t s);
 // kk_evict.cu: the tokens to keep by that weight, and their move
 constexpr int kMaxNodes = 256;  // drafted nodes of a request
+// Tokens of a request, at most: a tile, a chunk or a thread's step past the last one is still a 32-bit index.
+constexpr int kMaxTokens = 0x7FFF0000;
 cudaError_t launch_evict_select(const KCache& kc, const Table& bt, const float* mass, int sinks, int recent, int keep,
                                 int* kept, int* new_lens, int* err, cudaStream_t s);
 cudaError_t launch_evict_compact(const KCache& kc, const KCache& vc, const Table& bt, const int* kept, int keep,

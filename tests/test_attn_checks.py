@@ -111,3 +111,10 @@ def test_new_lengths_apart_from_the_old(kk):
     t = kk.kk_block_table(4096, 4096, 8192, 3, 4)
     for new in (8192, 8192 - 8, 8192 + 8):
         assert lib.kk_evict_select(B(d), B(t), 4096, 1, 2, 4, 4096, new, None) == kk.KK_ERR_INVALID
+
+
+def test_more_tokens_to_keep_than_a_request_has(kk):
+    B, lib, d, t = ctypes.byref, kk._lib, _desc(kk), _table(kk)
+    for keep in (2**31 - 65535, 2**31 - 1):
+        assert lib.kk_evict_select(B(d), B(t), 4096, 1, 2, keep, 4096, None, None) == kk.KK_ERR_UNSUPPORTED
+        assert lib.kk_evict_compact(B(d), None, B(t), 4096, keep, None, None, None, None) == kk.KK_ERR_UNSUPPORTED

@@ -1,0 +1,46 @@
+"""Requests near the 32-bit limit of token indices, and caches whose offsets pass 32 bits."""
+import pytest
+import torch
+
+from tests.attn_ref import Paged, attn_ref, check, mass_ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 32), ("bf16", 64), ("f32", 32)])
+@pytest.mark.parametrize("T", [2**31 - 1, 2**31 - 65535])
+def test_too_many_tokens_are_reported(cuda, dtype, D, T):
+    """A request past the limit (a table that names one page over and over) counts as without tokens; the
+    request next to it is served."""
+    from kv_cache_block_gb300 import kk
+
+    bs, P, nodes, G = 1 << 20, 1, 5, 7
+    pc = Paged([300], H=1, D=D, bs=bs, L=1, dtype=dtype, extra=0, fill=0.0).to_gpu()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    nb = (T + bs - 1) // bs
+    bt = kk.BlockTable(torch.zeros(nb + 1, dtype=torch.int32, device="cuda"), i32([0, nb, nb + 1]), i32([T, 300]), nb)
+    for n in (1, nodes):
+        q = torch.randn((2 * n, G, D), generator=torch.Generator().manual_seed(n)).to(pc.tdt)
+        out, lse = torch.ones(q.shape, dtype=q.dtype, device="cuda"), torch.ones(q.shape[:2], device="cuda")
+        ws = torch.empty(kk.kk_tree_attn_workspace_bytes(pc.kd, bt, n, G), dtype=torch.uint8, device="cuda")
+        kk.kk_tree_attn(pc.kd, pc.vd, bt, 0, kk.Tree(n), q.cuda(), 0.1, out, lse, workspace=ws)
+        assert kk.kk_device_error() == kk.KK_ERR_BAD_INDEX
+        ref = attn_ref(pc, 0, [0, n], q[n:], 0.1, G)
+        check(out[n:], ref[0], ref[2], "out")
+        check(lse[n:], ref[1], ref[3], "lse")
+        assert (out[:n] == 0).all()
+        mass = torch.full((1, P, 1, bs), -3.0, device="cuda")
+        kk.kk_attn_mass(pc.kd, bt, 0, kk.Tree(n), q.cuda(), 0.1, lse, None, mass)
+        assert kk.kk_device_error() == kk.KK_ERR_BAD_INDEX
+        want, tol = mass_ref(pc, 0, [0, n], q[n:], 0.1, G, lse[n:].cpu(), torch.zeros(1, P, 1, bs))
+        check(mass[..., :300], want[..., :300], tol[..., :300], "mass")
+        assert (mass[..., 300:] == -3.0).all()
+    kept, new = torch.full((2, 1, 1, 9), 5, dtype=torch.int32, device="cuda"), i32([7, 7])
+    kk.kk_evict_select(pc.kd, bt, torch.arange(bs, 0, -1, device="cuda").float().reshape(1, P, 1, bs), 0, 2, kept, new)
+    assert kk.kk_device_error() == kk.KK_ERR_BAD_INDEX
+    assert new.tolist() == [0, 9] and (kept[0] == -1).all()
+    assert kept[1, 0, 0].tolist() == [0, 1, 2, 3, 4, 5, 6, 298, 299]
+    kk.kk_evict_compact(pc.kd, pc.vd, bt, kept)
+    assert kk.kk_device_error() == kk.KK_ERR_BAD_INDEX
+    assert torch.equal(pc.gk[0, 0, 0, 7:9].cpu(), pc.k[0, 0, 0, 298:300])
+    assert torch.equal(pc.gk[0, 0, 0, 9:300].cpu(), pc.k[0, 0, 0, 9:300])
