@@ -8,6 +8,7 @@
 // us (29 MB read once: bound by instructions, 78 % of the issue slots, and by equal
 // weights meeting in one bin of a histogram), the move to new pages 287 us (1.87
 // GB, 6.6 TB/s), in place 378.
+#include <algorithm>
 #include <cmath>
 
 #include "kk_device.cuh"
@@ -259,6 +260,7 @@ struct MoveArgs {
   float* mass_out;
   const int* dst_pages;  // [R][dst_blocks], or null: the request's own pages
   int* err;
+  int items;  // rows of kept tokens: requests x layers x heads
 };
 
 // The sizes of the row of kept tokens that block x moves.
@@ -328,11 +330,13 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs
   constexpr int kRows = 8 * RI < 32 ? 8 * RI : 32;
   constexpr int U = kRows / RI;        // loads in flight, for K and for V each
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, sub = lane / P, c = lane % P * 16;
-  const MoveRow m = move_row(a, blockIdx.x, blockIdx.y == 0 && threadIdx.x == 0);
-  const int i0 = (blockIdx.y * (kMoveThreads / 32) + w) * kRows;
+  // the rows' first pieces, then their second ones, ... in one dimension of the grid, which has room for all
+  const int piece = blockIdx.x / a.items, item = blockIdx.x - piece * a.items;
+  const MoveRow m = move_row(a, item, piece == 0 && threadIdx.x == 0);
+  const int i0 = (piece * (kMoveThreads / 32) + w) * kRows;
   if (i0 >= m.n) return;
   const int es = a.kc.dtype == 1 ? 2 : 4;
-  const Move mv = lane < kRows ? move_at(a, m, a.kept + (long long)blockIdx.x * a.keep, i0 + lane) : Move{0, 0, 0, 0, false};
+  const Move mv = lane < kRows ? move_at(a, m, a.kept + (long long)item * a.keep, i0 + lane) : Move{0, 0, 0, 0, false};
   const uint32_t ok = __ballot_sync(kFull, mv.ok);
   const bool has_v = a.vc.base != nullptr;
   const long long ks = row_at(a.kc, m, mv.sp, mv.st, es), kd = row_at(a.kc, m, mv.dp, mv.dt, es);
@@ -410,10 +414,12 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const MoveA
 }
 
 template <int P>
-cudaError_t move_t(const MoveArgs& a, int items, cudaStream_t s) {
+cudaError_t move_t(const MoveArgs& a, long long most, cudaStream_t s) {
   constexpr int kRows = 8 * (32 / P) < 32 ? 8 * (32 / P) : 32;
   const int per = kMoveThreads / 32 * kRows;
-  evict_move_kernel<P><<<dim3((unsigned)items, (unsigned)((a.keep + per - 1) / per)), kMoveThreads, 0, s>>>(a);
+  const long long pieces = std::max((std::min<long long>(a.keep, most) + per - 1) / per, 1ll);  // one looks the tables over
+  if (pieces * a.items > 0x7FFFFFFFll) return cudaErrorNotSupported;
+  evict_move_kernel<P><<<(unsigned)(pieces * a.items), kMoveThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -446,13 +452,15 @@ cudaError_t launch_evict_select(const KCache& kc, const Table& bt, const float* 
 cudaError_t launch_evict_compact(const KCache& kc, const KCache& vc, const Table& bt, const int* kept, int keep,
                                  const float* mass_in, float* mass_out, const int* dst_pages, int* err,
                                  cudaStream_t s) {
-  const MoveArgs a{kc, vc, bt, kept, keep, (keep + kc.bs - 1) / kc.bs, mass_in, mass_out, dst_pages, err};
-  const int items = bt.R * kc.L * kc.H, P = kc.D * (kc.dtype == 1 ? 2 : 4) / 16;  // 16-byte pieces of a row
+  const int items = bt.R * kc.L * kc.H;
+  const MoveArgs a{kc, vc, bt, kept, keep, (keep - 1) / kc.bs + 1, mass_in, mass_out, dst_pages, err, items};
+  const int P = kc.D * (kc.dtype == 1 ? 2 : 4) / 16;  // 16-byte pieces of a row
+  const long long most = (long long)bt.max_blocks * kc.bs;  // tokens of a request
   if (dst_pages) switch (P) {
-      case 4: return move_t<4>(a, items, s);
-      case 8: return move_t<8>(a, items, s);
-      case 16: return move_t<16>(a, items, s);
-      case 32: return move_t<32>(a, items, s);
+      case 4: return move_t<4>(a, most, s);
+      case 8: return move_t<8>(a, most, s);
+      case 16: return move_t<16>(a, most, s);
+      case 32: return move_t<32>(a, most, s);
       default: return cudaErrorNotSupported;
     }
   // CTAs of a cluster: two, and up to eight when there are few rows. 2 / 4 / 8, us: 896 rows of 8192 tokens cut

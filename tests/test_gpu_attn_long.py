@@ -44,3 +44,28 @@ def test_too_many_tokens_are_reported(cuda, dtype, D, T):
     assert kk.kk_device_error() == kk.KK_ERR_BAD_INDEX
     assert torch.equal(pc.gk[0, 0, 0, 7:9].cpu(), pc.k[0, 0, 0, 298:300])
     assert torch.equal(pc.gk[0, 0, 0, 9:300].cpu(), pc.k[0, 0, 0, 9:300])
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 256), ("f32", 128), ("bf16", 128)])
+def test_moves_of_millions_of_tokens(cuda, dtype, D):
+    """More tokens to keep than 65535 groups of a block's rows; the source table names one page over and over."""
+    from kv_cache_block_gb300 import kk
+
+    bs, keep = 1 << 16, 65535 * 64 + 5001
+    kept = torch.arange(keep, dtype=torch.int32, device="cuda")
+    kept += kept // 64
+    T = int(kept[-1]) + 3
+    nb, nd = (T + bs - 1) // bs, (keep + bs - 1) // bs
+    tdt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    k = torch.zeros((1, 1 + nd, 1, bs, D), dtype=tdt, device="cuda")
+    k[0, 0].normal_(generator=torch.Generator("cuda").manual_seed(1))
+    kd = kk.kcache_desc(k, kk.KK_BF16 if dtype == "bf16" else kk.KK_F32, 1, 1, D, bs, 1 + nd, k.stride()[:4])
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    bt = kk.BlockTable(torch.zeros(nb, dtype=torch.int32, device="cuda"), i32([0, nb]), i32([T]), nb)
+    dst = torch.arange(1, 1 + nd, dtype=torch.int32, device="cuda").reshape(1, nd)
+    kk.kk_evict_compact(kd, None, bt, kept.reshape(1, 1, 1, keep), dst_pages=dst)
+    assert kk.kk_device_error() == 0
+    for i in range(nd):
+        part = kept[i * bs:(i + 1) * bs].long() % bs
+        assert torch.equal(k[0, 1 + i, 0, :len(part)], k[0, 0, 0][part])
+    assert not k[0, nd, 0, keep - (nd - 1) * bs:].any()
