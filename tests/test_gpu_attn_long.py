@@ -69,3 +69,67 @@ def test_moves_of_millions_of_tokens(cuda, dtype, D):
         part = kept[i * bs:(i + 1) * bs].long() % bs
         assert torch.equal(k[0, 1 + i, 0, :len(part)], k[0, 0, 0][part])
     assert not k[0, nd, 0, keep - (nd - 1) * bs:].any()
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+def test_offsets_past_32_bits(cuda, dtype, D):
+    """Pages and layers more than 2^32 elements apart: every kernel of every call reaches them."""
+    from kv_cache_block_gb300 import kk
+
+    H, bs, G, P, L = 2, 16, 7, 3, 2
+    tdt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    page, layer = 2**30 + 64, 2**31 + 2**30 + 256  # element strides
+    size = (L - 1) * layer + (P - 1) * page + H * bs * D
+    pc = Paged([40], H=H, D=D, bs=bs, L=L, dtype=dtype, extra=0, seed=D, fill=0.0)
+    store = [torch.empty(size, dtype=tdt, device="cuda") for _ in range(2)]
+    far = [x.as_strided((L, P, H, bs, D), (layer, page, bs * D, D, 1)) for x in store]
+    for x, y in zip(far, (pc.k, pc.v)):
+        x.copy_(y)
+    code = kk.KK_BF16 if dtype == "bf16" else kk.KK_F32
+    kd, vd = (kk.kcache_desc(x, code, L, H, D, bs, P, x.stride()[:4]) for x in far)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    for nodes, bound in ((1, 3), (40, 3), (40, 1 << 16)):  # each kernel of the type
+        bt = kk.BlockTable(pc.pages.cuda(), i32([0, 3]), i32([40]), bound)
+        q = torch.randn((nodes, H * G, D), generator=torch.Generator().manual_seed(nodes)).to(tdt)
+        out, lse = torch.ones(q.shape, dtype=tdt, device="cuda"), torch.ones(q.shape[:2], device="cuda")
+        ws = torch.empty(kk.kk_tree_attn_workspace_bytes(kd, bt, nodes, H * G), dtype=torch.uint8, device="cuda")
+        kk.kk_tree_attn(kd, vd, bt, 1, kk.Tree(nodes), q.cuda(), 0.1, out, lse, workspace=ws)
+        ref = attn_ref(pc, 1, [0, nodes], q, 0.1, G)
+        check(out, ref[0], ref[2], "out")
+        check(lse, ref[1], ref[3], "lse")
+        mass = torch.zeros((L, P, H, bs), device="cuda")
+        kk.kk_attn_mass(kd, bt, 1, kk.Tree(nodes), q.cuda(), 0.1, lse, None, mass)
+        want, tol = mass_ref(pc, 1, [0, nodes], q, 0.1, G, lse.cpu(), torch.zeros(L, P, H, bs))
+        check(mass, want, tol, "mass")
+    kept = torch.arange(0, 40, 3, dtype=torch.int32).expand(1, L, H, 14).contiguous()
+    want = [x.clone() for x in (pc.k, pc.v)]
+    for i, t in enumerate(range(0, 40, 3)):
+        for w, x in zip(want, (pc.k, pc.v)):
+            w[:, int(pc.pages[i // bs]), :, i % bs] = x[:, int(pc.pages[t // bs]), :, t % bs]
+    kk.kk_evict_compact(kd, vd, bt, kept.cuda())
+    assert kk.kk_device_error() == 0
+    assert all(torch.equal(x.cpu(), w) for x, w in zip(far, want))
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("bf16", 32), ("f32", 64)])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30, 2.5])
+@pytest.mark.parametrize("nodes,bound", [(1, 40), (20, 40), (20, 1 << 16)])
+def test_scales(cuda, dtype, D, scale, nodes, bound):
+    """Weights that are all equal (scale 0 or nearly), of the other sign, and nearly one-hot."""
+    from kv_cache_block_gb300 import kk
+
+    G = 7
+    pc = Paged([600, 33], H=1, D=D, bs=16, L=1, dtype=dtype, seed=D)
+    pc.bound = bound
+    pc.to_gpu()
+    x = torch.randn((2 * nodes, G + 2, D), generator=torch.Generator().manual_seed(nodes)).to(pc.tdt)
+    q, k, v = x[:, :G], x[:, G:G + 1], x[:, G + 1:]
+    y = x.cuda()
+    out, lse = torch.ones(q.shape, dtype=pc.tdt, device="cuda"), torch.ones(q.shape[:2], device="cuda")
+    ws = torch.empty(kk.kk_tree_attn_workspace_bytes(pc.kd, pc.bt, nodes, G), dtype=torch.uint8, device="cuda")
+    kk.kk_tree_attn(pc.kd, pc.vd, pc.bt, 0, kk.Tree(nodes, None, None, y[:, G:G + 1], y[:, G + 1:]), y[:, :G], scale, out,
+                    lse, workspace=ws)
+    assert kk.kk_device_error() == 0
+    ref = attn_ref(pc, 0, [0, nodes, 2 * nodes], q, scale, G, k, v)
+    check(out, ref[0], ref[2], "out")
+    check(lse, ref[1], ref[3], "lse")
