@@ -180,12 +180,11 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
       const uint32_t live = s_ok[w][st];
       const bool draft = t >= rq.tiles_c;
       const int j0 = (t - rq.tiles_c) * kTK + w * kTok;  // a drafted tile's first node
-      // scores of 8 tokens; the three kinds of product in sums of their own while
-      // registers allow, three chains instead of one
-      constexpr int NCH = MR <= 2 ? 3 : 1;
-      float s[MR][4], c3[NCH][MR][4];
+      // scores of 8 tokens; the three kinds of product in sums of their own, three
+      // chains instead of one
+      float s[MR][4], c3[3][MR][4];
 #pragma unroll
-      for (int x = 0; x < NCH; ++x)
+      for (int x = 0; x < 3; ++x)
 #pragma unroll
         for (int mr = 0; mr < MR; ++mr)
 #pragma unroll
@@ -207,8 +206,8 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             mma1688(c3[0][mr], al[x], b[2 * x].hi, b[2 * x + 1].hi);
-            mma1688(c3[NCH / 2][mr], ah[x], b[2 * x].lo, b[2 * x + 1].lo);
-            mma1688(c3[NCH - 1][mr], ah[x], b[2 * x].hi, b[2 * x + 1].hi);
+            mma1688(c3[1][mr], ah[x], b[2 * x].lo, b[2 * x + 1].lo);
+            mma1688(c3[2][mr], ah[x], b[2 * x].hi, b[2 * x + 1].hi);
           }
         }
       }
@@ -216,7 +215,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
       for (int mr = 0; mr < MR; ++mr)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          s[mr][e] = NCH == 1 ? c3[0][mr][e] : (c3[0][mr][e] + c3[NCH / 2][mr][e]) + c3[NCH - 1][mr][e];
+          s[mr][e] = (c3[0][mr][e] + c3[1][mr][e]) + c3[2][mr][e];
       // A Key without halves (infinite, or rounded to infinity) and an infinite query
       // leave NaN here: the scores are formed again from the whole values.
       bool nan = false;
