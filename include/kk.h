@@ -607,8 +607,9 @@ kk_status kk_evict_select(const kk_kcache_desc* kc, const kk_block_table* bt, co
  * same). Slot i is in block i / block_size of dst_pages[r] (device int32
  * [R][ceil(keep / block_size)]; pages of no table of the call, and of no other
  * request), or, with dst_pages NULL, of the request's own table: in place, for
- * which kept must ascend in every row, as kk_evict_select writes it. Other
- * slots keep what they held. The order of the tokens stays, so the last W
+ * which kept must ascend in every row, as kk_evict_select writes it, and no page
+ * may be in two requests' tables (a shared prefix would be moved for each).
+ * Other slots keep what they held. The order of the tokens stays, so the last W
  * slots are still the newest tokens as long as W <= recent. The caller then
  * shortens its table to ceil(new_lens[r] / block_size) blocks (and pools them
  * again: v_b of a compacted block is kk_pool_blocks').
