@@ -13,7 +13,7 @@
 // as long as both operands agree: it is chosen so that a lane reads 16 bytes of
 // a row at once, and so that the scores' registers are the next product's.
 // Measured, groups of 7, D = 64: one node, 8 x 8192 tokens and 2 heads (67 MB) 35
-// us; 8 nodes, 2 x 4096 tokens 26 us, of which the main kernel 22, half its issue
+// us; 8 nodes, 2 x 4096 tokens 27 us, of which the main kernel 22, half its issue
 // slots busy; on the CUDA cores 44 (8 nodes). 40 nodes, 8 x 8192: 26 TF/s of
 // products (78 of tf32 instructions'), bound by the issue of cuts and products.
 #include "kk_attn_ring.cuh"

@@ -9,9 +9,9 @@
 // no barrier between warps until the item ends, so loads never wait for a
 // neighbour. Two CTAs of three stages hold 128 KB in flight per SM at D = 128.
 // Measured, D = 128, groups of 7, one node: 8 requests of up to 32768 tokens (378
-// MB of K and V) 72 us with the join, 5.2 TB/s; a million tokens in pages of 16
-// (2.1 GB) 341 us, 6.3 TB/s; 64 selected blocks of 128 tokens for each of 32
-// requests (533 MB) 98 us, 5.4 TB/s. What is left: about 12 us of starting, first
+// MB of K and V) 73 us with the join, 5.2 TB/s; a million tokens in pages of 16
+// (2.1 GB) 343 us, 6.3 TB/s; 64 selected blocks of 128 tokens for each of 32
+// requests (533 MB) 99 us, 5.4 TB/s. What is left: about 12 us of starting, first
 // loads and join, and 230 registers, which hold an SM to two CTAs (72 % of DRAM's
 // cycles busy, the instruction stream a third).
 #include "kk_attn_ring.cuh"

@@ -27,12 +27,12 @@
 // copied by the loader's lanes, zeros for what is not there: a weight of zero
 // must not meet what such a place holds.
 //
-// Measured, D = 128, groups of 7: 8 requests of 32768 tokens and 64 nodes 212 us,
-// 1.14 PF/s (36 nodes 1.04, groups of 8 and 64 nodes 1.27: whole row tiles);
-// lengths from a tenth of that up and 1 to 64 nodes, 162 us for 125 GF and 384 MB.
+// Measured, D = 128, groups of 7: 8 requests of 32768 tokens and 64 nodes 214 us,
+// 1.12 PF/s (36 nodes 1.01, groups of 8 and 64 nodes 1.25: whole row tiles);
+// lengths from half of that up and 32 to 64 nodes, 164 us for 125 GF and 384 MB.
 // The tensor cores are busy 53 % of the time: a step of 64 tokens takes both
 // streams about 1900 cycles for 1280 of products, the rest is one thread waiting
-// for barriers and issuing 24 instructions; 518 MB come from DRAM (1.28 GB from
+// for barriers and issuing 24 instructions; 520 MB come from DRAM (1.28 GB from
 // L2), 77 % of a copy's time for them. A call costs about 20 us before its first
 // and after its last step (places, queries, the join).
 #include <cuda.h>
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // CTAs of the first pair have in hand then (a single, which does two tiles a
     // unit, those of two CTAs): K and V come from DRAM once, and from L2 for the
     // other row tiles (with every CTA in its own order the 64-node batch read 654 MB,
-    // in this one 518; once each would be 384).
+    // in this one 520; once each would be 384).
     int rot = 0, half = 0;  // rotation; tiles of the first of two runs (0: one run)
     auto place = [&](const Work& w, long long u) {
       const int units = w.at.single ? (w.tiles + 1) / 2 : w.tiles;
