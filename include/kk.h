@@ -46,10 +46,12 @@ typedef enum kk_status {
   KK_ERR_UNSUPPORTED = 2, /* valid but not handled: head_dim, alignment, strides */
   KK_ERR_CUDA = 3,        /* a CUDA runtime call or launch failed */
   KK_ERR_BAD_INDEX = 4,   /* (device) a page id, weight-set id or block table entry out of range */
-  KK_ERR_TIMEOUT = 5      /* (device) a bounded wait gave up */
+  KK_ERR_TIMEOUT = 5,     /* (device) a bounded wait gave up */
+  KK_ERR_NO_PAGES = 6     /* (device) no free page was left */
 } kk_status;
 
-typedef enum kk_dtype { KK_F32 = 0, KK_BF16 = 1 } kk_dtype;
+/* KK_E4M3 caches are read and written by the calls of the 8-bit cache below alone. */
+typedef enum kk_dtype { KK_F32 = 0, KK_BF16 = 1, KK_E4M3 = 2 } kk_dtype;
 
 /*
  * Paged K cache layout [KK §1] (fixed-size token blocks managed as pages).
@@ -617,6 +619,178 @@ kk_status kk_evict_select(const kk_kcache_desc* kc, const kk_block_table* bt, co
 kk_status kk_evict_compact(const kk_kcache_desc* kc, const kk_kcache_desc* vc, const kk_block_table* bt,
                            const int32_t* kept, int32_t keep, const float* mass_in, float* mass_out,
                            const int32_t* dst_pages, cudaStream_t stream);
+
+/*
+ * ---- around a serving step: queries and Keys made ready, an 8-bit cache, pages ----
+ */
+
+/* Rows [node][head][D] of a tensor: head h of node i at base + i*stride_node +
+ * h*stride_head (elements; 16-byte aligned, strides not negative and multiples of
+ * 16 bytes), of layer l l*stride_layer further (kk_kv8_write alone). */
+typedef struct kk_rows {
+  void* base; /* device */
+  int64_t stride_node, stride_head, stride_layer;
+} kk_rows;
+
+/*
+ * Rotation of the first rotary_dim dims of a head (a multiple of 16, at most
+ * head_dim; 0: none) in pairs (i, i + rotary_dim/2), or (2i, 2i + 1) when
+ * interleaved: pair (a, b) at position p becomes (a c - b s, b c + a s) with c =
+ * scale * cos(p * inv_freq[i]), s = scale * sin(p * inv_freq[i]) (inv_freq:
+ * device float [rotary_dim/2], finite). The angle is exact in inv_freq's float32
+ * values however far the position is, up to the rounding of its sine and cosine.
+ */
+typedef struct kk_rope {
+  const float* inv_freq;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  float scale;
+} kk_rope;
+
+/*
+ * kk_qk_norm_rope - queries and Keys made ready for attention in one pass: each
+ * head x of q and of k is normed with its weights (nullable device [D] of the
+ * tensors' type; NULL: no norm),
+ *   y = x * (mean x^2 + eps)^(-1/2) * weight,
+ * then rotated (rope nullable), in float32 and rounded once. Node i's position
+ * is positions[i] (nullable device int32 [num_nodes]; NULL: its position in the
+ * cache when bt is given, else i). Normed and rotated queries go to q_out, Keys to k_out
+ * (nullable) and, with kc, bt, into the cache (and the Values v, as they are,
+ * with vc): the nodes token_offsets[r] .. token_offsets[r+1] (device int32
+ * [R+1]; NULL: one node each) are the last tokens of request r, which
+ * seq_lens[r] counts and whose blocks the table holds already (as
+ * kk_append_tokens). Every page that receives tokens belongs to one request
+ * alone. q (nullable with num_q_heads 0), k (nullable with num_kv_heads 0) and v
+ * are read; q_out may be q and k_out k (the same address and strides), other
+ * outputs overlap no input. dtype: KK_BF16 or KK_F32, the caches' too. D is 32,
+ * 64, 128 or 256. A request whose table disagrees with seq_lens or holds a bad
+ * page, or with more nodes than tokens, is reported through the device error
+ * word, and its nodes are not written to the cache; without positions their
+ * position is 0.
+ */
+kk_status kk_qk_norm_rope(int32_t dtype, int32_t num_nodes, int32_t num_q_heads, int32_t num_kv_heads, int32_t D,
+                          const kk_rows* q, const kk_rows* k, const kk_rows* v, const void* q_weight,
+                          const void* k_weight, float eps, const int32_t* positions, const kk_rope* rope,
+                          const kk_rows* q_out, const kk_rows* k_out, const kk_kcache_desc* kc,
+                          const kk_kcache_desc* vc, const kk_block_table* bt, const int32_t* token_offsets,
+                          int32_t layer, cudaStream_t stream);
+
+/*
+ * The 8-bit cache: kk_kcache_desc with dtype KK_E4M3 (one byte an element; base
+ * and strides multiples of 16 bytes, head_dim 32, 64, 128 or 256) holds codes,
+ * and a scale for each block of tokens and head holds what they stand for:
+ *   K[l,p,h,t,d] = code[l,p,h,t,d] * k_scale[l][p][h]
+ * (device float [num_layers][num_pages][num_kv_heads]), Values the same with
+ * v_scale. Codes are e4m3 (4 exponent and 3 mantissa bits, largest 448, no
+ * infinity, NaN 0x7F and 0xFF).
+ *
+ * kk_kv8_write - new tokens written into it. The nodes token_offsets[r] ..
+ * token_offsets[r+1] (device int32 [R+1]; NULL: max_new nodes each, in order; at
+ * most max_new a request, num_nodes in all) are the last tokens of request r, as
+ * in kk_qk_norm_rope, with their Keys and Values at rows k and v of type dtype
+ * (KK_BF16 or KK_F32), for every layer of [layer, layer + num_layers). In each
+ * page they reach, the scale of a (layer, head) becomes
+ *   max(the scale so far, 2^e),  2^e the smallest power of two with amax / 448 <= 2^e, at least 2^-126
+ * (amax: the largest finite magnitude of the page's new tokens; the scale so
+ * far: 0 when the page held no older token of the request). New codes are value
+ * / scale rounded to nearest even; the page's older codes are multiplied by old
+ * scale / new scale and rounded, which is exact but for results below 2^-6 (a
+ * power of two changes no mantissa). What is not finite becomes NaN. Nothing
+ * behind a request's last token is written. No page may be in two requests'
+ * tables. k or v may be NULL with its cache NULL (Keys or Values alone).
+ */
+kk_status kk_kv8_write(const kk_kcache_desc* kc, float* k_scale, const kk_kcache_desc* vc, float* v_scale,
+                       const kk_block_table* bt, int32_t layer, int32_t num_layers, int32_t dtype, const kk_rows* k,
+                       const kk_rows* v, const int32_t* token_offsets, int32_t max_new, int32_t num_nodes,
+                       cudaStream_t stream);
+
+/*
+ * kk_tree_attn_kv8 - kk_tree_attn over an 8-bit cache: q, out and the drafted
+ * nodes' k and v are bf16, everything else as there. Codes are multiplied as
+ * float16, which holds them exactly, queries as float16 scaled by a power of two
+ * for each row (what that loses is below 2^-39 of the row's largest element),
+ * weights are rounded to float16 (of drafted nodes: bf16) before they multiply
+ * the Values; sums and softmax are float32. Scales are finite.
+ * Workspace: kk_tree_attn_kv8_workspace_bytes().
+ */
+size_t kk_tree_attn_kv8_workspace_bytes(const kk_kcache_desc* kc, const kk_block_table* bt, int32_t max_nodes,
+                                        int32_t num_q_heads);
+kk_status kk_tree_attn_kv8(const kk_kcache_desc* kc, const float* k_scale, const kk_kcache_desc* vc,
+                           const float* v_scale, const kk_block_table* bt, int32_t layer, const kk_selection* sel,
+                           const kk_tree* tree, const void* q, int64_t q_stride_node, int64_t q_stride_head,
+                           int32_t num_q_heads, float scale, void* out, float* lse, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Pages with reference counts: refs[p] (device int32 [num_pages], caller-owned)
+ * is the number of tables that hold page p, 0 when it is free. Every call takes
+ * the counts from refs_in and leaves them in refs_out, which may be the same
+ * array. What lives with a page (K, V, their scales, v_b, running sums, masses) is
+ * described by page arrays: slice s of page p is `bytes` bytes at base +
+ * s*stride_slice + p*stride_page (bytes; all multiples of 4; a cache whose pages
+ * are contiguous has its layers as slices).
+ */
+typedef struct kk_page_array {
+  void* base; /* device */
+  int64_t stride_slice, stride_page, bytes;
+  int32_t slices;
+} kk_page_array;
+
+/*
+ * kk_pages_alloc - out[i] (device int32 [n]) becomes the next free page for
+ * every i < n with want[i] != 0 (nullable: all), free pages in ascending order,
+ * its count 1; out[i] = -1 where want[i] is 0, or where no page is left
+ * (KK_ERR_NO_PAGES in the device error word).
+ *
+ * kk_pages_free - the count of every page of bt's tables falls by one for every
+ * place it has in them; a page out of range, or whose count is 0 already, is reported
+ * (KK_ERR_BAD_INDEX) and left.
+ */
+kk_status kk_pages_alloc(const int32_t* refs_in, int32_t* refs_out, int32_t num_pages, const int32_t* want, int32_t n,
+                         int32_t* out, cudaStream_t stream);
+kk_status kk_pages_free(const kk_block_table* bt, const int32_t* refs_in, int32_t* refs_out, int32_t num_pages,
+                        cudaStream_t stream);
+
+/*
+ * kk_pages_fork - children of requests (the beams of a search, the samples of a
+ * prompt). Child i < F continues request parent[i] of bt (device int32 [F]): its
+ * table, written to child_pages (device int32, of child_capacity >= F *
+ * bt->max_blocks entries, those past the last table left as they were),
+ * child_offsets [F+1] and child_lens [F], is the parent's: full blocks are
+ * shared, and a last block that is not full (block_size tokens) is the child's
+ * own, as it will be written: the next free page in child order, and every
+ * page array's page of the parent copied to it. keep_parents: the parents stay
+ * as they are. Otherwise their tables are consumed: the first child of each
+ * takes its last block as it is, and the pages of a request without children
+ * lose a count. Counts are right afterwards for the children's tables (and the
+ * parents' when they stay). Free pages are taken as of after that. A parent out
+ * of [0, R) gives a child without tokens (KK_ERR_BAD_INDEX); so does one whose
+ * table disagrees with its length, whose counts stay. Where no
+ * page is left the child's last entry is -1 (KK_ERR_NO_PAGES).
+ * child tables may not overlap bt's. arrays: n_arrays (0..8) host structs, read during the call.
+ * workspace: device, 256-byte aligned, no initial contents.
+ */
+size_t kk_pages_fork_workspace_bytes(int32_t num_requests, int32_t F);
+kk_status kk_pages_fork(const kk_block_table* bt, int32_t block_size, const int32_t* parent, int32_t F,
+                        int32_t keep_parents, const int32_t* refs_in, int32_t* refs_out, int32_t num_pages,
+                        int32_t* child_pages, int64_t child_capacity, int32_t* child_offsets, int32_t* child_lens,
+                        const kk_page_array* arrays, int32_t n_arrays, void* workspace, size_t workspace_bytes,
+                        cudaStream_t stream);
+
+/*
+ * kk_pages_compact - the U pages with a count move to the front of the pool: the
+ * used pages from U on go to the free ones below U, both in ascending order
+ * (every page array's page copied, the pages from U on keep what they held).
+ * remap (device int32 [num_pages]) gives every page's new place, -1 for free
+ * ones; used[0] = U; refs_out the moved counts; and the n entries of the live
+ * tables are rewritten: pages_out[i] = remap[pages_in[i]] (may be the same
+ * array; -1 stays, an entry out of range or of a free page becomes -1 and is
+ * reported as KK_ERR_BAD_INDEX). arrays and workspace as above.
+ */
+size_t kk_pages_compact_workspace_bytes(int32_t num_pages);
+kk_status kk_pages_compact(const int32_t* refs_in, int32_t* refs_out, int32_t num_pages, const int32_t* pages_in,
+                           int32_t* pages_out, int64_t n, int32_t* remap, int32_t* used, const kk_page_array* arrays,
+                           int32_t n_arrays, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

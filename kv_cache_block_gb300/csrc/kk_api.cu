@@ -139,6 +139,7 @@ const char* kk_status_str(kk_status s) {
     case KK_ERR_CUDA: return "CUDA error";
     case KK_ERR_BAD_INDEX: return "index out of range in device data";
     case KK_ERR_TIMEOUT: return "device wait timed out";
+    case KK_ERR_NO_PAGES: return "no free page left";
   }
   return "unknown status";
 }

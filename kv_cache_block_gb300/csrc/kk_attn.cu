@@ -4,8 +4,8 @@
 // Affinity" page §5.2 step 4: only they are loaded) and the drafted nodes a
 // node may see. One pass over the tokens with a running maximum and sum per
 // row; the work division is kk_attn.cuh's. The main kernels are in kk_attn_f32.cu
-// (float32 caches), kk_attn_mma.cu (bf16, few rows) and kk_attn_tc.cu (bf16, many
-// rows); this file chooses one and adds up the parts of the items that were cut.
+// (float32 caches), kk_attn_mma.cu (bf16, few rows), kk_attn_tc.cu (bf16, many
+// rows) and kk_attn_kv8.cu (e4m3 with scales); this file chooses one and adds up the parts of the items that were cut.
 #include <algorithm>
 
 #include "kk_attn.cuh"
@@ -321,6 +321,7 @@ constexpr long long kWideTokens = 256 << 10;
 
 AttnPlan plan(const KCache& kc, const KCache& vc, int max_nodes, int G, long long tokens) {
   const int rows = max_nodes * G;
+  if (kc.dtype == 2) return attn_kv8_plan(kc, rows);
   if (kc.dtype != 1) return attn_f32_plan(kc, rows);
   if (tokens * ((rows - 1) / 16) >= kTcWork && attn_tc_suits(kc) && attn_tc_suits(vc)) return attn_tc_plan();
   return attn_mma_plan(kc, rows > 16 && tokens >= kWideTokens);
@@ -348,6 +349,7 @@ size_t attn_workspace_bytes(const KCache& kc, int R, int max_nodes, int G) {
   // enough for any: which one runs also depends on the V cache's strides and the tokens
   const int rows = max_nodes * G;
   auto size = [&](const AttnPlan& pl) { return cut_bytes(pl, R, kc.H, rows) + plan_bytes(pl, kc.D); };
+  if (kc.dtype == 2) return size(attn_kv8_plan(kc, rows));
   if (kc.dtype != 1) return size(attn_f32_plan(kc, rows));
   const size_t n = size(attn_mma_plan(kc, false));
   if (rows <= 16) return n;
@@ -363,12 +365,14 @@ cudaError_t launch_tree_attn(AttnArgs a, cudaStream_t s) {
   a.mt_max = (rows + pl.M - 1) / pl.M;
   a.cuts = reinterpret_cast<int4*>(a.ws);
   a.ws = reinterpret_cast<float*>(reinterpret_cast<char*>(a.ws) + cut_bytes(pl, a.bt.R, a.kc.H, rows));
-  const bool bf = a.kc.dtype == 1;
+  const bool bf = a.kc.dtype != 0;  // the queries' and results' type
   cudaError_t e = cudaErrorNotSupported;
   if (pl.kind == AttnPlan::kTc) {
     e = launch_attn_tc(a, s);
   } else if (pl.kind == AttnPlan::kMma) {
     e = launch_attn_mma(a, pl, s);
+  } else if (pl.kind == AttnPlan::kKv8) {
+    e = launch_attn_kv8(a, pl, s);
   } else {
     e = launch_attn_f32(a, pl, s);
   }

@@ -49,6 +49,9 @@ struct AttnArgs {
   float decay;
   const float* mass_in;
   float* mass_out;
+  // 8-bit caches only: [L][num_pages][H]
+  const float* k_scale;
+  const float* v_scale;
   unsigned long long wait_ns;
   long long skip_tile;  // failure-detection tests: CTA 0 waits for 16 bytes more than this Key tile has (-1: none)
   int* err;
@@ -56,7 +59,7 @@ struct AttnArgs {
 
 // How a call runs: which kernel, its row and token tiles, its grid.
 struct AttnPlan {
-  enum Kind { kF32, kMma, kTc };
+  enum Kind { kF32, kMma, kTc, kKv8 };
   Kind kind;
   int M, TK, grid;
 };
@@ -66,6 +69,9 @@ cudaError_t launch_attn_mma(const AttnArgs& a, const AttnPlan& pl, cudaStream_t 
 // kk_attn_f32.cu (float32; rows: query rows of a request and KV head, at most)
 AttnPlan attn_f32_plan(const KCache& kc, int rows);
 cudaError_t launch_attn_f32(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s);
+// kk_attn_kv8.cu (e4m3 with scales)
+AttnPlan attn_kv8_plan(const KCache& kc, int rows);
+cudaError_t launch_attn_kv8(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s);
 // kk_attn_tc.cu (bf16, D 64 or 128, both caches of layouts it suits)
 bool attn_tc_suits(const KCache& kc);
 AttnPlan attn_tc_plan();

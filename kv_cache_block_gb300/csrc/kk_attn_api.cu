@@ -27,12 +27,11 @@ bool rows_ok(const void* p, int64_t sn, int64_t sh, int es) {
   return aligned(p, 16) && sn >= 0 && sh >= 0 && sn * es % 16 == 0 && sh * es % 16 == 0;
 }
 
-// Cache, table, nodes and queries, as kk_tree_attn and kk_attn_mass share them.
-kk_status common_args(const kk_kcache_desc* kc, const kk_block_table* bt, int32_t layer, const kk_tree* tree,
-                      const void* q, int64_t q_sn, int64_t q_sh, int32_t Hq, float scale, kk::AttnArgs* a) {
-  kk_status st = kk::check_kcache_desc(kc, &a->kc);
+// Table, nodes and queries, as the attention calls and kk_attn_mass share them; a->kc is set.
+kk_status common_args(const kk_block_table* bt, int32_t layer, const kk_tree* tree, const void* q, int64_t q_sn,
+                      int64_t q_sh, int32_t Hq, float scale, kk::AttnArgs* a) {
+  const kk_status st = kk::check_block_table(bt, &a->bt);
   if (st != KK_OK) return st;
-  if ((st = kk::check_block_table(bt, &a->bt)) != KK_OK) return st;
   if (layer < 0 || layer >= a->kc.L || !tree || !std::isfinite(scale)) return KK_ERR_INVALID;
   if (tree->max_nodes < 1 || tree->max_nodes > kk::kMaxNodes || tree->total_nodes < 0) return KK_ERR_INVALID;
   if (!tree->node_offsets && (long long)tree->max_nodes * a->bt.R != tree->total_nodes) return KK_ERR_INVALID;
@@ -64,6 +63,49 @@ kk_status done(cudaError_t e) {
 
 }  // namespace
 
+namespace kk {
+// kk_tree_attn and kk_tree_attn_kv8 (kk_serve_api.cu) once the caches are checked: a->kc, a->vc and the scales are set.
+kk_status tree_attn_call(AttnArgs* a, const kk_block_table* bt, int32_t layer, const kk_selection* sel,
+                         const kk_tree* tree, const void* q, int64_t q_sn, int64_t q_sh, int32_t Hq, float scale,
+                         void* out, float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  const kk_status st = common_args(bt, layer, tree, q, q_sn, q_sh, Hq, scale, a);
+  if (st != KK_OK) return st;
+  const int es = a->kc.dtype == KK_F32 ? 4 : 2;
+  if ((tree->k == nullptr) != (tree->v == nullptr)) return KK_ERR_INVALID;
+  if (tree->k) {
+    if (!rows_ok(tree->k, tree->k_stride_node, tree->k_stride_head, es) ||
+        !rows_ok(tree->v, tree->v_stride_node, tree->v_stride_head, es) || !aligned(tree->mask, 4))
+      return KK_ERR_UNSUPPORTED;
+    a->dk = tree->k;
+    a->dv = tree->v;
+    a->dk_sn = tree->k_stride_node;
+    a->dk_sh = tree->k_stride_head;
+    a->dv_sn = tree->v_stride_node;
+    a->dv_sh = tree->v_stride_head;
+    a->mask = tree->mask;
+  }
+  if (sel) {
+    if (!sel->pages || !sel->logical || !sel->count || sel->K < 1) return KK_ERR_INVALID;
+    if (!aligned(sel->pages, 4) || !aligned(sel->logical, 4) || !aligned(sel->count, 4)) return KK_ERR_UNSUPPORTED;
+    a->sel_pages = sel->pages;
+    a->sel_logical = sel->logical;
+    a->sel_count = sel->count;
+    a->selK = sel->K;
+  }
+  if (a->bt.R == 0 || a->total_nodes == 0) return KK_OK;
+  if (!out) return KK_ERR_INVALID;
+  if (!aligned(out, 16) || !aligned(lse, 4)) return KK_ERR_UNSUPPORTED;
+  if ((long long)a->bt.R * a->kc.H * a->max_nodes * a->G > 0x7FFFFFFFll) return KK_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < attn_workspace_bytes(a->kc, a->bt.R, a->max_nodes, a->G)) return KK_ERR_INVALID;
+  if (!aligned(workspace, 256)) return KK_ERR_UNSUPPORTED;
+  a->out = out;
+  a->lse = lse;
+  a->ws = static_cast<float*>(workspace);
+  if (!(a->err = device_error_word())) return KK_ERR_CUDA;
+  return done(launch_tree_attn(*a, stream));
+}
+}  // namespace kk
+
 extern "C" {
 
 size_t kk_tree_attn_workspace_bytes(const kk_kcache_desc* kc, const kk_block_table* bt, int32_t max_nodes,
@@ -82,43 +124,11 @@ kk_status kk_tree_attn(const kk_kcache_desc* kc, const kk_kcache_desc* vc, const
                        int64_t q_stride_head, int32_t num_q_heads, float scale, void* out, float* lse,
                        void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   kk::AttnArgs a = {};
-  kk_status st = common_args(kc, bt, layer, tree, q, q_stride_node, q_stride_head, num_q_heads, scale, &a);
-  if (st != KK_OK) return st;
-  if ((st = kk::check_kcache_desc(vc, &a.vc)) != KK_OK) return st;
+  kk_status st = kk::check_kcache_desc(kc, &a.kc);
+  if (st != KK_OK || (st = kk::check_kcache_desc(vc, &a.vc)) != KK_OK) return st;
   if (!same_sizes(a.kc, a.vc)) return KK_ERR_INVALID;
-  const int es = a.kc.dtype == KK_F32 ? 4 : 2;
-  if ((tree->k == nullptr) != (tree->v == nullptr)) return KK_ERR_INVALID;
-  if (tree->k) {
-    if (!rows_ok(tree->k, tree->k_stride_node, tree->k_stride_head, es) ||
-        !rows_ok(tree->v, tree->v_stride_node, tree->v_stride_head, es) || !aligned(tree->mask, 4))
-      return KK_ERR_UNSUPPORTED;
-    a.dk = tree->k;
-    a.dv = tree->v;
-    a.dk_sn = tree->k_stride_node;
-    a.dk_sh = tree->k_stride_head;
-    a.dv_sn = tree->v_stride_node;
-    a.dv_sh = tree->v_stride_head;
-    a.mask = tree->mask;
-  }
-  if (sel) {
-    if (!sel->pages || !sel->logical || !sel->count || sel->K < 1) return KK_ERR_INVALID;
-    if (!aligned(sel->pages, 4) || !aligned(sel->logical, 4) || !aligned(sel->count, 4)) return KK_ERR_UNSUPPORTED;
-    a.sel_pages = sel->pages;
-    a.sel_logical = sel->logical;
-    a.sel_count = sel->count;
-    a.selK = sel->K;
-  }
-  if (a.bt.R == 0 || a.total_nodes == 0) return KK_OK;
-  if (!out) return KK_ERR_INVALID;
-  if (!aligned(out, 16) || !aligned(lse, 4)) return KK_ERR_UNSUPPORTED;
-  if ((long long)a.bt.R * a.kc.H * a.max_nodes * a.G > 0x7FFFFFFFll) return KK_ERR_UNSUPPORTED;
-  if (!workspace || workspace_bytes < kk::attn_workspace_bytes(a.kc, a.bt.R, a.max_nodes, a.G)) return KK_ERR_INVALID;
-  if (!aligned(workspace, 256)) return KK_ERR_UNSUPPORTED;
-  a.out = out;
-  a.lse = lse;
-  a.ws = static_cast<float*>(workspace);
-  if (!(a.err = kk::device_error_word())) return KK_ERR_CUDA;
-  return done(kk::launch_tree_attn(a, stream));
+  return kk::tree_attn_call(&a, bt, layer, sel, tree, q, q_stride_node, q_stride_head, num_q_heads, scale, out, lse,
+                            workspace, workspace_bytes, stream);
 }
 
 kk_status kk_attn_mass(const kk_kcache_desc* kc, const kk_block_table* bt, int32_t layer, const kk_tree* tree,
@@ -126,8 +136,9 @@ kk_status kk_attn_mass(const kk_kcache_desc* kc, const kk_block_table* bt, int32
                        const float* lse, const float* row_w, const int32_t* row_lens, const int32_t* old_lens,
                        float decay, const float* mass_in, float* mass_out, cudaStream_t stream) {
   kk::AttnArgs a = {};
-  kk_status st = common_args(kc, bt, layer, tree, q, q_stride_node, q_stride_head, num_q_heads, scale, &a);
+  kk_status st = kk::check_kcache_desc(kc, &a.kc);
   if (st != KK_OK) return st;
+  if ((st = common_args(bt, layer, tree, q, q_stride_node, q_stride_head, num_q_heads, scale, &a)) != KK_OK) return st;
   if (!std::isfinite(decay)) return KK_ERR_INVALID;
   if (a.bt.R == 0) return KK_OK;
   if (!mass_out || (a.total_nodes > 0 && !lse)) return KK_ERR_INVALID;

@@ -1,0 +1,615 @@
+// kk_tree_attn_kv8: attention over a cache of e4m3 codes with a scale for each
+// page and KV head, K = code * k_scale, V = code * v_scale; bound by the bytes of
+// the codes.
+//
+// Four warps share an item's rows (M = 8, 16 or 32) and take 16 tokens each of
+// every 64-token tile, streamed through a ring of shared-memory stages of their
+// own as in kk_attn_mma.cu. Tokens are the M axis of the products (S^T = K Q^T,
+// O^T = V^T P^T with m16n8k16 matrix instructions), query rows the N axis: a
+// decode token's group of at most 8 rows fills it, where rows along M would
+// leave half of 16 empty, and every 16 x 16 codes cost one instruction.
+//
+// e4m3 values are exact in float16, so codes are widened two at a time and
+// multiplied as float16; a scale never meets the products, it multiplies the
+// score (K) or the weight (V) of its page. The axes a product sums over and the
+// dims of O may be in any order as long as both operands agree, so a thread
+// reads whole words of codes: for K four dims of a token feed a whole step; for
+// V the bytes of two tokens are interleaved (prmt) and widened into an operand
+// register. No ldmatrix, no transposed copy; the weights, which come out of the
+// first product with tokens along the wrong axis, are turned by movmatrix.
+//
+// Softmax. Two references a row (log2 domain): one for the sum of weights, 2^(s -
+// ref_s) in float32, one for what multiplies the codes of V, 2^(s - ref_v + 6) *
+// v_scale, which has to fit float16 whatever the pages' scales are. Both are
+// left alone until a score passes one by 2^8 (one vote a step); until then sums
+// below 2^8 cost nothing and no reduction over lanes is needed.
+#pragma once
+#include "kk_attn_ring.cuh"
+#include "kk_pdl.cuh"
+
+namespace kk {
+namespace {
+
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kTK = kRingTK, kTok = kTK / kWarps;  // tokens of a warp's share of a tile
+constexpr float kNone = -1e30f;                    // a reference before the first score
+constexpr float kLift = 6.f;  // a weight is below 2^(6 + 8) * 2 (a scale's mantissa): float16 holds 65504
+
+// Two e4m3 codes (the low or the high half of a word) as float16, exactly.
+__device__ __forceinline__ uint32_t widen(uint32_t w, int half) {
+  uint32_t r;
+  const uint16_t x = (uint16_t)(half ? w >> 16 : w);
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// The transpose of an 8 x 8 tile of 16-bit values (lane 4g + t holds row g, columns 2t and 2t + 1).
+__device__ __forceinline__ uint32_t turn(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+template <bool BF>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  if constexpr (BF)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// N consecutive words of shared memory.
+template <int N>
+__device__ __forceinline__ void lds(uint32_t (&x)[N], const unsigned char* p) {
+  if constexpr (N == 4) {
+    const uint4 y = *reinterpret_cast<const uint4*>(p);
+    x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+  } else if constexpr (N == 2) {
+    const uint2 y = *reinterpret_cast<const uint2*>(p);
+    x[0] = y.x, x[1] = y.y;
+  } else {
+    x[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
+}
+
+// Byte offset of byte x (a multiple of 4) of token `row` in a stage's K or V: 16-byte pieces are
+// exchanged so that the eight lanes of a quarter warp that read together (K: two tokens' four
+// pieces; V: two pieces of four tokens two apart) fall into different banks.
+template <int D>
+__device__ __forceinline__ uint32_t at_k(int row, int x) {
+  return D >= 128 ? row * D + (x ^ ((row & 1) << 6)) : row * D + x;
+}
+template <int D>
+__device__ __forceinline__ uint32_t at_v(int row, int x) {
+  return D >= 64 ? ((row * D + x) ^ (((row >> 1) & 3) << 5)) : row * D + x;
+}
+
+// A finite scale as m * 2^e, |m| < 2.
+__device__ __forceinline__ void split_scale(float x, float* e, float* m) {
+  const uint32_t b = __float_as_uint(x), f = (b >> 23) & 0xFFu;
+  *e = f ? (float)((int)f - 127) : -126.f;
+  *m = f ? __uint_as_float((b & 0x807FFFFFu) | 0x3F800000u) : x * 0x1p126f;
+}
+
+// What a warp loads next: a lane's token (its address in K and V and where its scale is).
+struct Tok8 {
+  const char *k, *v;
+  long long sc;
+  int page, tok;
+  bool ok;
+};
+
+// PG: 16 consecutive slots lie in one page (block_size is a multiple of 16); every lane holds the
+// first of them and `n`, how many hold a token. Else a lane holds the token of its own number.
+template <bool PG>
+__device__ __forceinline__ Tok8 find_tok8(const AttnArgs& a, int r, const AttnReq& rq, int t, int w, int lane) {
+  Tok8 x;
+  TokenAt at;
+  x.ok = false;
+  x.page = x.tok = 0;
+  if (t >= rq.tiles_c) return x;
+  const int v = t * kTK + w * kTok + (PG ? 0 : lane & (kTok - 1));
+  x.ok = token_at(a, r, rq, v, true, &at);
+  x.page = at.page;
+  x.tok = at.tok;
+  return x;
+}
+// How many of the 16 slots from slot v on hold a token, given that the first one does (PG).
+__device__ __forceinline__ int run_of(const AttnArgs& a, int r, const AttnReq& rq, int v, int tok) {
+  long long left = (long long)rq.T - v;
+  if (a.sel_pages) left = (long long)rq.T - ((long long)a.sel_logical[(long long)r * a.selK + v / a.kc.bs] * a.kc.bs + tok);
+  return (int)(left < kTok ? left : kTok);
+}
+
+template <int D>
+__host__ __device__ constexpr int kv8_stages() {
+  return D >= 128 ? 3 : D == 64 ? 5 : 8;
+}
+template <int D, int NT>
+struct Kv8Smem {
+  static constexpr int M = NT * 8, kStage = kTok * D * 2;
+  static constexpr int ring = kWarps * kv8_stages<D>() * kStage, join = kWarps * M * (D + 2) * 4;
+  static constexpr int scales = ring > join ? ring : join;       // [warps][stages][32] floats
+  static constexpr int raw = scales + kWarps * kv8_stages<D>() * 32 * 4;  // queries as they are, bf16 [M][D]
+  static constexpr int frag = raw + M * D * 2;                   // and as float16 operands [NT][D/16][32 lanes]
+  static constexpr int qf = frag + M * D * 2;                    // [M] what the scores are multiplied with
+  static constexpr int bytes = qf + M * 4;
+};
+
+template <int D, int NT>
+constexpr int kv8_blocks() {
+  return NT == 1 ? (D <= 128 ? 4 : 2) : NT == 2 ? (D <= 128 ? 3 : 2) : 2;
+}
+
+template <int D, int NT, bool PG>
+__global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kernel(const AttnArgs a) {
+  using Sm = Kv8Smem<D, NT>;
+  constexpr int M = NT * 8, KS = D / 16, S = kv8_stages<D>();
+  constexpr bool kQReg = NT * D <= 256;  // query operands stay in registers
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ long long s_place[kWarps + 4];
+  __shared__ uint32_t s_ok[kWarps][S];
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  unsigned char* ring = smem + w * S * Sm::kStage;
+  const uint32_t ring_at = smem_u32(ring);
+  float* sc = reinterpret_cast<float*>(smem + Sm::scales) + w * S * 32;
+  const uint32_t sc_at = smem_u32(sc);
+  uint2* frag = reinterpret_cast<uint2*>(smem + Sm::frag);
+  float* qf_s = reinterpret_cast<float*>(smem + Sm::qf);
+  float* join = reinterpret_cast<float*>(smem);  // after an item: [warps][M][D], maxima, sums
+  pdl_launch_dependents();
+  const AttnPlace pl = find_place<kThreads>(a, blockIdx.x, M, kTK, s_place, tid);
+  int r = pl.r;
+  long long base = pl.base;
+  for (long long u = pl.u0; u < pl.u1;) {
+    const AttnReq rq = load_req(a, r, M, kTK, false);
+    const long long units = req_units(a, rq);
+    if (u >= base + units) {
+      base += units;
+      ++r;
+      continue;
+    }
+    ItemAt it = item_at(rq, u - base);
+    it.t1 = (int)min((long long)rq.tiles, it.t0 + (pl.u1 - u));
+    const int t0 = it.t0, t1 = it.t1, h = it.h, row0 = it.mt * M;
+    const int rows = min(M, rq.n * a.G - row0);
+
+    // copies a share of a tile (16 tokens of K and V, their scales) into stage st
+    auto load = [&](const Tok8& x, int st, int t, bool on) {
+      const uint32_t kst = ring_at + st * Sm::kStage, vst = kst + kTok * D;
+      constexpr int CH = D / 16, RI = 32 / CH;  // pieces of a row, rows per instruction
+      const int c = lane % CH, sub = lane / CH;
+      const long long kl = a.layer * a.kc.sL + h * a.kc.sH, vl = a.layer * a.vc.sL + h * a.vc.sH;
+      const long long s0 = (long long)a.layer * a.kc.num_pages;
+      uint32_t live;
+      if constexpr (PG) {
+        const int n = on && x.ok ? run_of(a, r, rq, t * kTK + w * kTok, x.tok) : 0;
+        live = (1u << n) - 1u;
+        const char* k = static_cast<const char*>(a.kc.base) + kl + x.page * a.kc.sP + x.tok * a.kc.sT + c * 16;
+        const char* v = static_cast<const char*>(a.vc.base) + vl + x.page * a.vc.sP + x.tok * a.vc.sT + c * 16;
+        if (on) {
+#pragma unroll
+          for (int i = 0; i < (kTok + RI - 1) / RI; ++i) {
+            const int row = i * RI + sub;
+            cp_async16(kst + at_k<D>(row, c * 16), row < n ? k + row * a.kc.sT : k, row < n);
+            cp_async16(vst + at_v<D>(row, c * 16), row < n ? v + row * a.vc.sT : v, row < n);
+          }
+          if (lane < 2)
+            cp_async4(sc_at + (st * 32 + lane) * 4,
+                      (lane ? a.v_scale : a.k_scale) + (s0 + x.page) * a.kc.H + h, n > 0);
+        }
+      } else {
+        const uint32_t ok = __ballot_sync(kFull, on && x.ok);
+        live = ok & 0xFFFFu;
+        const long long ko = kl + x.page * a.kc.sP + x.tok * a.kc.sT, vo = vl + x.page * a.vc.sP + x.tok * a.vc.sT;
+        if (on) {
+#pragma unroll
+          for (int i = 0; i < (kTok + RI - 1) / RI; ++i) {
+            const int row = i * RI + sub;
+            const char* k = static_cast<const char*>(a.kc.base) + __shfl_sync(kFull, ko, row) + c * 16;
+            const char* v = static_cast<const char*>(a.vc.base) + __shfl_sync(kFull, vo, row) + c * 16;
+            cp_async16(kst + at_k<D>(row, c * 16), k, (ok >> row) & 1);
+            cp_async16(vst + at_v<D>(row, c * 16), v, (ok >> row) & 1);
+          }
+          cp_async4(sc_at + (st * 32 + lane) * 4, (lane < 16 ? a.k_scale : a.v_scale) + (s0 + x.page) * a.kc.H + h,
+                    x.ok);
+        }
+      }
+      cp_commit();
+      if (lane == 0) s_ok[w][st] = live;
+    };
+
+    // the first tiles' copies go out before the queries are read
+    Tok8 nx = find_tok8<PG>(a, r, rq, t0, w, lane);
+#pragma unroll 1
+    for (int st = 0; st < S - 1; ++st) {
+      load(nx, st, t0 + st, t0 + st < t1 && t0 + st < rq.tiles_c);
+      nx = find_tok8<PG>(a, r, rq, min(t0 + st + 1, t1 - 1), w, lane);
+    }
+    for (int i = tid; i < M * (D / 8); i += kThreads) {
+      const int m = i / (D / 8), c = i - m * (D / 8), row = row0 + m;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (m < rows)
+        x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (rq.node0 + row / a.G) * a.q_sn +
+                                            (long long)(h * a.G + row % a.G) * a.q_sh + c * 8);
+      *reinterpret_cast<uint4*>(smem + Sm::raw + m * D * 2 + c * 16) = x;
+    }
+    __syncthreads();
+    // Queries as float16 operands: the row's largest element is brought to [2^14, 2^15) by a power of two, so
+    // that what float16 cannot hold of a row is below 2^-39 of it. Step j's four dims of thread t4 are those of
+    // word j of the codes it reads.
+    for (int nt = w; nt < NT; nt += kWarps) {
+      const uint16_t* qr = reinterpret_cast<const uint16_t*>(smem + Sm::raw) + (nt * 8 + g) * D;
+      auto dim = [&](int j) { return D >= 64 ? (j >> 2) * 64 + t4 * 16 + (j & 3) * 4 : t4 * 8 + j * 4; };
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < KS; ++j) {
+        const uint2 x = *reinterpret_cast<const uint2*>(qr + dim(j));
+        top = max(max(top, max(x.x & 0x7FFFu, (x.x >> 16) & 0x7FFFu)), max(x.y & 0x7FFFu, (x.y >> 16) & 0x7FFFu));
+      }
+      top = max(top, __shfl_xor_sync(kFull, top, 1));
+      top = max(top, __shfl_xor_sync(kFull, top, 2));
+      const int e = (int)(top >> 7);  // the exponent field; 0xFF: not finite, which stays so
+      const int sh = e == 0xFF ? 0 : min(max(e - 127 - 14, -110), 113);
+      const float down = __uint_as_float((uint32_t)(127 - sh) << 23);  // 2^-sh, sh in [-110, 113]
+#pragma unroll
+      for (int j = 0; j < KS; ++j) {
+        const uint2 x = *reinterpret_cast<const uint2*>(qr + dim(j));
+        frag[(nt * KS + j) * 32 + lane] = make_uint2(pack_f16(bf16_lo(x.x) * down, bf16_hi(x.x) * down),
+                                                     pack_f16(bf16_lo(x.y) * down, bf16_hi(x.y) * down));
+      }
+      if (t4 == 0) qf_s[nt * 8 + g] = a.scale_log2 * __uint_as_float((uint32_t)(127 + sh) << 23);
+    }
+    __syncthreads();
+    uint2 qr[kQReg ? NT : 1][kQReg ? KS : 1];
+    if constexpr (kQReg) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < KS; ++j) qr[nt][j] = frag[(nt * KS + j) * 32 + lane];
+    }
+    float qf[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      qf[nt][0] = qf_s[nt * 8 + 2 * t4];
+      qf[nt][1] = qf_s[nt * 8 + 2 * t4 + 1];
+    }
+
+    float o[NT][KS][4], ref_s[NT][2], ref_v[NT][2], l_run[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int n = 0; n < KS; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][n][e] = 0.f;
+      ref_s[nt][0] = ref_s[nt][1] = ref_v[nt][0] = ref_v[nt][1] = kNone;
+      l_run[nt][0] = l_run[nt][1] = 0.f;
+    }
+    // Moves the references of rows whose scores passed them; lv: the exponent of the Values' scale of tokens g and g + 8.
+    auto settle = [&](const float (&s)[NT][4], float lv0, float lv1) {
+      bool rise = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          rise |= s[nt][e] > ref_s[nt][e & 1] + 8.f || s[nt][e] + (e < 2 ? lv0 : lv1) > ref_v[nt][e & 1] + 8.f;
+      if (!__any_sync(kFull, rise)) return;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float ms = fmaxf(s[nt][e], s[nt][e + 2]), mv = fmaxf(s[nt][e] + lv0, s[nt][e + 2] + lv1);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) {
+            ms = fmaxf(ms, __shfl_xor_sync(kFull, ms, x));
+            mv = fmaxf(mv, __shfl_xor_sync(kFull, mv, x));
+          }
+          ms = fmaxf(ms, ref_s[nt][e]);
+          mv = fmaxf(mv, ref_v[nt][e]);
+          l_run[nt][e] *= ex2(ref_s[nt][e] - ms);
+          f[e] = ex2(ref_v[nt][e] - mv);
+          ref_s[nt][e] = ms;
+          ref_v[nt][e] = mv;
+        }
+#pragma unroll
+        for (int n = 0; n < KS; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nt][n][e] *= f[e & 1];
+      }
+    };
+
+    int st = 0;
+#pragma unroll 1
+    for (int t = t0; t < t1; ++t) {
+      cp_wait<S - 2>();
+      __syncwarp();
+      {  // refill the stage read in the last turn
+        const int tn = t + S - 1;
+        load(nx, st == 0 ? S - 1 : st - 1, tn, tn < t1 && tn < rq.tiles_c);
+        nx = find_tok8<PG>(a, r, rq, min(t + S, t1 - 1), w, lane);
+      }
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+      if (t < rq.tiles_c) {
+        const unsigned char *kst = ring + st * Sm::kStage, *vst = kst + kTok * D;
+        const uint32_t live = s_ok[w][st];
+        constexpr int KW = D >= 64 ? 4 : 2;  // words of codes read at once
+#pragma unroll
+        for (int i = 0; i < KS / KW; ++i) {
+          uint32_t x[KW], y[KW];
+          lds<KW>(x, kst + at_k<D>(g, i * 64 + t4 * KW * 4));
+          lds<KW>(y, kst + at_k<D>(g + 8, i * 64 + t4 * KW * 4));
+#pragma unroll
+          for (int c = 0; c < KW; ++c) {
+            const uint32_t a0 = widen(x[c], 0), a1 = widen(y[c], 0), a2 = widen(x[c], 1), a3 = widen(y[c], 1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              uint2 b;
+              if constexpr (kQReg) b = qr[nt][i * KW + c];
+              else b = frag[(nt * KS + i * KW + c) * 32 + lane];
+              mma<false>(s[nt], a0, a1, a2, a3, b.x, b.y);
+            }
+          }
+        }
+        const float* ss = sc + st * 32;
+        const float ks0 = ss[PG ? 0 : g], ks1 = PG ? ks0 : ss[g + 8];
+        float lv0, lv1, vm0, vm1;
+        split_scale(ss[PG ? 1 : 16 + g], &lv0, &vm0);
+        lv1 = lv0, vm1 = vm0;
+        if (!PG) split_scale(ss[24 + g], &lv1, &vm1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool see = (live >> (e < 2 ? g : g + 8)) & 1;
+            // selected, whatever a place without a token holds
+            s[nt][e] = see ? s[nt][e] * qf[nt][e & 1] * (e < 2 ? ks0 : ks1) : -INFINITY;
+          }
+        settle(s, lv0, lv1);
+        uint32_t b0[NT], b1[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            l_run[nt][e & 1] += ex2(s[nt][e] - ref_s[nt][e & 1]);
+            p[e] = ex2(s[nt][e] + (e < 2 ? lv0 : lv1) - ref_v[nt][e & 1] + kLift) * (e < 2 ? vm0 : vm1);
+          }
+          b0[nt] = turn(pack_f16(p[0], p[1]));  // the weights' one rounding: float16 feeds the product
+          b1[nt] = turn(pack_f16(p[2], p[3]));
+        }
+        constexpr int VW = D >= 128 ? 4 : D / 32;  // words of a thread's D/8 dims read at once
+#pragma unroll
+        for (int i = 0; i < KS / (2 * VW); ++i) {
+          uint32_t x[4][VW];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            lds<VW>(x[k], vst + at_v<D>(2 * t4 + (k & 1) + (k >> 1) * 8, i * 128 + g * VW * 4));
+#pragma unroll
+          for (int c = 0; c < VW; ++c)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const uint32_t p = __byte_perm(x[0][c], x[1][c], hf ? 0x7362 : 0x5140);
+              const uint32_t q = __byte_perm(x[2][c], x[3][c], hf ? 0x7362 : 0x5140);
+              const uint32_t a0 = widen(p, 0), a1 = widen(p, 1), a2 = widen(q, 0), a3 = widen(q, 1);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma<false>(o[nt][(i * VW + c) * 2 + hf], a0, a1, a2, a3, b0[nt], b1[nt]);
+            }
+        }
+      } else if (a.dk) {
+        // drafted nodes, bf16, straight from where they lie; at most 16 of these steps an item
+        const int j0 = (t - rq.tiles_c) * kTK + w * kTok;
+        if (j0 < rq.n) {
+          const uint16_t* dk = static_cast<const uint16_t*>(a.dk) + rq.node0 * a.dk_sn + h * a.dk_sh;
+          const uint16_t* dv = static_cast<const uint16_t*>(a.dv) + rq.node0 * a.dv_sn + h * a.dv_sh;
+          const unsigned char* raw = smem + Sm::raw;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            uint4 x = make_uint4(0, 0, 0, 0), y = x;
+            if (j0 + g < rq.n) x = *reinterpret_cast<const uint4*>(dk + (j0 + g) * a.dk_sn + i * 32 + t4 * 8);
+            if (j0 + g + 8 < rq.n) y = *reinterpret_cast<const uint4*>(dk + (j0 + g + 8) * a.dk_sn + i * 32 + t4 * 8);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint4 b = *reinterpret_cast<const uint4*>(raw + ((nt * 8 + g) * D + i * 32 + t4 * 8) * 2);
+              mma<true>(s[nt], x.x, y.x, x.y, y.y, b.x, b.y);
+              mma<true>(s[nt], x.z, y.z, x.w, y.w, b.z, b.w);
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int row = row0 + nt * 8 + 2 * t4 + (e & 1), j = j0 + (e < 2 ? g : g + 8);
+              const bool see = j < rq.n && row < rq.n * a.G && sees(a, rq, row / a.G, j);
+              s[nt][e] = see ? s[nt][e] * a.scale_log2 : -INFINITY;
+            }
+          settle(s, 0.f, 0.f);
+          uint32_t b0[NT], b1[NT];
+          float p[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              l_run[nt][e & 1] += ex2(s[nt][e] - ref_s[nt][e & 1]);
+              p[nt][e] = ex2(s[nt][e] - ref_v[nt][e & 1] + kLift);
+            }
+            b0[nt] = turn(pack_bf16(p[nt][0], p[nt][1]));  // bf16, as the Values they meet
+            b1[nt] = turn(pack_bf16(p[nt][2], p[nt][3]));
+          }
+          // A Value that is not finite must not meet the zero weights of the nodes that do not see it: it is
+          // taken out of the product and added for the nodes that do.
+          bool odd = false;
+          constexpr int VP = D >= 64 ? 4 : 2;  // words (of two dims) read at once
+#pragma unroll
+          for (int i = 0; i < KS / VP; ++i) {
+            // the thread's dims, as the codes' products have them: D/8 in a row (D = 256: 16 and 16)
+            const int d = D == 256 ? (i >> 1) * 128 + g * 16 + (i & 1) * 8 : g * (D / 8) + i * 8;
+            uint32_t x[4][VP];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int j = j0 + 2 * t4 + (k & 1) + (k >> 1) * 8;
+#pragma unroll
+              for (int c = 0; c < VP; ++c) x[k][c] = 0;
+              if (j < rq.n) {
+                const uint16_t* v = dv + j * a.dv_sn + d;
+                if constexpr (VP == 4) {
+                  const uint4 y = *reinterpret_cast<const uint4*>(v);
+                  x[k][0] = y.x, x[k][1] = y.y, x[k][2] = y.z, x[k][3] = y.w;
+                } else {
+                  const uint2 y = *reinterpret_cast<const uint2*>(v);
+                  x[k][0] = y.x, x[k][1] = y.y;
+                }
+#pragma unroll
+                for (int c = 0; c < VP; ++c) {
+                  if ((x[k][c] & 0x7F800000u) == 0x7F800000u) x[k][c] &= 0x0000FFFFu, odd = true;
+                  if ((x[k][c] & 0x00007F80u) == 0x00007F80u) x[k][c] &= 0xFFFF0000u, odd = true;
+                }
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < VP; ++c) {
+              const uint32_t a0 = __byte_perm(x[0][c], x[1][c], 0x5410), a1 = __byte_perm(x[0][c], x[1][c], 0x7632);
+              const uint32_t a2 = __byte_perm(x[2][c], x[3][c], 0x5410), a3 = __byte_perm(x[2][c], x[3][c], 0x7632);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma<true>(o[nt][i * VP + c], a0, a1, a2, a3, b0[nt], b1[nt]);
+            }
+          }
+          if (__any_sync(kFull, odd)) {
+#pragma unroll 1
+            for (int k = 0; k < kTok && j0 + k < rq.n; ++k)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float w0 = __shfl_sync(kFull, p[nt][e], (k & 7) * 4 + t4);
+                  const float w1 = __shfl_sync(kFull, p[nt][e + 2], (k & 7) * 4 + t4);
+                  const int row = row0 + nt * 8 + 2 * t4 + e;
+                  if (row >= rq.n * a.G || !sees(a, rq, row / a.G, j0 + k)) continue;
+#pragma unroll
+                  for (int n = 0; n < KS; ++n)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                      const int d = (D == 256 ? (n >> 3) * 128 + g * 16 + (n & 7) * 2 : g * (D / 8) + n * 2) + x;
+                      const uint32_t v = dv[(j0 + k) * a.dv_sn + d];
+                      if ((v & 0x7F80u) == 0x7F80u) o[nt][n][x * 2 + e] += (k < 8 ? w0 : w1) * __uint_as_float(v << 16);
+                    }
+                }
+          }
+        }
+      }
+      __syncwarp();
+      st = st == S - 1 ? 0 : st + 1;
+    }
+    cp_wait<0>();
+    __syncthreads();
+    // the warps' shares, joined through the ring's memory, in terms of ref_s
+    float* jm = join + kWarps * M * D;
+    float* jl = jm + kWarps * M;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int m = nt * 8 + 2 * t4 + e;
+        float l = l_run[nt][e];
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(kFull, l, x);
+        if (g == 0) {
+          jm[w * M + m] = ref_s[nt][e] == kNone ? -INFINITY : ref_s[nt][e];
+          jl[w * M + m] = l;
+        }
+        const float f = ex2(ref_v[nt][e] - kLift - ref_s[nt][e]);
+#pragma unroll
+        for (int n = 0; n < KS; ++n) {
+          const int d = D == 256 ? (n >> 3) * 128 + g * 16 + (n & 7) * 2 : g * (D / 8) + n * 2;
+          *reinterpret_cast<float2*>(join + (w * M + m) * D + d) = make_float2(o[nt][n][e] * f, o[nt][n][e + 2] * f);
+        }
+      }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == rq.tiles;
+    float* part = partial_slot(a, blockIdx.x, u == pl.u0 ? 0 : 1, M, D);
+    for (int i = tid; i < rows * (D / 4); i += kThreads) {
+      const int m = i / (D / 4), d = (i - m * (D / 4)) * 4;
+      float mm = jm[m];
+#pragma unroll
+      for (int x = 1; x < kWarps; ++x) mm = fmaxf(mm, jm[x * M + m]);
+      const float ref = mm == -INFINITY ? 0.f : mm;
+      float l = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) {
+        const float f = ex2(jm[x * M + m] - ref);
+        const float4 y = *reinterpret_cast<const float4*>(join + (x * M + m) * D + d);
+        l += jl[x * M + m] * f;
+        acc.x += y.x * f;
+        acc.y += y.y * f;
+        acc.z += y.z * f;
+        acc.w += y.w * f;
+      }
+      if (whole) {
+        const int row = row0 + m;
+        const long long at = (long long)(rq.node0 + row / a.G) * a.Hq + h * a.G + row % a.G;
+        const float inv = row_inv(l);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + d) =
+            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        if (d == 0 && a.lse) a.lse[at] = row_lse(mm, l);
+      } else {
+        *reinterpret_cast<float4*>(part + m * D + d) = acc;
+        if (d == 0) {
+          part[M * D + m] = mm;
+          part[M * D + M + m] = l;
+        }
+      }
+    }
+    __syncthreads();
+    u += t1 - t0;
+  }
+}
+
+template <int D, int NT, bool PG>
+cudaError_t go(const AttnArgs& a, cudaStream_t s) {
+  constexpr int smem = Kv8Smem<D, NT>::bytes;
+  const cudaError_t e =
+      cudaFuncSetAttribute(attn_kv8_kernel<D, NT, PG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  attn_kv8_kernel<D, NT, PG><<<a.grid, kThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D, int NT>
+AttnPlan plan_n() {
+  int per = 227 * 1024 / (Kv8Smem<D, NT>::bytes + 1024 + 256);
+  if (per > kv8_blocks<D, NT>()) per = kv8_blocks<D, NT>();
+  return AttnPlan{AttnPlan::kKv8, NT * 8, kTK, sm_count() * (per < 1 ? 1 : per)};
+}
+template <int D>
+AttnPlan plan_d(int rows) {
+  if (rows <= 8) return plan_n<D, 1>();
+  if (rows <= 16 || D == 256) return plan_n<D, 2>();
+  return plan_n<D, D == 256 ? 2 : 4>();
+}
+template <int D>
+cudaError_t go_d(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
+  const bool pg = a.kc.bs % kTok == 0;
+  if (pl.M == 8) return pg ? go<D, 1, true>(a, s) : go<D, 1, false>(a, s);
+  if (pl.M == 16) return pg ? go<D, 2, true>(a, s) : go<D, 2, false>(a, s);
+  return pg ? go<D, D == 256 ? 2 : 4, true>(a, s) : go<D, D == 256 ? 2 : 4, false>(a, s);
+}
+
+}  // namespace
+}  // namespace kk

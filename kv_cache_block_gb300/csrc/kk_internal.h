@@ -11,7 +11,7 @@ constexpr int kMaxK = 256;         // top-K
 constexpr int kMaxCluster = 16;    // CTAs per request in the step kernel
 constexpr int kMergeSlots = 2048;  // cluster size * K
 
-enum ErrorCode { kErrBadIndex = 4, kErrTimeout = 5 };
+enum ErrorCode { kErrBadIndex = 4, kErrTimeout = 5, kErrNoPages = 6 };
 
 // Stability-ranked keys keep a block index in 27 bits (see make_stab_key).
 constexpr int kStabIdxBits = 27;
@@ -19,7 +19,7 @@ constexpr uint32_t kStabIdxMask = (1u << kStabIdxBits) - 1u;
 
 struct KCache {
   const void* base;
-  int dtype;  // 0 f32, 1 bf16
+  int dtype;  // 0 f32, 1 bf16, 2 e4m3
   int L, H, D, bs, num_pages;
   long long sL, sP, sH, sT;  // element strides
 };

@@ -1,0 +1,180 @@
+// kk_kv8_write: new tokens' Keys and Values as e4m3 codes with a power-of-two
+// scale for each (page, layer, KV head), bound by the bytes of the new tokens.
+//
+// An item is what one request adds to one page of one (layer, head), Keys or
+// Values: the largest finite magnitude of its new tokens gives the scale, then
+// they are divided by it (a multiplication by its inverse, exact) and rounded
+// once, to nearest even. Where the page held older tokens and its scale grows,
+// their codes move with it. One warp takes an item of few tokens (a decode
+// step: the item is one row), a block of eight warps one of many. The new
+// tokens stay in registers between the two passes, up to 8 vectors of 16 bytes
+// a thread (a page of 128 tokens of 128 bf16 dims in a block); larger items
+// read them again, from L2.
+#include "kk_device.cuh"
+#include "kk_write8.cuh"
+
+namespace kk {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kKeep = 8;  // vectors a thread keeps
+
+// Two values as e4m3, each rounded to nearest even; NaN for what is not finite.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float only_finite(float x) {
+  return (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u ? __uint_as_float(0x7FFFFFFFu) : x;
+}
+
+// The smallest power of two that is at least amax / 448, and at least 2^-126.
+__device__ __forceinline__ float pow2_scale(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  // 448 = 1.75 * 2^8: one exponent more where the mantissa is above 1.75
+  const int e = (int)(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u);
+  return __uint_as_float((uint32_t)(e < 1 ? 1 : e) << 23);
+}
+
+
+template <typename T, int D, int W>
+__global__ void __launch_bounds__(kThreads) write8_kernel(const Write8Args a) {
+  constexpr int E = Vec16<T>::kElems, CH = D / E;  // elements of a vector, vectors of a row
+  constexpr int NTH = W * 32, IPB = kThreads / NTH;  // threads of an item, items of a block
+  __shared__ float s_max[kThreads / 32];
+  const int tid = threadIdx.x % NTH, sub = threadIdx.x / NTH;
+  const int r = blockIdx.z, H = a.kc.H;
+  const int item = blockIdx.y * IPB + sub, items = a.layers * H * a.sides;
+  // the request's new tokens, and the page this item is about
+  const int n0 = a.token_off ? a.token_off[r] : r * a.max_new;
+  const int n = (a.token_off ? a.token_off[r + 1] : n0 + a.max_new) - n0;
+  const int off = a.bt.offsets[r], nb = a.bt.offsets[r + 1] - off, T1 = a.bt.seq_lens[r], bs = a.kc.bs;
+  const bool ok = n0 >= 0 && n >= 0 && n <= a.max_new && n0 + (long long)n <= a.num_nodes && T1 >= n &&
+                  T1 <= kMaxTokens && nb >= 0 && nb <= a.bt.max_blocks &&
+                  nb == (int)(((unsigned)T1 + (unsigned)bs - 1u) / (unsigned)bs);
+  const bool first = threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0;
+  if (!ok) {
+    if (first) flag_error(a.err, kErrBadIndex);
+    return;
+  }
+  const int t0 = T1 - n;
+  const long long bl = t0 / bs + (long long)blockIdx.x;
+  if (n == 0 || bl >= nb) return;
+  const int b = (int)bl;
+  const int page = a.bt.pages[off + b];
+  if (page < 0 || page >= a.kc.num_pages) {
+    if (threadIdx.x == 0 && blockIdx.y == 0) flag_error(a.err, kErrBadIndex);
+    return;
+  }
+  const bool real = item < items;  // a block of several items may have some left over
+  const int kv = real ? item % a.sides : 0, h = real ? item / a.sides % H : 0, l = real ? item / (a.sides * H) : 0;
+  const Write8Side& x = a.side[kv];
+  const int lo = max(t0, b * bs), hi = min((long long)T1, (b + 1ll) * bs), had = lo - b * bs;
+  const int vecs = real ? (hi - lo) * CH : 0;
+  const long long src = (l * x.sl + (n0 + lo - t0) * x.sn + h * x.sh) * (16 / E);
+  const char* from = static_cast<const char*>(x.src) + src;
+  const long long row_bytes = x.sn * (16 / E);
+  uint4 keep[kKeep];
+  float top = 0.f;
+  auto measure = [&](const uint4& v) {
+    float f[E];
+    Vec16<T>::unpack(v, f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float y = fabsf(f[e]);
+      top = fmaxf(top, y < INFINITY ? y : 0.f);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) {
+    const int i = tid + k * NTH;
+    keep[k] = make_uint4(0, 0, 0, 0);
+    if (i < vecs) keep[k] = *reinterpret_cast<const uint4*>(from + (i / CH) * row_bytes + (i % CH) * 16);
+  }
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) measure(keep[k]);
+  for (int i = tid + kKeep * NTH; i < vecs; i += NTH)
+    measure(*reinterpret_cast<const uint4*>(from + (i / CH) * row_bytes + (i % CH) * 16));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W; ++w) top = fmaxf(top, s_max[w]);
+  }
+  if (!real) return;
+  float* at = x.scale + ((long long)(a.layer + l) * a.kc.num_pages + page) * H + h;
+  const float old = had ? *at : 0.f, fresh = pow2_scale(top), now = fmaxf(old, fresh);
+  const float inv = 1.f / now;
+  char* codes = static_cast<char*>(x.codes) + (a.layer + l) * x.dL + page * x.dP + h * x.dH;
+  if constexpr (W > 1) __syncthreads();  // every thread has read the scale
+  else __syncwarp();
+  if (tid == 0) *at = now;
+  auto store = [&](int i, const uint4& v) {
+    float f[E];
+    Vec16<T>::unpack(v, f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = only_finite(f[e]) * inv;
+    char* to = codes + (had + i / CH) * x.dT + (i % CH) * E;
+    const uint32_t p = to_e4m3x2(f[0], f[1]) | to_e4m3x2(f[2], f[3]) << 16;
+    if constexpr (E == 8)
+      *reinterpret_cast<uint2*>(to) = make_uint2(p, to_e4m3x2(f[4], f[5]) | to_e4m3x2(f[6], f[7]) << 16);
+    else
+      *reinterpret_cast<uint32_t*>(to) = p;
+  };
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k)
+    if (tid + k * NTH < vecs) store(tid + k * NTH, keep[k]);
+  for (int i = tid + kKeep * NTH; i < vecs; i += NTH)
+    store(i, *reinterpret_cast<const uint4*>(from + (i / CH) * row_bytes + (i % CH) * 16));
+  if (had && old > 0.f && old < now) {  // the page's older codes, in terms of the new scale
+    const float f = old * inv;
+    for (int i = tid; i < had * (D / 4); i += NTH) {
+      uint32_t* p = reinterpret_cast<uint32_t*>(codes + (i / (D / 4)) * x.dT + (i % (D / 4)) * 4);
+      const uint32_t c = *p;
+      float y[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t two;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"((uint16_t)(e ? c >> 16 : c)));
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+            : "=f"(y[2 * e]), "=f"(y[2 * e + 1])
+            : "r"(two));
+      }
+      *p = to_e4m3x2(y[0] * f, y[1] * f) | to_e4m3x2(y[2] * f, y[3] * f) << 16;
+    }
+  }
+}
+
+template <typename T, int D>
+cudaError_t go(const Write8Args& a, cudaStream_t s) {
+  const long long pieces = (a.max_new + a.kc.bs - 2ll) / a.kc.bs + 1;  // pages that max_new tokens reach, at most
+  const int items = a.layers * a.kc.H * a.sides;
+  // a warp an item while its threads keep every vector
+  const bool small = std::min(a.max_new, a.kc.bs) * (D / Vec16<T>::kElems) <= kKeep * 32;
+  const int ipb = small ? kThreads / 32 : 1;
+  const dim3 grid((unsigned)pieces, (unsigned)((items + ipb - 1) / ipb), (unsigned)a.bt.R);
+  if (small) write8_kernel<T, D, 1><<<grid, kThreads, 0, s>>>(a);
+  else write8_kernel<T, D, kThreads / 32><<<grid, kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t go_t(const Write8Args& a, cudaStream_t s) {
+  switch (a.kc.D) {
+    case 32: return go<T, 32>(a, s);
+    case 64: return go<T, 64>(a, s);
+    case 128: return go<T, 128>(a, s);
+    case 256: return go<T, 256>(a, s);
+  }
+  return cudaErrorNotSupported;
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_write(const Write8Args& a, cudaStream_t s) {
+  return a.f32 ? go_t<float>(a, s) : go_t<bf16_t>(a, s);
+}
+
+}  // namespace kk

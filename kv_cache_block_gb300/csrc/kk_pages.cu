@@ -1,0 +1,469 @@
+// Pages with reference counts: taken, given back, forked and compacted
+// (kk_pages_alloc, kk_pages_free, kk_pages_fork, kk_pages_compact).
+//
+// What is to be done is planned on the device, so that a beam search's step
+// needs no word from the host: one cluster of up to eight CTAs goes through the
+// tables and counts in phases that a cluster barrier separates (a few
+// microseconds, where a launch a phase would cost each of them its latency), and
+// leaves a list of (from, to) pages. The copies, the part that moves bytes,
+// follow in a launch that fills the GPU. Counts change by integer atomics and
+// free pages are taken in ascending order: the result does not depend on timing.
+#include "kk_pages.cuh"
+
+#include <algorithm>
+#include <climits>
+
+#include "kk_device.cuh"
+#include "kk_pdl.cuh"
+
+namespace kk {
+namespace {
+
+constexpr int kPlan = 1024;       // threads of a planning CTA
+constexpr int kPlanCtas = 8;      // CTAs of the planning cluster, at most
+constexpr int kStep = kPlan * 4;  // counts a CTA looks at in a turn
+
+__device__ __forceinline__ void cluster_sync() {
+  __threadfence();
+  cluster_arrive_release();
+  cluster_wait_acquire();
+}
+struct Place {  // of a thread in the planning cluster
+  int cta, ctas, tid, all, n;  // its number among all n threads
+};
+__device__ __forceinline__ Place place() {
+  Place p;
+  p.cta = (int)cluster_rank();
+  p.ctas = (int)cluster_size();
+  p.tid = threadIdx.x;
+  p.all = p.cta * kPlan + p.tid;
+  p.n = p.ctas * kPlan;
+  return p;
+}
+
+// Exclusive sum of x over the CTA's threads; *total gets the sum. `sh`: 33 ints.
+__device__ __forceinline__ int block_scan(int x, int* sh, int* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int v = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, v, o);
+    if (lane >= o) v += y;
+  }
+  __syncthreads();
+  if (lane == 31) sh[w] = v;
+  __syncthreads();
+  if (w == 0) {
+    int y = sh[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(kFull, y, o);
+      if (lane >= o) y += z;
+    }
+    sh[lane] = y;
+  }
+  __syncthreads();
+  *total = sh[31];
+  return v - x + (w ? sh[w - 1] : 0);
+}
+
+// The same integer of every CTA of the cluster, summed over those before this one and over all.
+// `box`: kPlanCtas ints of shared memory, not used again before the next cluster barrier but one.
+__device__ __forceinline__ void cluster_sums(int mine, int* box, const Place& p, int* before, int* total) {
+  if (p.tid < p.ctas) st_cluster_s32(map_to_rank(smem_u32(box + p.cta), (uint32_t)p.tid), mine);
+  cluster_arrive_release();
+  cluster_wait_acquire();
+  int b = 0, t = 0;
+  for (int c = 0; c < p.ctas; ++c) {
+    if (c < p.cta) b += box[c];
+    t += box[c];
+  }
+  *before = b;
+  *total = t;
+}
+
+__device__ __forceinline__ void copy_refs(const int* in, int* out, int n, const Place& p) {
+  if (in == out) return;
+  for (int i = p.all; i < n; i += p.n) out[i] = in[i];
+}
+
+// Calls take(k, page) for the k-th free page in ascending order, k < need; returns how many there were, at most
+// `need`. All threads of the cluster call it. Reads counts past L1: they change during the kernel.
+template <typename F>
+__device__ __forceinline__ int take_free(const int* refs, int pages, int need, const Place& p, int* sh, int* box,
+                                         F take) {
+  int found = 0;
+  for (long long at = 0, turn = 0; at < pages && found < need; at += (long long)p.ctas * kStep, turn ^= 1) {
+    const long long i0 = at + (long long)p.cta * kStep + p.tid * 4;
+    int free4 = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (i0 + e < pages && __ldcg(refs + i0 + e) == 0) free4 |= 1 << e;
+    int mine, before, total;
+    int k = block_scan(__popc(free4), sh, &mine);
+    cluster_sums(mine, box + turn * kPlanCtas, p, &before, &total);
+    k += found + before;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (free4 >> e & 1) {
+        if (k < need) take(k, (int)(i0 + e));
+        ++k;
+      }
+    found += total;
+  }
+  return min(found, need);
+}
+
+// Warps [first, n) of the cluster share out the items of x < count, each item's `parts` warps having a part of
+// it: calls f(item, first element of the lane, step).
+template <typename F>
+__device__ __forceinline__ void share_warps(int wid, int n, int count, F f) {
+  if (wid < 0 || count <= 0) return;
+  const int parts = max(1, n / count), lane = threadIdx.x & 31;
+  for (long long x = wid; x < (long long)count * parts; x += n)
+    f((int)(x / parts), (int)(x % parts) * 32 + lane, parts * 32);
+}
+
+__global__ void __launch_bounds__(kPlan) pages_free_kernel(Table bt, const int* refs_in, int* refs_out, int pages,
+                                                           int* err) {
+  const Place p = place();
+  copy_refs(refs_in, refs_out, pages, p);
+  if (refs_in != refs_out) cluster_sync();
+  share_warps(p.all >> 5, p.n >> 5, bt.R, [&](int r, int j0, int step) {
+    const int off = bt.offsets[r], nb = bt.offsets[r + 1] - off;
+    if (nb < 0 || nb > bt.max_blocks) {
+      flag_error(err, kErrBadIndex);
+      return;
+    }
+    for (int j = j0; j < nb; j += step) {
+      const int page = bt.pages[off + j];
+      if (page < 0 || page >= pages) {
+        flag_error(err, kErrBadIndex);
+      } else if (atomicSub(refs_out + page, 1) <= 0) {  // was free: as many succeed as there were counts
+        atomicAdd(refs_out + page, 1);
+        flag_error(err, kErrBadIndex);
+      }
+    }
+  });
+}
+
+__global__ void __launch_bounds__(kPlan) pages_alloc_kernel(const int* refs_in, int* refs_out, int pages,
+                                                            const int* want, int n, int* out, int* err) {
+  __shared__ int sh[33], box[2 * kPlanCtas];
+  const Place p = place();
+  copy_refs(refs_in, refs_out, pages, p);
+  int need = n;
+  if (want) {  // every CTA counts for itself
+    int mine = 0;
+    for (int i = p.tid; i < n; i += kPlan) mine += want[i] != 0;
+    int total;
+    block_scan(mine, sh, &total);
+    need = total;
+  }
+  cluster_sync();
+  // pages in the order of the takers first: taker k's page at out[k]
+  const int got = take_free(refs_out, pages, need, p, sh, box, [&](int k, int page) {
+    refs_out[page] = 1;
+    out[k] = page;
+  });
+  cluster_sync();
+  if (p.cta) return;
+  if (got < need && p.tid == 0) flag_error(err, kErrNoPages);
+  // then to the takers' places, the last ones first: taker k's place is not before k, so what is still to be
+  // read lies in front of everything written
+  int left = need;
+  for (int c = (n + kPlan - 1) / kPlan - 1; c >= 0; --c) {
+    const int i = c * kPlan + p.tid;
+    const bool takes = i < n && (!want || want[i] != 0);
+    int total;
+    const int k = left + block_scan(takes ? 1 : 0, sh, &total) - total;
+    left -= total;
+    const int page = takes && k < got ? __ldcg(out + k) : -1;
+    __syncthreads();
+    if (i < n) out[i] = page;
+    __syncthreads();
+  }
+}
+
+// A parent as its children take it; n < 0: its table disagrees with its length.
+struct Parent {
+  int off, n, T;
+  bool part;  // its last block is not full
+};
+__device__ __forceinline__ Parent parent_of(const ForkArgs& a, int r) {
+  Parent x;
+  x.off = a.bt.offsets[r];
+  x.n = a.bt.offsets[r + 1] - x.off;
+  x.T = a.bt.seq_lens[r];
+  if (x.T < 0 || x.T > kMaxTokens || x.n < 0 || x.n > a.bt.max_blocks ||
+      x.n != (int)(((unsigned)x.T + (unsigned)a.bs - 1u) / (unsigned)a.bs))
+    x.n = -1;
+  x.part = x.n > 0 && x.T % a.bs != 0;
+  return x;
+}
+
+__global__ void __launch_bounds__(kPlan) pages_fork_kernel(const ForkArgs a) {
+  __shared__ int sh[33], box[2 * kPlanCtas];
+  const Place p = place();
+  pdl_launch_dependents();
+  copy_refs(a.refs_in, a.refs_out, a.num_pages, p);
+  for (int r = p.all; r < a.bt.R; r += p.n) {
+    a.kids[r] = 0;
+    a.first[r] = INT_MAX;
+  }
+  cluster_sync();
+  for (int i = p.all; i < a.F; i += p.n) {
+    const int r = a.parent[i];
+    const bool ok = r >= 0 && r < a.bt.R && parent_of(a, r).n >= 0;
+    if (!ok) {
+      flag_error(a.err, kErrBadIndex);
+      continue;
+    }
+    atomicAdd(a.kids + r, 1);
+    atomicMin(a.first + r, i);
+  }
+  cluster_sync();
+  // CTA 0 lays the children out, the others (or it, alone) move the counts
+  if (p.cta == 0) {
+    int off = 0, copies = 0;
+    for (int i0 = 0; i0 < a.F; i0 += kPlan) {
+      const int i = i0 + p.tid;
+      int r = -1, n = 0, T = 0, last = 0;
+      bool copy = false;
+      if (i < a.F) {
+        r = a.parent[i];
+        if (r >= 0 && r < a.bt.R) {
+          const Parent x = parent_of(a, r);
+          if (x.n >= 0) {
+            n = x.n;
+            T = x.T;
+            copy = x.part && (a.keep || __ldcg(a.first + r) != i);
+            if (copy) last = a.bt.pages[x.off + n - 1];
+          }
+        }
+      }
+      int total;
+      const int to = off + block_scan(n, sh, &total);
+      off += total;
+      const int k = copies + block_scan(copy ? 1 : 0, sh, &total);
+      copies += total;
+      if (i < a.F) {
+        a.child_offsets[i] = to;
+        a.child_lens[i] = T;
+        if (copy) {
+          a.pairs[k] = make_int2(last, -1);
+          a.at[k] = to + n - 1;
+        }
+      }
+    }
+    if (p.tid == 0) {
+      a.child_offsets[a.F] = off;
+      a.at[a.F] = copies;
+    }
+  }
+  const int lead = p.ctas > 1 ? kPlan / 32 : 0;  // CTA 0's warps stay out
+  share_warps((p.all >> 5) - lead, (p.n >> 5) - lead, a.bt.R, [&](int r, int j0, int step) {
+    const Parent x = parent_of(a, r);
+    const int kids = __ldcg(a.kids + r);
+    for (int j = j0; j < x.n; j += step) {
+      const int page = a.bt.pages[x.off + j];
+      const int more = j == x.n - 1 && x.part ? (a.keep ? 0 : (kids ? 0 : -1)) : (a.keep ? kids : kids - 1);
+      if (page < 0 || page >= a.num_pages) {
+        flag_error(a.err, kErrBadIndex);
+      } else if (more) {
+        if (atomicAdd(a.refs_out + page, more) + more < 0) flag_error(a.err, kErrBadIndex);
+      }
+    }
+  });
+  cluster_sync();
+  share_warps(p.all >> 5, p.n >> 5, a.F, [&](int i, int j0, int step) {
+    const int to = __ldcg(a.child_offsets + i), n = __ldcg(a.child_offsets + i + 1) - to;
+    if (n == 0) return;
+    const int r = a.parent[i];
+    const Parent x = parent_of(a, r);
+    const bool copy = x.part && (a.keep || __ldcg(a.first + r) != i);
+    for (int j = j0; j < n - (copy ? 1 : 0); j += step) a.child_pages[to + j] = a.bt.pages[x.off + j];
+  });
+  const int need = __ldcg(a.at + a.F);
+  const int got = take_free(a.refs_out, a.num_pages, need, p, sh, box, [&](int k, int page) {
+    a.refs_out[page] = 1;
+    a.pairs[k].y = page;
+    a.child_pages[__ldcg(a.at + k)] = page;
+  });
+  for (int k = got + p.all; k < need; k += p.n) a.child_pages[__ldcg(a.at + k)] = -1;
+  if (p.all == 0) {
+    *a.n_pairs = got;
+    if (got < need) flag_error(a.err, kErrNoPages);
+  }
+}
+
+__global__ void __launch_bounds__(kPlan) pages_compact_kernel(const CompactArgs a) {
+  __shared__ int sh[33], box[2 * kPlanCtas];
+  const Place p = place();
+  pdl_launch_dependents();
+  cluster_sync();  // every CTA of the cluster runs before another writes to its shared memory
+  // a CTA's share of the pages, in order
+  const long long per = ((long long)a.num_pages + p.ctas - 1) / p.ctas;
+  const int lo = (int)min((long long)a.num_pages, per * p.cta), hi = (int)min((long long)a.num_pages, per * (p.cta + 1));
+  int mine = 0, total, before, used;
+  for (int i = lo + p.tid; i < hi; i += kPlan) mine += a.refs_in[i] != 0;
+  block_scan(mine, sh, &total);
+  cluster_sums(total, box, p, &before, &used);
+  // `before`: used pages in front of the share; those below `used` stay
+  mine = 0;
+  for (int i = lo + p.tid; i < min(hi, used); i += kPlan) mine += a.refs_in[i] != 0;
+  block_scan(mine, sh, &total);
+  int dummy, stay;
+  cluster_sums(total, box + kPlanCtas, p, &dummy, &stay);
+  const int moves = used - stay;
+  int seen = before;
+  for (int i0 = lo; i0 < hi; i0 += kStep) {
+    int f = 0, n;
+    const int i = i0 + p.tid * 4;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (i + e < hi && a.refs_in[i + e] != 0) f |= 1 << e;
+    int k = seen + block_scan(__popc(f), sh, &n);  // used pages in front of page i
+    seen += n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int page = i + e;
+      if (page >= hi) break;
+      const bool on = f >> e & 1;
+      a.remap[page] = on ? page : -1;
+      if (on && page >= used) a.pairs[k - stay].x = page;
+      if (!on && page < used) a.pairs[page - k].y = page;
+      k += on;
+    }
+  }
+  cluster_sync();  // the counts have been read: they may be moved where they lie
+  copy_refs(a.refs_in, a.refs_out, a.num_pages, p);
+  if (a.refs_in != a.refs_out) cluster_sync();
+  for (int k = p.all; k < moves; k += p.n) {
+    const int2 m = __ldcg(a.pairs + k);
+    a.remap[m.x] = m.y;
+    a.refs_out[m.y] = __ldcg(a.refs_out + m.x);
+    a.refs_out[m.x] = 0;
+  }
+  if (p.all == 0) {
+    *a.n_pairs = moves;
+    *a.used = used;
+  }
+  cluster_sync();
+  for (long long i = p.all; i < a.n; i += p.n) {
+    const int page = a.pages_in[i];
+    int to = -1;
+    if (page >= 0 && page < a.num_pages) to = __ldcg(a.remap + page);
+    if (to < 0 && page != -1) flag_error(a.err, kErrBadIndex);
+    a.pages_out[i] = to;
+  }
+}
+
+// One page of every array is cut into chunks of kUnroll vectors a thread; CTAs take (pair, chunk) in turn.
+constexpr int kCopy = 256, kUnroll = 8;
+
+template <typename V>
+__device__ __forceinline__ void copy_chunk(const char* from, char* to, long long n) {
+  V x[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int i = u * kCopy + threadIdx.x;
+    if (i < n) x[u] = __ldcs(reinterpret_cast<const V*>(from) + i);
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int i = u * kCopy + threadIdx.x;
+    if (i < n) reinterpret_cast<V*>(to)[i] = x[u];
+  }
+}
+
+__global__ void __launch_bounds__(kCopy) pages_copy_kernel(const PageArrays pa, const int2* pairs, const int* n_pairs,
+                                                           int num_pages) {
+  pdl_wait();
+  const long long units = (long long)*n_pairs * pa.chunks;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const long long pair = u / pa.chunks, c0 = u - pair * pa.chunks;
+    const int2 m = pairs[pair];
+    if (m.x < 0 || m.x >= num_pages || m.y < 0 || m.y >= num_pages) continue;  // a bad page of a parent's table
+    int x = 0;
+    while (x + 1 < pa.n && c0 >= pa.a[x + 1].first) ++x;
+    const PageArray& d = pa.a[x];
+    const long long per = d.chunks / d.slices, c = c0 - d.first, s = c / per, b = (c - s * per) * kCopy * kUnroll * d.vec;
+    const char* from = d.base + s * d.slice + m.x * d.page + b;
+    char* to = d.base + s * d.slice + m.y * d.page + b;
+    const long long n = (d.bytes - b) / d.vec;
+    if (d.vec == 16) copy_chunk<uint4>(from, to, n);
+    else copy_chunk<uint32_t>(from, to, n);
+  }
+}
+
+// The planning cluster: as many CTAs as there is work for.
+template <typename... P, typename... A>
+cudaError_t launch_plan(void (*k)(P...), long long work, cudaStream_t s, A... args) {
+  int ctas = 1;
+  while (ctas < kPlanCtas && work > (long long)ctas * kStep) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kPlan);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)ctas;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+cudaError_t launch_copies(const PageArrays& pa, const int2* pairs, const int* n_pairs, long long most, int num_pages,
+                          cudaStream_t s) {
+  if (pa.n == 0 || most == 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::max(1ll, std::min(most * pa.chunks, 8ll * sm_count())));
+  cfg.blockDim = dim3(kCopy);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, pages_copy_kernel, pa, pairs, n_pairs, num_pages);
+}
+
+}  // namespace
+
+void plan_page_arrays(PageArrays* pa) {
+  pa->chunks = 0;
+  for (int i = 0; i < pa->n; ++i) {
+    PageArray& d = pa->a[i];
+    d.vec = (reinterpret_cast<uintptr_t>(d.base) | (uintptr_t)d.slice | (uintptr_t)d.page | (uintptr_t)d.bytes) % 16 ? 4 : 16;
+    const long long chunk = (long long)kCopy * kUnroll * d.vec;
+    d.chunks = (d.bytes + chunk - 1) / chunk * d.slices;
+    d.first = pa->chunks;
+    pa->chunks += d.chunks;
+  }
+}
+
+cudaError_t launch_pages_alloc(const int* refs_in, int* refs_out, int num_pages, const int* want, int n, int* out,
+                               int* err, cudaStream_t s) {
+  return launch_plan(pages_alloc_kernel, num_pages, s, refs_in, refs_out, num_pages, want, n, out, err);
+}
+
+cudaError_t launch_pages_free(const Table& bt, const int* refs_in, int* refs_out, int num_pages, int* err,
+                              cudaStream_t s) {
+  const long long work = (long long)bt.R * bt.max_blocks + (refs_in == refs_out ? 0 : num_pages);
+  return launch_plan(pages_free_kernel, work, s, bt, refs_in, refs_out, num_pages, err);
+}
+
+cudaError_t launch_pages_fork(const ForkArgs& f, const PageArrays& pa, cudaStream_t s) {
+  const long long work = std::max<long long>(f.num_pages, 2ll * f.F * f.bt.max_blocks);
+  const cudaError_t e = launch_plan(pages_fork_kernel, work, s, f);
+  return e != cudaSuccess ? e : launch_copies(pa, f.pairs, f.n_pairs, f.F, f.num_pages, s);
+}
+
+cudaError_t launch_pages_compact(const CompactArgs& c, const PageArrays& pa, cudaStream_t s) {
+  const cudaError_t e = launch_plan(pages_compact_kernel, std::max<long long>(c.num_pages, c.n / 2), s, c);
+  return e != cudaSuccess ? e : launch_copies(pa, c.pairs, c.n_pairs, c.num_pages / 2, c.num_pages, s);
+}
+
+}  // namespace kk

@@ -18,8 +18,8 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkk.so")
 
-KK_OK, KK_ERR_INVALID, KK_ERR_UNSUPPORTED, KK_ERR_CUDA, KK_ERR_BAD_INDEX, KK_ERR_TIMEOUT = range(6)
-KK_F32, KK_BF16 = 0, 1
+KK_OK, KK_ERR_INVALID, KK_ERR_UNSUPPORTED, KK_ERR_CUDA, KK_ERR_BAD_INDEX, KK_ERR_TIMEOUT, KK_ERR_NO_PAGES = range(7)
+KK_F32, KK_BF16, KK_E4M3 = 0, 1, 2
 
 
 class KKError(RuntimeError):
@@ -76,6 +76,21 @@ class kk_selection(ctypes.Structure):
                 ("K", ctypes.c_int32)]
 
 
+class kk_rows(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("stride_node", ctypes.c_int64), ("stride_head", ctypes.c_int64),
+                ("stride_layer", ctypes.c_int64)]
+
+
+class kk_rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class kk_page_array(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("stride_slice", ctypes.c_int64), ("stride_page", ctypes.c_int64),
+                ("bytes", ctypes.c_int64), ("slices", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m kv_cache_block_gb300.build`")
@@ -84,6 +99,7 @@ def _load():
     KC, BT = ctypes.POINTER(kk_kcache_desc), ctypes.POINTER(kk_block_table)
     RG, OP = ctypes.POINTER(kk_anchor_ring), ctypes.POINTER(kk_step_options)
     TR, SL = ctypes.POINTER(kk_tree), ctypes.POINTER(kk_selection)
+    RW, RP, PA = ctypes.POINTER(kk_rows), ctypes.POINTER(kk_rope), ctypes.POINTER(kk_page_array)
     sig = {
         "kk_status_str": (ctypes.c_char_p, [ctypes.c_int]),
         "kk_debug_set_wait_limit": (ctypes.c_int, [ctypes.c_uint64]),
@@ -121,6 +137,17 @@ def _load():
         "kk_attn_mass": (ctypes.c_int, [KC, BT, I32, TR, P, I64, I64, I32, F, P, P, P, P, F, P, P, P]),
         "kk_evict_select": (ctypes.c_int, [KC, BT, P, I32, I32, I32, P, P, P]),
         "kk_evict_compact": (ctypes.c_int, [KC, KC, BT, P, I32, P, P, P, P]),
+        "kk_qk_norm_rope": (ctypes.c_int, [I32, I32, I32, I32, I32, RW, RW, RW, P, P, F, P, RP, RW, RW, KC, KC, BT, P,
+                                           I32, P]),
+        "kk_kv8_write": (ctypes.c_int, [KC, P, KC, P, BT, I32, I32, I32, RW, RW, P, I32, I32, P]),
+        "kk_tree_attn_kv8_workspace_bytes": (SZ, [KC, BT, I32, I32]),
+        "kk_tree_attn_kv8": (ctypes.c_int, [KC, P, KC, P, BT, I32, SL, TR, P, I64, I64, I32, F, P, P, P, SZ, P]),
+        "kk_pages_alloc": (ctypes.c_int, [P, P, I32, P, I32, P, P]),
+        "kk_pages_free": (ctypes.c_int, [BT, P, P, I32, P]),
+        "kk_pages_fork_workspace_bytes": (SZ, [I32, I32]),
+        "kk_pages_fork": (ctypes.c_int, [BT, I32, P, I32, I32, P, P, I32, P, I64, P, P, PA, I32, P, SZ, P]),
+        "kk_pages_compact_workspace_bytes": (SZ, [I32]),
+        "kk_pages_compact": (ctypes.c_int, [P, P, I32, P, P, I64, P, P, PA, I32, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -144,6 +171,9 @@ EXPORTS = (
     "kk_score_pool_batched", "kk_coarse_means", "kk_hier_pool_coarse_rows", "kk_hier_pool_reps",
     "kk_hier_select_pool_workspace_bytes", "kk_hier_select_pool",
     "kk_tree_attn_workspace_bytes", "kk_tree_attn", "kk_attn_mass", "kk_evict_select", "kk_evict_compact",
+    "kk_qk_norm_rope", "kk_kv8_write", "kk_tree_attn_kv8_workspace_bytes", "kk_tree_attn_kv8",
+    "kk_pages_alloc", "kk_pages_free", "kk_pages_fork_workspace_bytes", "kk_pages_fork",
+    "kk_pages_compact_workspace_bytes", "kk_pages_compact",
 )
 
 
@@ -238,7 +268,7 @@ def _strided(t, name):
 
 
 def _check_elems(kc, t, name):
-    """The element type and head_dim of a query-side tensor are the cache's."""
+    """The element type and head_dim of a query-side tensor are the cache's (of an 8-bit cache's: bf16)."""
     want = (torch.float32,) if kc.dtype == KK_F32 else (torch.bfloat16, torch.int16)
     if t.dtype not in want:
         raise TypeError(f"{name} has dtype {t.dtype}, the cache holds {want[0]}")
@@ -617,3 +647,224 @@ def kk_evict_compact(kc, vc, bt: BlockTable, kept, mass_in=None, mass_out=None, 
         ctypes.byref(kc), None if vc is None else ctypes.byref(vc), ctypes.byref(bt.c), _kept_ptr(kc, bt, kept),
         kept.shape[-1], _mass_ptr(kc, mass_in, "mass_in"), _mass_ptr(kc, mass_out, "mass_out"),
         _ptr(dst_pages, torch.int32, "dst_pages"), _stream(stream)))
+
+
+# ---- around a serving step -------------------------------------------------
+
+_ELEMS = {torch.float32: KK_F32, torch.bfloat16: KK_BF16, torch.int16: KK_BF16}
+
+
+class Rope:
+    """The rotation of a model (see kk_rope in include/kk.h); keeps its tensor alive.
+
+    ``inv_freq`` float32 [rotary_dim / 2]; ``scale`` multiplies sines and cosines."""
+
+    def __init__(self, inv_freq, rotary_dim: int, interleaved: bool = False, scale: float = 1.0):
+        if inv_freq.numel() != int(rotary_dim) // 2:
+            raise ValueError(f"inv_freq must have {int(rotary_dim) // 2} elements")
+        self.inv_freq = inv_freq
+        self.c = kk_rope(_ptr(inv_freq, torch.float32, "inv_freq"), int(rotary_dim), int(bool(interleaved)), float(scale))
+
+
+def _rows(t, name, nodes=None, heads=None, D=None, dtype=None):
+    """kk_rows of a [nodes][heads][D] tensor, or [layers][nodes][heads][D], whose last dim is dense."""
+    if t is None:
+        return None
+    x = t if t.dim() != 4 else t[0]
+    addr, sn, sh = _strided(x, name)
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    for got, want, what in ((x.shape[0], nodes, "nodes"), (x.shape[1], heads, "heads"), (x.shape[2], D, "dims")):
+        if want is not None and got != want:
+            raise ValueError(f"{name} has {got} {what}, expected {want}")
+    return kk_rows(addr, sn, sh, t.stride(0) if t.dim() == 4 else 0)
+
+
+def _ref(c):
+    return None if c is None else ctypes.byref(c)
+
+
+def kk_qk_norm_rope(q, k, rope, q_out, k_out=None, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                    v=None, kc=None, vc=None, bt=None, token_offsets=None, layer: int = 0, stream=None):
+    """Norm of every head of ``q`` and ``k`` [nodes][heads][D] (with its weights [D], else none), rotation
+    (``rope``: a :class:`Rope` or None), results to ``q_out``, ``k_out`` and the caches' slots of the new tokens."""
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("q or k must be given")
+    n, D, dt = some.shape[0], some.shape[2], some.dtype
+    if dt not in _ELEMS:
+        raise TypeError(f"q has dtype {dt}")
+    Hq, H = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and w.numel() != D:
+            raise ValueError(f"{name} must have {D} elements")
+    if positions is not None and positions.numel() != n:
+        raise ValueError(f"positions must have {n} elements")
+    if token_offsets is not None and (bt is None or token_offsets.numel() != bt.num_requests + 1):
+        raise ValueError("token_offsets must have an element more than the table has requests")
+    rows = [_rows(t, name, n, heads, D, dt) for t, name, heads in
+            ((q, "q", Hq), (k, "k", H), (v, "v", H), (q_out, "q_out", Hq), (k_out, "k_out", H))]
+    _check("kk_qk_norm_rope", _lib.kk_qk_norm_rope(
+        _ELEMS[dt], n, Hq, H, D, _ref(rows[0]), _ref(rows[1]), _ref(rows[2]), _ptr(q_weight, dt, "q_weight"),
+        _ptr(k_weight, dt, "k_weight"), float(eps), _ptr(positions, torch.int32, "positions"),
+        None if rope is None else ctypes.byref(rope.c), _ref(rows[3]), _ref(rows[4]), _ref(kc), _ref(vc),
+        None if bt is None else ctypes.byref(bt.c), _ptr(token_offsets, torch.int32, "token_offsets"), layer,
+        _stream(stream)))
+
+
+def _scale_ptr(kc, scale, name):
+    if kc is not None and (scale is None or scale.numel() != kc.num_layers * kc.num_pages * kc.num_kv_heads):
+        raise ValueError(f"{name} must be [layers][pages][KV heads]")
+    return _ptr(scale, torch.float32, name)
+
+
+def kk_kv8_write(kc, k_scale, vc, v_scale, bt: BlockTable, layer: int, k, v, max_new: int, token_offsets=None,
+                 stream=None):
+    """The requests' newest tokens into 8-bit caches: ``k``, ``v`` [layers][nodes][KV heads][D] (or without the
+    first dim: one layer), for the layers from ``layer`` on; at most ``max_new`` a request."""
+    some, c = (k, kc) if k is not None else (v, vc)
+    if some is None or c is None:
+        raise ValueError("Keys or Values must be given, with their cache")
+    if some.dtype not in _ELEMS:
+        raise TypeError(f"k has dtype {some.dtype}")
+    n = some.shape[-3]
+    layers = some.shape[0] if some.dim() == 4 else 1
+    for t, name in ((k, "k"), (v, "v")):
+        if t is not None and t.shape != some.shape:
+            raise ValueError(f"{name} must have the other's shape")
+    if token_offsets is not None and token_offsets.numel() != bt.num_requests + 1:
+        raise ValueError(f"token_offsets must have {bt.num_requests + 1} elements")
+    rows = [_rows(t, name, n, c.num_kv_heads, c.head_dim, some.dtype) for t, name in ((k, "k"), (v, "v"))]
+    _check("kk_kv8_write", _lib.kk_kv8_write(
+        _ref(kc), _scale_ptr(kc, k_scale, "k_scale"), _ref(vc), _scale_ptr(vc, v_scale, "v_scale"), ctypes.byref(bt.c),
+        layer, layers, _ELEMS[some.dtype], _ref(rows[0]), _ref(rows[1]),
+        _ptr(token_offsets, torch.int32, "token_offsets"), max_new, n, _stream(stream)))
+
+
+def kk_tree_attn_kv8_workspace_bytes(kc, bt: BlockTable, max_nodes: int, num_q_heads: int) -> int:
+    return _lib.kk_tree_attn_kv8_workspace_bytes(ctypes.byref(kc), ctypes.byref(bt.c), max_nodes, num_q_heads)
+
+
+def kk_tree_attn_kv8(kc, k_scale, vc, v_scale, bt: BlockTable, layer: int, tree: Tree, q, scale: float, out, lse=None,
+                     sel=None, workspace=None, stream=None):
+    """kk_tree_attn over 8-bit caches (``q``, ``out`` and drafted nodes are bf16)."""
+    _check_elems(kc, q, "q")
+    _check_elems(kc, out, "out")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is not None and lse.numel() != q.shape[0] * q.shape[1]:
+        raise ValueError("lse must be [nodes][query heads]")
+    if sel is not None and sel.pages.shape[0] != bt.num_requests:
+        raise ValueError("the selection has another number of requests than the table")
+    nodes = tree.bind(kc, q, bt)
+    qp, qn, qh = _strided(q, "q")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("kk_tree_attn_kv8", _lib.kk_tree_attn_kv8(
+        ctypes.byref(kc), _scale_ptr(kc, k_scale, "k_scale"), ctypes.byref(vc), _scale_ptr(vc, v_scale, "v_scale"),
+        ctypes.byref(bt.c), layer, None if sel is None else ctypes.byref(sel.c), nodes, qp, qn, qh, q.shape[1],
+        float(scale), _ptr(out, name="out"), _ptr(lse, torch.float32, "lse"), _ptr(workspace, name="workspace"),
+        ws_bytes, _stream(stream)))
+
+
+class PageArrays:
+    """What lives with the pages: (tensor, the dim that numbers its pages) each, up to 8; keeps them alive.
+
+    A page's elements lie densely, in any order; the dims in front of the page dim are its slices."""
+
+    def __init__(self, tensors):
+        self.tensors = [t for t, _ in tensors]
+        self.pages = {t.shape[d] for t, d in tensors}
+        if len(self.tensors) > 8:
+            raise ValueError("at most 8 arrays")
+        self.c = (kk_page_array * max(1, len(tensors)))()
+        for i, (t, d) in enumerate(tensors):
+            if not t.is_cuda:
+                raise ValueError("page arrays must live on a CUDA device")
+            es, want = t.element_size(), 1
+            for size, stride in sorted((x for x in zip(t.shape[d + 1:], t.stride()[d + 1:]) if x[0] > 1), key=lambda x: x[1]):
+                if stride != want:
+                    raise ValueError("a page's elements must lie densely")
+                want *= size
+            lead = [x for x in zip(t.shape[:d], t.stride()[:d]) if x[0] > 1]
+            if any(a[1] != b[1] * b[0] for a, b in zip(lead, lead[1:])):
+                raise ValueError("slices must be evenly spaced")
+            slices = 1
+            for size, _ in lead:
+                slices *= size
+            self.c[i] = kk_page_array(t.data_ptr(), (lead[-1][1] if lead else 0) * es, t.stride(d) * es, want * es, slices)
+
+    def bind(self, num_pages: int):
+        if any(p != num_pages for p in self.pages):
+            raise ValueError(f"page arrays must have {num_pages} pages")
+        return self.c, len(self.tensors)
+
+
+def _arrays(arrays, num_pages):
+    return (None, 0) if arrays is None else arrays.bind(num_pages)
+
+
+def _refs(refs_in, refs_out):
+    if refs_in.numel() != refs_out.numel():
+        raise ValueError("refs_in and refs_out must have an element a page")
+    return _ptr(refs_in, torch.int32, "refs_in"), _ptr(refs_out, torch.int32, "refs_out"), refs_in.numel()
+
+
+def _ws(workspace):
+    return _ptr(workspace, name="workspace"), 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def kk_pages_alloc(refs_in, refs_out, out, want=None, stream=None):
+    """A free page for every element of ``out`` (int32) whose ``want`` (int32, None: all) is not 0, else -1."""
+    if want is not None and want.numel() != out.numel():
+        raise ValueError("want must have out's size")
+    ri, ro, P = _refs(refs_in, refs_out)
+    _check("kk_pages_alloc", _lib.kk_pages_alloc(ri, ro, P, _ptr(want, torch.int32, "want"), out.numel(),
+                                                 _ptr(out, torch.int32, "out"), _stream(stream)))
+
+
+def kk_pages_free(bt: BlockTable, refs_in, refs_out, stream=None):
+    """The pages of every table of ``bt`` lose a count."""
+    ri, ro, P = _refs(refs_in, refs_out)
+    _check("kk_pages_free", _lib.kk_pages_free(ctypes.byref(bt.c), ri, ro, P, _stream(stream)))
+
+
+def kk_pages_fork_workspace_bytes(num_requests: int, F: int) -> int:
+    return _lib.kk_pages_fork_workspace_bytes(num_requests, F)
+
+
+def kk_pages_fork(bt: BlockTable, block_size: int, parent, refs_in, refs_out, child_pages, child_offsets, child_lens,
+                  keep_parents: bool = True, arrays=None, workspace=None, stream=None):
+    """The table (``child_pages``, ``child_offsets``, ``child_lens``) of children of ``parent`` (int32 [F]),
+    as a BlockTable with ``bt``'s max_blocks takes it; ``arrays``: a :class:`PageArrays` whose pages are copied
+    where a child needs its own."""
+    F = parent.numel()
+    if child_offsets.numel() != F + 1 or child_lens.numel() != F:
+        raise ValueError(f"child_offsets must have {F + 1} elements, child_lens {F}")
+    ri, ro, P = _refs(refs_in, refs_out)
+    pa, n = _arrays(arrays, P)
+    wp, wn = _ws(workspace)
+    _check("kk_pages_fork", _lib.kk_pages_fork(
+        ctypes.byref(bt.c), block_size, _ptr(parent, torch.int32, "parent"), F, int(bool(keep_parents)), ri, ro, P,
+        _ptr(child_pages, torch.int32, "child_pages"), child_pages.numel(),
+        _ptr(child_offsets, torch.int32, "child_offsets"), _ptr(child_lens, torch.int32, "child_lens"), pa, n, wp, wn,
+        _stream(stream)))
+
+
+def kk_pages_compact_workspace_bytes(num_pages: int) -> int:
+    return _lib.kk_pages_compact_workspace_bytes(num_pages)
+
+
+def kk_pages_compact(refs_in, refs_out, pages_in, pages_out, remap, used, arrays=None, workspace=None, stream=None):
+    """Used pages to the front of the pool: ``pages_out`` are the tables' entries ``pages_in`` rewritten,
+    ``remap`` (int32, an element a page) every page's new place, ``used`` (int32 [1]) their number."""
+    ri, ro, P = _refs(refs_in, refs_out)
+    if pages_out.numel() != pages_in.numel() or remap.numel() != P or used.numel() != 1:
+        raise ValueError("pages_out must have pages_in's size, remap an element a page, used one")
+    pa, n = _arrays(arrays, P)
+    wp, wn = _ws(workspace)
+    _check("kk_pages_compact", _lib.kk_pages_compact(
+        ri, ro, P, _ptr(pages_in, torch.int32, "pages_in"), _ptr(pages_out, torch.int32, "pages_out"),
+        pages_in.numel(), _ptr(remap, torch.int32, "remap"), _ptr(used, torch.int32, "used"), pa, n, wp, wn,
+        _stream(stream)))
