@@ -67,6 +67,9 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void cp_full16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // N consecutive words of shared memory.
 template <int N>
 __device__ __forceinline__ void lds(uint32_t (&x)[N], const unsigned char* p) {
@@ -103,34 +106,51 @@ __device__ __forceinline__ void split_scale(float x, float* e, float* m) {
   *m = f ? __uint_as_float((b & 0x807FFFFFu) | 0x3F800000u) : x * 0x1p126f;
 }
 
-// What a warp loads next: a lane's token (its address in K and V and where its scale is).
-struct Tok8 {
-  const char *k, *v;
-  long long sc;
-  int page, tok;
-  bool ok;
+// What a warp loads next: 16 slots from slot o of `page`, the first n of which hold a token (PG: block_size is
+// a multiple of 16, so they lie in one page), or the token of a lane's own number (n: 0 or 1).
+struct Group {
+  int page, o, n;
 };
-
-// PG: 16 consecutive slots lie in one page (block_size is a multiple of 16); every lane holds the
-// first of them and `n`, how many hold a token. Else a lane holds the token of its own number.
+// Where that is: slot v of the request's context, slot o of its block b. It moves on by a tile at a time.
+struct Cursor {
+  int v, b, o, step_b, step_o;
+  __device__ __forceinline__ Cursor(int slot, int bs) : v(slot), b(slot / bs), o(slot - slot / bs * bs) {
+    step_b = kTK / bs;
+    step_o = kTK - step_b * bs;
+  }
+  __device__ __forceinline__ void next(int bs) {
+    v += kTK;
+    b += step_b;
+    o += step_o;
+    if (o >= bs) o -= bs, ++b;
+  }
+};
 template <bool PG>
-__device__ __forceinline__ Tok8 find_tok8(const AttnArgs& a, int r, const AttnReq& rq, int t, int w, int lane) {
-  Tok8 x;
-  TokenAt at;
-  x.ok = false;
-  x.page = x.tok = 0;
-  if (t >= rq.tiles_c) return x;
-  const int v = t * kTK + w * kTok + (PG ? 0 : lane & (kTok - 1));
-  x.ok = token_at(a, r, rq, v, true, &at);
-  x.page = at.page;
-  x.tok = at.tok;
+__device__ __forceinline__ Group find_group(const AttnArgs& a, int r, const AttnReq& rq, const Cursor& c) {
+  Group x = {0, 0, 0};
+  if (c.v >= rq.ctx) return x;
+  int left = rq.T - c.v;
+  if (a.sel_pages) {
+    const long long at = (long long)r * a.selK + c.b;
+    const int logical = a.sel_logical[at];
+    x.page = a.sel_pages[at];
+    const long long first = (long long)logical * a.kc.bs;
+    if (logical < 0 || first >= rq.T) {
+      flag_error(a.err, kErrBadIndex);
+      return x;
+    }
+    left = (int)min((long long)rq.T - first - c.o, (long long)kTok);
+  } else {
+    x.page = a.bt.pages[rq.off + c.b];
+  }
+  if (x.page < 0 || x.page >= a.kc.num_pages) {
+    flag_error(a.err, kErrBadIndex);
+    x.page = 0;
+    return x;
+  }
+  x.o = c.o;
+  x.n = max(0, min(left, PG ? kTok : 1));
   return x;
-}
-// How many of the 16 slots from slot v on hold a token, given that the first one does (PG).
-__device__ __forceinline__ int run_of(const AttnArgs& a, int r, const AttnReq& rq, int v, int tok) {
-  long long left = (long long)rq.T - v;
-  if (a.sel_pages) left = (long long)rq.T - ((long long)a.sel_logical[(long long)r * a.selK + v / a.kc.bs] * a.kc.bs + tok);
-  return (int)(left < kTok ? left : kTok);
 }
 
 template <int D>
@@ -186,45 +206,56 @@ __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kern
     const int t0 = it.t0, t1 = it.t1, h = it.h, row0 = it.mt * M;
     const int rows = min(M, rq.n * a.G - row0);
 
-    // copies a share of a tile (16 tokens of K and V, their scales) into stage st
-    auto load = [&](const Tok8& x, int st, int t, bool on) {
+    // Copies a share of a tile (16 tokens of K and V, their scales) into stage st. A lane copies the pieces c of
+    // rows sub, sub + RI, ...; what does not change over the tiles is worked out here.
+    constexpr int CH = D / 16, RI = 32 / CH, NI = kTok / RI > 0 ? kTok / RI : 1;
+    const int c = lane % CH, sub = lane / CH;
+    const char* k_lane = static_cast<const char*>(a.kc.base) + a.layer * a.kc.sL + h * a.kc.sH + c * 16 + (PG ? sub * a.kc.sT : 0);
+    const char* v_lane = static_cast<const char*>(a.vc.base) + a.layer * a.vc.sL + h * a.vc.sH + c * 16 + (PG ? sub * a.vc.sT : 0);
+    const float* s_lane = ((PG ? lane & 1 : lane >> 4) ? a.v_scale : a.k_scale) + (long long)a.layer * a.kc.num_pages * a.kc.H + h;
+    auto load = [&](const Group& x, int st, bool on) {
       const uint32_t kst = ring_at + st * Sm::kStage, vst = kst + kTok * D;
-      constexpr int CH = D / 16, RI = 32 / CH;  // pieces of a row, rows per instruction
-      const int c = lane % CH, sub = lane / CH;
-      const long long kl = a.layer * a.kc.sL + h * a.kc.sH, vl = a.layer * a.vc.sL + h * a.vc.sH;
-      const long long s0 = (long long)a.layer * a.kc.num_pages;
       uint32_t live;
       if constexpr (PG) {
-        const int n = on && x.ok ? run_of(a, r, rq, t * kTK + w * kTok, x.tok) : 0;
+        const int n = on ? x.n : 0;
         live = (1u << n) - 1u;
-        const char* k = static_cast<const char*>(a.kc.base) + kl + x.page * a.kc.sP + x.tok * a.kc.sT + c * 16;
-        const char* v = static_cast<const char*>(a.vc.base) + vl + x.page * a.vc.sP + x.tok * a.vc.sT + c * 16;
         if (on) {
+          const char* k = k_lane + x.page * a.kc.sP + x.o * a.kc.sT;
+          const char* v = v_lane + x.page * a.vc.sP + x.o * a.vc.sT;
+          if (n == kTok) {
 #pragma unroll
-          for (int i = 0; i < (kTok + RI - 1) / RI; ++i) {
-            const int row = i * RI + sub;
-            cp_async16(kst + at_k<D>(row, c * 16), row < n ? k + row * a.kc.sT : k, row < n);
-            cp_async16(vst + at_v<D>(row, c * 16), row < n ? v + row * a.vc.sT : v, row < n);
+            for (int i = 0; i < NI; ++i) {
+              cp_full16(kst + at_k<D>(i * RI + sub, c * 16), k);
+              cp_full16(vst + at_v<D>(i * RI + sub, c * 16), v);
+              k += RI * a.kc.sT;
+              v += RI * a.vc.sT;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+              const bool real = i * RI + sub < n;
+              cp_async16(kst + at_k<D>(i * RI + sub, c * 16), real ? k : k_lane, real);
+              cp_async16(vst + at_v<D>(i * RI + sub, c * 16), real ? v : v_lane, real);
+              k += RI * a.kc.sT;
+              v += RI * a.vc.sT;
+            }
           }
-          if (lane < 2)
-            cp_async4(sc_at + (st * 32 + lane) * 4,
-                      (lane ? a.v_scale : a.k_scale) + (s0 + x.page) * a.kc.H + h, n > 0);
+          if (lane < 2) cp_async4(sc_at + (st * 32 + lane) * 4, s_lane + x.page * a.kc.H, n > 0);
         }
       } else {
-        const uint32_t ok = __ballot_sync(kFull, on && x.ok);
+        const uint32_t ok = __ballot_sync(kFull, on && x.n > 0);
         live = ok & 0xFFFFu;
-        const long long ko = kl + x.page * a.kc.sP + x.tok * a.kc.sT, vo = vl + x.page * a.vc.sP + x.tok * a.vc.sT;
+        const long long ko = x.page * a.kc.sP + x.o * a.kc.sT, vo = x.page * a.vc.sP + x.o * a.vc.sT;
         if (on) {
 #pragma unroll
-          for (int i = 0; i < (kTok + RI - 1) / RI; ++i) {
+          for (int i = 0; i < NI; ++i) {
             const int row = i * RI + sub;
-            const char* k = static_cast<const char*>(a.kc.base) + __shfl_sync(kFull, ko, row) + c * 16;
-            const char* v = static_cast<const char*>(a.vc.base) + __shfl_sync(kFull, vo, row) + c * 16;
+            const char* k = k_lane + __shfl_sync(kFull, ko, row);
+            const char* v = v_lane + __shfl_sync(kFull, vo, row);
             cp_async16(kst + at_k<D>(row, c * 16), k, (ok >> row) & 1);
             cp_async16(vst + at_v<D>(row, c * 16), v, (ok >> row) & 1);
           }
-          cp_async4(sc_at + (st * 32 + lane) * 4, (lane < 16 ? a.k_scale : a.v_scale) + (s0 + x.page) * a.kc.H + h,
-                    x.ok);
+          cp_async4(sc_at + (st * 32 + lane) * 4, s_lane + (long long)x.page * a.kc.H, x.n > 0);
         }
       }
       cp_commit();
@@ -232,11 +263,15 @@ __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kern
     };
 
     // the first tiles' copies go out before the queries are read
-    Tok8 nx = find_tok8<PG>(a, r, rq, t0, w, lane);
+    const int tc = min(t1, rq.tiles_c);  // tiles of cached tokens end here
+    Cursor at(t0 * kTK + w * kTok + (PG ? 0 : lane & (kTok - 1)), a.kc.bs);
+    Group nx = {0, 0, 0};
+    if (t0 < tc) nx = find_group<PG>(a, r, rq, at);
 #pragma unroll 1
     for (int st = 0; st < S - 1; ++st) {
-      load(nx, st, t0 + st, t0 + st < t1 && t0 + st < rq.tiles_c);
-      nx = find_tok8<PG>(a, r, rq, min(t0 + st + 1, t1 - 1), w, lane);
+      load(nx, st, t0 + st < tc);
+      at.next(a.kc.bs);
+      if (t0 + st + 1 < tc) nx = find_group<PG>(a, r, rq, at);
     }
     for (int i = tid; i < M * (D / 8); i += kThreads) {
       const int m = i / (D / 8), c = i - m * (D / 8), row = row0 + m;
@@ -303,8 +338,11 @@ __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kern
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          rise |= s[nt][e] > ref_s[nt][e & 1] + 8.f || s[nt][e] + (e < 2 ? lv0 : lv1) > ref_v[nt][e & 1] + 8.f;
+        for (int e = 0; e < 2; ++e) {
+          const float top = PG ? fmaxf(s[nt][e], s[nt][e + 2]) : s[nt][e];
+          rise |= top > 8.f + fminf(ref_s[nt][e], ref_v[nt][e] - lv0);
+          if (!PG) rise |= s[nt][e + 2] > 8.f + fminf(ref_s[nt][e], ref_v[nt][e] - lv1);
+        }
       if (!__any_sync(kFull, rise)) return;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -337,9 +375,9 @@ __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kern
       cp_wait<S - 2>();
       __syncwarp();
       {  // refill the stage read in the last turn
-        const int tn = t + S - 1;
-        load(nx, st == 0 ? S - 1 : st - 1, tn, tn < t1 && tn < rq.tiles_c);
-        nx = find_tok8<PG>(a, r, rq, min(t + S, t1 - 1), w, lane);
+        load(nx, st == 0 ? S - 1 : st - 1, t + S - 1 < tc);
+        at.next(a.kc.bs);
+        if (t + S < tc) nx = find_group<PG>(a, r, rq, at);
       }
       float s[NT][4];
 #pragma unroll
@@ -376,11 +414,14 @@ __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kern
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool see = (live >> (e < 2 ? g : g + 8)) & 1;
-            // selected, whatever a place without a token holds
-            s[nt][e] = see ? s[nt][e] * qf[nt][e & 1] * (e < 2 ? ks0 : ks1) : -INFINITY;
-          }
+          for (int e = 0; e < 4; ++e) s[nt][e] *= qf[nt][e & 1] * (e < 2 ? ks0 : ks1);
+        if (live != 0xFFFFu) {  // selected, whatever a place without a token holds
+          const bool see0 = (live >> g) & 1, see1 = (live >> (g + 8)) & 1;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nt][e] = (e < 2 ? see0 : see1) ? s[nt][e] : -INFINITY;
+        }
         settle(s, lv0, lv1);
         uint32_t b0[NT], b1[NT];
 #pragma unroll
@@ -389,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kern
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             l_run[nt][e & 1] += ex2(s[nt][e] - ref_s[nt][e & 1]);
-            p[e] = ex2(s[nt][e] + (e < 2 ? lv0 : lv1) - ref_v[nt][e & 1] + kLift) * (e < 2 ? vm0 : vm1);
+            p[e] = ex2(s[nt][e] + ((e < 2 ? lv0 : lv1) - ref_v[nt][e & 1] + kLift)) * (e < 2 ? vm0 : vm1);
           }
           b0[nt] = turn(pack_f16(p[0], p[1]));  // the weights' one rounding: float16 feeds the product
           b1[nt] = turn(pack_f16(p[2], p[3]));
