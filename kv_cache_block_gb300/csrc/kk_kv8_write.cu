@@ -19,15 +19,41 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kKeep = 8;  // vectors a thread keeps
 
-// Two values as e4m3, each rounded to nearest even; NaN for what is not finite.
+// Two values as e4m3, each rounded to nearest even; NaN stays NaN.
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float only_finite(float x) {
+__device__ __forceinline__ float only_finite(float x) {  // infinity becomes NaN
   return (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u ? __uint_as_float(0x7FFFFFFFu) : x;
 }
+
+// The largest magnitude of vectors, as the bits of the type (they order like the values, infinity and NaN
+// above all): two bf16 halves at a time.
+template <typename T>
+struct Top;
+template <>
+struct Top<bf16_t> {
+  static constexpr uint32_t kInf = 0x7F80u;
+  uint32_t x = 0;
+  __device__ __forceinline__ void add(const uint4& v) {
+    x = __vmaxu2(__vmaxu2(x, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu)),
+                 __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+  }
+  __device__ __forceinline__ uint32_t bits() const { return max(x & 0xFFFFu, x >> 16); }
+  __device__ static float value(uint32_t b) { return __uint_as_float(b << 16); }
+};
+template <>
+struct Top<float> {
+  static constexpr uint32_t kInf = 0x7F800000u;
+  uint32_t x = 0;
+  __device__ __forceinline__ void add(const uint4& v) {
+    x = max(max(max(x, v.x & 0x7FFFFFFFu), max(v.y & 0x7FFFFFFFu, v.z & 0x7FFFFFFFu)), v.w & 0x7FFFFFFFu);
+  }
+  __device__ __forceinline__ uint32_t bits() const { return x; }
+  __device__ static float value(uint32_t b) { return __uint_as_float(b); }
+};
 
 // The smallest power of two that is at least amax / 448, and at least 2^-126.
 __device__ __forceinline__ float pow2_scale(float amax) {
@@ -39,10 +65,10 @@ __device__ __forceinline__ float pow2_scale(float amax) {
 
 
 template <typename T, int D, int W>
-__global__ void __launch_bounds__(kThreads) write8_kernel(const Write8Args a) {
+__global__ void __launch_bounds__(kThreads, 4) write8_kernel(const Write8Args a) {
   constexpr int E = Vec16<T>::kElems, CH = D / E;  // elements of a vector, vectors of a row
   constexpr int NTH = W * 32, IPB = kThreads / NTH;  // threads of an item, items of a block
-  __shared__ float s_max[kThreads / 32];
+  __shared__ uint32_t s_max[kThreads / 32];
   const int tid = threadIdx.x % NTH, sub = threadIdx.x / NTH;
   const int r = blockIdx.z, H = a.kc.H;
   const int item = blockIdx.y * IPB + sub, items = a.layers * H * a.sides;
@@ -75,35 +101,45 @@ __global__ void __launch_bounds__(kThreads) write8_kernel(const Write8Args a) {
   const long long src = (l * x.sl + (n0 + lo - t0) * x.sn + h * x.sh) * (16 / E);
   const char* from = static_cast<const char*>(x.src) + src;
   const long long row_bytes = x.sn * (16 / E);
-  uint4 keep[kKeep];
-  float top = 0.f;
-  auto measure = [&](const uint4& v) {
-    float f[E];
-    Vec16<T>::unpack(v, f);
+  auto at_vec = [&](int i) { return *reinterpret_cast<const uint4*>(from + (i / CH) * row_bytes + (i % CH) * 16); };
+  // The largest of the item's threads.
+  auto largest = [&](uint32_t x) {
+    x = __reduce_max_sync(kFull, x);
+    if constexpr (W > 1) {
+      if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = x;
+      __syncthreads();
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float y = fabsf(f[e]);
-      top = fmaxf(top, y < INFINITY ? y : 0.f);
+      for (int w = 0; w < W; ++w) x = max(x, s_max[w]);
+      __syncthreads();
     }
+    return x;
   };
+  uint4 keep[kKeep];
 #pragma unroll
   for (int k = 0; k < kKeep; ++k) {
     const int i = tid + k * NTH;
     keep[k] = make_uint4(0, 0, 0, 0);
-    if (i < vecs) keep[k] = *reinterpret_cast<const uint4*>(from + (i / CH) * row_bytes + (i % CH) * 16);
+    if (i < vecs) keep[k] = at_vec(i);
   }
+  Top<T> all;
 #pragma unroll
-  for (int k = 0; k < kKeep; ++k) measure(keep[k]);
-  for (int i = tid + kKeep * NTH; i < vecs; i += NTH)
-    measure(*reinterpret_cast<const uint4*>(from + (i / CH) * row_bytes + (i % CH) * 16));
+  for (int k = 0; k < kKeep; ++k) all.add(keep[k]);
+  for (int i = tid + kKeep * NTH; i < vecs; i += NTH) all.add(at_vec(i));
+  uint32_t bits = largest(all.bits());
+  const bool odd = bits >= Top<T>::kInf;  // something is not finite: the same for the item
+  if (odd) {
+    float top = 0.f;
+    for (int i = tid; i < vecs; i += NTH) {
+      float f[E];
+      Vec16<T>::unpack(at_vec(i), f);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  if constexpr (W > 1) {
-    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < W; ++w) top = fmaxf(top, s_max[w]);
+      for (int e = 0; e < E; ++e)
+        if (fabsf(f[e]) < INFINITY) top = fmaxf(top, fabsf(f[e]));
+    }
+    bits = __float_as_uint(top) >> (E == 8 ? 16 : 0);
   }
+  if (odd) bits = largest(bits);
+  const float top = Top<T>::value(bits);
   if (!real) return;
   float* at = x.scale + ((long long)(a.layer + l) * a.kc.num_pages + page) * H + h;
   const float old = had ? *at : 0.f, fresh = pow2_scale(top), now = fmaxf(old, fresh);
@@ -116,7 +152,10 @@ __global__ void __launch_bounds__(kThreads) write8_kernel(const Write8Args a) {
     float f[E];
     Vec16<T>::unpack(v, f);
 #pragma unroll
-    for (int e = 0; e < E; ++e) f[e] = only_finite(f[e]) * inv;
+    for (int e = 0; e < E; ++e) f[e] *= inv;
+    if (odd)
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = only_finite(f[e]);
     char* to = codes + (had + i / CH) * x.dT + (i % CH) * E;
     const uint32_t p = to_e4m3x2(f[0], f[1]) | to_e4m3x2(f[2], f[3]) << 16;
     if constexpr (E == 8)
@@ -128,7 +167,7 @@ __global__ void __launch_bounds__(kThreads) write8_kernel(const Write8Args a) {
   for (int k = 0; k < kKeep; ++k)
     if (tid + k * NTH < vecs) store(tid + k * NTH, keep[k]);
   for (int i = tid + kKeep * NTH; i < vecs; i += NTH)
-    store(i, *reinterpret_cast<const uint4*>(from + (i / CH) * row_bytes + (i % CH) * 16));
+    store(i, at_vec(i));
   if (had && old > 0.f && old < now) {  // the page's older codes, in terms of the new scale
     const float f = old * inv;
     for (int i = tid; i < had * (D / 4); i += NTH) {
