@@ -13,7 +13,7 @@
 #include <algorithm>
 #include <climits>
 
-#include "kk_device.cuh"
+#include "kk_attn.cuh"
 #include "kk_pdl.cuh"
 
 namespace kk {
@@ -32,6 +32,8 @@ struct Place {  // of a thread in the planning cluster
   int cta, ctas, tid, all, n;  // its number among all n threads
 };
 __device__ __forceinline__ Place place() {
+  pdl_wait();  // what ran before in the stream has finished; what comes next may be launched
+  pdl_launch_dependents();
   Place p;
   p.cta = (int)cluster_rank();
   p.ctas = (int)cluster_size();
@@ -205,7 +207,6 @@ __device__ __forceinline__ Parent parent_of(const ForkArgs& a, int r) {
 __global__ void __launch_bounds__(kPlan) pages_fork_kernel(const ForkArgs a) {
   __shared__ int sh[33], box[2 * kPlanCtas];
   const Place p = place();
-  pdl_launch_dependents();
   copy_refs(a.refs_in, a.refs_out, a.num_pages, p);
   for (int r = p.all; r < a.bt.R; r += p.n) {
     a.kids[r] = 0;
@@ -300,7 +301,6 @@ __global__ void __launch_bounds__(kPlan) pages_fork_kernel(const ForkArgs a) {
 __global__ void __launch_bounds__(kPlan) pages_compact_kernel(const CompactArgs a) {
   __shared__ int sh[33], box[2 * kPlanCtas];
   const Place p = place();
-  pdl_launch_dependents();
   cluster_sync();  // every CTA of the cluster runs before another writes to its shared memory
   // a CTA's share of the pages, in order
   const long long per = ((long long)a.num_pages + p.ctas - 1) / p.ctas;
@@ -359,41 +359,46 @@ __global__ void __launch_bounds__(kPlan) pages_compact_kernel(const CompactArgs 
   }
 }
 
-// One page of every array is cut into chunks of kUnroll vectors a thread; CTAs take (pair, chunk) in turn.
-constexpr int kCopy = 256, kUnroll = 8;
+// One page of an array is a run of vectors, slice after slice, cut into chunks of kUnroll a thread (a chunk spans
+// slices where they are small); CTAs take (pair, chunk) in turn.
+constexpr int kCopy = 256, kUnroll = 8, kChunk = kCopy * kUnroll;
 
 template <typename V>
-__device__ __forceinline__ void copy_chunk(const char* from, char* to, long long n) {
+__device__ __forceinline__ void copy_chunk(const PageArray& d, const int2 m, int first) {
+  const int left = d.vecs - first - (int)threadIdx.x;  // vectors of the page from the thread's first on
+  const int s0 = (first + (int)threadIdx.x) / d.per, o0 = first + (int)threadIdx.x - s0 * d.per;
   V x[kUnroll];
+  auto each = [&](auto f) {
+    int s = s0, o = o0;
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int i = u * kCopy + threadIdx.x;
-    if (i < n) x[u] = __ldcs(reinterpret_cast<const V*>(from) + i);
-  }
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int i = u * kCopy + threadIdx.x;
-    if (i < n) reinterpret_cast<V*>(to)[i] = x[u];
-  }
+    for (int u = 0; u < kUnroll; ++u) {
+      if (u * kCopy < left) f(u, s * d.slice + (long long)o * (int)sizeof(V));
+      s += d.step_s;
+      o += d.step_o;
+      if (o >= d.per) o -= d.per, ++s;
+    }
+  };
+  const char* from = d.base + m.x * d.page;
+  each([&](int u, long long at) { x[u] = __ldcs(reinterpret_cast<const V*>(from + at)); });
+  char* to = d.base + m.y * d.page;
+  each([&](int u, long long at) { *reinterpret_cast<V*>(to + at) = x[u]; });
 }
 
-__global__ void __launch_bounds__(kCopy) pages_copy_kernel(const PageArrays pa, const int2* pairs, const int* n_pairs,
+__global__ void __launch_bounds__(kCopy, 4) pages_copy_kernel(const PageArrays pa, const int2* pairs, const int* n_pairs,
                                                            int num_pages) {
   pdl_wait();
+  pdl_launch_dependents();
   const long long units = (long long)*n_pairs * pa.chunks;
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const long long pair = u / pa.chunks, c0 = u - pair * pa.chunks;
+    const long long pair = udiv(u, pa.chunks);
+    const int c = (int)(u - pair * pa.chunks);
     const int2 m = pairs[pair];
     if (m.x < 0 || m.x >= num_pages || m.y < 0 || m.y >= num_pages) continue;  // a bad page of a parent's table
     int x = 0;
-    while (x + 1 < pa.n && c0 >= pa.a[x + 1].first) ++x;
+    while (x + 1 < pa.n && c >= pa.a[x + 1].first) ++x;
     const PageArray& d = pa.a[x];
-    const long long per = d.chunks / d.slices, c = c0 - d.first, s = c / per, b = (c - s * per) * kCopy * kUnroll * d.vec;
-    const char* from = d.base + s * d.slice + m.x * d.page + b;
-    char* to = d.base + s * d.slice + m.y * d.page + b;
-    const long long n = (d.bytes - b) / d.vec;
-    if (d.vec == 16) copy_chunk<uint4>(from, to, n);
-    else copy_chunk<uint32_t>(from, to, n);
+    if (d.vec == 16) copy_chunk<uint4>(d, m, (c - d.first) * kChunk);
+    else copy_chunk<uint32_t>(d, m, (c - d.first) * kChunk);
   }
 }
 
@@ -406,12 +411,14 @@ cudaError_t launch_plan(void (*k)(P...), long long work, cudaStream_t s, A... ar
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kPlan);
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)ctas;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
@@ -432,16 +439,21 @@ cudaError_t launch_copies(const PageArrays& pa, const int2* pairs, const int* n_
 
 }  // namespace
 
-void plan_page_arrays(PageArrays* pa) {
+bool plan_page_arrays(PageArrays* pa) {
   pa->chunks = 0;
   for (int i = 0; i < pa->n; ++i) {
     PageArray& d = pa->a[i];
     d.vec = (reinterpret_cast<uintptr_t>(d.base) | (uintptr_t)d.slice | (uintptr_t)d.page | (uintptr_t)d.bytes) % 16 ? 4 : 16;
-    const long long chunk = (long long)kCopy * kUnroll * d.vec;
-    d.chunks = (d.bytes + chunk - 1) / chunk * d.slices;
+    const long long per = d.bytes / d.vec, vecs = per * d.slices, chunks = (vecs + kChunk - 1) / kChunk;
+    if (per > 0x7FFF0000 || vecs > 0x7FFF0000 || pa->chunks + chunks > 0x7FFF0000) return false;
+    d.per = (int)per;
+    d.vecs = (int)vecs;
+    d.step_s = kCopy / d.per;
+    d.step_o = kCopy % d.per;
     d.first = pa->chunks;
-    pa->chunks += d.chunks;
+    pa->chunks += (int)chunks;
   }
+  return true;
 }
 
 cudaError_t launch_pages_alloc(const int* refs_in, int* refs_out, int num_pages, const int* want, int n, int* out,

@@ -9,13 +9,15 @@ constexpr int kMaxPageArrays = 8;
 struct PageArray {
   char* base;
   long long slice, page, bytes;  // strides and size in bytes
-  int slices, vec;               // bytes of a load: 16 or 4
-  long long chunks, first;       // chunks of one page (of all slices), and those of the arrays before
+  int slices, vec;               // vec: bytes of a load, 16 or 4
+  int per, vecs;                 // vectors of a slice, of a page
+  int step_s, step_o;            // slices and vectors a thread moves on by from one of its vectors to the next
+  int first;                     // chunks of the arrays before
 };
 struct PageArrays {
   PageArray a[kMaxPageArrays];
   int n;
-  long long chunks;  // of one page of every array
+  int chunks;  // of one page of every array
 };
 struct ForkArgs {
   Table bt;
@@ -42,7 +44,7 @@ struct CompactArgs {
   int* n_pairs;
   int* err;
 };
-void plan_page_arrays(PageArrays* pa);  // fills vec, chunks and first
+bool plan_page_arrays(PageArrays* pa);  // fills vec and what follows; false: too large
 cudaError_t launch_pages_alloc(const int* refs_in, int* refs_out, int num_pages, const int* want, int n, int* out,
                                int* err, cudaStream_t s);
 cudaError_t launch_pages_free(const Table& bt, const int* refs_in, int* refs_out, int num_pages, int* err,

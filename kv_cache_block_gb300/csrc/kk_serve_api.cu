@@ -62,10 +62,9 @@ kk_status check_arrays(const kk_page_array* arrays, int32_t n, kk::PageArrays* o
     const kk_page_array& a = arrays[i];
     if (!a.base || a.bytes <= 0 || a.slices <= 0 || a.stride_slice < 0 || a.stride_page < a.bytes) return KK_ERR_INVALID;
     if (!aligned(a.base, 4) || a.bytes % 4 || a.stride_slice % 4 || a.stride_page % 4) return KK_ERR_UNSUPPORTED;
-    out->a[i] = kk::PageArray{static_cast<char*>(a.base), a.stride_slice, a.stride_page, a.bytes, a.slices, 0, 0, 0};
+    out->a[i] = kk::PageArray{static_cast<char*>(a.base), a.stride_slice, a.stride_page, a.bytes, a.slices};
   }
-  kk::plan_page_arrays(out);
-  return KK_OK;
+  return kk::plan_page_arrays(out) ? KK_OK : KK_ERR_UNSUPPORTED;
 }
 
 kk_status check_refs(const int32_t* in, int32_t* out, int32_t num_pages) {
