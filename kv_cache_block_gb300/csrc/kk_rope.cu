@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxPairs = 128;
-constexpr int kBatch = 8;  // nodes of a block, at most
+constexpr int kBatch = 32;  // nodes of a block, at most
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
@@ -50,12 +50,12 @@ __device__ __forceinline__ unsigned long long turns_of(float f) {
          (unsigned long long)(long long)rint(q * 18446744073709551616.0);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int batch) {
+template <typename T, int D, bool HALF>
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a, int batch) {
   constexpr int E = Vec16<T>::kElems, LPR = D / (2 * E), RPW = 32 / LPR;  // lanes of a row, rows of a warp
   constexpr int ES = 16 / E;
   __shared__ unsigned long long s_turn[kMaxPairs];
-  __shared__ float2 s_cs[kBatch][kMaxPairs];
+  extern __shared__ float2 s_cs[];  // [nodes][E][pairs / E] (cosine, sine): the lanes of a row read neighbours
   __shared__ long long s_slot[kBatch][2];  // byte offset of the node's slot in K and V, -1: none
   __shared__ int s_pos[kBatch];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -106,89 +106,113 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int ba
     const unsigned long long turn = (unsigned long long)(long long)s_pos[k] * s_turn[p];
     float sn, cs;
     sincospif((float)(int)(turn >> 32) * 0x1p-31f, &sn, &cs);
-    s_cs[k][p] = make_float2(cs * a.rope_scale, sn * a.rope_scale);
+    s_cs[k * pairs + p % E * (pairs / E) + p / E] = make_float2(cs * a.rope_scale, sn * a.rope_scale);
   }
   __syncthreads();
 
   // the lane's two pieces of a row, and its first pair (none: past rotary_dim)
   const int j = lane % LPR, turned = a.rd / (2 * E);
   const bool rot = j < turned;
-  const int p0 = a.half && rot ? j : 2 * j, p1 = a.half && rot ? j + turned : 2 * j + 1;
-  const int heads = a.Hq + a.H + (a.v ? a.H : 0), per = (heads + gridDim.y - 1) / gridDim.y;
-  const int h0 = blockIdx.y * per, h1 = min(heads, h0 + per);
-  if (h0 >= h1) return;
-  const int rows = nodes * (h1 - h0);
-  const float inv_d = 1.f / D;
-  for (int row = w * RPW + lane / LPR;; row += kWarps * RPW) {
-    if (__all_sync(kFull, row >= rows)) break;
-    const bool real = row < rows;
-    const int k = real ? row / (h1 - h0) : 0, hh = real ? h0 + row - k * (h1 - h0) : h0, node = node0 + k;
-    const int kind = hh < a.Hq ? 0 : hh < a.Hq + a.H ? 1 : 2, h = hh - (kind ? a.Hq : 0) - (kind == 2 ? a.H : 0);
+  const int p0 = HALF && rot ? j : 2 * j, p1 = HALF && rot ? j + turned : 2 * j + 1;
+  // A warp takes RPW heads of one node and one kind at a time, two such chunks together so that four loads a
+  // lane are under way; queries first, then Keys, then Values, each with its weights in registers.
+  const int slot = lane / LPR;
+  const int cq = (a.Hq + RPW - 1) / RPW, ck = (a.H + RPW - 1) / RPW;
+  for (int kind = 0; kind < (a.v ? 3 : 2); ++kind) {
+    const int heads = kind ? a.H : a.Hq, all = kind ? ck : cq;
+    const int per = (all + gridDim.y - 1) / gridDim.y;
+    const int c0 = blockIdx.y * per, chunks = min(all, c0 + per) - c0;  // this block's share of the heads
+    if (chunks <= 0) continue;
     const RopeRows& x = kind == 0 ? a.q : kind == 1 ? a.k : a.v_rows;
-    const char* from = static_cast<const char*>(x.base) + (node * x.sn + h * x.sh) * ES;
-    uint4 u = make_uint4(0, 0, 0, 0), v = u;
-    if (real) {
-      u = *reinterpret_cast<const uint4*>(from + p0 * 16);
-      v = *reinterpret_cast<const uint4*>(from + p1 * 16);
+    const void* wt = kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr;
+    float g[2 * E];
+    if (wt) {
+      Vec16<T>::unpack(*reinterpret_cast<const uint4*>(static_cast<const char*>(wt) + p0 * 16), g);
+      Vec16<T>::unpack(*reinterpret_cast<const uint4*>(static_cast<const char*>(wt) + p1 * 16), g + E);
     }
-    float f[2 * E];
-    Vec16<T>::unpack(u, f);
-    Vec16<T>::unpack(v, f + E);
-    float ss = 0.f;
-    if (a.q_weight || a.k_weight) {  // the same for all lanes: rows of a warp may be of different kinds
+    int node = w / chunks, chunk = w - node * chunks;
+    const int step_n = kWarps / chunks, step_c = kWarps - step_n * chunks;
+    while (node < nodes) {
+      uint4 u[2], v[2];
+      int k[2], h[2];
+      bool real[2];
 #pragma unroll
-      for (int e = 0; e < 2 * E; ++e) ss += f[e] * f[e];
-#pragma unroll
-      for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-    }
-    if (kind != 2) {
-      const void* wt = kind ? a.k_weight : a.q_weight;
-      if (wt) {
-        float g[2 * E];
-        Vec16<T>::unpack(*reinterpret_cast<const uint4*>(static_cast<const char*>(wt) + p0 * 16), g);
-        Vec16<T>::unpack(*reinterpret_cast<const uint4*>(static_cast<const char*>(wt) + p1 * 16), g + E);
-        const float s = rsqrtf(ss * inv_d + a.eps);
-#pragma unroll
-        for (int e = 0; e < 2 * E; ++e) f[e] = f[e] * s * g[e];
+      for (int i = 0; i < 2; ++i) {
+        k[i] = node;
+        h[i] = (c0 + chunk) * RPW + slot;
+        real[i] = node < nodes && h[i] < heads;
+        u[i] = v[i] = make_uint4(0, 0, 0, 0);
+        if (real[i]) {
+          const char* from = static_cast<const char*>(x.base) + ((node0 + k[i]) * x.sn + h[i] * x.sh) * ES;
+          u[i] = *reinterpret_cast<const uint4*>(from + p0 * 16);
+          v[i] = *reinterpret_cast<const uint4*>(from + p1 * 16);
+        }
+        node += step_n;
+        chunk += step_c;
+        if (chunk >= chunks) chunk -= chunks, ++node;
       }
-      if (rot) {
-        const float2* cs = s_cs[k] + j * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float2 t = cs[e];
-          float* p = a.half ? f + e : f + 2 * e;
-          float* q = a.half ? f + E + e : f + 2 * e + 1;
-          const float y = *p, z = *q;
-          *p = y * t.x - z * t.y;
-          *q = z * t.x + y * t.y;
+      for (int i = 0; i < 2; ++i) {
+        if (kind != 2) {  // the same for the warp
+          float f[2 * E];
+          Vec16<T>::unpack(u[i], f);
+          Vec16<T>::unpack(v[i], f + E);
+          if (wt) {
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2 * E; ++e) ss += f[e] * f[e];
+#pragma unroll
+            for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+            const float s = rsqrtf(ss * (1.f / D) + a.eps);
+#pragma unroll
+            for (int e = 0; e < 2 * E; ++e) f[e] = f[e] * s * g[e];
+          }
+          if (rot) {
+            const float2* cs = s_cs + (k[i] < nodes ? k[i] : 0) * pairs + j;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              const float2 t = cs[e * turned];
+              float* y = HALF ? f + e : f + 2 * e;
+              float* z = HALF ? f + E + e : f + 2 * e + 1;
+              const float p = *y, q = *z;
+              *y = p * t.x - q * t.y;
+              *z = q * t.x + p * t.y;
+            }
+          }
+          u[i] = pack_vec<T>(f);
+          v[i] = pack_vec<T>(f + E);
+        }
+        if (!real[i]) continue;
+        auto put = [&](char* to) {
+          *reinterpret_cast<uint4*>(to + p0 * 16) = u[i];
+          *reinterpret_cast<uint4*>(to + p1 * 16) = v[i];
+        };
+        const long long n = node0 + k[i];
+        if (kind == 0) {
+          put(static_cast<char*>(a.q_out.base) + (n * a.q_out.sn + h[i] * a.q_out.sh) * ES);
+        } else if (kind == 1) {
+          if (a.k_out.base) put(static_cast<char*>(a.k_out.base) + (n * a.k_out.sn + h[i] * a.k_out.sh) * ES);
+          if (a.kc && s_slot[k[i]][0] >= 0) put(static_cast<char*>(a.kc) + s_slot[k[i]][0] + h[i] * a.kH * ES);
+        } else if (s_slot[k[i]][1] >= 0) {
+          put(static_cast<char*>(a.vc) + s_slot[k[i]][1] + h[i] * a.vH * ES);
         }
       }
-      u = pack_vec<T>(f);
-      v = pack_vec<T>(f + E);
     }
-    if (!real) continue;
-    auto put = [&](char* to) {
-      *reinterpret_cast<uint4*>(to + p0 * 16) = u;
-      *reinterpret_cast<uint4*>(to + p1 * 16) = v;
-    };
-    if (kind == 0) put(static_cast<char*>(a.q_out.base) + (node * a.q_out.sn + h * a.q_out.sh) * ES);
-    if (kind == 1 && a.k_out.base) put(static_cast<char*>(a.k_out.base) + (node * a.k_out.sn + h * a.k_out.sh) * ES);
-    if (kind == 1 && a.kc && s_slot[k][0] >= 0) put(static_cast<char*>(a.kc) + s_slot[k][0] + h * a.kH * ES);
-    if (kind == 2 && s_slot[k][1] >= 0) put(static_cast<char*>(a.vc) + s_slot[k][1] + h * a.vH * ES);
   }
 }
 
 template <typename T, int D>
 cudaError_t go(const RopeArgs& a, cudaStream_t s) {
-  const int sms = sm_count(), heads = a.Hq + 2 * a.H;
-  // nodes of a block: as many as leave every SM several blocks; few nodes: their heads are spread over blocks
-  int batch = kBatch;
-  while (batch > 1 && (long long)((a.nodes + batch - 1) / batch) < 4ll * sms) batch >>= 1;
-  constexpr int rows = kWarps * (32 / (D / (2 * Vec16<T>::kElems)));
-  const int blocks = (a.nodes + batch - 1) / batch;
-  int split = std::max(1, std::min((heads + rows - 1) / rows * batch, sms / blocks));
-  split = std::min(split, heads);
-  rope_kernel<T, D><<<dim3((unsigned)blocks, (unsigned)split), kThreads, 0, s>>>(a, batch);
+  // Nodes of a block: an equal share of them for each of three blocks an SM (their look-ups and sines are a chain
+  // of latencies that a block pays once), at most kBatch; few nodes: their heads are spread over blocks.
+  const int sms = sm_count();
+  const int batch = std::min(kBatch, (a.nodes + 3 * sms - 1) / (3 * sms)), blocks = (a.nodes + batch - 1) / batch;
+  constexpr int rows = 32 / (D / (2 * Vec16<T>::kElems));  // heads of a warp
+  const int split = std::max(1, std::min((a.Hq + rows - 1) / rows, sms / blocks));
+  const int smem = batch * (a.rd / 2) * (int)sizeof(float2);
+  const dim3 grid((unsigned)blocks, (unsigned)split);
+  if (a.half) rope_kernel<T, D, true><<<grid, kThreads, smem, s>>>(a, batch);
+  else rope_kernel<T, D, false><<<grid, kThreads, smem, s>>>(a, batch);
   return cudaGetLastError();
 }
 template <typename T>
