@@ -46,8 +46,9 @@ kk_status check_cache8(const kk_kcache_desc* kc, kk::KCache* out) {
   return KK_OK;
 }
 
-kk_status check_rows(const kk_rows* r, int es) {
-  if (!r || !r->base) return KK_ERR_INVALID;
+// Rows of n nodes (a tensor without any has no address).
+kk_status check_rows(const kk_rows* r, int es, int n) {
+  if (!r || (!r->base && n > 0)) return KK_ERR_INVALID;
   if (!aligned(r->base, 16)) return KK_ERR_UNSUPPORTED;
   for (int64_t st : {r->stride_node, r->stride_head, r->stride_layer})
     if (st < 0 || st * es % 16) return KK_ERR_UNSUPPORTED;
@@ -98,7 +99,7 @@ kk_status kk_qk_norm_rope(int32_t dtype, int32_t num_nodes, int32_t num_q_heads,
   a.D = D;
   kk_status st;
   auto rows = [&](const kk_rows* r, kk::RopeRows* out) {
-    const kk_status s = check_rows(r, es);
+    const kk_status s = check_rows(r, es, num_nodes);
     if (s == KK_OK) *out = kk::RopeRows{r->base, r->stride_node, r->stride_head};
     return s;
   };
@@ -163,7 +164,7 @@ kk_status kk_kv8_write(const kk_kcache_desc* kc, float* k_scale, const kk_kcache
   auto side = [&](const kk_kcache_desc* desc, float* scale, const kk_rows* src) {
     kk::KCache c;
     kk_status s = check_cache8(desc, &c);
-    if (s != KK_OK || (s = check_rows(src, es)) != KK_OK) return s;
+    if (s != KK_OK || (s = check_rows(src, es, num_nodes)) != KK_OK) return s;
     if (!scale || (a.sides && !same_sizes(c, a.kc))) return KK_ERR_INVALID;
     if (!aligned(scale, 4)) return KK_ERR_UNSUPPORTED;
     a.kc = c;

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -99,7 +100,7 @@ def _load():
     KC, BT = ctypes.POINTER(kk_kcache_desc), ctypes.POINTER(kk_block_table)
     RG, OP = ctypes.POINTER(kk_anchor_ring), ctypes.POINTER(kk_step_options)
     TR, SL = ctypes.POINTER(kk_tree), ctypes.POINTER(kk_selection)
-    RW, RP, PA = ctypes.POINTER(kk_rows), ctypes.POINTER(kk_rope), ctypes.POINTER(kk_page_array)
+    RW, RP, PA = P, ctypes.POINTER(kk_rope), ctypes.POINTER(kk_page_array)  # kk_rows: packed bytes (_rows), or byref
     sig = {
         "kk_status_str": (ctypes.c_char_p, [ctypes.c_int]),
         "kk_debug_set_wait_limit": (ctypes.c_int, [ctypes.c_uint64]),
@@ -666,18 +667,24 @@ class Rope:
         self.c = kk_rope(_ptr(inv_freq, torch.float32, "inv_freq"), int(rotary_dim), int(bool(interleaved)), float(scale))
 
 
-def _rows(t, name, nodes=None, heads=None, D=None, dtype=None):
-    """kk_rows of a [nodes][heads][D] tensor, or [layers][nodes][heads][D], whose last dim is dense."""
+# kk_rows as packed bytes: a third of the host time of filling a ctypes structure, five of which a call takes
+_pack_rows = struct.Struct("@4q").pack
+
+
+def _rows(t, name, dtype, shape):
+    """kk_rows of a tensor of that shape, [nodes][heads][D] or [layers][nodes][heads][D], whose last dim is dense."""
     if t is None:
         return None
-    x = t if t.dim() != 4 else t[0]
-    addr, sn, sh = _strided(x, name)
-    if dtype is not None and t.dtype is not dtype:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    for got, want, what in ((x.shape[0], nodes, "nodes"), (x.shape[1], heads, "heads"), (x.shape[2], D, "dims")):
-        if want is not None and got != want:
-            raise ValueError(f"{name} has {got} {what}, expected {want}")
-    return kk_rows(addr, sn, sh, t.stride(0) if t.dim() == 4 else 0)
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must have a dense last dimension")
+    return _pack_rows(t.data_ptr(), st[-3], st[-2], st[0] if len(shape) == 4 else 0)
 
 
 def _ref(c):
@@ -691,25 +698,27 @@ def kk_qk_norm_rope(q, k, rope, q_out, k_out=None, positions=None, q_weight=None
     some = q if q is not None else k
     if some is None:
         raise ValueError("q or k must be given")
-    n, D, dt = some.shape[0], some.shape[2], some.dtype
+    if some.dim() != 3:
+        raise ValueError("q and k must be [nodes][heads][D]")
+    n, Hs, D = some.shape
+    dt = some.dtype
     if dt not in _ELEMS:
         raise TypeError(f"q has dtype {dt}")
-    Hq, H = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
+    Hq = 0 if q is None else Hs
+    H = 0 if k is None else Hs if q is None else k.shape[1]
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out come together")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and w.numel() != D:
-            raise ValueError(f"{name} must have {D} elements")
-    if positions is not None and positions.numel() != n:
-        raise ValueError(f"positions must have {n} elements")
+    for t, name, size in ((q_weight, "q_weight", D), (k_weight, "k_weight", D), (positions, "positions", n)):
+        if t is not None and t.numel() != size:
+            raise ValueError(f"{name} must have {size} elements")
     if token_offsets is not None and (bt is None or token_offsets.numel() != bt.num_requests + 1):
         raise ValueError("token_offsets must have an element more than the table has requests")
-    rows = [_rows(t, name, n, heads, D, dt) for t, name, heads in
-            ((q, "q", Hq), (k, "k", H), (v, "v", H), (q_out, "q_out", Hq), (k_out, "k_out", H))]
+    qs, ks = (n, Hq, D), (n, H, D)
     _check("kk_qk_norm_rope", _lib.kk_qk_norm_rope(
-        _ELEMS[dt], n, Hq, H, D, _ref(rows[0]), _ref(rows[1]), _ref(rows[2]), _ptr(q_weight, dt, "q_weight"),
-        _ptr(k_weight, dt, "k_weight"), float(eps), _ptr(positions, torch.int32, "positions"),
-        None if rope is None else ctypes.byref(rope.c), _ref(rows[3]), _ref(rows[4]), _ref(kc), _ref(vc),
+        _ELEMS[dt], n, Hq, H, D, _rows(q, "q", dt, qs), _rows(k, "k", dt, ks), _rows(v, "v", dt, ks),
+        _ptr(q_weight, dt, "q_weight"), _ptr(k_weight, dt, "k_weight"), float(eps),
+        _ptr(positions, torch.int32, "positions"), None if rope is None else ctypes.byref(rope.c),
+        _rows(q_out, "q_out", dt, qs), _rows(k_out, "k_out", dt, ks), _ref(kc), _ref(vc),
         None if bt is None else ctypes.byref(bt.c), _ptr(token_offsets, torch.int32, "token_offsets"), layer,
         _stream(stream)))
 
@@ -727,20 +736,17 @@ def kk_kv8_write(kc, k_scale, vc, v_scale, bt: BlockTable, layer: int, k, v, max
     some, c = (k, kc) if k is not None else (v, vc)
     if some is None or c is None:
         raise ValueError("Keys or Values must be given, with their cache")
-    if some.dtype not in _ELEMS:
-        raise TypeError(f"k has dtype {some.dtype}")
-    n = some.shape[-3]
-    layers = some.shape[0] if some.dim() == 4 else 1
-    for t, name in ((k, "k"), (v, "v")):
-        if t is not None and t.shape != some.shape:
-            raise ValueError(f"{name} must have the other's shape")
+    dt, shape = some.dtype, tuple(some.shape)
+    if dt not in _ELEMS:
+        raise TypeError(f"k has dtype {dt}")
+    if len(shape) not in (3, 4) or shape[-2:] != (c.num_kv_heads, c.head_dim):
+        raise ValueError(f"k and v must be [layers][nodes][{c.num_kv_heads}][{c.head_dim}]")
     if token_offsets is not None and token_offsets.numel() != bt.num_requests + 1:
         raise ValueError(f"token_offsets must have {bt.num_requests + 1} elements")
-    rows = [_rows(t, name, n, c.num_kv_heads, c.head_dim, some.dtype) for t, name in ((k, "k"), (v, "v"))]
     _check("kk_kv8_write", _lib.kk_kv8_write(
         _ref(kc), _scale_ptr(kc, k_scale, "k_scale"), _ref(vc), _scale_ptr(vc, v_scale, "v_scale"), ctypes.byref(bt.c),
-        layer, layers, _ELEMS[some.dtype], _ref(rows[0]), _ref(rows[1]),
-        _ptr(token_offsets, torch.int32, "token_offsets"), max_new, n, _stream(stream)))
+        layer, shape[0] if len(shape) == 4 else 1, _ELEMS[dt], _rows(k, "k", dt, shape), _rows(v, "v", dt, shape),
+        _ptr(token_offsets, torch.int32, "token_offsets"), max_new, shape[-3], _stream(stream)))
 
 
 def kk_tree_attn_kv8_workspace_bytes(kc, bt: BlockTable, max_nodes: int, num_q_heads: int) -> int:
