@@ -24,14 +24,19 @@
 // left alone until a score passes one by 2^8 (one vote a step); until then sums
 // below 2^8 cost nothing and no reduction over lanes is needed.
 #pragma once
-#include "kk_attn_ring.cuh"
+#include "kk_attn.cuh"
 #include "kk_pdl.cuh"
 
 namespace kk {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kTK = kRingTK, kTok = kTK / kWarps;  // tokens of a warp's share of a tile
+// 16-token groups of a warp's share of a tile: two while registers allow, so that two chains of products are under
+// way and what a step costs besides them is paid once for 32 tokens.
+template <int D, int NT>
+__host__ __device__ constexpr int kv8_groups() {
+  return NT <= 2 && D <= 128 ? 2 : 1;
+}
 constexpr float kNone = -1e30f;                    // a reference before the first score
 constexpr float kLift = 6.f;  // a weight is below 2^(6 + 8) * 2 (a scale's mantissa): float16 holds 65504
 
@@ -67,6 +72,24 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// Two float32 operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+__device__ __forceinline__ void set2(float* p, float2 x) { p[0] = x.x, p[1] = x.y; }
 __device__ __forceinline__ void cp_full16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -113,15 +136,13 @@ struct Group {
 };
 // Where that is: slot v of the request's context, slot o of its block b. It moves on by a tile at a time.
 struct Cursor {
-  int v, b, o, step_b, step_o;
-  __device__ __forceinline__ Cursor(int slot, int bs) : v(slot), b(slot / bs), o(slot - slot / bs * bs) {
-    step_b = kTK / bs;
-    step_o = kTK - step_b * bs;
-  }
-  __device__ __forceinline__ void next(int bs) {
-    v += kTK;
-    b += step_b;
-    o += step_o;
+  int v, b, o;
+  __device__ __forceinline__ Cursor(int slot, int bs) : v(slot), b(slot / bs), o(slot - slot / bs * bs) {}
+  // n slots on: n = nb * bs + no
+  __device__ __forceinline__ void move(int n, int nb, int no, int bs) {
+    v += n;
+    b += nb;
+    o += no;
     if (o >= bs) o -= bs, ++b;
   }
 };
@@ -139,7 +160,7 @@ __device__ __forceinline__ Group find_group(const AttnArgs& a, int r, const Attn
       flag_error(a.err, kErrBadIndex);
       return x;
     }
-    left = (int)min((long long)rq.T - first - c.o, (long long)kTok);
+    left = (int)min((long long)rq.T - first - c.o, 16ll);
   } else {
     x.page = a.bt.pages[rq.off + c.b];
   }
@@ -149,20 +170,20 @@ __device__ __forceinline__ Group find_group(const AttnArgs& a, int r, const Attn
     return x;
   }
   x.o = c.o;
-  x.n = max(0, min(left, PG ? kTok : 1));
+  x.n = max(0, min(left, PG ? 16 : 1));
   return x;
 }
 
-template <int D>
+template <int D, int NT>
 __host__ __device__ constexpr int kv8_stages() {
-  return D >= 128 ? 3 : D == 64 ? 5 : 8;
+  return (D >= 128 ? 4 : D == 64 ? 6 : 8) / kv8_groups<D, NT>() - (D == 256 || NT == 4 ? 1 : 0);
 }
 template <int D, int NT>
 struct Kv8Smem {
-  static constexpr int M = NT * 8, kStage = kTok * D * 2;
-  static constexpr int ring = kWarps * kv8_stages<D>() * kStage, join = kWarps * M * (D + 2) * 4;
-  static constexpr int scales = ring > join ? ring : join;       // [warps][stages][32] floats
-  static constexpr int raw = scales + kWarps * kv8_stages<D>() * 32 * 4;  // queries as they are, bf16 [M][D]
+  static constexpr int M = NT * 8, S = kv8_stages<D, NT>(), kTok = 16 * kv8_groups<D, NT>(), kStage = kTok * D * 2;
+  static constexpr int ring = kWarps * S * kStage, join = kWarps * M * (D + 2) * 4;
+  static constexpr int scales = ring > join ? ring : join;       // [warps][stages][K, V][kTok] floats
+  static constexpr int raw = scales + kWarps * S * 2 * kTok * 4;  // queries as they are, bf16 [M][D]
   static constexpr int frag = raw + M * D * 2;                   // and as float16 operands [NT][D/16][32 lanes]
   static constexpr int qf = frag + M * D * 2;                    // [M] what the scores are multiplied with
   static constexpr int bytes = qf + M * 4;
@@ -170,13 +191,13 @@ struct Kv8Smem {
 
 template <int D, int NT>
 constexpr int kv8_blocks() {
-  return NT == 1 ? (D <= 128 ? 4 : 2) : NT == 2 ? (D <= 128 ? 3 : 2) : 2;
+  return NT == 1 ? (D < 128 ? 4 : D == 128 ? 3 : 2) : NT == 2 ? (D <= 128 ? 3 : 2) : 2;
 }
 
 template <int D, int NT, bool PG>
 __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kernel(const AttnArgs a) {
   using Sm = Kv8Smem<D, NT>;
-  constexpr int M = NT * 8, KS = D / 16, S = kv8_stages<D>();
+  constexpr int M = NT * 8, KS = D / 16, S = Sm::S, U = kv8_groups<D, NT>(), kTok = Sm::kTok, kTK = kTok * kWarps;
   constexpr bool kQReg = NT * D <= 256;  // query operands stay in registers
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long s_place[kWarps + 4];
@@ -184,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kern
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   unsigned char* ring = smem + w * S * Sm::kStage;
   const uint32_t ring_at = smem_u32(ring);
-  float* sc = reinterpret_cast<float*>(smem + Sm::scales) + w * S * 32;
+  float* sc = reinterpret_cast<float*>(smem + Sm::scales) + w * S * 2 * kTok;
   const uint32_t sc_at = smem_u32(sc);
   uint2* frag = reinterpret_cast<uint2*>(smem + Sm::frag);
   float* qf_s = reinterpret_cast<float*>(smem + Sm::qf);
@@ -206,56 +227,65 @@ __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kern
     const int t0 = it.t0, t1 = it.t1, h = it.h, row0 = it.mt * M;
     const int rows = min(M, rq.n * a.G - row0);
 
-    // Copies a share of a tile (16 tokens of K and V, their scales) into stage st. A lane copies the pieces c of
-    // rows sub, sub + RI, ...; what does not change over the tiles is worked out here.
-    constexpr int CH = D / 16, RI = 32 / CH, NI = kTok / RI > 0 ? kTok / RI : 1;
+    // Copies a share of a tile (U groups of 16 tokens of K and V, their scales) into stage st. A lane copies the
+    // pieces c of rows sub, sub + RI, ...; what does not change over the tiles is worked out here.
+    constexpr int CH = D / 16, RI = 32 / CH, NI = 16 / RI > 0 ? 16 / RI : 1;
     const int c = lane % CH, sub = lane / CH;
     const char* k_lane = static_cast<const char*>(a.kc.base) + a.layer * a.kc.sL + h * a.kc.sH + c * 16 + (PG ? sub * a.kc.sT : 0);
     const char* v_lane = static_cast<const char*>(a.vc.base) + a.layer * a.vc.sL + h * a.vc.sH + c * 16 + (PG ? sub * a.vc.sT : 0);
-    const float* s_lane = ((PG ? lane & 1 : lane >> 4) ? a.v_scale : a.k_scale) + (long long)a.layer * a.kc.num_pages * a.kc.H + h;
-    auto load = [&](const Group& x, int st, bool on) {
-      const uint32_t kst = ring_at + st * Sm::kStage, vst = kst + kTok * D;
-      uint32_t live;
+    const long long s_at = (long long)a.layer * a.kc.num_pages * a.kc.H + h;
+    constexpr int NG = PG ? U : 1;  // groups a lane knows: all of the share, or (its own token) one
+    auto load = [&](const Group (&x)[NG], int st, bool on) {
+      const uint32_t kst = ring_at + st * Sm::kStage, vst = kst + kTok * D, sst = sc_at + st * (2 * kTok * 4);
+      uint32_t live = 0;
       if constexpr (PG) {
-        const int n = on ? x.n : 0;
-        live = (1u << n) - 1u;
         if (on) {
-          const char* k = k_lane + x.page * a.kc.sP + x.o * a.kc.sT;
-          const char* v = v_lane + x.page * a.vc.sP + x.o * a.vc.sT;
-          if (n == kTok) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-              cp_full16(kst + at_k<D>(i * RI + sub, c * 16), k);
-              cp_full16(vst + at_v<D>(i * RI + sub, c * 16), v);
-              k += RI * a.kc.sT;
-              v += RI * a.vc.sT;
-            }
-          } else {
+          for (int i = 0; i < U; ++i) {
+            const int n = x[i].n;
+            live |= ((1u << n) - 1u) << (16 * i);
+            const char* k = k_lane + x[i].page * a.kc.sP + x[i].o * a.kc.sT;
+            const char* v = v_lane + x[i].page * a.vc.sP + x[i].o * a.vc.sT;
+            if (n == 16) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-              const bool real = i * RI + sub < n;
-              cp_async16(kst + at_k<D>(i * RI + sub, c * 16), real ? k : k_lane, real);
-              cp_async16(vst + at_v<D>(i * RI + sub, c * 16), real ? v : v_lane, real);
-              k += RI * a.kc.sT;
-              v += RI * a.vc.sT;
+              for (int j = 0; j < NI; ++j) {
+                cp_full16(kst + at_k<D>(i * 16 + j * RI + sub, c * 16), k);
+                cp_full16(vst + at_v<D>(i * 16 + j * RI + sub, c * 16), v);
+                k += RI * a.kc.sT;
+                v += RI * a.vc.sT;
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < NI; ++j) {
+                const bool real = j * RI + sub < n;
+                cp_async16(kst + at_k<D>(i * 16 + j * RI + sub, c * 16), real ? k : k_lane, real);
+                cp_async16(vst + at_v<D>(i * 16 + j * RI + sub, c * 16), real ? v : v_lane, real);
+                k += RI * a.kc.sT;
+                v += RI * a.vc.sT;
+              }
             }
+            if (lane < 2)
+              cp_async4(sst + (lane * kTok + i) * 4, (lane ? a.v_scale : a.k_scale) + s_at + x[i].page * a.kc.H, n > 0);
           }
-          if (lane < 2) cp_async4(sc_at + (st * 32 + lane) * 4, s_lane + x.page * a.kc.H, n > 0);
         }
       } else {
-        const uint32_t ok = __ballot_sync(kFull, on && x.n > 0);
-        live = ok & 0xFFFFu;
-        const long long ko = x.page * a.kc.sP + x.o * a.kc.sT, vo = x.page * a.vc.sP + x.o * a.vc.sT;
+        live = __ballot_sync(kFull, on && x[0].n > 0);
+        if (kTok == 16) live &= 0xFFFFu;
+        const long long ko = x[0].page * a.kc.sP + x[0].o * a.kc.sT, vo = x[0].page * a.vc.sP + x[0].o * a.vc.sT;
         if (on) {
 #pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            const int row = i * RI + sub;
+          for (int j = 0; j < NI * U; ++j) {
+            const int row = j * RI + sub;
             const char* k = k_lane + __shfl_sync(kFull, ko, row);
             const char* v = v_lane + __shfl_sync(kFull, vo, row);
-            cp_async16(kst + at_k<D>(row, c * 16), k, (ok >> row) & 1);
-            cp_async16(vst + at_v<D>(row, c * 16), v, (ok >> row) & 1);
+            cp_async16(kst + at_k<D>(row, c * 16), k, (live >> row) & 1);
+            cp_async16(vst + at_v<D>(row, c * 16), v, (live >> row) & 1);
           }
-          cp_async4(sc_at + (st * 32 + lane) * 4, s_lane + (long long)x.page * a.kc.H, x.n > 0);
+          const long long at = s_at + (long long)x[0].page * a.kc.H;
+          if (lane < kTok) {
+            cp_async4(sst + lane * 4, a.k_scale + at, x[0].n > 0);
+            cp_async4(sst + (kTok + lane) * 4, a.v_scale + at, x[0].n > 0);
+          }
         }
       }
       cp_commit();
@@ -264,14 +294,24 @@ __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kern
 
     // the first tiles' copies go out before the queries are read
     const int tc = min(t1, rq.tiles_c);  // tiles of cached tokens end here
-    Cursor at(t0 * kTK + w * kTok + (PG ? 0 : lane & (kTok - 1)), a.kc.bs);
-    Group nx = {0, 0, 0};
-    if (t0 < tc) nx = find_group<PG>(a, r, rq, at);
+    const int bs = a.kc.bs, tile_b = kTK / bs, tile_o = kTK - tile_b * bs;
+    Cursor at(t0 * kTK + w * kTok + (PG ? 0 : lane & (kTok - 1)), bs);
+    auto find = [&](Group (&x)[NG]) {
+      Cursor y = at;
+      x[0] = find_group<PG>(a, r, rq, y);
+#pragma unroll
+      for (int i = 1; i < NG; ++i) {
+        y.move(16, 0, 16, bs);
+        x[i] = find_group<PG>(a, r, rq, y);
+      }
+    };
+    Group nx[NG] = {};
+    if (t0 < tc) find(nx);
 #pragma unroll 1
     for (int st = 0; st < S - 1; ++st) {
       load(nx, st, t0 + st < tc);
-      at.next(a.kc.bs);
-      if (t0 + st + 1 < tc) nx = find_group<PG>(a, r, rq, at);
+      at.move(kTK, tile_b, tile_o, bs);
+      if (t0 + st + 1 < tc) find(nx);
     }
     for (int i = tid; i < M * (D / 8); i += kThreads) {
       const int m = i / (D / 8), c = i - m * (D / 8), row = row0 + m;
@@ -332,24 +372,33 @@ __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kern
       ref_s[nt][0] = ref_s[nt][1] = ref_v[nt][0] = ref_v[nt][1] = kNone;
       l_run[nt][0] = l_run[nt][1] = 0.f;
     }
-    // Moves the references of rows whose scores passed them; lv: the exponent of the Values' scale of tokens g and g + 8.
-    auto settle = [&](const float (&s)[NT][4], float lv0, float lv1) {
+    // Moves the references of rows whose scores passed them; lv: the exponent of the Values' scale of a group's
+    // tokens g and g + 8 (PG: the same).
+    auto settle = [&](const auto& s, const auto& lv) {
+      constexpr int N = sizeof(s) / sizeof(s[0]);
       bool rise = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float top = PG ? fmaxf(s[nt][e], s[nt][e + 2]) : s[nt][e];
-          rise |= top > 8.f + fminf(ref_s[nt][e], ref_v[nt][e] - lv0);
-          if (!PG) rise |= s[nt][e + 2] > 8.f + fminf(ref_s[nt][e], ref_v[nt][e] - lv1);
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float top = PG ? fmaxf(s[i][nt][e], s[i][nt][e + 2]) : s[i][nt][e];
+            rise |= top > 8.f + fminf(ref_s[nt][e], ref_v[nt][e] - lv[i][0]);
+            if (!PG) rise |= s[i][nt][e + 2] > 8.f + fminf(ref_s[nt][e], ref_v[nt][e] - lv[i][1]);
+          }
       if (!__any_sync(kFull, rise)) return;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float ms = fmaxf(s[nt][e], s[nt][e + 2]), mv = fmaxf(s[nt][e] + lv0, s[nt][e + 2] + lv1);
+          float ms = -INFINITY, mv = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            ms = fmaxf(ms, fmaxf(s[i][nt][e], s[i][nt][e + 2]));
+            mv = fmaxf(mv, fmaxf(s[i][nt][e] + lv[i][0], s[i][nt][e + 2] + lv[i][1]));
+          }
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) {
             ms = fmaxf(ms, __shfl_xor_sync(kFull, ms, x));
@@ -376,87 +425,120 @@ __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kern
       __syncwarp();
       {  // refill the stage read in the last turn
         load(nx, st == 0 ? S - 1 : st - 1, t + S - 1 < tc);
-        at.next(a.kc.bs);
-        if (t + S < tc) nx = find_group<PG>(a, r, rq, at);
+        at.move(kTK, tile_b, tile_o, bs);
+        if (t + S < tc) find(nx);
       }
-      float s[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
       if (t < rq.tiles_c) {
         const unsigned char *kst = ring + st * Sm::kStage, *vst = kst + kTok * D;
         const uint32_t live = s_ok[w][st];
-        constexpr int KW = D >= 64 ? 4 : 2;  // words of codes read at once
+        float s[U][NT][4];
 #pragma unroll
-        for (int i = 0; i < KS / KW; ++i) {
-          uint32_t x[KW], y[KW];
-          lds<KW>(x, kst + at_k<D>(g, i * 64 + t4 * KW * 4));
-          lds<KW>(y, kst + at_k<D>(g + 8, i * 64 + t4 * KW * 4));
-#pragma unroll
-          for (int c = 0; c < KW; ++c) {
-            const uint32_t a0 = widen(x[c], 0), a1 = widen(y[c], 0), a2 = widen(x[c], 1), a3 = widen(y[c], 1);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              uint2 b;
-              if constexpr (kQReg) b = qr[nt][i * KW + c];
-              else b = frag[(nt * KS + i * KW + c) * 32 + lane];
-              mma<false>(s[nt], a0, a1, a2, a3, b.x, b.y);
-            }
-          }
-        }
-        const float* ss = sc + st * 32;
-        const float ks0 = ss[PG ? 0 : g], ks1 = PG ? ks0 : ss[g + 8];
-        float lv0, lv1, vm0, vm1;
-        split_scale(ss[PG ? 1 : 16 + g], &lv0, &vm0);
-        lv1 = lv0, vm1 = vm0;
-        if (!PG) split_scale(ss[24 + g], &lv1, &vm1);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[nt][e] *= qf[nt][e & 1] * (e < 2 ? ks0 : ks1);
-        if (live != 0xFFFFu) {  // selected, whatever a place without a token holds
-          const bool see0 = (live >> g) & 1, see1 = (live >> (g + 8)) & 1;
+        for (int k = 0; k < U; ++k)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] = (e < 2 ? see0 : see1) ? s[nt][e] : -INFINITY;
-        }
-        settle(s, lv0, lv1);
-        uint32_t b0[NT], b1[NT];
+            for (int e = 0; e < 4; ++e) s[k][nt][e] = 0.f;
+        constexpr int KW = D >= 64 ? 4 : 2;  // words of codes read at once
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float p[4];
+        for (int i = 0; i < KS / KW; ++i) {
+          uint32_t x[U][KW], y[U][KW];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            l_run[nt][e & 1] += ex2(s[nt][e] - ref_s[nt][e & 1]);
-            p[e] = ex2(s[nt][e] + ((e < 2 ? lv0 : lv1) - ref_v[nt][e & 1] + kLift)) * (e < 2 ? vm0 : vm1);
+          for (int k = 0; k < U; ++k) {
+            lds<KW>(x[k], kst + at_k<D>(k * 16 + g, i * 64 + t4 * KW * 4));
+            lds<KW>(y[k], kst + at_k<D>(k * 16 + g + 8, i * 64 + t4 * KW * 4));
           }
-          b0[nt] = turn(pack_f16(p[0], p[1]));  // the weights' one rounding: float16 feeds the product
-          b1[nt] = turn(pack_f16(p[2], p[3]));
-        }
-        constexpr int VW = D >= 128 ? 4 : D / 32;  // words of a thread's D/8 dims read at once
 #pragma unroll
-        for (int i = 0; i < KS / (2 * VW); ++i) {
-          uint32_t x[4][VW];
+          for (int c = 0; c < KW; ++c)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            lds<VW>(x[k], vst + at_v<D>(2 * t4 + (k & 1) + (k >> 1) * 8, i * 128 + g * VW * 4));
+            for (int k = 0; k < U; ++k) {
+              const uint32_t a0 = widen(x[k][c], 0), a1 = widen(y[k][c], 0), a2 = widen(x[k][c], 1), a3 = widen(y[k][c], 1);
 #pragma unroll
-          for (int c = 0; c < VW; ++c)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const uint32_t p = __byte_perm(x[0][c], x[1][c], hf ? 0x7362 : 0x5140);
-              const uint32_t q = __byte_perm(x[2][c], x[3][c], hf ? 0x7362 : 0x5140);
-              const uint32_t a0 = widen(p, 0), a1 = widen(p, 1), a2 = widen(q, 0), a3 = widen(q, 1);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma<false>(o[nt][(i * VW + c) * 2 + hf], a0, a1, a2, a3, b0[nt], b1[nt]);
+              for (int nt = 0; nt < NT; ++nt) {
+                uint2 b;
+                if constexpr (kQReg) b = qr[nt][i * KW + c];
+                else b = frag[(nt * KS + i * KW + c) * 32 + lane];
+                mma<false>(s[k][nt], a0, a1, a2, a3, b.x, b.y);
+              }
             }
         }
+        const float* ss = sc + st * 2 * kTok;
+        float lv[U][2], vm[U][2];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const float ks0 = ss[PG ? k : k * 16 + g], ks1 = PG ? ks0 : ss[k * 16 + 8 + g];
+          split_scale(ss[kTok + (PG ? k : k * 16 + g)], &lv[k][0], &vm[k][0]);
+          lv[k][1] = lv[k][0], vm[k][1] = vm[k][0];
+          if (!PG) split_scale(ss[kTok + k * 16 + 8 + g], &lv[k][1], &vm[k][1]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float2 f0 = mul2(make_float2(qf[nt][0], qf[nt][1]), make_float2(ks0, ks0));
+            const float2 f1 = PG ? f0 : mul2(make_float2(qf[nt][0], qf[nt][1]), make_float2(ks1, ks1));
+            set2(&s[k][nt][0], mul2(make_float2(s[k][nt][0], s[k][nt][1]), f0));
+            set2(&s[k][nt][2], mul2(make_float2(s[k][nt][2], s[k][nt][3]), f1));
+          }
+        }
+        if (live != (kTok == 32 ? 0xFFFFFFFFu : 0xFFFFu)) {  // selected, whatever a place without a token holds
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            const bool see0 = (live >> (k * 16 + g)) & 1, see1 = (live >> (k * 16 + 8 + g)) & 1;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[k][nt][e] = (e < 2 ? see0 : see1) ? s[k][nt][e] : -INFINITY;
+          }
+        }
+        settle(s, lv);
+        uint32_t b0[U][NT], b1[U][NT];
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float2 down = make_float2(-ref_s[nt][0], -ref_s[nt][1]);
+            float2 sum = make_float2(l_run[nt][0], l_run[nt][1]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float2 y = make_float2(s[k][nt][2 * x], s[k][nt][2 * x + 1]);
+              const float2 p = add2(y, down);
+              sum = add2(sum, make_float2(ex2(p.x), ex2(p.y)));
+              const float up = lv[k][x] + kLift;
+              const float2 q = add2(y, make_float2(up - ref_v[nt][0], up - ref_v[nt][1]));
+              const float2 z = mul2(make_float2(ex2(q.x), ex2(q.y)), make_float2(vm[k][x], vm[k][x]));
+              // the weights' one rounding: float16 feeds the product
+              (x ? b1 : b0)[k][nt] = turn(pack_f16(z.x, z.y));
+            }
+            l_run[nt][0] = sum.x;
+            l_run[nt][1] = sum.y;
+          }
+        constexpr int VW = D >= 128 ? 4 : D / 32;  // words of a thread's D/8 dims read at once
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+          for (int i = 0; i < KS / (2 * VW); ++i) {
+            uint32_t x[4][VW];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              lds<VW>(x[j], vst + at_v<D>(k * 16 + 2 * t4 + (j & 1) + (j >> 1) * 8, i * 128 + g * VW * 4));
+#pragma unroll
+            for (int c = 0; c < VW; ++c)
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                const uint32_t p = __byte_perm(x[0][c], x[1][c], hf ? 0x7362 : 0x5140);
+                const uint32_t q = __byte_perm(x[2][c], x[3][c], hf ? 0x7362 : 0x5140);
+                const uint32_t a0 = widen(p, 0), a1 = widen(p, 1), a2 = widen(q, 0), a3 = widen(q, 1);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma<false>(o[nt][(i * VW + c) * 2 + hf], a0, a1, a2, a3, b0[k][nt], b1[k][nt]);
+              }
+          }
       } else if (a.dk) {
-        // drafted nodes, bf16, straight from where they lie; at most 16 of these steps an item
-        const int j0 = (t - rq.tiles_c) * kTK + w * kTok;
-        if (j0 < rq.n) {
+        // drafted nodes, bf16, 16 at a time straight from where they lie; at most 16 of these steps an item
+#pragma unroll 1
+        for (int j0 = (t - rq.tiles_c) * kTK + w * kTok, je = min(rq.n, j0 + kTok); j0 < je; j0 += 16) {
+          float s[1][NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[0][nt][e] = 0.f;
           const uint16_t* dk = static_cast<const uint16_t*>(a.dk) + rq.node0 * a.dk_sn + h * a.dk_sh;
           const uint16_t* dv = static_cast<const uint16_t*>(a.dv) + rq.node0 * a.dv_sn + h * a.dv_sh;
           const unsigned char* raw = smem + Sm::raw;
@@ -468,8 +550,8 @@ __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kern
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const uint4 b = *reinterpret_cast<const uint4*>(raw + ((nt * 8 + g) * D + i * 32 + t4 * 8) * 2);
-              mma<true>(s[nt], x.x, y.x, x.y, y.y, b.x, b.y);
-              mma<true>(s[nt], x.z, y.z, x.w, y.w, b.z, b.w);
+              mma<true>(s[0][nt], x.x, y.x, x.y, y.y, b.x, b.y);
+              mma<true>(s[0][nt], x.z, y.z, x.w, y.w, b.z, b.w);
             }
           }
 #pragma unroll
@@ -478,17 +560,18 @@ __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kern
             for (int e = 0; e < 4; ++e) {
               const int row = row0 + nt * 8 + 2 * t4 + (e & 1), j = j0 + (e < 2 ? g : g + 8);
               const bool see = j < rq.n && row < rq.n * a.G && sees(a, rq, row / a.G, j);
-              s[nt][e] = see ? s[nt][e] * a.scale_log2 : -INFINITY;
+              s[0][nt][e] = see ? s[0][nt][e] * a.scale_log2 : -INFINITY;
             }
-          settle(s, 0.f, 0.f);
+          const float lv[1][2] = {{0.f, 0.f}};
+          settle(s, lv);
           uint32_t b0[NT], b1[NT];
           float p[NT][4];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              l_run[nt][e & 1] += ex2(s[nt][e] - ref_s[nt][e & 1]);
-              p[nt][e] = ex2(s[nt][e] - ref_v[nt][e & 1] + kLift);
+              l_run[nt][e & 1] += ex2(s[0][nt][e] - ref_s[nt][e & 1]);
+              p[nt][e] = ex2(s[0][nt][e] - ref_v[nt][e & 1] + kLift);
             }
             b0[nt] = turn(pack_bf16(p[nt][0], p[nt][1]));  // bf16, as the Values they meet
             b1[nt] = turn(pack_bf16(p[nt][2], p[nt][3]));
@@ -533,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kern
           }
           if (__any_sync(kFull, odd)) {
 #pragma unroll 1
-            for (int k = 0; k < kTok && j0 + k < rq.n; ++k)
+            for (int k = 0; k < 16 && j0 + k < rq.n; ++k)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -636,7 +719,7 @@ template <int D, int NT>
 AttnPlan plan_n() {
   int per = 227 * 1024 / (Kv8Smem<D, NT>::bytes + 1024 + 256);
   if (per > kv8_blocks<D, NT>()) per = kv8_blocks<D, NT>();
-  return AttnPlan{AttnPlan::kKv8, NT * 8, kTK, sm_count() * (per < 1 ? 1 : per)};
+  return AttnPlan{AttnPlan::kKv8, NT * 8, Kv8Smem<D, NT>::kTok * kWarps, sm_count() * (per < 1 ? 1 : per)};
 }
 template <int D>
 AttnPlan plan_d(int rows) {
@@ -646,7 +729,7 @@ AttnPlan plan_d(int rows) {
 }
 template <int D>
 cudaError_t go_d(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
-  const bool pg = a.kc.bs % kTok == 0;
+  const bool pg = a.kc.bs % 16 == 0;
   if (pl.M == 8) return pg ? go<D, 1, true>(a, s) : go<D, 1, false>(a, s);
   if (pl.M == 16) return pg ? go<D, 2, true>(a, s) : go<D, 2, false>(a, s);
   return pg ? go<D, D == 256 ? 2 : 4, true>(a, s) : go<D, D == 256 ? 2 : 4, false>(a, s);
