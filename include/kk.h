@@ -105,9 +105,9 @@ typedef struct kk_block_table {
  *   wait for that box runs out; -1 cancels. The request is used up by that
  *   launch. KK_ERR_INVALID for box < -1.
  * kk_debug_skip_tile_copy: the same for tile `tile` of the Keys that the first
- *   CTA of the next launch of a tensor-core kernel (kk_tree_attn on many rows,
- *   kk_attn_mass) loads by TMA: its wait expects one copy of 16 bytes more than
- *   is issued.
+ *   CTA of the next launch of a tensor-core kernel (kk_tree_attn and
+ *   kk_tree_attn_kv8 on many rows, kk_attn_mass) loads: its wait expects one copy
+ *   of 16 bytes more than is issued.
  *   KK_ERR_INVALID for tile < -1.
  */
 kk_status kk_debug_set_wait_limit(uint64_t ns);
@@ -710,7 +710,9 @@ kk_status kk_kv8_write(const kk_kcache_desc* kc, float* k_scale, const kk_kcache
  * float16, which holds them exactly, queries as float16 scaled by a power of two
  * for each row (what that loses is below 2^-39 of the row's largest element),
  * weights are rounded to float16 (of drafted nodes: bf16) before they multiply
- * the Values; sums and softmax are float32. Scales are finite.
+ * the Values; where max_nodes * num_q_heads / num_kv_heads > 80, with 64 or 128
+ * dims, weights are rounded to bf16, and values as bf16 (exact where their scale
+ * is a power of two). Sums and softmax are float32. Scales are finite.
  * Workspace: kk_tree_attn_kv8_workspace_bytes().
  */
 size_t kk_tree_attn_kv8_workspace_bytes(const kk_kcache_desc* kc, const kk_block_table* bt, int32_t max_nodes,

@@ -312,6 +312,13 @@ cudaError_t combine_t(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
 // 18.8, 64 K x 3 26.9 / 25.8, 64 K x 5 32.5 / 26.9. One tile of 16 rows: 1 M tokens
 // 97.0 / 96.5 and 131 K 26.9 / 31.5 (D = 64: 57.4 / 65.8 and 20.7 / 28.9).
 constexpr long long kTcWork = 72 << 10;
+// The same over an 8-bit cache, where the loaders' conversions, which are the same for 1 row as for 256, bound the
+// tensor-memory kernel: from 80 rows on (8 requests of up to 32768 tokens, 4 KV heads, groups of 7, few rows / tensor
+// memory: 9 nodes 145 / 163 us, 16 nodes 211 / 170, 36 nodes 434 / 177, 64 nodes 744 / 447; up to 8192 tokens
+// 50 / 55, 67 / 64, 127 / 68, 211 / 132; up to 1024 tokens 25 / 27, 29 / 28, 47 / 37, 77 / 43; 64 dims and up to 32768 93 / 111,
+// 133 / 113 at 9 and 16 nodes), and not for a few thousand tokens, which it starts too slowly for.
+constexpr int kTcRows8 = 80;
+constexpr long long kTcTokens8 = 16 << 10;
 // From where the mma kernel's tiles have 32 rows (layouts that do not suit the
 // other kernel): 512 K tokens of 128 dims and 28, 63, 91 rows 90 / 153 / 215 us
 // against 100 / 176 / 252 with 16, but 64 K tokens 31 / 41 / 51 against 29 / 37 / 47;
@@ -321,7 +328,8 @@ constexpr long long kWideTokens = 256 << 10;
 
 AttnPlan plan(const KCache& kc, const KCache& vc, int max_nodes, int G, long long tokens) {
   const int rows = max_nodes * G;
-  if (kc.dtype == 2) return attn_kv8_plan(kc, rows);
+  if (kc.dtype == 2)
+    return rows > kTcRows8 && tokens >= kTcTokens8 && attn_tc8_suits(kc) ? attn_tc_plan() : attn_kv8_plan(kc, rows);
   if (kc.dtype != 1) return attn_f32_plan(kc, rows);
   if (tokens * ((rows - 1) / 16) >= kTcWork && attn_tc_suits(kc) && attn_tc_suits(vc)) return attn_tc_plan();
   return attn_mma_plan(kc, rows > 16 && tokens >= kWideTokens);
@@ -349,7 +357,10 @@ size_t attn_workspace_bytes(const KCache& kc, int R, int max_nodes, int G) {
   // enough for any: which one runs also depends on the V cache's strides and the tokens
   const int rows = max_nodes * G;
   auto size = [&](const AttnPlan& pl) { return cut_bytes(pl, R, kc.H, rows) + plan_bytes(pl, kc.D); };
-  if (kc.dtype == 2) return size(attn_kv8_plan(kc, rows));
+  if (kc.dtype == 2) {
+    const size_t n = size(attn_kv8_plan(kc, rows));
+    return rows > kTcRows8 && attn_tc8_suits(kc) ? std::max(n, size(attn_tc_plan())) : n;
+  }
   if (kc.dtype != 1) return size(attn_f32_plan(kc, rows));
   const size_t n = size(attn_mma_plan(kc, false));
   if (rows <= 16) return n;
@@ -368,7 +379,7 @@ cudaError_t launch_tree_attn(AttnArgs a, cudaStream_t s) {
   const bool bf = a.kc.dtype != 0;  // the queries' and results' type
   cudaError_t e = cudaErrorNotSupported;
   if (pl.kind == AttnPlan::kTc) {
-    e = launch_attn_tc(a, s);
+    e = a.kc.dtype == 2 ? launch_attn_tc8(a, s) : launch_attn_tc(a, s);
   } else if (pl.kind == AttnPlan::kMma) {
     e = launch_attn_mma(a, pl, s);
   } else if (pl.kind == AttnPlan::kKv8) {

@@ -76,6 +76,9 @@ cudaError_t launch_attn_kv8(const AttnArgs& a, const AttnPlan& pl, cudaStream_t 
 bool attn_tc_suits(const KCache& kc);
 AttnPlan attn_tc_plan();
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t s);
+// kk_attn_tc8.cu (e4m3 with scales, D 64 or 128, any layout)
+inline bool attn_tc8_suits(const KCache& kc) { return kc.D == 64 || kc.D == 128; }
+cudaError_t launch_attn_tc8(const AttnArgs& a, cudaStream_t s);
 
 // kk_mass_tc.cu (bf16, D 64, 128 or 256, a layout it suits)
 bool mass_tc_suits(const KCache& kc);

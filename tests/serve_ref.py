@@ -67,8 +67,13 @@ class Paged8(Paged):
 
 
 def attn8_ref(pc, layer, no, q, scale, G, dk=None, dv=None, see=None, sel=None):
-    """out, lse and elementwise bounds on their errors. `see`: per request [n][n] booleans."""
+    """out, lse and elementwise bounds on their errors. `see`: per request [n][n] booleans.
+
+    Weights are rounded to float16; where a request may have more than 80 query rows per KV head (64 and 128 dims)
+    they may be bf16, and so may values be whose scale is no power of two (a code times a power of two is exact)."""
     n, Hq, D = q.shape
+    many = max(int(b - a) for a, b in zip(no, no[1:])) * G > 80 and D in (64, 128)
+    odd = lambda s: (torch.frexp(s)[0].abs() != 0.5) & (s != 0)  # noqa: E731  no power of two
     out, lse = torch.zeros((n, Hq, D), dtype=torch.float64), torch.full((n, Hq), -math.inf, dtype=torch.float64)
     tol, ltol = torch.zeros_like(out), torch.zeros_like(lse)
     for r, T in enumerate(pc.lens):
@@ -80,8 +85,10 @@ def attn8_ref(pc, layer, no, q, scale, G, dk=None, dv=None, see=None, sel=None):
         for h in range(pc.H):
             k, v = (pc.tokens(x, layer, r, h, where) for x in (pc.k, pc.v))
             vs = pc.vs[layer, pg[where // pc.bs], h].double().abs() if len(where) else where.double()
+            kodd, vodd = (odd(x[layer, pg[where // pc.bs], h]) * (BF16 if many else 0.0) if len(where) else where.double()
+                          for x in (pc.ks, pc.vs))
             for i in range(a, b):
-                ki, vi, si = k, v, vs
+                ki, vi, si, ko, vo = k, v, vs, kodd, vodd
                 nd = 0
                 if dk is not None:
                     js = [j for j in range(b - a) if (see[r][i - a, j] if see is not None else j <= i - a)]
@@ -89,6 +96,7 @@ def attn8_ref(pc, layer, no, q, scale, G, dk=None, dv=None, see=None, sel=None):
                     ki = torch.cat([k, dk[[a + j for j in js], h].double()])
                     vi = torch.cat([v, dv[[a + j for j in js], h].double()])
                     si = torch.cat([vs, torch.ones(nd, dtype=torch.float64)])
+                    ko, vo = (torch.cat([x, torch.zeros(nd, dtype=torch.float64)]) for x in (kodd, vodd))
                 if len(ki) == 0:
                     continue
                 for hq in range(h * G, (h + 1) * G):
@@ -100,9 +108,12 @@ def attn8_ref(pc, layer, no, q, scale, G, dk=None, dv=None, see=None, sel=None):
                     # float32: a product's sum is off by D roundings of its parts (and the scales' own), the
                     # exponent's argument by those and a few more of its size, the sums by one per token
                     es = (D + 6) * F32 * abs(scale) * float((ki.abs() @ x.abs()).max()) + 6 * F32 * float(s.abs().max())
+                    es += abs(scale) * float((ko * (ki.abs() @ x.abs())).max())
                     rel = 2 * es + (2 * len(ki) + 32) * F32
-                    w = torch.full((len(ki),), F16, dtype=torch.float64)  # the weights' rounding
+                    # the weights' rounding, and the Values'
+                    w = torch.full((len(ki),), BF16 if many else F16, dtype=torch.float64) + vo * (1 + BF16)
                     w[len(ki) - nd:] = BF16
+                    rel = math.expm1(rel)
                     # float16 weights are at least 2^6 at the largest p * v_scale, and lose 2^-25 at the bottom
                     low = 2.0 ** -31 * float((p * si).max()) * (vi / si.clamp(min=1e-300)[:, None]).abs().sum(0)
                     tol[i, hq] = rel * (p @ vi.abs()) + (w * p) @ vi.abs() + low

@@ -14,6 +14,12 @@ from tests.serve_ref import Paged8, attn8_ref
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True, params=[0, 1 << 16], ids=["tight", "loose"])
+def table_bound(request, monkeypatch):
+    """Short lengths under a tight and a loose bound: every kernel at every size."""
+    monkeypatch.setattr(Paged8, "bound", request.param)
+
+
 def _nodes(counts, Hq, D, H, seed):
     g = torch.Generator().manual_seed(seed)
     x = torch.randn((sum(counts), Hq + 2 * H, D), generator=g).bfloat16()
@@ -44,7 +50,7 @@ def _run(pc, layer, counts, G, draft=False, see=None, sel=None, seed=5, scale=No
                    _gpu(dv) if draft else None)
     gsel = None
     if sel is not None:
-        K = max(max(len(s) for s in sel), 1) + 1
+        K = max(max(len(s) for s in sel), 1, min(Paged8.bound, 2000)) + 1
         lg = torch.full((len(sel), K), -1, dtype=torch.int32)
         pg = lg.clone()
         for r, s in enumerate(sel):
@@ -91,6 +97,8 @@ def test_long_rows_are_split_and_joined(cuda, D, H, G, lens, counts):
     pc = Paged8(lens, H=H, D=D, bs=16, L=1, seed=9)
     _check(*_run(pc, 0, counts, G))
     _check(*_run(pc, 0, [min(5, 3 * c) for c in counts], G, draft=True))
+    if sum(lens) < 10000:
+        _check(*_run(pc, 0, [150 // G] * len(lens), G, draft=True))
 
 
 @pytest.mark.parametrize("D", [32, 64, 128, 256])
@@ -113,6 +121,7 @@ def test_selected_blocks(cuda, bs):
     sel = [[0, 3, 4, 9], [1, 3], [0], []]
     _check(*_run(pc, 1, [1, 3, 1, 1], 7, sel=sel))
     _check(*_run(pc, 0, [2, 3, 1, 4], 7, draft=True, sel=sel))
+    _check(*_run(pc, 0, [2, 17, 1, 4], 7, draft=True, sel=sel))
 
 
 @pytest.mark.parametrize("bs", [16, 12])
@@ -129,6 +138,7 @@ def test_scales_far_apart(cuda, bs):
     pc.refresh()
     _check(*_run(pc, 0, [1, 3], 5))
     _check(*_run(pc, 0, [2, 9], 5, draft=True))
+    _check(*_run(pc, 0, [2, 65], 5, draft=True))
 
 
 def test_one_value_far_above_the_others(cuda):
@@ -150,26 +160,28 @@ def test_flat_weights(cuda):
     _check(*_run(pc, 0, [1], 7, scale=1.0))
 
 
-def test_nan_codes_count_where_they_are_seen(cuda):
+@pytest.mark.parametrize("nodes", [1, 24])
+def test_nan_codes_count_where_they_are_seen(cuda, nodes):
     pc = Paged8([50, 33], H=2, D=64, bs=16, L=1, seed=11)
     p = int(pc.pages[2])
     pc.vc[0, p, 1, 3, 5] = 0x7F  # one dim of one head's Value
     pc.refresh()
-    out, lse, ref = _run(pc, 0, [1, 1], 4)
+    out, lse, ref = _run(pc, 0, [nodes, 1], 4)
     _check(out, lse, ref)
-    assert torch.isnan(out[0, 4:, 5]).all() and int(torch.isnan(out).sum()) == 4
+    assert torch.isnan(out[:nodes, 4:, 5]).all() and int(torch.isnan(out).sum()) == 4 * nodes
 
 
-def test_drafted_values_that_are_not_finite(cuda):
+@pytest.mark.parametrize("n", [6, 40])
+def test_drafted_values_that_are_not_finite(cuda, n):
     def spoil(no, q, dk, dv):
         dv[2, 0, 7] = math.inf
         dv[5, 1, 9] = math.nan
         dk[3, 0, 1] = math.nan  # of a node that no other sees
 
-    see = [np.eye(6, dtype=bool)]
+    see = [np.eye(n, dtype=bool)]
     see[0][4, 2] = True
     pc = Paged8([37], H=2, D=128, bs=16, L=1, seed=12)
-    out, lse, ref = _run(pc, 0, [6], 3, draft=True, see=see, spoil=spoil)
+    out, lse, ref = _run(pc, 0, [n], 3, draft=True, see=see, spoil=spoil)
     finite = torch.isfinite(ref[0])
     assert torch.equal(torch.isfinite(out).cpu(), finite)
     o = torch.where(finite.cuda(), out, 0)
@@ -244,3 +256,32 @@ def test_bad_device_data_is_reported(cuda):
     assert (out[0] == 0).all() and (lse[0] == -math.inf).all()
     call(pc.bt)
     assert kk.kk_device_error() == 0
+
+
+def test_a_wait_that_runs_out(cuda):
+    """A tile of Keys that never comes: the call reports it and returns, and the next one is sound."""
+    from kv_cache_block_gb300 import kk
+
+    pc = Paged8([3000, 2000], H=2, D=128, bs=16, L=1, seed=16).to_gpu()
+    pc.bt = kk.BlockTable(pc.bt.pages, pc.bt.offsets, pc.bt.seq_lens, 1 << 12)
+    no, q, _, _ = _nodes([16, 16], 14, 128, 2, 5)
+    tree, gq = kk.Tree(16), q.contiguous().cuda()
+    ws = torch.empty(kk.kk_tree_attn_kv8_workspace_bytes(pc.kd, pc.bt, 16, 14), dtype=torch.uint8, device="cuda")
+
+    def call():
+        out, lse = torch.zeros((32, 14, 128), dtype=torch.bfloat16, device="cuda"), torch.zeros((32, 14), device="cuda")
+        kk.kk_tree_attn_kv8(pc.kd, pc.gks, pc.vd, pc.gvs, pc.bt, 0, tree, gq, 0.09, out, lse, workspace=ws)
+        return out, lse, kk.kk_device_error()
+
+    want = call()
+    assert want[2] == 0
+    kk.kk_debug_set_wait_limit(200000)
+    try:
+        for tile in (0, 1):
+            kk.kk_debug_skip_tile_copy(tile)
+            assert call()[2] == kk.KK_ERR_TIMEOUT
+    finally:
+        kk.kk_debug_set_wait_limit(0)
+        kk.kk_debug_skip_tile_copy(-1)
+    got = call()
+    assert got[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
