@@ -365,17 +365,32 @@ constexpr int kCopy = 256, kUnroll = 8, kChunk = kCopy * kUnroll;
 
 template <typename V>
 __device__ __forceinline__ void copy_chunk(const PageArray& d, const int2 m, int first) {
+  if (d.whole) {  // the chunk is a run of one slice
+    const int s = first / d.per;
+    const long long at = s * d.slice + (long long)(first - s * d.per + (int)threadIdx.x) * (int)sizeof(V);
+    const V* from = reinterpret_cast<const V*>(d.base + m.x * d.page + at);
+    V* to = reinterpret_cast<V*>(d.base + m.y * d.page + at);
+    V x[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) x[u] = __ldcs(from + u * kCopy);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) to[u * kCopy] = x[u];
+    return;
+  }
   const int left = d.vecs - first - (int)threadIdx.x;  // vectors of the page from the thread's first on
   const int s0 = (first + (int)threadIdx.x) / d.per, o0 = first + (int)threadIdx.x - s0 * d.per;
   V x[kUnroll];
+  // from one of a thread's vectors to the next: `step` bytes, or `step` and on to the next slice
+  const long long step = d.step_s * d.slice + d.step_o * (int)sizeof(V), over = d.slice - (long long)d.per * (int)sizeof(V);
   auto each = [&](auto f) {
-    int s = s0, o = o0;
+    long long at = s0 * d.slice + (long long)o0 * (int)sizeof(V);
+    int o = o0;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (u * kCopy < left) f(u, s * d.slice + (long long)o * (int)sizeof(V));
-      s += d.step_s;
+      if (u * kCopy < left) f(u, at);
+      at += step;
       o += d.step_o;
-      if (o >= d.per) o -= d.per, ++s;
+      if (o >= d.per) o -= d.per, at += over;
     }
   };
   const char* from = d.base + m.x * d.page;
@@ -384,7 +399,7 @@ __device__ __forceinline__ void copy_chunk(const PageArray& d, const int2 m, int
   each([&](int u, long long at) { *reinterpret_cast<V*>(to + at) = x[u]; });
 }
 
-__global__ void __launch_bounds__(kCopy, 4) pages_copy_kernel(const PageArrays pa, const int2* pairs, const int* n_pairs,
+__global__ void __launch_bounds__(kCopy, 3) pages_copy_kernel(const __grid_constant__ PageArrays pa, const int2* pairs, const int* n_pairs,
                                                            int num_pages) {
   pdl_wait();
   pdl_launch_dependents();
@@ -450,6 +465,7 @@ bool plan_page_arrays(PageArrays* pa) {
     d.vecs = (int)vecs;
     d.step_s = kCopy / d.per;
     d.step_o = kCopy % d.per;
+    d.whole = d.per % kChunk == 0;
     d.first = pa->chunks;
     pa->chunks += (int)chunks;
   }

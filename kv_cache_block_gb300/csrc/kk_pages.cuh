@@ -13,6 +13,7 @@ struct PageArray {
   int per, vecs;                 // vectors of a slice, of a page
   int step_s, step_o;            // slices and vectors a thread moves on by from one of its vectors to the next
   int first;                     // chunks of the arrays before
+  bool whole;                    // slices are whole chunks
 };
 struct PageArrays {
   PageArray a[kMaxPageArrays];

@@ -61,9 +61,9 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a, int
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int node0 = blockIdx.x * batch, nodes = min(batch, a.nodes - node0);
   const int pairs = a.rd / 2;
-  if (tid < pairs) s_turn[tid] = turns_of(a.inv_freq[tid]);
-  if (tid < nodes) {
-    const int node = node0 + tid;
+  // The position and the cache slots of node node0 + k, by one thread: a chain of four or five loads.
+  auto look_up = [&](int k) {
+    const int node = node0 + k;
     int pos = node;
     long long ks = -1, vs = -1;
     if (a.bt.offsets) {
@@ -94,11 +94,18 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a, int
           vs = (a.layer * a.vL + page * a.vP + o * a.vT) * ES;
         }
       }
-      if (!ok) flag_error(a.err, kErrBadIndex);
+      if (!ok && blockIdx.y == 0) flag_error(a.err, kErrBadIndex);
     }
-    s_slot[tid][0] = ks;
-    s_slot[tid][1] = vs;
-    s_pos[tid] = a.positions ? a.positions[node] : pos;
+    s_slot[k][0] = ks;
+    s_slot[k][1] = vs;
+    return pos;
+  };
+  // Given positions need no table: the slots are looked up by the last warp while the others are at the queries.
+  const bool late = a.positions != nullptr && a.Hq > 0;
+  if (tid < pairs) s_turn[tid] = turns_of(a.inv_freq[tid]);
+  if (tid < nodes) {
+    const int pos = late ? 0 : look_up(tid);
+    s_pos[tid] = a.positions ? a.positions[node0 + tid] : pos;
   }
   __syncthreads();
   for (int i = tid; i < nodes * pairs; i += kThreads) {
@@ -109,6 +116,8 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a, int
     s_cs[k * pairs + p % E * (pairs / E) + p / E] = make_float2(cs * a.rope_scale, sn * a.rope_scale);
   }
   __syncthreads();
+  if (late && w == kWarps - 1 && lane < nodes) look_up(lane);
+  __syncwarp();
 
   // the lane's two pieces of a row, and its first pair (none: past rotary_dim)
   const int j = lane % LPR, turned = a.rd / (2 * E);
@@ -120,6 +129,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a, int
   const int cq = (a.Hq + RPW - 1) / RPW, ck = (a.H + RPW - 1) / RPW;
   for (int kind = 0; kind < (a.v ? 3 : 2); ++kind) {
     const int heads = kind ? a.H : a.Hq, all = kind ? ck : cq;
+    if (kind == 1 && late) __syncthreads();  // the slots
     const int per = (all + gridDim.y - 1) / gridDim.y;
     const int c0 = blockIdx.y * per, chunks = min(all, c0 + per) - c0;  // this block's share of the heads
     if (chunks <= 0) continue;
