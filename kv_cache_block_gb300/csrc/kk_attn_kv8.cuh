@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kern
               }
             }
             if (lane < 2)
-              cp_async4(sst + (lane * kTok + i) * 4, (lane ? a.v_scale : a.k_scale) + s_at + x[i].page * a.kc.H, n > 0);
+              cp_async4(sst + (lane * kTok + i) * 4, (lane ? a.v_scale : a.k_scale) + s_at + (long long)x[i].page * a.kc.H, n > 0);
           }
         }
       } else {

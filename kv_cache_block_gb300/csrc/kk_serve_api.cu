@@ -1,7 +1,6 @@
 // C ABI of the calls around a serving step (include/kk.h): norm and rotation, the
 // 8-bit cache, pages. Argument checks on the host, then launches.
 #include <cmath>
-#include <cstdlib>
 
 #include "../../include/kk.h"
 
@@ -68,11 +67,33 @@ kk_status check_arrays(const kk_page_array* arrays, int32_t n, kk::PageArrays* o
   return kk::plan_page_arrays(out) ? KK_OK : KK_ERR_UNSUPPORTED;
 }
 
+// An array of ints of a call, and whether two of them share memory.
+struct Ints {
+  const int32_t* p;
+  long long n;
+};
+bool share(const Ints& a, const Ints& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.n > 0 && b.n > 0 && x < y + 4 * (unsigned long long)b.n && y < x + 4 * (unsigned long long)a.n;
+}
+// Whether any of what is written shares memory with what is read while it is, or with another of them.
+template <size_t W, size_t N>
+bool collide(const Ints (&written)[W], const Ints (&read)[N]) {
+  for (size_t i = 0; i < W; ++i) {
+    for (size_t j = 0; j < i; ++j)
+      if (share(written[i], written[j])) return true;
+    for (const Ints& r : read)
+      if (share(written[i], r)) return true;
+  }
+  return false;
+}
+
+constexpr int kMaxInts = 1 << 30;  // pages, or elements of a list
+
 kk_status check_refs(const int32_t* in, int32_t* out, int32_t num_pages) {
   if (!in || !out || num_pages < 1) return KK_ERR_INVALID;
-  if (!aligned(in, 4) || !aligned(out, 4)) return KK_ERR_UNSUPPORTED;
-  const intptr_t apart = reinterpret_cast<intptr_t>(in) - reinterpret_cast<intptr_t>(out);
-  return apart != 0 && std::llabs(apart) < 4ll * num_pages ? KK_ERR_INVALID : KK_OK;  // the same, or apart
+  if (!aligned(in, 4) || !aligned(out, 4) || num_pages > kMaxInts) return KK_ERR_UNSUPPORTED;
+  return in != out && share({in, num_pages}, {out, num_pages}) ? KK_ERR_INVALID : KK_OK;  // the same, or apart
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -218,7 +239,10 @@ kk_status kk_pages_alloc(const int32_t* refs_in, int32_t* refs_out, int32_t num_
   const kk_status st = check_refs(refs_in, refs_out, num_pages);
   if (st != KK_OK) return st;
   if (n < 0 || (n > 0 && !out)) return KK_ERR_INVALID;
-  if (!aligned(want, 4) || !aligned(out, 4)) return KK_ERR_UNSUPPORTED;
+  if (!aligned(want, 4) || !aligned(out, 4) || n > kMaxInts) return KK_ERR_UNSUPPORTED;
+  if (collide({{out, n}, {refs_out, num_pages}}, {{want, n}}) ||
+      (refs_in != refs_out && share({out, n}, {refs_in, num_pages})))
+    return KK_ERR_INVALID;
   if (n == 0 && refs_in == refs_out) return KK_OK;
   int* err = kk::device_error_word();
   if (!err) return KK_ERR_CUDA;
@@ -230,6 +254,7 @@ kk_status kk_pages_free(const kk_block_table* bt, const int32_t* refs_in, int32_
   kk::Table t;
   kk_status st = kk::check_block_table(bt, &t);
   if (st != KK_OK || (st = check_refs(refs_in, refs_out, num_pages)) != KK_OK) return st;
+  if (collide({{refs_out, num_pages}}, {{t.offsets, t.R + 1ll}, {t.pages, t.max_blocks > 0 ? 1 : 0}})) return KK_ERR_INVALID;
   if (t.R == 0 && refs_in == refs_out) return KK_OK;
   int* err = kk::device_error_word();
   if (!err) return KK_ERR_CUDA;
@@ -258,9 +283,10 @@ kk_status kk_pages_fork(const kk_block_table* bt, int32_t block_size, const int3
   if (most > 0x7FFFFFFFll) return KK_ERR_UNSUPPORTED;
   if (!aligned(parent, 4) || !aligned(child_pages, 4) || !aligned(child_offsets, 4) || !aligned(child_lens, 4))
     return KK_ERR_UNSUPPORTED;
-  // children are laid out while their parents are read
-  if (child_offsets == a.bt.offsets || (child_pages && child_pages == a.bt.pages) ||
-      (child_lens && child_lens == a.bt.seq_lens))
+  // children are laid out, and counts moved, while their parents are read (how long bt's pages are is not known here)
+  if (collide({{child_pages, most}, {child_offsets, F + 1ll}, {child_lens, F}, {refs_out, num_pages}},
+              {{parent, F}, {a.bt.offsets, a.bt.R + 1ll}, {a.bt.seq_lens, a.bt.R}, {a.bt.pages, a.bt.max_blocks > 0 ? 1 : 0}}) ||
+      (refs_in != refs_out && collide({{child_pages, most}, {child_offsets, F + 1ll}, {child_lens, F}}, {{refs_in, num_pages}})))
     return KK_ERR_INVALID;
   if (!workspace || workspace_bytes < kk_pages_fork_workspace_bytes(a.bt.R, F)) return KK_ERR_INVALID;
   if (!aligned(workspace, 256)) return KK_ERR_UNSUPPORTED;
@@ -301,8 +327,11 @@ kk_status kk_pages_compact(const int32_t* refs_in, int32_t* refs_out, int32_t nu
   if (n < 0 || (n > 0 && (!pages_in || !pages_out)) || !remap || !used) return KK_ERR_INVALID;
   if (!aligned(pages_in, 4) || !aligned(pages_out, 4) || !aligned(remap, 4) || !aligned(used, 4))
     return KK_ERR_UNSUPPORTED;
-  const intptr_t apart = reinterpret_cast<intptr_t>(pages_in) - reinterpret_cast<intptr_t>(pages_out);
-  if (apart != 0 && std::llabs(apart) < 4ll * n) return KK_ERR_INVALID;  // the same, or apart
+  if ((pages_in != pages_out && share({pages_in, n}, {pages_out, n})) ||  // the same, or apart
+      collide({{pages_out, n}, {remap, num_pages}, {used, 1}, {refs_out, num_pages}}, {{nullptr, 0}}) ||
+      (refs_in != refs_out && collide({{pages_out, n}, {remap, num_pages}, {used, 1}}, {{refs_in, num_pages}})) ||
+      (pages_in != pages_out && collide({{remap, num_pages}, {used, 1}, {refs_out, num_pages}}, {{pages_in, n}})))
+    return KK_ERR_INVALID;
   if (!workspace || workspace_bytes < kk_pages_compact_workspace_bytes(num_pages)) return KK_ERR_INVALID;
   if (!aligned(workspace, 256)) return KK_ERR_UNSUPPORTED;
   a.num_pages = num_pages;

@@ -285,3 +285,34 @@ def test_a_wait_that_runs_out(cuda):
         kk.kk_debug_skip_tile_copy(-1)
     got = call()
     assert got[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("D,nodes", [(64, 1), (128, 5), (128, 30)])
+def test_offsets_past_32_bits(cuda, D, nodes):
+    """Pages more than 2^32 bytes apart, in Keys and Values and (written) in new tokens' places."""
+    from kv_cache_block_gb300 import kk
+
+    pc = Paged8([30, 17], H=2, D=D, bs=16, L=1, seed=17)
+    pc.to_gpu()
+    sP = (1 << 30) + 4096  # 4 pages apart: past 2^32
+    far = []
+    for x in (pc.gk, pc.gv):
+        big = torch.zeros(sP * (pc.P - 1) + 2 * 16 * D, dtype=torch.uint8, device="cuda")
+        y = big.as_strided(x.shape, (0, sP, 16 * D, D, 1))
+        y.copy_(x)
+        far.append(y)
+    assert (pc.P - 1) * sP > 1 << 32
+    desc = lambda x: kk.kcache_desc(x, kk.KK_E4M3, 1, 2, D, 16, pc.P, (0, *x.stride()[1:4]))  # noqa: E731
+    q = torch.randn((2 * nodes, 6, D), device="cuda").bfloat16()
+    res = []
+    for k, v in ((pc.gk, pc.gv), far):
+        out, lse = torch.zeros_like(q), torch.zeros((2 * nodes, 6), device="cuda")
+        kd, vd = desc(k), desc(v)
+        ws = torch.empty(kk.kk_tree_attn_kv8_workspace_bytes(kd, pc.bt, nodes, 6), dtype=torch.uint8, device="cuda")
+        kk.kk_tree_attn_kv8(kd, pc.gks, vd, pc.gvs, pc.bt, 0, kk.Tree(nodes), q, 0.1, out, lse, workspace=ws)
+        new = torch.randn((2, 2, D), device="cuda", generator=torch.Generator("cuda").manual_seed(1)).bfloat16()
+        ks, vs = pc.gks.clone(), pc.gvs.clone()
+        kk.kk_kv8_write(kd, ks, vd, vs, pc.bt, 0, new, new, 1)
+        res.append((out, lse, k.clone(), v.clone(), ks, vs))
+    assert kk.kk_device_error() == 0
+    assert all(torch.equal(torch.nan_to_num(a), torch.nan_to_num(b)) for a, b in zip(*res))

@@ -242,3 +242,43 @@ def test_on_another_stream_and_in_a_graph(cuda):
     torch.cuda.synchronize()
     assert cp.tolist()[:5] == [3, 0, 5, 3, 1] and out.tolist() == [-1, 6, -1]
     assert kk.kk_device_error() == 0
+
+
+def test_a_large_pool_in_a_graph(cuda):
+    """The planning cluster of several CTAs, captured: fork, compaction of the children's pages, and again."""
+    from kv_cache_block_gb300 import kk
+
+    gen = np.random.default_rng(3)
+    P = 40000
+    tables, lens, refs = _tables(40, P, gen, 16, longest=300, shared=5)
+    off, pages = csr(tables)
+    nb = max(len(t) for t in tables)
+    parent = gen.integers(0, 40, 64).tolist()
+    bt, r = kk.BlockTable(i32(pages), i32(off), i32(lens), nb), i32(refs)
+    pool = Pool(refs)
+    kids, copies = pool.fork(tables, lens, 16, parent, False)
+    vb = torch.randn((P, 8), device="cuda")
+    first = vb.clone()
+    mid, out, remap, used = torch.empty_like(r), torch.empty_like(r), torch.empty_like(r), i32([0])
+    cp, co, cl = (torch.full((n,), -1, dtype=torch.int32, device="cuda") for n in (64 * nb, 65, 64))
+    moved, arrays, gp = torch.empty_like(cp), kk.PageArrays([(vb, 0)]), i32(parent)
+    ws = _ws(max(kk.kk_pages_fork_workspace_bytes(40, 64), kk.kk_pages_compact_workspace_bytes(P)))
+
+    def step():
+        kk.kk_pages_fork(bt, 16, gp, r, mid, cp, co, cl, False, arrays, ws)
+        kk.kk_pages_compact(mid, out, cp, moved, remap, used, arrays, ws)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    want = _apply([(first, 0)], copies)[0]
+    place, moves, n = pool.compact()
+    want = _apply([(want, 0)], moves)[0]
+    for _ in range(2):
+        vb.copy_(first)
+        g.replay()
+        torch.cuda.synchronize()
+        assert kk.kk_device_error() == 0
+        assert out.tolist() == pool.refs and remap.tolist() == place and used.item() == n
+        flat = [place[p] for t, _ in kids for p in t]
+        assert moved.tolist() == flat + [-1] * (64 * nb - len(flat)) and torch.equal(vb, want)

@@ -111,39 +111,47 @@ def test_pages_host_errors(kk):
     B, lib = ctypes.byref, kk._lib
     INV, UNS, OK = kk.KK_ERR_INVALID, kk.KK_ERR_UNSUPPORTED, kk.KK_OK
     t = _table(kk)
-    al = lambda ri=4096, ro=8192, P=8, want=None, n=1, out=4096: lib.kk_pages_alloc(ri, ro, P, want, n, out, None)  # noqa: E731
+    K = 1 << 20  # apart from one another
+    al = lambda ri=K, ro=2 * K, P=8, want=None, n=1, out=3 * K: lib.kk_pages_alloc(ri, ro, P, want, n, out, None)  # noqa: E731
     assert al(ri=None) == INV and al(ro=None) == INV and al(P=0) == INV and al(n=-1) == INV and al(out=None) == INV
-    assert al(ro=4100) == INV  # overlapping, not the same
-    assert al(ri=4098) == UNS and al(want=4097) == UNS and al(n=0, ro=4096) == OK
-    fr = lambda bt=t, ri=4096, ro=8192, P=8: lib.kk_pages_free(None if bt is None else B(bt), ri, ro, P, None)  # noqa: E731
-    assert fr(bt=None) == INV and fr(ri=None) == INV and fr(P=0) == INV and fr(ro=8194) == UNS
-    assert fr(bt=_table(kk, R=0), ro=4096) == OK
+    assert al(ro=K + 4) == INV  # overlapping, not the same
+    assert al(want=3 * K) == INV and al(out=K) == INV and al(out=2 * K + 28) == INV and al(want=2 * K) == INV
+    assert al(ri=K + 2) == UNS and al(want=4 * K + 1) == UNS and al(P=(1 << 30) + 1) == UNS and al(n=(1 << 30) + 1) == UNS
+    assert al(n=0, ro=K) == OK
+    fr = lambda bt=t, ri=K, ro=2 * K, P=8: lib.kk_pages_free(None if bt is None else B(bt), ri, ro, P, None)  # noqa: E731
+    assert fr(bt=None) == INV and fr(ri=None) == INV and fr(P=0) == INV and fr(ro=2 * K + 2) == UNS
+    assert fr(ro=t.offsets) == INV and fr(bt=_table(kk, R=0), ro=K) == OK
 
     A = kk.kk_page_array
     size = lib.kk_pages_fork_workspace_bytes(t.num_requests, 3)
     assert size > 0 and lib.kk_pages_fork_workspace_bytes(-1, 3) == 0 and lib.kk_pages_compact_workspace_bytes(0) == 0
     cap = 3 * t.max_blocks
 
-    def fork(bt=t, bs=16, parent=4096, F=3, ri=4096, ro=8192, P=8, cp=4096 * 5, cap=cap, co=4096 * 6, cl=4096 * 7, arr=None,
-             n=0, ws=4096, wn=size):
+    def fork(bt=t, bs=16, parent=8 * K, F=3, ri=K, ro=2 * K, P=8, cp=3 * K, cap=cap, co=4 * K, cl=5 * K, arr=None, n=0,
+             ws=6 * K, wn=size):
         return lib.kk_pages_fork(None if bt is None else B(bt), bs, parent, F, 1, ri, ro, P, cp, cap, co, cl, arr, n, ws, wn, None)
 
     assert fork(bt=None) == INV and fork(bs=0) == INV and fork(parent=None) == INV and fork(F=-1) == INV and fork(cp=None) == INV
     assert fork(cap=cap - 1) == INV and fork(co=None) == INV and fork(cl=None) == INV and fork(ws=None) == INV
-    assert fork(wn=size - 1) == INV and fork(ws=4096 + 16) == UNS and fork(cp=4097) == UNS and fork(n=9) == INV and fork(n=1) == INV
+    assert fork(wn=size - 1) == INV and fork(ws=6 * K + 16) == UNS and fork(cp=3 * K + 1) == UNS and fork(n=9) == INV and fork(n=1) == INV
     for bad, st in (((None, 0, 64, 64, 1), INV), ((4096, 0, 64, 0, 1), INV), ((4096, 0, 60, 64, 1), INV), ((4096, 0, 64, 64, 0), INV),
-                    ((4096, -64, 64, 64, 1), INV), ((4098, 0, 64, 64, 1), UNS), ((4096, 0, 64, 62, 1), UNS), ((4096, 6, 64, 64, 1), UNS)):
+                    ((4096, -64, 64, 64, 1), INV), ((4098, 0, 64, 64, 1), UNS), ((4096, 0, 64, 62, 1), UNS), ((4096, 6, 64, 64, 1), UNS),
+                    ((4096, 0, 1 << 41, 1 << 40, 1), UNS)):
         assert fork(arr=(A * 1)(A(*bad)), n=1) == st, bad
-    assert fork(cp=t.pages) == INV and fork(co=t.offsets) == INV  # over the parents' own tables
+    assert fork(cp=t.pages) == INV and fork(co=t.offsets) == INV and fork(cl=t.seq_lens) == INV  # over the parents' own tables
+    assert fork(cl=8 * K) == INV and fork(cl=8 * K + 8) == INV and fork(co=5 * K + 4) == INV and fork(cp=2 * K) == INV
+    assert fork(co=K) == INV and fork(ro=8 * K) == INV
 
     size = lib.kk_pages_compact_workspace_bytes(8)
 
-    def compact(ri=4096, ro=8192, P=8, pi=4096, po=8192, n=4, remap=4096, used=4096, ws=4096, wn=size):
+    def compact(ri=K, ro=2 * K, P=8, pi=3 * K, po=4 * K, n=4, remap=5 * K, used=6 * K, ws=7 * K, wn=size):
         return lib.kk_pages_compact(ri, ro, P, pi, po, n, remap, used, None, 0, ws, wn, None)
 
     assert compact(ri=None) == INV and compact(P=0) == INV and compact(pi=None) == INV and compact(n=-1) == INV
-    assert compact(remap=None) == INV and compact(used=None) == INV and compact(po=4100) == INV and compact(used=4097) == UNS
-    assert compact(ws=None) == INV and compact(wn=size - 1) == INV and compact(ws=4096 + 64) == UNS
+    assert compact(remap=None) == INV and compact(used=None) == INV and compact(po=3 * K + 4) == INV and compact(used=6 * K + 1) == UNS
+    assert compact(ws=None) == INV and compact(wn=size - 1) == INV and compact(ws=7 * K + 64) == UNS
+    assert compact(remap=K) == INV and compact(remap=2 * K) == INV and compact(used=5 * K + 4) == INV and compact(po=2 * K) == INV
+    assert compact(remap=3 * K) == INV and compact(ro=3 * K) == INV and compact(po=K) == INV
 
 
 def test_binding_checks(kk):
