@@ -302,14 +302,15 @@ class Tree:
         n = q.shape[0]
         if self.node_offsets is not None and self.node_offsets.numel() != bt.num_requests + 1:
             raise ValueError(f"node_offsets must have {bt.num_requests + 1} elements")
-        for t, name in ((self.mask, "mask"), (self.k, "k"), (self.v, "v")):
-            if t is not None and t.shape[0] < n:
-                raise ValueError(f"{name} has fewer rows than q")
-        for t, name in ((self.k, "k"), (self.v, "v")):
-            if t is not None:
-                _check_elems(kc, t, name)
-                if t.shape[1] != kc.num_kv_heads:
-                    raise ValueError(f"{name} has {t.shape[1]} heads, the cache {kc.num_kv_heads}")
+        if self.mask is not None or self.k is not None:
+            for t, name in ((self.mask, "mask"), (self.k, "k"), (self.v, "v")):
+                if t is not None and t.shape[0] < n:
+                    raise ValueError(f"{name} has fewer rows than q")
+            for t, name in ((self.k, "k"), (self.v, "v")):
+                if t is not None:
+                    _check_elems(kc, t, name)
+                    if t.shape[1] != kc.num_kv_heads:
+                        raise ValueError(f"{name} has {t.shape[1]} heads, the cache {kc.num_kv_heads}")
         c = kk_tree.from_buffer_copy(self.c)
         c.total_nodes = n
         return ctypes.byref(c)
@@ -756,22 +757,24 @@ def kk_tree_attn_kv8_workspace_bytes(kc, bt: BlockTable, max_nodes: int, num_q_h
 def kk_tree_attn_kv8(kc, k_scale, vc, v_scale, bt: BlockTable, layer: int, tree: Tree, q, scale: float, out, lse=None,
                      sel=None, workspace=None, stream=None):
     """kk_tree_attn over 8-bit caches (``q``, ``out`` and drafted nodes are bf16)."""
-    _check_elems(kc, q, "q")
-    _check_elems(kc, out, "out")
-    if out.shape != q.shape:
+    shape = q.shape
+    if q.dtype is not torch.bfloat16 or shape[-1] != kc.head_dim:
+        _check_elems(kc, q, "q")
+    if out.dtype is not torch.bfloat16:
+        _check_elems(kc, out, "out")
+    if out.shape != shape:
         raise ValueError("out must have q's shape")
-    if lse is not None and lse.numel() != q.shape[0] * q.shape[1]:
+    if lse is not None and lse.numel() != shape[0] * shape[1]:
         raise ValueError("lse must be [nodes][query heads]")
     if sel is not None and sel.pages.shape[0] != bt.num_requests:
         raise ValueError("the selection has another number of requests than the table")
     nodes = tree.bind(kc, q, bt)
     qp, qn, qh = _strided(q, "q")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    wp, wn = _ws(workspace)
     _check("kk_tree_attn_kv8", _lib.kk_tree_attn_kv8(
         ctypes.byref(kc), _scale_ptr(kc, k_scale, "k_scale"), ctypes.byref(vc), _scale_ptr(vc, v_scale, "v_scale"),
-        ctypes.byref(bt.c), layer, None if sel is None else ctypes.byref(sel.c), nodes, qp, qn, qh, q.shape[1],
-        float(scale), _ptr(out, name="out"), _ptr(lse, torch.float32, "lse"), _ptr(workspace, name="workspace"),
-        ws_bytes, _stream(stream)))
+        ctypes.byref(bt.c), layer, None if sel is None else ctypes.byref(sel.c), nodes, qp, qn, qh, shape[1], scale,
+        _ptr(out, None, "out"), _ptr(lse, torch.float32, "lse"), wp, wn, _stream(stream)))
 
 
 class PageArrays:
