@@ -11,6 +11,7 @@
 // a thread (a page of 128 tokens of 128 bf16 dims in a block); larger items
 // read them again, from L2.
 #include "kk_device.cuh"
+#include "kk_pdl.cuh"
 #include "kk_write8.cuh"
 
 namespace kk {
@@ -69,6 +70,8 @@ __global__ void __launch_bounds__(kThreads, 4) write8_kernel(const Write8Args a)
   constexpr int E = Vec16<T>::kElems, CH = D / E;  // elements of a vector, vectors of a row
   constexpr int NTH = W * 32, IPB = kThreads / NTH;  // threads of an item, items of a block
   __shared__ uint32_t s_max[kThreads / 32];
+  pdl_wait();
+  pdl_launch_dependents();
   const int tid = threadIdx.x % NTH, sub = threadIdx.x / NTH;
   const int r = blockIdx.z, H = a.kc.H;
   const int item = blockIdx.y * IPB + sub, items = a.layers * H * a.sides;
@@ -195,9 +198,7 @@ cudaError_t go(const Write8Args& a, cudaStream_t s) {
   const bool small = std::min(a.max_new, a.kc.bs) * (D / Vec16<T>::kElems) <= kKeep * 32;
   const int ipb = small ? kThreads / 32 : 1;
   const dim3 grid((unsigned)pieces, (unsigned)((items + ipb - 1) / ipb), (unsigned)a.bt.R);
-  if (small) write8_kernel<T, D, 1><<<grid, kThreads, 0, s>>>(a);
-  else write8_kernel<T, D, kThreads / 32><<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(small ? write8_kernel<T, D, 1> : write8_kernel<T, D, kThreads / 32>, grid, kThreads, 0, s, a);
 }
 template <typename T>
 cudaError_t go_t(const Write8Args& a, cudaStream_t s) {

@@ -359,6 +359,215 @@ __global__ void __launch_bounds__(kPlan) pages_compact_kernel(const CompactArgs 
   }
 }
 
+// ---- small pools: one CTA, counts and tables' sizes in shared memory -----------------------------------------------
+// At most kFastPages pages and kFastRows requests and children: what the phases above exchange through L2 stays in the
+// CTA, so that a call waits for memory two or three times (a fork of 32 samples of 61 blocks 14.3 -> 8.2 us, a step of 16 beams
+// 12.8 -> 8.2, a page for each of 16 requests 6.2 -> 4.1, compaction's plan of 509 pages 10.3 -> 4.6; an empty launch takes 4.1).
+constexpr int kFast = 512, kFastPer = 8, kFastPages = kFast * kFastPer, kFastRows = 512;
+
+// Exclusive sums of two numbers over the CTA's kFast threads, and their totals. `sh`: 2 x 17 ints.
+__device__ __forceinline__ int2 fast_scan(int2 x, int (*sh)[17], int2* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int2 v = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(kFull, v.x, o), b = __shfl_up_sync(kFull, v.y, o);
+    if (lane >= o) v.x += a, v.y += b;
+  }
+  __syncthreads();
+  if (lane == 31) sh[0][w] = v.x, sh[1][w] = v.y;
+  __syncthreads();
+  int2 before = make_int2(0, 0);
+  *total = before;
+#pragma unroll
+  for (int i = 0; i < kFast / 32; ++i) {
+    const int a = sh[0][i], b = sh[1][i];
+    if (i < w) before.x += a, before.y += b;
+    total->x += a;
+    total->y += b;
+  }
+  return make_int2(before.x + v.x - x.x, before.y + v.y - x.y);
+}
+// The thread's kFastPer pages from tid * kFastPer on: its bits of those that are free (past the pool: none).
+template <typename F>
+__device__ __forceinline__ int own_pages(int pages, F is) {
+  int m = 0;
+#pragma unroll
+  for (int e = 0; e < kFastPer; ++e) {
+    const int page = threadIdx.x * kFastPer + e;
+    if (page < pages && is(page)) m |= 1 << e;
+  }
+  return m;
+}
+
+__global__ void __launch_bounds__(kFast) pages_alloc_fast_kernel(const int* refs_in, int* refs_out, int pages,
+                                                                 const int* want, int n, int* out, int* err) {
+  __shared__ int sh[2][17], s_page[kFastRows];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x;
+  int count[kFastPer];
+#pragma unroll
+  for (int e = 0; e < kFastPer; ++e) {
+    const int page = tid * kFastPer + e;
+    count[e] = page < pages ? refs_in[page] : 1;
+  }
+  const bool takes = tid < n && (!want || want[tid] != 0);
+  int free = 0;
+#pragma unroll
+  for (int e = 0; e < kFastPer; ++e) free |= (count[e] == 0) << e;
+  int2 total;
+  const int2 at = fast_scan(make_int2(__popc(free), takes), sh, &total);
+  int k = at.x;
+#pragma unroll
+  for (int e = 0; e < kFastPer; ++e) {
+    const int page = tid * kFastPer + e;
+    const bool take = (free >> e & 1) && k < total.y;
+    if (take) s_page[k] = page;
+    k += free >> e & 1;
+    if (page < pages && (take || refs_in != refs_out)) refs_out[page] = take ? 1 : count[e];
+  }
+  __syncthreads();
+  if (tid < n) out[tid] = takes && at.y < total.x ? s_page[at.y] : -1;
+  if (tid == 0 && total.y > total.x) flag_error(err, kErrNoPages);
+}
+
+__global__ void __launch_bounds__(kFast) pages_fork_fast_kernel(const ForkArgs a) {
+  __shared__ int sh[2][17];
+  __shared__ int s_refs[kFastPages];
+  __shared__ Parent s_par[kFastRows];
+  __shared__ int s_kids[kFastRows], s_first[kFastRows];
+  __shared__ int s_of[kFastRows], s_to[kFastRows + 1], s_at[kFastRows];  // a child's parent and first entry; a copy's entry
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, wid = tid >> 5;
+  for (int p = tid; p < a.num_pages; p += kFast) s_refs[p] = a.refs_in[p];
+  if (tid < a.bt.R) {
+    s_par[tid] = parent_of(a, tid);
+    s_kids[tid] = 0;
+    s_first[tid] = INT_MAX;
+  }
+  const int r = tid < a.F ? a.parent[tid] : -1;
+  __syncthreads();
+  const bool ok = tid < a.F && r >= 0 && r < a.bt.R && s_par[r].n >= 0;
+  if (ok) {
+    atomicAdd(s_kids + r, 1);
+    atomicMin(s_first + r, tid);
+  } else if (tid < a.F) {
+    flag_error(a.err, kErrBadIndex);
+  }
+  __syncthreads();
+  const int n = ok ? s_par[r].n : 0;
+  const bool copy = ok && s_par[r].part && (a.keep || s_first[r] != tid);
+  int2 total;
+  const int2 at = fast_scan(make_int2(n, copy), sh, &total);
+  if (tid < a.F) {
+    s_of[tid] = n ? r : -1;
+    s_to[tid] = at.x;
+    a.child_offsets[tid] = at.x;
+    a.child_lens[tid] = ok ? s_par[r].T : 0;
+    if (copy) {
+      s_at[at.y] = at.x + n - 1;
+      a.pairs[at.y].x = a.bt.pages[s_par[r].off + n - 1];
+    }
+  }
+  if (tid == 0) s_to[a.F] = a.child_offsets[a.F] = total.x;
+  __syncthreads();
+  share_warps(wid, kFast / 32, a.bt.R, [&](int q, int j0, int step) {
+    const Parent x = s_par[q];
+    const int kids = s_kids[q];
+    for (int j = j0; j < x.n; j += step) {
+      const int page = a.bt.pages[x.off + j];
+      const int more = j == x.n - 1 && x.part ? (a.keep ? 0 : (kids ? 0 : -1)) : (a.keep ? kids : kids - 1);
+      if (page < 0 || page >= a.num_pages) flag_error(a.err, kErrBadIndex);
+      else if (more && atomicAdd(s_refs + page, more) + more < 0) flag_error(a.err, kErrBadIndex);
+    }
+  });
+  share_warps(wid, kFast / 32, a.F, [&](int i, int j0, int step) {
+    const int q = s_of[i];
+    if (q < 0) return;
+    const Parent x = s_par[q];
+    const int own = x.part && (a.keep || s_first[q] != i);  // the last entry is the copy's
+    for (int j = j0; j < x.n - own; j += step) a.child_pages[s_to[i] + j] = a.bt.pages[x.off + j];
+  });
+  __syncthreads();
+  const int free = own_pages(a.num_pages, [&](int page) { return s_refs[page] == 0; });
+  const int need = total.y;
+  int2 found;
+  int k = fast_scan(make_int2(__popc(free), 0), sh, &found).x;
+#pragma unroll
+  for (int e = 0; e < kFastPer; ++e)
+    if (free >> e & 1) {
+      if (k < need) {
+        const int page = tid * kFastPer + e;
+        s_refs[page] = 1;
+        a.pairs[k].y = page;
+        a.child_pages[s_at[k]] = page;
+      }
+      ++k;
+    }
+  for (k = found.x + tid; k < need; k += kFast) a.child_pages[s_at[k]] = -1;
+  __syncthreads();
+  for (int p = tid; p < a.num_pages; p += kFast) a.refs_out[p] = s_refs[p];
+  if (tid == 0) {
+    *a.n_pairs = min(found.x, need);
+    if (found.x < need) flag_error(a.err, kErrNoPages);
+  }
+}
+
+__global__ void __launch_bounds__(kFast) pages_compact_fast_kernel(const CompactArgs a) {
+  __shared__ int sh[2][17], s_stay;
+  __shared__ int s_refs[kFastPages], s_map[kFastPages];
+  __shared__ unsigned short s_from[kFastPages / 2], s_to[kFastPages / 2];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x;
+  for (int p = tid; p < a.num_pages; p += kFast) s_refs[p] = a.refs_in[p];
+  __syncthreads();
+  const int on = own_pages(a.num_pages, [&](int page) { return s_refs[page] != 0; });
+  int2 total;
+  const int first = fast_scan(make_int2(__popc(on), 0), sh, &total).x;
+  const int used = total.x;
+  if (used / kFastPer == tid) s_stay = first + __popc(on & ((1 << used % kFastPer) - 1));  // used pages in front of page `used`
+  if (tid == 0 && used == kFastPages) s_stay = used;
+  __syncthreads();
+  const int stay = s_stay, moves = used - stay;
+  int k = first;
+#pragma unroll
+  for (int e = 0; e < kFastPer; ++e) {
+    const int page = tid * kFastPer + e;
+    if (page >= a.num_pages) break;
+    const bool in = on >> e & 1;
+    s_map[page] = in ? page : -1;
+    if (in && page >= used) s_from[k - stay] = (unsigned short)page;
+    if (!in && page < used) s_to[page - k] = (unsigned short)page;
+    k += in;
+  }
+  __syncthreads();
+  for (int i = tid; i < moves; i += kFast) {
+    const int from = s_from[i], to = s_to[i];
+    a.pairs[i] = make_int2(from, to);
+    s_map[from] = to;
+    s_refs[to] = s_refs[from];
+    s_refs[from] = 0;
+  }
+  if (tid == 0) {
+    *a.n_pairs = moves;
+    *a.used = used;
+  }
+  __syncthreads();
+  for (int p = tid; p < a.num_pages; p += kFast) {
+    a.remap[p] = s_map[p];
+    a.refs_out[p] = s_refs[p];
+  }
+  for (long long i = tid; i < a.n; i += kFast) {
+    const int page = a.pages_in[i];
+    const int to = page >= 0 && page < a.num_pages ? s_map[page] : -1;
+    if (to < 0 && page != -1) flag_error(a.err, kErrBadIndex);
+    a.pages_out[i] = to;
+  }
+}
+
 // One page of an array is a run of vectors, slice after slice, cut into chunks of kUnroll a thread (a chunk spans
 // slices where they are small); CTAs take (pair, chunk) in turn.
 constexpr int kCopy = 256, kUnroll = 8, kChunk = kCopy * kUnroll;
@@ -417,14 +626,12 @@ __global__ void __launch_bounds__(kCopy, 3) pages_copy_kernel(const __grid_const
   }
 }
 
-// The planning cluster: as many CTAs as there is work for.
+// A planning kernel, which may start while the launch before it ends.
 template <typename... P, typename... A>
-cudaError_t launch_plan(void (*k)(P...), long long work, cudaStream_t s, A... args) {
-  int ctas = 1;
-  while (ctas < kPlanCtas && work > (long long)ctas * kStep) ctas *= 2;
+cudaError_t launch_cluster(void (*k)(P...), int ctas, int threads, cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kPlan);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = s;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -437,6 +644,13 @@ cudaError_t launch_plan(void (*k)(P...), long long work, cudaStream_t s, A... ar
   return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
+// The planning cluster: as many CTAs as there is work for.
+template <typename... P, typename... A>
+cudaError_t launch_plan(void (*k)(P...), long long work, cudaStream_t s, A... args) {
+  int ctas = 1;
+  while (ctas < kPlanCtas && work > (long long)ctas * kStep) ctas *= 2;
+  return launch_cluster(k, ctas, kPlan, s, args...);
+}
 cudaError_t launch_copies(const PageArrays& pa, const int2* pairs, const int* n_pairs, long long most, int num_pages,
                           cudaStream_t s) {
   if (pa.n == 0 || most == 0) return cudaSuccess;
@@ -474,6 +688,8 @@ bool plan_page_arrays(PageArrays* pa) {
 
 cudaError_t launch_pages_alloc(const int* refs_in, int* refs_out, int num_pages, const int* want, int n, int* out,
                                int* err, cudaStream_t s) {
+  if (num_pages <= kFastPages && n <= kFastRows)
+    return launch_cluster(pages_alloc_fast_kernel, 1, kFast, s, refs_in, refs_out, num_pages, want, n, out, err);
   return launch_plan(pages_alloc_kernel, num_pages, s, refs_in, refs_out, num_pages, want, n, out, err);
 }
 
@@ -485,12 +701,15 @@ cudaError_t launch_pages_free(const Table& bt, const int* refs_in, int* refs_out
 
 cudaError_t launch_pages_fork(const ForkArgs& f, const PageArrays& pa, cudaStream_t s) {
   const long long work = std::max<long long>(f.num_pages, 2ll * f.F * f.bt.max_blocks);
-  const cudaError_t e = launch_plan(pages_fork_kernel, work, s, f);
+  const bool fast = f.num_pages <= kFastPages && f.F <= kFastRows && f.bt.R <= kFastRows && work <= 4 * kStep;
+  const cudaError_t e = fast ? launch_cluster(pages_fork_fast_kernel, 1, kFast, s, f) : launch_plan(pages_fork_kernel, work, s, f);
   return e != cudaSuccess ? e : launch_copies(pa, f.pairs, f.n_pairs, f.F, f.num_pages, s);
 }
 
 cudaError_t launch_pages_compact(const CompactArgs& c, const PageArrays& pa, cudaStream_t s) {
-  const cudaError_t e = launch_plan(pages_compact_kernel, std::max<long long>(c.num_pages, c.n / 2), s, c);
+  const bool fast = c.num_pages <= kFastPages && c.n <= 4 * kStep;
+  const cudaError_t e = fast ? launch_cluster(pages_compact_fast_kernel, 1, kFast, s, c)
+                             : launch_plan(pages_compact_kernel, std::max<long long>(c.num_pages, c.n / 2), s, c);
   return e != cudaSuccess ? e : launch_copies(pa, c.pairs, c.n_pairs, c.num_pages / 2, c.num_pages, s);
 }
 

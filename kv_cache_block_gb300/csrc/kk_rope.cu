@@ -16,6 +16,7 @@
 // top 32 bits go to sincospi; a float32 product p * f would be off by whole
 // radians at the far positions of a long context, and float64 is slow here.
 #include "kk_device.cuh"
+#include "kk_pdl.cuh"
 #include "kk_rope.cuh"
 
 namespace kk {
@@ -58,6 +59,8 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a, int
   extern __shared__ float2 s_cs[];  // [nodes][E][pairs / E] (cosine, sine): the lanes of a row read neighbours
   __shared__ long long s_slot[kBatch][2];  // byte offset of the node's slot in K and V, -1: none
   __shared__ int s_pos[kBatch];
+  pdl_wait();
+  pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int node0 = blockIdx.x * batch, nodes = min(batch, a.nodes - node0);
   const int pairs = a.rd / 2;
@@ -221,9 +224,7 @@ cudaError_t go(const RopeArgs& a, cudaStream_t s) {
   const int split = std::max(1, std::min((a.Hq + rows - 1) / rows, sms / blocks));
   const int smem = batch * (a.rd / 2) * (int)sizeof(float2);
   const dim3 grid((unsigned)blocks, (unsigned)split);
-  if (a.half) rope_kernel<T, D, true><<<grid, kThreads, smem, s>>>(a, batch);
-  else rope_kernel<T, D, false><<<grid, kThreads, smem, s>>>(a, batch);
-  return cudaGetLastError();
+  return launch_pdl(a.half ? rope_kernel<T, D, true> : rope_kernel<T, D, false>, grid, kThreads, smem, s, a, batch);
 }
 template <typename T>
 cudaError_t go_t(const RopeArgs& a, cudaStream_t s) {

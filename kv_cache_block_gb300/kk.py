@@ -185,6 +185,8 @@ def status_str(status: int) -> str:
 def _ptr(t, dtype=None, name="tensor"):
     if t is None:
         return None
+    if type(t) is torch.Tensor and t.is_cuda and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if not t.is_cuda:

@@ -55,7 +55,8 @@ def _tables(R, P, gen, bs, longest=9, shared=0):
 @pytest.mark.parametrize("R,F,P,bs,shared,keep", [
     (1, 1, 40, 16, 0, True), (1, 5, 40, 16, 3, True), (4, 4, 90, 16, 2, False), (16, 16, 400, 128, 5, False),
     (3, 0, 50, 16, 1, False), (0, 0, 10, 16, 0, True), (7, 40, 300, 1, 0, False), (33, 70, 700, 5, 9, True),
-    (5, 9, 70000, 16, 2, False), (1500, 2600, 20000, 16, 1, False), (1500, 2600, 20000, 16, 0, True)])
+    (5, 9, 70000, 16, 2, False), (512, 512, 4096, 16, 1, False), (512, 513, 4096, 16, 1, True), (100, 60, 4096, 16, 30, True),
+    (1500, 2600, 20000, 16, 1, False), (1500, 2600, 20000, 16, 0, True)])
 @pytest.mark.parametrize("in_place", [True, False])
 def test_fork(cuda, R, F, P, bs, shared, keep, in_place):
     from kv_cache_block_gb300 import kk
@@ -121,7 +122,8 @@ def test_fork_with_bad_device_data(cuda):
     assert cp[:4].tolist() == [900, 900, 900, 4] and all(torch.equal(t, w) for (t, _), w in zip(arrays, want))
 
 
-@pytest.mark.parametrize("P,n,share", [(1, 1, 0.0), (10, 3, 0.5), (5000, 700, 0.9), (70000, 3000, 0.99), (40000, 2500, 0.0)])
+@pytest.mark.parametrize("P,n,share", [(1, 1, 0.0), (10, 3, 0.5), (10, 7, 0.9), (4096, 512, 0.8), (4097, 512, 0.8),
+                                       (4096, 513, 0.95), (5000, 700, 0.9), (70000, 3000, 0.99), (40000, 2500, 0.0)])
 @pytest.mark.parametrize("wants", [True, False])
 def test_alloc(cuda, P, n, share, wants):
     from kv_cache_block_gb300 import kk
@@ -170,7 +172,7 @@ def test_free_twice_is_reported(cuda):
     assert kk.kk_device_error() == kk.KK_ERR_BAD_INDEX and r.tolist() == [0, 0, 0, 1]
 
 
-@pytest.mark.parametrize("P,used", [(1, 1.0), (1, 0.0), (7, 0.5), (500, 0.3), (4096, 0.5), (5000, 0.9), (5000, 0.0), (5000, 1.0),
+@pytest.mark.parametrize("P,used", [(1, 1.0), (1, 0.0), (7, 0.5), (500, 0.3), (4095, 0.5), (4096, 0.5), (4096, 1.0), (4097, 0.5), (5000, 0.9), (5000, 0.0), (5000, 1.0),
                                     (70001, 0.4)])
 @pytest.mark.parametrize("in_place", [True, False])
 def test_compact(cuda, P, used, in_place):
