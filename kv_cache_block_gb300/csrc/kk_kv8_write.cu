@@ -10,6 +10,13 @@
 // tokens stay in registers between the two passes, up to 8 vectors of 16 bytes
 // a thread (a page of 128 tokens of 128 bf16 dims in a block); larger items
 // read them again, from L2.
+//
+// Measured: one token of 8 requests in 28 layers of 4 heads of 128 dims 6.2 us
+// (a launch and a chain of four loads); prompts of 22.5 K tokens, one layer (69 MB read
+// and written), 13.2 us, 5.2 TB/s, with the codes written to L2. Two and a half
+// rounds of blocks, each a chain of look-ups, loads and a block-wide maximum,
+// are what is left; magnitudes as packed integers and 64 registers, four blocks
+// an SM instead of two, took it there from 22.5.
 #include "kk_device.cuh"
 #include "kk_pdl.cuh"
 #include "kk_write8.cuh"

