@@ -677,7 +677,8 @@ kk_status kk_qk_norm_rope(int32_t dtype, int32_t num_nodes, int32_t num_q_heads,
 
 /*
  * The 8-bit cache: kk_kcache_desc with dtype KK_E4M3 (one byte an element; base
- * and strides multiples of 16 bytes, head_dim 32, 64, 128 or 256) holds codes,
+ * and strides multiples of 16 bytes, head_dim 32, 64, 128 or 256, block_size at
+ * most 65536) holds codes,
  * and a scale for each block of tokens and head holds what they stand for:
  *   K[l,p,h,t,d] = code[l,p,h,t,d] * k_scale[l][p][h]
  * (device float [num_layers][num_pages][num_kv_heads]), Values the same with
@@ -686,7 +687,7 @@ kk_status kk_qk_norm_rope(int32_t dtype, int32_t num_nodes, int32_t num_q_heads,
  *
  * kk_kv8_write - new tokens written into it. The nodes token_offsets[r] ..
  * token_offsets[r+1] (device int32 [R+1]; NULL: max_new nodes each, in order; at
- * most max_new a request, num_nodes in all) are the last tokens of request r, as
+ * most max_new a request, a bound far above which costs time, num_nodes in all) are the last tokens of request r, as
  * in kk_qk_norm_rope, with their Keys and Values at rows k and v of type dtype
  * (KK_BF16 or KK_F32), for every layer of [layer, layer + num_layers). In each
  * page they reach, the scale of a (layer, head) becomes
@@ -767,7 +768,8 @@ kk_status kk_pages_free(const kk_block_table* bt, const int32_t* refs_in, int32_
  * lose a count. Counts are right afterwards for the children's tables (and the
  * parents' when they stay). Free pages are taken as of after that. A parent out
  * of [0, R) gives a child without tokens (KK_ERR_BAD_INDEX); so does one whose
- * table disagrees with its length, whose counts stay. Where no
+ * table disagrees with its length, whose counts stay. A page out of range, or in
+ * a table with a count of 0, is reported (KK_ERR_BAD_INDEX). Where no
  * page is left the child's last entry is -1 (KK_ERR_NO_PAGES).
  * child tables may not overlap bt's. arrays: n_arrays (0..8) host structs, read during the call.
  * workspace: device, 256-byte aligned, no initial contents.

@@ -273,8 +273,9 @@ __global__ void __launch_bounds__(kPlan) pages_fork_kernel(const ForkArgs a) {
       const int more = j == x.n - 1 && x.part ? (a.keep ? 0 : (kids ? 0 : -1)) : (a.keep ? kids : kids - 1);
       if (page < 0 || page >= a.num_pages) {
         flag_error(a.err, kErrBadIndex);
-      } else if (more) {
-        if (atomicAdd(a.refs_out + page, more) + more < 0) flag_error(a.err, kErrBadIndex);
+      } else {  // this table's own count is still there, whatever the others' did
+        const int had = more ? atomicAdd(a.refs_out + page, more) : __ldcg(a.refs_out + page);
+        if (had <= 0) flag_error(a.err, kErrBadIndex);
       }
     }
   });
@@ -482,7 +483,7 @@ __global__ void __launch_bounds__(kFast) pages_fork_fast_kernel(const ForkArgs a
       const int page = a.bt.pages[x.off + j];
       const int more = j == x.n - 1 && x.part ? (a.keep ? 0 : (kids ? 0 : -1)) : (a.keep ? kids : kids - 1);
       if (page < 0 || page >= a.num_pages) flag_error(a.err, kErrBadIndex);
-      else if (more && atomicAdd(s_refs + page, more) + more < 0) flag_error(a.err, kErrBadIndex);
+      else if ((more ? atomicAdd(s_refs + page, more) : s_refs[page]) <= 0) flag_error(a.err, kErrBadIndex);
     }
   });
   share_warps(wid, kFast / 32, a.F, [&](int i, int j0, int step) {

@@ -37,7 +37,7 @@ kk_status check_cache8(const kk_kcache_desc* kc, kk::KCache* out) {
   if (kc->num_layers <= 0 || kc->num_kv_heads <= 0 || kc->head_dim <= 0 || kc->block_size <= 0 || kc->num_pages <= 0)
     return KK_ERR_INVALID;
   if ((long long)kc->num_layers * kc->num_kv_heads > kk::kMaxLH || !dim_ok(kc->head_dim)) return KK_ERR_UNSUPPORTED;
-  if (!aligned(kc->base, 16)) return KK_ERR_UNSUPPORTED;
+  if (!aligned(kc->base, 16) || kc->block_size > 65536) return KK_ERR_UNSUPPORTED;
   for (int64_t st : {kc->stride_layer, kc->stride_page, kc->stride_head, kc->stride_token})
     if (st < 0 || st % 16) return KK_ERR_UNSUPPORTED;
   *out = kk::KCache{kc->base,      kc->dtype,        kc->num_layers,   kc->num_kv_heads, kc->head_dim,    kc->block_size,

@@ -284,3 +284,19 @@ def test_a_large_pool_in_a_graph(cuda):
         assert out.tolist() == pool.refs and remap.tolist() == place and used.item() == n
         flat = [place[p] for t, _ in kids for p in t]
         assert moved.tolist() == flat + [-1] * (64 * nb - len(flat)) and torch.equal(vb, want)
+
+
+@pytest.mark.parametrize("P", [8, 9000])  # planned by one CTA, by a cluster
+@pytest.mark.parametrize("keep", [True, False])
+def test_fork_reports_pages_without_a_count(cuda, P, keep):
+    from kv_cache_block_gb300 import kk
+
+    for zero in (0, 1):  # a full block's page, the open one's
+        refs = torch.zeros(P, dtype=torch.int32)
+        refs[:2] = 1
+        refs[zero] = 0
+        r = refs.cuda()
+        cp, co, cl = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (2, 2, 1))
+        kk.kk_pages_fork(kk.BlockTable(i32([0, 1]), i32([0, 2]), i32([20]), 2), 16, i32([0]), r, r, cp, co, cl, keep, None,
+                         _ws(kk.kk_pages_fork_workspace_bytes(1, 1)))
+        assert kk.kk_device_error() == kk.KK_ERR_BAD_INDEX

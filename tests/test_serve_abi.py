@@ -82,6 +82,7 @@ def test_kv8_write_host_errors(kk):
     assert call(layer=-1) == INV and call(layer=1) == INV and call(layers=0) == INV and call(most=0) == INV and call(n=-1) == INV
     assert call(no=None, n=5) == INV and call(no=4097) == UNS and call(k=_rows(kk, base=4098)) == UNS
     assert call(v=_rows(kk, sl=-16)) == UNS and call(kc=_d8(kk, stride_token=8)) == UNS and call(kc=_d8(kk, head_dim=48)) == UNS
+    assert call(kc=_d8(kk, block_size=65537)) == UNS
     assert call(bt=_table(kk, R=0), n=0) == kk.KK_OK and call(n=0) == kk.KK_OK
 
 
