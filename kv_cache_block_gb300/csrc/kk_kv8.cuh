@@ -121,6 +121,7 @@ __device__ __forceinline__ Group find_group(const AttnArgs& a, int r, const Attn
     const long long first = (long long)logical * a.kc.bs;
     if (logical < 0 || first >= rq.T) {
       flag_error(a.err, kErrBadIndex);
+      x.page = 0;
       return x;
     }
     left = (int)min((long long)rq.T - first - c.o, 16ll);

@@ -258,6 +258,29 @@ def test_bad_device_data_is_reported(cuda):
     assert kk.kk_device_error() == 0
 
 
+@pytest.mark.parametrize("bs", [16, 12])
+@pytest.mark.parametrize("nodes", [1, 41])
+def test_bad_selections_are_reported_and_skipped(cuda, bs, nodes):
+    """Entries with a block or a page out of range count as no tokens; the others as ever."""
+    from kv_cache_block_gb300 import kk
+
+    pc = Paged8([100, 40], H=2, D=64, bs=bs, L=1, seed=18)
+    pc.to_gpu()
+    no, q, _, _ = _nodes([nodes, nodes], 4, 64, 2, 5)
+    K = max(5, min(Paged8.bound, 2000))
+    lg, pg = (torch.full((2, K), -1, dtype=torch.int32) for _ in range(2))
+    good = [[1, 3], [0]]
+    lg[0, :4], pg[0, :4] = torch.tensor([1, 3, 1 << 30, -7]), torch.tensor([int(pc.pages[1]), int(pc.pages[3]), 1 << 30, -5])
+    lg[1, :3], pg[1, :3] = torch.tensor([0, 1, 2]), torch.tensor([int(pc.pages[pc.off[1]]), 1 << 30, -(1 << 31)])
+    sel = kk.Selection(pg.cuda(), lg.cuda(), torch.tensor([4, 3], dtype=torch.int32).cuda())
+    out, lse = torch.zeros((2 * nodes, 4, 64), dtype=torch.bfloat16, device="cuda"), torch.zeros((2 * nodes, 4), device="cuda")
+    ws = torch.empty(kk.kk_tree_attn_kv8_workspace_bytes(pc.kd, pc.bt, nodes, 4), dtype=torch.uint8, device="cuda")
+    kk.kk_tree_attn_kv8(pc.kd, pc.gks, pc.vd, pc.gvs, pc.bt, 0, kk.Tree(nodes), q.contiguous().cuda(), 0.1, out, lse, sel=sel,
+                        workspace=ws)
+    assert kk.kk_device_error() == kk.KK_ERR_BAD_INDEX
+    _check(out, lse, attn8_ref(pc, 0, no, q, 0.1, 2, sel=good))
+
+
 def test_a_wait_that_runs_out(cuda):
     """A tile of Keys that never comes: the call reports it and returns, and the next one is sound."""
     from kv_cache_block_gb300 import kk
