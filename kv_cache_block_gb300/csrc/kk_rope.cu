@@ -21,6 +21,7 @@
 // nodes 62 (their look-ups and sines, a chain of latencies, came 3.4 times to an
 // SM), with sines as they are numbered, four lanes to a bank, 46.
 #include "kk_device.cuh"
+#include "kk_f32x2.cuh"
 #include "kk_pdl.cuh"
 #include "kk_rope.cuh"
 
@@ -61,7 +62,8 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a, int
   constexpr int E = Vec16<T>::kElems, LPR = D / (2 * E), RPW = 32 / LPR;  // lanes of a row, rows of a warp
   constexpr int ES = 16 / E;
   __shared__ unsigned long long s_turn[kMaxPairs];
-  extern __shared__ float2 s_cs[];  // [nodes][E][pairs / E] (cosine, sine): the lanes of a row read neighbours
+  // [nodes][E / 2][pairs / E]: the cosines and the sines of two pairs; the lanes of a row read neighbours
+  extern __shared__ float4 s_cs[];
   __shared__ long long s_slot[kBatch][2];  // byte offset of the node's slot in K and V, -1: none
   __shared__ int s_pos[kBatch];
   pdl_wait();
@@ -121,7 +123,9 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a, int
     const unsigned long long turn = (unsigned long long)(long long)s_pos[k] * s_turn[p];
     float sn, cs;
     sincospif((float)(int)(turn >> 32) * 0x1p-31f, &sn, &cs);
-    s_cs[k * pairs + p % E * (pairs / E) + p / E] = make_float2(cs * a.rope_scale, sn * a.rope_scale);
+    float* to = reinterpret_cast<float*>(s_cs + k * (pairs / 2) + p % E / 2 * (pairs / E) + p / E) + (p & 1);
+    to[0] = cs * a.rope_scale;
+    to[2] = sn * a.rope_scale;
   }
   __syncthreads();
   if (late && w == kWarps - 1 && lane < nodes) look_up(lane);
@@ -175,26 +179,39 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a, int
           float f[2 * E];
           Vec16<T>::unpack(u[i], f);
           Vec16<T>::unpack(v[i], f + E);
+          auto two = [&](int e) { return make_float2(f[e], f[e + 1]); };
           if (wt) {
-            float ss = 0.f;
+            float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < 2 * E; ++e) ss += f[e] * f[e];
+            for (int e = 0; e < 2 * E; e += 2) sq = fma2(two(e), two(e), sq);
+            float ss = sq.x + sq.y;
 #pragma unroll
             for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
             const float s = rsqrtf(ss * (1.f / D) + a.eps);
 #pragma unroll
-            for (int e = 0; e < 2 * E; ++e) f[e] = f[e] * s * g[e];
+            for (int e = 0; e < 2 * E; e += 2)
+              set2(f + e, mul2(mul2(two(e), make_float2(s, s)), make_float2(g[e], g[e + 1])));
           }
           if (rot) {
-            const float2* cs = s_cs + (k[i] < nodes ? k[i] : 0) * pairs + j;
+            const float4* cs = s_cs + (k[i] < nodes ? k[i] : 0) * (pairs / 2) + j;
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-              const float2 t = cs[e * turned];
-              float* y = HALF ? f + e : f + 2 * e;
-              float* z = HALF ? f + E + e : f + 2 * e + 1;
-              const float p = *y, q = *z;
-              *y = p * t.x - q * t.y;
-              *z = q * t.x + p * t.y;
+            for (int e = 0; e < E; e += 2) {
+              const float4 t = cs[e / 2 * turned];
+              const float2 c = make_float2(t.x, t.y), n = make_float2(t.z, t.w);
+              float2 y = two(HALF ? e : 2 * e), z = two(HALF ? E + e : 2 * e + 2);
+              if (!HALF) {  // as they lie: a pair each
+                const float x1 = y.y;
+                y.y = z.x;
+                z.x = x1;
+              }
+              const float2 p = sub2(mul2(y, c), mul2(z, n)), q = fma2(y, n, mul2(z, c));
+              if (HALF) {
+                set2(f + e, p);
+                set2(f + E + e, q);
+              } else {
+                set2(f + 2 * e, make_float2(p.x, q.x));
+                set2(f + 2 * e + 2, make_float2(p.y, q.y));
+              }
             }
           }
           u[i] = pack_vec<T>(f);
