@@ -5,7 +5,8 @@
 // node may see. One pass over the tokens with a running maximum and sum per
 // row; the work division is kk_attn.cuh's. The main kernels are in kk_attn_f32.cu
 // (float32 caches), kk_attn_mma.cu (bf16, few rows), kk_attn_tc.cu (bf16, many
-// rows) and kk_attn_kv8.cu (e4m3 with scales); this file chooses one and adds up the parts of the items that were cut.
+// rows) and kk_attn_kv8.cu (e4m3 with scales); this file chooses one and adds up
+// the parts of the items that were cut.
 #include <algorithm>
 
 #include "kk_attn.cuh"
@@ -312,13 +313,19 @@ cudaError_t combine_t(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
 // 18.8, 64 K x 3 26.9 / 25.8, 64 K x 5 32.5 / 26.9. One tile of 16 rows: 1 M tokens
 // 97.0 / 96.5 and 131 K 26.9 / 31.5 (D = 64: 57.4 / 65.8 and 20.7 / 28.9).
 constexpr long long kTcWork = 72 << 10;
-// The same over an 8-bit cache, where the loaders' conversions, which are the same for 1 row as for 256, bound the
-// tensor-memory kernel: from 80 rows on (8 requests of up to 32768 tokens, 4 KV heads, groups of 7, few rows / tensor
-// memory: 9 nodes 145 / 163 us, 16 nodes 211 / 170, 36 nodes 434 / 177, 64 nodes 744 / 447; up to 8192 tokens
-// 50 / 55, 67 / 64, 127 / 68, 211 / 132; up to 1024 tokens 25 / 27, 29 / 28, 47 / 37, 77 / 43; 64 dims and up to 32768 93 / 111,
-// 133 / 113 at 9 and 16 nodes), and not for a few thousand tokens, which it starts too slowly for.
+// The same over an 8-bit cache, where the loaders' conversions, which are the same
+// for 1 row as for 256, bound the tensor-memory kernel: from 80 rows on (8 requests
+// of up to 32768 tokens, 4 KV heads, groups of 7, few rows / tensor memory, us: 9
+// nodes 145 / 163, 16 nodes 211 / 170, 36 nodes 434 / 177, 64 nodes 744 / 447; up to
+// 8192 tokens 50 / 55, 67 / 64, 127 / 68, 211 / 132; up to 1024 tokens 25 / 27,
+// 29 / 28, 47 / 37, 77 / 43; 64 dims and up to 32768 93 / 111, 133 / 113 at 9 and 16
+// nodes), and where tokens x tiles, counted as above, pass 48 K, since it takes longer
+// to start (D = 128, tokens x tiles: 2 K x 15 22.6 / 23.1, 2 K x 27 28.8 / 24.6,
+// 4 K x 6 18.5 / 20.5, 4 K x 15 29.4 / 24.6, 8 K x 5 18.9 / 20.5, 8 K x 6 24.6 / 22.6;
+// D = 64: 18.5 / 17.3, 22.6 / 18.5, 14.4 / 17.5, 22.6 / 18.5, 16.4 / 18.5,
+// 18.5 / 18.5).
 constexpr int kTcRows8 = 80;
-constexpr long long kTcTokens8 = 16 << 10;
+constexpr long long kTcWork8 = 48 << 10;
 // From where the mma kernel's tiles have 32 rows (layouts that do not suit the
 // other kernel): 512 K tokens of 128 dims and 28, 63, 91 rows 90 / 153 / 215 us
 // against 100 / 176 / 252 with 16, but 64 K tokens 31 / 41 / 51 against 29 / 37 / 47;
@@ -328,10 +335,11 @@ constexpr long long kWideTokens = 256 << 10;
 
 AttnPlan plan(const KCache& kc, const KCache& vc, int max_nodes, int G, long long tokens) {
   const int rows = max_nodes * G;
+  const long long work = tokens * ((rows - 1) / 16);
   if (kc.dtype == 2)
-    return rows > kTcRows8 && tokens >= kTcTokens8 && attn_tc8_suits(kc) ? attn_tc_plan() : attn_kv8_plan(kc, rows);
+    return rows > kTcRows8 && work >= kTcWork8 && attn_tc8_suits(kc) ? attn_tc_plan() : attn_kv8_plan(kc, rows);
   if (kc.dtype != 1) return attn_f32_plan(kc, rows);
-  if (tokens * ((rows - 1) / 16) >= kTcWork && attn_tc_suits(kc) && attn_tc_suits(vc)) return attn_tc_plan();
+  if (work >= kTcWork && attn_tc_suits(kc) && attn_tc_suits(vc)) return attn_tc_plan();
   return attn_mma_plan(kc, rows > 16 && tokens >= kWideTokens);
 }
 

@@ -113,8 +113,10 @@ __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kern
     // pieces c of rows sub, sub + RI, ...; what does not change over the tiles is worked out here.
     constexpr int CH = D / 16, RI = 32 / CH, NI = 16 / RI > 0 ? 16 / RI : 1;
     const int c = lane % CH, sub = lane / CH;
-    const char* k_lane = static_cast<const char*>(a.kc.base) + a.layer * a.kc.sL + h * a.kc.sH + c * 16 + (PG ? sub * a.kc.sT : 0);
-    const char* v_lane = static_cast<const char*>(a.vc.base) + a.layer * a.vc.sL + h * a.vc.sH + c * 16 + (PG ? sub * a.vc.sT : 0);
+    const char* k_lane =
+        static_cast<const char*>(a.kc.base) + a.layer * a.kc.sL + h * a.kc.sH + c * 16 + (PG ? sub * a.kc.sT : 0);
+    const char* v_lane =
+        static_cast<const char*>(a.vc.base) + a.layer * a.vc.sL + h * a.vc.sH + c * 16 + (PG ? sub * a.vc.sT : 0);
     const long long s_at = (long long)a.layer * a.kc.num_pages * a.kc.H + h;
     constexpr int NG = PG ? U : 1;  // groups a lane knows: all of the share, or (its own token) one
     auto load = [&](const Group (&x)[NG], int st, bool on) {
@@ -147,7 +149,8 @@ __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kern
               }
             }
             if (lane < 2)
-              cp_async4(sst + (lane * kTok + i) * 4, (lane ? a.v_scale : a.k_scale) + s_at + (long long)x[i].page * a.kc.H, n > 0);
+              cp_async4(sst + (lane * kTok + i) * 4,
+                        (lane ? a.v_scale : a.k_scale) + s_at + (long long)x[i].page * a.kc.H, n > 0);
           }
         }
       } else {
@@ -246,7 +249,8 @@ __global__ void __launch_bounds__(kThreads, (kv8_blocks<D, NT>())) attn_kv8_kern
           for (int c = 0; c < KW; ++c)
 #pragma unroll
             for (int k = 0; k < U; ++k) {
-              const uint32_t a0 = widen(x[k][c], 0), a1 = widen(y[k][c], 0), a2 = widen(x[k][c], 1), a3 = widen(y[k][c], 1);
+              const uint32_t a0 = widen(x[k][c], 0), a1 = widen(y[k][c], 0);
+              const uint32_t a2 = widen(x[k][c], 1), a3 = widen(y[k][c], 1);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 uint2 b;

@@ -1,10 +1,12 @@
-// What the kernels of attention over an 8-bit cache share: codes widened to matrix operands, where tokens lie, and
-// the state of a warp's query rows.
+// The pieces of the attention over an 8-bit cache: codes widened to matrix operands,
+// where tokens lie, and the state of a warp's query rows.
 //
-// A product's operands (m16n8k16): tokens are the M axis of S^T = K Q^T and dims that of O^T = V^T P^T, query rows
-// the N axis. Lane 4g + t4 holds, of K, four dims of tokens g and g + 8 a step; of V, two dims of tokens 2 t4, 2 t4 + 1,
-// 2 t4 + 8, 2 t4 + 9; of results, rows 2 t4 and 2 t4 + 1 of tokens (dims) g and g + 8. The axis a product sums over, and the dims
-// of O, may be in any order as long as both operands agree, so that a lane takes whole words of codes.
+// A product's operands (m16n8k16): tokens are the M axis of S^T = K Q^T and dims
+// that of O^T = V^T P^T, query rows the N axis. Lane 4g + t4 holds, of K, four dims
+// of tokens g and g + 8 a step; of V, two dims of tokens 2 t4, 2 t4 + 1, 2 t4 + 8 and
+// 2 t4 + 9; of results, rows 2 t4 and 2 t4 + 1 of tokens (dims) g and g + 8. The axis a
+// product sums over, and the dims of O, may be in any order as long as both
+// operands agree, so that a lane takes whole words of codes.
 #pragma once
 #include "kk_attn.cuh"
 #include "kk_f32x2.cuh"
@@ -153,7 +155,8 @@ __device__ __forceinline__ void query_operands(const unsigned char* raw, float s
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) {
     q[j] = *reinterpret_cast<const uint2*>(row + (D >= 64 ? (j >> 2) * 64 + t4 * 16 + (j & 3) * 4 : t4 * 8 + j * 4));
-    top = max(max(top, max(q[j].x & 0x7FFFu, (q[j].x >> 16) & 0x7FFFu)), max(q[j].y & 0x7FFFu, (q[j].y >> 16) & 0x7FFFu));
+    top = max(top, max(max(q[j].x & 0x7FFFu, (q[j].x >> 16) & 0x7FFFu),
+                       max(q[j].y & 0x7FFFu, (q[j].y >> 16) & 0x7FFFu)));
   }
   top = max(top, __shfl_xor_sync(kFull, top, 1));
   top = max(top, __shfl_xor_sync(kFull, top, 2));
@@ -190,7 +193,8 @@ struct Rows {
   // Scores of 16 tokens from their products: times the rows' factors and the Keys' scales; ONE: the tokens share a
   // page. Places without a token are hidden whatever they hold.
   template <bool ONE>
-  __device__ __forceinline__ void score(float (&s)[NT][4], const float (&qf)[NT][2], float ks0, float ks1, uint32_t live) {
+  __device__ __forceinline__ void score(float (&s)[NT][4], const float (&qf)[NT][2], float ks0, float ks1,
+                                        uint32_t live) {
     const int g = (threadIdx.x & 31) >> 2;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -275,8 +279,8 @@ struct Rows {
 
   // Drafted nodes j0 .. j0 + 15, bf16, straight from where they lie. raw: the rows' staged queries, the first of
   // them row `row0` of the request.
-  __device__ __forceinline__ void drafts(const AttnArgs& a, const AttnReq& rq, int h, const unsigned char* raw, int row0,
-                                         int j0) {
+  __device__ __forceinline__ void drafts(const AttnArgs& a, const AttnReq& rq, int h, const unsigned char* raw,
+                                         int row0, int j0) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     float s[1][NT][4];
 #pragma unroll

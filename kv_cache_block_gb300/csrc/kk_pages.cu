@@ -307,7 +307,8 @@ __global__ void __launch_bounds__(kPlan) pages_compact_kernel(const CompactArgs 
   cluster_sync();  // every CTA of the cluster runs before another writes to its shared memory
   // a CTA's share of the pages, in order
   const long long per = ((long long)a.num_pages + p.ctas - 1) / p.ctas;
-  const int lo = (int)min((long long)a.num_pages, per * p.cta), hi = (int)min((long long)a.num_pages, per * (p.cta + 1));
+  const int lo = (int)min((long long)a.num_pages, per * p.cta);
+  const int hi = (int)min((long long)a.num_pages, per * (p.cta + 1));
   int mine = 0, total, before, used;
   for (int i = lo + p.tid; i < hi; i += kPlan) mine += a.refs_in[i] != 0;
   block_scan(mine, sh, &total);
@@ -364,8 +365,9 @@ __global__ void __launch_bounds__(kPlan) pages_compact_kernel(const CompactArgs 
 
 // ---- small pools: one CTA, counts and tables' sizes in shared memory -----------------------------------------------
 // At most kFastPages pages and kFastRows requests and children: what the phases above exchange through L2 stays in the
-// CTA, so that a call waits for memory two or three times (a fork of 32 samples of 61 blocks 14.3 -> 8.2 us, a step of 16 beams
-// 12.8 -> 8.2, a page for each of 16 requests 6.2 -> 4.1, compaction's plan of 509 pages 10.3 -> 4.6; an empty launch takes 4.1).
+// CTA, so that a call waits for memory two or three times (a fork of 32 samples of 61 blocks 14.3 -> 8.2 us, a step of
+// 16 beams 12.8 -> 8.2, a page for each of 16 requests 6.2 -> 4.1, compaction's plan of 509 pages 10.3 -> 4.6; an empty
+// launch takes 4.1).
 constexpr int kFast = 512, kFastPer = 8, kFastPages = kFast * kFastPer, kFastRows = 512;
 
 // Exclusive sums of two numbers over the CTA's kFast threads, and their totals. `sh`: 2 x 17 ints.
@@ -440,7 +442,8 @@ __global__ void __launch_bounds__(kFast) pages_fork_fast_kernel(const ForkArgs a
   __shared__ int s_refs[kFastPages];
   __shared__ Parent s_par[kFastRows];
   __shared__ int s_kids[kFastRows], s_first[kFastRows];
-  __shared__ int s_of[kFastRows], s_to[kFastRows + 1], s_at[kFastRows];  // a child's parent and first entry; a copy's entry
+  // a child's parent and first entry; a copy's entry
+  __shared__ int s_of[kFastRows], s_to[kFastRows + 1], s_at[kFastRows];
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, wid = tid >> 5;
@@ -531,7 +534,8 @@ __global__ void __launch_bounds__(kFast) pages_compact_fast_kernel(const Compact
   int2 total;
   const int first = fast_scan(make_int2(__popc(on), 0), sh, &total).x;
   const int used = total.x;
-  if (used / kFastPer == tid) s_stay = first + __popc(on & ((1 << used % kFastPer) - 1));  // used pages in front of page `used`
+  // used pages in front of page `used`
+  if (used / kFastPer == tid) s_stay = first + __popc(on & ((1 << used % kFastPer) - 1));
   if (tid == 0 && used == kFastPages) s_stay = used;
   __syncthreads();
   const int stay = s_stay, moves = used - stay;
@@ -593,7 +597,8 @@ __device__ __forceinline__ void copy_chunk(const PageArray& d, const int2 m, int
   const int s0 = (first + (int)threadIdx.x) / d.per, o0 = first + (int)threadIdx.x - s0 * d.per;
   V x[kUnroll];
   // from one of a thread's vectors to the next: `step` bytes, or `step` and on to the next slice
-  const long long step = d.step_s * d.slice + d.step_o * (int)sizeof(V), over = d.slice - (long long)d.per * (int)sizeof(V);
+  const long long step = d.step_s * d.slice + d.step_o * (int)sizeof(V);
+  const long long over = d.slice - (long long)d.per * (int)sizeof(V);
   auto each = [&](auto f) {
     long long at = s0 * d.slice + (long long)o0 * (int)sizeof(V);
     int o = o0;
@@ -611,8 +616,8 @@ __device__ __forceinline__ void copy_chunk(const PageArray& d, const int2 m, int
   each([&](int u, long long at) { *reinterpret_cast<V*>(to + at) = x[u]; });
 }
 
-__global__ void __launch_bounds__(kCopy, 3) pages_copy_kernel(const __grid_constant__ PageArrays pa, const int2* pairs, const int* n_pairs,
-                                                           int num_pages) {
+__global__ void __launch_bounds__(kCopy, 3) pages_copy_kernel(const __grid_constant__ PageArrays pa,
+                                                              const int2* pairs, const int* n_pairs, int num_pages) {
   pdl_wait();
   pdl_launch_dependents();
   const long long units = (long long)*n_pairs * pa.chunks;
@@ -675,7 +680,8 @@ bool plan_page_arrays(PageArrays* pa) {
   pa->chunks = 0;
   for (int i = 0; i < pa->n; ++i) {
     PageArray& d = pa->a[i];
-    d.vec = (reinterpret_cast<uintptr_t>(d.base) | (uintptr_t)d.slice | (uintptr_t)d.page | (uintptr_t)d.bytes) % 16 ? 4 : 16;
+    const uintptr_t all = reinterpret_cast<uintptr_t>(d.base) | d.slice | d.page | d.bytes;
+    d.vec = all % 16 ? 4 : 16;
     const long long per = d.bytes / d.vec, vecs = per * d.slices, chunks = (vecs + kChunk - 1) / kChunk;
     if (per > 0x7FFF0000 || vecs > 0x7FFF0000 || pa->chunks + chunks > 0x7FFF0000) return false;
     d.per = (int)per;
@@ -705,7 +711,8 @@ cudaError_t launch_pages_free(const Table& bt, const int* refs_in, int* refs_out
 cudaError_t launch_pages_fork(const ForkArgs& f, const PageArrays& pa, cudaStream_t s) {
   const long long work = std::max<long long>(f.num_pages, 2ll * f.F * f.bt.max_blocks);
   const bool fast = f.num_pages <= kFastPages && f.F <= kFastRows && f.bt.R <= kFastRows && work <= 4 * kStep;
-  const cudaError_t e = fast ? launch_cluster(pages_fork_fast_kernel, 1, kFast, s, f) : launch_plan(pages_fork_kernel, work, s, f);
+  const cudaError_t e =
+      fast ? launch_cluster(pages_fork_fast_kernel, 1, kFast, s, f) : launch_plan(pages_fork_kernel, work, s, f);
   return e != cudaSuccess ? e : launch_copies(pa, f.pairs, f.n_pairs, f.F, f.num_pages, s);
 }
 

@@ -60,7 +60,8 @@ kk_status check_arrays(const kk_page_array* arrays, int32_t n, kk::PageArrays* o
   out->n = n;
   for (int i = 0; i < n; ++i) {
     const kk_page_array& a = arrays[i];
-    if (!a.base || a.bytes <= 0 || a.slices <= 0 || a.stride_slice < 0 || a.stride_page < a.bytes) return KK_ERR_INVALID;
+    if (!a.base || a.bytes <= 0 || a.slices <= 0 || a.stride_slice < 0 || a.stride_page < a.bytes)
+      return KK_ERR_INVALID;
     if (!aligned(a.base, 4) || a.bytes % 4 || a.stride_slice % 4 || a.stride_page % 4) return KK_ERR_UNSUPPORTED;
     out->a[i] = kk::PageArray{static_cast<char*>(a.base), a.stride_slice, a.stride_page, a.bytes, a.slices};
   }
@@ -108,9 +109,11 @@ kk_status kk_qk_norm_rope(int32_t dtype, int32_t num_nodes, int32_t num_q_heads,
                           const kk_rows* q_out, const kk_rows* k_out, const kk_kcache_desc* kc,
                           const kk_kcache_desc* vc, const kk_block_table* bt, const int32_t* token_offsets,
                           int32_t layer, cudaStream_t stream) {
-  if ((dtype != KK_BF16 && dtype != KK_F32) || num_nodes < 0 || num_q_heads < 0 || num_kv_heads < 0) return KK_ERR_INVALID;
+  if ((dtype != KK_BF16 && dtype != KK_F32) || num_nodes < 0 || num_q_heads < 0 || num_kv_heads < 0)
+    return KK_ERR_INVALID;
   if (num_q_heads + (long long)num_kv_heads == 0 || !(eps >= 0.f) || !std::isfinite(eps)) return KK_ERR_INVALID;
-  if (!dim_ok(D) || num_nodes > kk::kMaxTokens || num_q_heads > 65536 || num_kv_heads > 65536) return KK_ERR_UNSUPPORTED;
+  if (!dim_ok(D) || num_nodes > kk::kMaxTokens || num_q_heads > 65536 || num_kv_heads > 65536)
+    return KK_ERR_UNSUPPORTED;
   const int es = dtype == KK_F32 ? 4 : 2;
   kk::RopeArgs a = {};
   a.f32 = dtype == KK_F32;
@@ -254,7 +257,8 @@ kk_status kk_pages_free(const kk_block_table* bt, const int32_t* refs_in, int32_
   kk::Table t;
   kk_status st = kk::check_block_table(bt, &t);
   if (st != KK_OK || (st = check_refs(refs_in, refs_out, num_pages)) != KK_OK) return st;
-  if (collide({{refs_out, num_pages}}, {{t.offsets, t.R + 1ll}, {t.pages, t.max_blocks > 0 ? 1 : 0}})) return KK_ERR_INVALID;
+  if (collide({{refs_out, num_pages}}, {{t.offsets, t.R + 1ll}, {t.pages, t.max_blocks > 0 ? 1 : 0}}))
+    return KK_ERR_INVALID;
   if (t.R == 0 && refs_in == refs_out) return KK_OK;
   int* err = kk::device_error_word();
   if (!err) return KK_ERR_CUDA;
@@ -285,8 +289,12 @@ kk_status kk_pages_fork(const kk_block_table* bt, int32_t block_size, const int3
     return KK_ERR_UNSUPPORTED;
   // children are laid out, and counts moved, while their parents are read (how long bt's pages are is not known here)
   if (collide({{child_pages, most}, {child_offsets, F + 1ll}, {child_lens, F}, {refs_out, num_pages}},
-              {{parent, F}, {a.bt.offsets, a.bt.R + 1ll}, {a.bt.seq_lens, a.bt.R}, {a.bt.pages, a.bt.max_blocks > 0 ? 1 : 0}}) ||
-      (refs_in != refs_out && collide({{child_pages, most}, {child_offsets, F + 1ll}, {child_lens, F}}, {{refs_in, num_pages}})))
+              {{parent, F},
+               {a.bt.offsets, a.bt.R + 1ll},
+               {a.bt.seq_lens, a.bt.R},
+               {a.bt.pages, a.bt.max_blocks > 0 ? 1 : 0}}) ||
+      (refs_in != refs_out &&
+       collide({{child_pages, most}, {child_offsets, F + 1ll}, {child_lens, F}}, {{refs_in, num_pages}})))
     return KK_ERR_INVALID;
   if (!workspace || workspace_bytes < kk_pages_fork_workspace_bytes(a.bt.R, F)) return KK_ERR_INVALID;
   if (!aligned(workspace, 256)) return KK_ERR_UNSUPPORTED;
