@@ -712,8 +712,8 @@ kk_status kk_kv8_write(const kk_kcache_desc* kc, float* k_scale, const kk_kcache
  * for each row (what that loses is below 2^-39 of the row's largest element),
  * weights are rounded to float16 (of drafted nodes: bf16) before they multiply
  * the Values; where max_nodes * num_q_heads / num_kv_heads > 80, with 64 or 128
- * dims, weights are rounded to bf16, and values as bf16 (exact where their scale
- * is a power of two). Sums and softmax are float32. Scales are finite.
+ * dims and tables of some thousand tokens on, weights are rounded to bf16, and
+ * codes times their scales too (exact where a scale is a power of two). Sums and softmax are float32. Scales are finite.
  * Workspace: kk_tree_attn_kv8_workspace_bytes().
  */
 size_t kk_tree_attn_kv8_workspace_bytes(const kk_kcache_desc* kc, const kk_block_table* bt, int32_t max_nodes,

@@ -71,7 +71,6 @@ __device__ __forceinline__ float pow2_scale(float amax) {
   return __uint_as_float((uint32_t)(e < 1 ? 1 : e) << 23);
 }
 
-
 template <typename T, int D, int W>
 __global__ void __launch_bounds__(kThreads, 4) write8_kernel(const Write8Args a) {
   constexpr int E = Vec16<T>::kElems, CH = D / E;  // elements of a vector, vectors of a row

@@ -16,8 +16,8 @@
 // top 32 bits go to sincospi; a float32 product p * f would be off by whole
 // radians at the far positions of a long context, and float64 is slow here.
 //
-// Measured, 28 + 4 heads of 128 bf16 dims with the Values: 11.2 K nodes (207 MB) 40 us,
-// 5.2 TB/s; one node of 8 requests 8.2 us (11 with the host). With blocks of 8
+// Measured, 28 + 4 heads of 128 bf16 dims with the Values: 11.2 K nodes (207 MB) 39.4 us,
+// 5.3 TB/s; one node of 8 requests 8.2 us (11 with the host). With blocks of 8
 // nodes 62 (their look-ups and sines, a chain of latencies, came 3.4 times to an
 // SM), with sines as they are numbered, four lanes to a bank, 46.
 #include "kk_device.cuh"
