@@ -691,12 +691,14 @@ kk_status kk_qk_norm_rope(int32_t dtype, int32_t num_nodes, int32_t num_q_heads,
  * in kk_qk_norm_rope, with their Keys and Values at rows k and v of type dtype
  * (KK_BF16 or KK_F32), for every layer of [layer, layer + num_layers). In each
  * page they reach, the scale of a (layer, head) becomes
- *   max(the scale so far, 2^e),  2^e the smallest power of two with amax / 448 <= 2^e, at least 2^-126
+ *   max(|the scale so far|, 2^e),  2^e the smallest power of two with amax / 448 <= 2^e, at least 2^-126
  * (amax: the largest finite magnitude of the page's new tokens; the scale so
- * far: 0 when the page held no older token of the request). New codes are value
- * / scale rounded to nearest even; the page's older codes are multiplied by old
- * scale / new scale and rounded, which is exact but for results below 2^-6 (a
- * power of two changes no mantissa). What is not finite becomes NaN. Nothing
+ * far: 0 when the page held no older token of the request, else finite). New
+ * codes are value / scale rounded once, to nearest even; the page's older codes
+ * are multiplied by old scale / new scale and rounded once. That is exact but for
+ * results below 2^-6 as long as the scales are this call's (a power of two
+ * changes no mantissa); a caller's own may be 0, below 0 or no powers of two:
+ * older tokens keep what they stood for. What is not finite becomes NaN. Nothing
  * behind a request's last token is written. No page may be in two requests'
  * tables. k or v may be NULL with its cache NULL (Keys or Values alone).
  */

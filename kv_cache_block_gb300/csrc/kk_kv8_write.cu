@@ -4,10 +4,11 @@
 // An item is what one request adds to one page of one (layer, head), Keys or
 // Values: the largest finite magnitude of its new tokens gives the scale, then
 // they are divided by it (a multiplication by its inverse, exact) and rounded
-// once, to nearest even. Where the page held older tokens and its scale grows,
-// their codes move with it. One warp takes an item of few tokens (a decode
-// step: the item is one row), a block of eight warps one of many. The new
-// tokens stay in registers between the two passes, up to 8 vectors of 16 bytes
+// once, to nearest even. Where the page held older tokens and its scale changes,
+// their codes move with it. A scale of the caller's own that is no power of two
+// costs its item a second round of stores, with exact divisions. One warp takes
+// an item of few tokens (a decode step: the item is one row), a block of eight
+// warps one of many. The new tokens stay in registers between the two passes, up to 8 vectors of 16 bytes
 // a thread (a page of 128 tokens of 128 bf16 dims in a block); larger items
 // read them again, from L2.
 //
@@ -69,6 +70,15 @@ __device__ __forceinline__ float pow2_scale(float amax) {
   // 448 = 1.75 * 2^8: one exponent more where the mantissa is above 1.75
   const int e = (int)(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u);
   return __uint_as_float((uint32_t)(e < 1 ? 1 : e) << 23);
+}
+
+// q, rounded from a value that is r's sign further on (r 0: exact): moved off e4m3's halfway points by its last bit,
+// so that rounding it once more gives what the value itself rounds to. (Halfway points have 5 bits; a product or
+// quotient of two float32 numbers that rounds to one lies next to it.)
+__device__ __forceinline__ float keep_side(float q, float r) {
+  const uint32_t b = __float_as_uint(q);
+  if (r == 0.f || (b & 0xFFFFu) || q == 0.f || !(fabsf(q) <= 448.f)) return q;
+  return __uint_as_float((r > 0.f) == (q > 0.f) ? b + 1 : b - 1);
 }
 
 template <typename T, int D, int W>
@@ -151,17 +161,17 @@ __global__ void __launch_bounds__(kThreads, 4) write8_kernel(const Write8Args a)
   const float top = Top<T>::value(bits);
   if (!real) return;
   float* at = x.scale + ((long long)(a.layer + l) * a.kc.num_pages + page) * H + h;
-  const float old = had ? *at : 0.f, fresh = pow2_scale(top), now = fmaxf(old, fresh);
+  const float old = had ? *at : 0.f, now = fmaxf(fabsf(old), pow2_scale(top));
   const float inv = 1.f / now;
   char* codes = static_cast<char*>(x.codes) + (a.layer + l) * x.dL + page * x.dP + h * x.dH;
   if constexpr (W > 1) __syncthreads();  // every thread has read the scale
   else __syncwarp();
   if (tid == 0) *at = now;
-  auto store = [&](int i, const uint4& v) {
+  auto store = [&](int i, const uint4& v, auto divide) {
     float f[E];
     Vec16<T>::unpack(v, f);
 #pragma unroll
-    for (int e = 0; e < E; ++e) f[e] *= inv;
+    for (int e = 0; e < E; ++e) f[e] = divide(f[e]);
     if (odd)
 #pragma unroll
       for (int e = 0; e < E; ++e) f[e] = only_finite(f[e]);
@@ -172,13 +182,22 @@ __global__ void __launch_bounds__(kThreads, 4) write8_kernel(const Write8Args a)
     else
       *reinterpret_cast<uint32_t*>(to) = p;
   };
+  auto scaled = [&](float x) { return x * inv; };
 #pragma unroll
   for (int k = 0; k < kKeep; ++k)
-    if (tid + k * NTH < vecs) store(tid + k * NTH, keep[k]);
+    if (tid + k * NTH < vecs) store(tid + k * NTH, keep[k], scaled);
   for (int i = tid + kKeep * NTH; i < vecs; i += NTH)
-    store(i, at_vec(i));
-  if (had && old > 0.f && old < now) {  // the page's older codes, in terms of the new scale
-    const float f = old * inv;
+    store(i, at_vec(i), scaled);
+  if ((__float_as_uint(now) & 0x7FFFFFu) != 0) {  // no power of two: over again, as exact quotients round
+    const float up = now < 0x1p-60f ? 0x1p64f : 1.f, by = now * up;  // remainders stay in float32's normal range
+    for (int i = tid; i < vecs; i += NTH)
+      store(i, at_vec(i), [&](float x) {
+        const float y = x * up / by;
+        return keep_side(y, fmaf(-y, by, x * up));
+      });
+  }
+  if (had && old != now) {  // the page's older codes, in terms of the new scale
+    const float f = old == -now ? -1.f : old * inv;  // else `now` is the new tokens' power of two
     for (int i = tid; i < had * (D / 4); i += NTH) {
       uint32_t* p = reinterpret_cast<uint32_t*>(codes + (i / (D / 4)) * x.dT + (i % (D / 4)) * 4);
       const uint32_t c = *p;
@@ -191,7 +210,12 @@ __global__ void __launch_bounds__(kThreads, 4) write8_kernel(const Write8Args a)
             : "=f"(y[2 * e]), "=f"(y[2 * e + 1])
             : "r"(two));
       }
-      *p = to_e4m3x2(y[0] * f, y[1] * f) | to_e4m3x2(y[2] * f, y[3] * f) << 16;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float z = y[e] * f;
+        y[e] = keep_side(z, fmaf(y[e], f, -z));
+      }
+      *p = to_e4m3x2(y[0], y[1]) | to_e4m3x2(y[2], y[3]) << 16;
     }
   }
 }
