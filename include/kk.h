@@ -771,7 +771,9 @@ kk_status kk_pages_free(const kk_block_table* bt, const int32_t* refs_in, int32_
  * parents' when they stay). Free pages are taken as of after that. A parent out
  * of [0, R) gives a child without tokens (KK_ERR_BAD_INDEX); so does one whose
  * table disagrees with its length, whose counts stay. A page out of range, or in
- * a table with a count of 0, is reported (KK_ERR_BAD_INDEX). Where no
+ * a table with a count of 0, is reported (KK_ERR_BAD_INDEX); the latter has one
+ * count afterwards for every place it has in the children's tables (and the
+ * parents' when they stay), and no count falls below 0. Where no
  * page is left the child's last entry is -1 (KK_ERR_NO_PAGES).
  * child tables may not overlap bt's. arrays: n_arrays (0..8) host structs, read during the call.
  * workspace: device, 256-byte aligned, no initial contents.

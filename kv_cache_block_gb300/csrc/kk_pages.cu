@@ -206,6 +206,26 @@ __device__ __forceinline__ Parent parent_of(const ForkArgs& a, int r) {
   return x;
 }
 
+// How a fork changes the count of a page for a place it has in a parent's table: the open block's (`open`), or another.
+__device__ __forceinline__ int change_of(const ForkArgs& a, int kids, bool open) {
+  return open ? (a.keep ? 0 : (kids ? 0 : -1)) : (a.keep ? kids : kids - 1);
+}
+
+// Counts that were missing. A table's own count is there until its change, whatever the others do, so a change finds
+// 0 only where tables have more places than the page has counts. The changes are then taken back and made
+// again by make_count, in three passes over the tables: a count of 0 becomes kMissing plus the places that hold the page
+// afterwards, in whatever order the tables come, and real_count says what that is.
+constexpr int kMissing = -(1 << 30);
+__device__ __forceinline__ void make_count(int* at, int more) {
+  int c = 0;
+  for (;;) {
+    const int seen = atomicCAS(at, c, c > 0 ? c + more : (c < kMissing / 2 ? c : kMissing) + more + 1);
+    if (seen == c) return;
+    c = seen;
+  }
+}
+__device__ __forceinline__ int real_count(int c) { return c >= 0 ? c : max(0, c < kMissing / 2 ? c - kMissing : 0); }
+
 __global__ void __launch_bounds__(kPlan) pages_fork_kernel(const ForkArgs a) {
   __shared__ int sh[33], box[2 * kPlanCtas];
   const Place p = place();
@@ -214,6 +234,8 @@ __global__ void __launch_bounds__(kPlan) pages_fork_kernel(const ForkArgs a) {
     a.kids[r] = 0;
     a.first[r] = INT_MAX;
   }
+  int* missing = a.n_pairs + 1;  // whether a place in a table had no count
+  if (p.all == 0) *missing = 0;
   cluster_sync();
   for (int i = p.all; i < a.F; i += p.n) {
     const int r = a.parent[i];
@@ -265,21 +287,26 @@ __global__ void __launch_bounds__(kPlan) pages_fork_kernel(const ForkArgs a) {
     }
   }
   const int lead = p.ctas > 1 ? kPlan / 32 : 0;  // CTA 0's warps stay out
-  share_warps((p.all >> 5) - lead, (p.n >> 5) - lead, a.bt.R, [&](int r, int j0, int step) {
-    const Parent x = parent_of(a, r);
-    const int kids = __ldcg(a.kids + r);
-    for (int j = j0; j < x.n; j += step) {
-      const int page = a.bt.pages[x.off + j];
-      const int more = j == x.n - 1 && x.part ? (a.keep ? 0 : (kids ? 0 : -1)) : (a.keep ? kids : kids - 1);
-      if (page < 0 || page >= a.num_pages) {
-        flag_error(a.err, kErrBadIndex);
-      } else {  // this table's own count is still there, whatever the others' did
-        const int had = more ? atomicAdd(a.refs_out + page, more) : __ldcg(a.refs_out + page);
-        if (had <= 0) flag_error(a.err, kErrBadIndex);
+  auto places = [&](auto f) {  // f(page, change) for every place of a page in the tables; a page out of range is reported
+    share_warps((p.all >> 5) - lead, (p.n >> 5) - lead, a.bt.R, [&](int r, int j0, int step) {
+      const Parent x = parent_of(a, r);
+      const int kids = __ldcg(a.kids + r);
+      for (int j = j0; j < x.n; j += step) {
+        const int page = a.bt.pages[x.off + j];
+        if (page < 0 || page >= a.num_pages) flag_error(a.err, kErrBadIndex);
+        else f(page, change_of(a, kids, j == x.n - 1 && x.part));
       }
+    });
+  };
+  places([&](int page, int more) {
+    const int had = more ? atomicAdd(a.refs_out + page, more) : __ldcg(a.refs_out + page);
+    if (had <= 0) {
+      *missing = 1;
+      flag_error(a.err, kErrBadIndex);
     }
   });
   cluster_sync();
+  const bool mend = __ldcg(missing) != 0;  // the same for the cluster
   share_warps(p.all >> 5, p.n >> 5, a.F, [&](int i, int j0, int step) {
     const int to = __ldcg(a.child_offsets + i), n = __ldcg(a.child_offsets + i + 1) - to;
     if (n == 0) return;
@@ -288,6 +315,17 @@ __global__ void __launch_bounds__(kPlan) pages_fork_kernel(const ForkArgs a) {
     const bool copy = x.part && (a.keep || __ldcg(a.first + r) != i);
     for (int j = j0; j < n - (copy ? 1 : 0); j += step) a.child_pages[to + j] = a.bt.pages[x.off + j];
   });
+  if (mend) {
+    places([&](int page, int more) { atomicSub(a.refs_out + page, more); });
+    cluster_sync();
+    places([&](int page, int more) { make_count(a.refs_out + page, more); });
+    cluster_sync();
+    for (int i = p.all; i < a.num_pages; i += p.n) {
+      const int c = __ldcg(a.refs_out + i);
+      if (c < 0) a.refs_out[i] = real_count(c);
+    }
+    cluster_sync();
+  }
   const int need = __ldcg(a.at + a.F);
   const int got = take_free(a.refs_out, a.num_pages, need, p, sh, box, [&](int k, int page) {
     a.refs_out[page] = 1;
@@ -479,15 +517,20 @@ __global__ void __launch_bounds__(kFast) pages_fork_fast_kernel(const ForkArgs a
   }
   if (tid == 0) s_to[a.F] = a.child_offsets[a.F] = total.x;
   __syncthreads();
-  share_warps(wid, kFast / 32, a.bt.R, [&](int q, int j0, int step) {
-    const Parent x = s_par[q];
-    const int kids = s_kids[q];
-    for (int j = j0; j < x.n; j += step) {
-      const int page = a.bt.pages[x.off + j];
-      const int more = j == x.n - 1 && x.part ? (a.keep ? 0 : (kids ? 0 : -1)) : (a.keep ? kids : kids - 1);
-      if (page < 0 || page >= a.num_pages) flag_error(a.err, kErrBadIndex);
-      else if ((more ? atomicAdd(s_refs + page, more) : s_refs[page]) <= 0) flag_error(a.err, kErrBadIndex);
-    }
+  bool missing = false;
+  auto places = [&](auto f) {  // as above
+    share_warps(wid, kFast / 32, a.bt.R, [&](int q, int j0, int step) {
+      const Parent x = s_par[q];
+      const int kids = s_kids[q];
+      for (int j = j0; j < x.n; j += step) {
+        const int page = a.bt.pages[x.off + j];
+        if (page < 0 || page >= a.num_pages) flag_error(a.err, kErrBadIndex);
+        else f(page, change_of(a, kids, j == x.n - 1 && x.part));
+      }
+    });
+  };
+  places([&](int page, int more) {
+    if ((more ? atomicAdd(s_refs + page, more) : s_refs[page]) <= 0) missing = true;
   });
   share_warps(wid, kFast / 32, a.F, [&](int i, int j0, int step) {
     const int q = s_of[i];
@@ -496,7 +539,15 @@ __global__ void __launch_bounds__(kFast) pages_fork_fast_kernel(const ForkArgs a
     const int own = x.part && (a.keep || s_first[q] != i);  // the last entry is the copy's
     for (int j = j0; j < x.n - own; j += step) a.child_pages[s_to[i] + j] = a.bt.pages[x.off + j];
   });
-  __syncthreads();
+  if (__syncthreads_or(missing)) {
+    if (tid == 0) flag_error(a.err, kErrBadIndex);
+    places([&](int page, int more) { atomicSub(s_refs + page, more); });
+    __syncthreads();
+    places([&](int page, int more) { make_count(s_refs + page, more); });
+    __syncthreads();
+    for (int p = tid; p < a.num_pages; p += kFast) s_refs[p] = real_count(s_refs[p]);
+    __syncthreads();
+  }
   const int free = own_pages(a.num_pages, [&](int page) { return s_refs[page] == 0; });
   const int need = total.y;
   int2 found;
