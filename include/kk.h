@@ -770,7 +770,8 @@ kk_status kk_pages_free(const kk_block_table* bt, const int32_t* refs_in, int32_
  * lose a count. Counts are right afterwards for the children's tables (and the
  * parents' when they stay). Free pages are taken as of after that. A parent out
  * of [0, R) gives a child without tokens (KK_ERR_BAD_INDEX); so does one whose
- * table disagrees with its length, whose counts stay. A page out of range, or in
+ * table disagrees with its length, whose counts stay (of consumed parents it is
+ * reported without children too). A page out of range, or in
  * a table with a count of 0, is reported (KK_ERR_BAD_INDEX); the latter has one
  * count afterwards for every place it has in the children's tables (and the
  * parents' when they stay), and no count falls below 0. Where no

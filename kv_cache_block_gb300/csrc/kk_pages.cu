@@ -291,6 +291,7 @@ __global__ void __launch_bounds__(kPlan) pages_fork_kernel(const ForkArgs a) {
     share_warps((p.all >> 5) - lead, (p.n >> 5) - lead, a.bt.R, [&](int r, int j0, int step) {
       const Parent x = parent_of(a, r);
       const int kids = __ldcg(a.kids + r);
+      if (x.n < 0 && !a.keep && j0 == 0) flag_error(a.err, kErrBadIndex);  // its counts cannot be given back
       for (int j = j0; j < x.n; j += step) {
         const int page = a.bt.pages[x.off + j];
         if (page < 0 || page >= a.num_pages) flag_error(a.err, kErrBadIndex);
@@ -522,6 +523,7 @@ __global__ void __launch_bounds__(kFast) pages_fork_fast_kernel(const ForkArgs a
     share_warps(wid, kFast / 32, a.bt.R, [&](int q, int j0, int step) {
       const Parent x = s_par[q];
       const int kids = s_kids[q];
+      if (x.n < 0 && !a.keep && j0 == 0) flag_error(a.err, kErrBadIndex);
       for (int j = j0; j < x.n; j += step) {
         const int page = a.bt.pages[x.off + j];
         if (page < 0 || page >= a.num_pages) flag_error(a.err, kErrBadIndex);
