@@ -402,11 +402,14 @@ struct Rows {
           jm[p * M + m] = ref_s[nt][e] == kNone ? -INFINITY : ref_s[nt][e];
           jl[p * M + m] = l;
         }
-        const float f = ex2(ref_v[nt][e] - kLift - ref_s[nt][e]);
+        // In two factors, of which the second is 1 but for Values below 2^-94: their scales and the lift may together be
+        // below what one power of two holds.
+        const float x = ref_v[nt][e] - kLift - ref_s[nt][e];
+        const float f = ex2(fmaxf(x, -100.f)), f2 = ex2(fminf(x + 100.f, 0.f));
 #pragma unroll
         for (int n = 0; n < KS; ++n)
           *reinterpret_cast<float2*>(join + (p * M + m) * D + dim_of<D>(n, g)) =
-              make_float2(o[nt][n][e] * f, o[nt][n][e + 2] * f);
+              make_float2(o[nt][n][e] * f * f2, o[nt][n][e + 2] * f * f2);
       }
   }
 };
