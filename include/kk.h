@@ -543,7 +543,7 @@ typedef struct kk_selection {
  * (layer `layer`; all seq_lens[r] of them, or with sel the valid tokens of the
  * selected blocks) and the drafted nodes it may see. For node i and query
  * head hq, with KV head h = hq / (num_q_heads / num_kv_heads):
- *   s_t = scale * q . k_t,  lse = log sum_t e^{s_t},  out = sum_t e^{s_t - lse} v_t
+ *   s_t = scale * q . k_t,  lse = log sum_t e^{s_t},  out = sum_t e^{s_t - lse} v_t (|s_t| < 2^30)
  * q: device, the cache's element type, head hq of node i at q + i*q_stride_node
  * + hq*q_stride_head (elements; 16-byte aligned, strides multiples of 16
  * bytes). out: device [total_nodes][num_q_heads][D] of the cache's type; lse:

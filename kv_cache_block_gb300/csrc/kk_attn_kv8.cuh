@@ -18,7 +18,7 @@
 // along the wrong axis, are turned by movmatrix.
 //
 // Softmax. Two references a row (log2 domain): one for the sum of weights, 2^(s -
-// ref_s) in float32, one for what multiplies the codes of V, 2^(s - ref_v + 6) *
+// ref) in float32, one for what multiplies the codes of V, 2^(s - ref - gap + 6) *
 // v_scale, which has to fit float16 whatever the pages' scales are. Both are
 // left alone until a score passes one by 2^8 (one vote a step); until then sums
 // below 2^8 cost nothing and no reduction over lanes is needed.

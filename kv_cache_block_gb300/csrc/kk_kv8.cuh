@@ -8,6 +8,8 @@
 // product sums over, and the dims of O, may be in any order as long as both
 // operands agree, so that a lane takes whole words of codes.
 #pragma once
+#include <cfloat>
+
 #include "kk_attn.cuh"
 #include "kk_f32x2.cuh"
 
@@ -15,7 +17,7 @@ namespace kk {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr float kNone = -1e30f;  // a reference before the first score
+constexpr float kNone = -FLT_MAX;  // a reference before the first score, below every finite one
 constexpr float kLift = 6.f;     // a weight is below 2^(6 + 8) * 2 (a scale's mantissa): float16 holds 65504
 
 // Two e4m3 codes (the low or the high half of a word) as float16, exactly.
@@ -172,11 +174,13 @@ __device__ __forceinline__ void query_operands(const unsigned char* raw, float s
   qf[1] = __shfl_sync(kFull, f, t4 * 8 + 4);
 }
 
-// A warp's 8 NT query rows: accumulators, references and sums.
+// A warp's 8 NT query rows: accumulators, references and sums. ref_s: the reference of the sum of weights; gap: how far
+// the other one, of weight times the Values' scale, lies above it. Exponents come from differences to ref_s alone, which
+// are small where they matter however large the scores are.
 template <int D, int NT>
 struct Rows {
   static constexpr int KS = D / 16;
-  float o[NT][KS][4], ref_s[NT][2], ref_v[NT][2], sum[NT][2];
+  float o[NT][KS][4], ref_s[NT][2], gap[NT][2], sum[NT][2];
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -185,8 +189,8 @@ struct Rows {
       for (int n = 0; n < KS; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][n][e] = 0.f;
-      ref_s[nt][0] = ref_s[nt][1] = ref_v[nt][0] = ref_v[nt][1] = kNone;
-      sum[nt][0] = sum[nt][1] = 0.f;
+      ref_s[nt][0] = ref_s[nt][1] = kNone;
+      gap[nt][0] = gap[nt][1] = sum[nt][0] = sum[nt][1] = 0.f;
     }
   }
 
@@ -219,36 +223,41 @@ struct Rows {
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float top = ONE ? fmaxf(s[i][nt][e], s[i][nt][e + 2]) : s[i][nt][e];
-          rise |= top > 8.f + fminf(ref_s[nt][e], ref_v[nt][e] - lv[i][0]);
-          if (!ONE) rise |= s[i][nt][e + 2] > 8.f + fminf(ref_s[nt][e], ref_v[nt][e] - lv[i][1]);
+      for (int nt = 0; nt < NT; ++nt) {
+        const float2 r = make_float2(ref_s[nt][0], ref_s[nt][1]);
+        const float2 top = ONE ? make_float2(fmaxf(s[i][nt][0], s[i][nt][2]), fmaxf(s[i][nt][1], s[i][nt][3]))
+                               : make_float2(s[i][nt][0], s[i][nt][1]);
+        const float2 p = sub2(top, r);
+        rise |= p.x > 8.f + fminf(0.f, gap[nt][0] - lv[i][0]);
+        rise |= p.y > 8.f + fminf(0.f, gap[nt][1] - lv[i][0]);
+        if (!ONE) {
+          const float2 q = sub2(make_float2(s[i][nt][2], s[i][nt][3]), r);
+          rise |= q.x > 8.f + fminf(0.f, gap[nt][0] - lv[i][1]);
+          rise |= q.y > 8.f + fminf(0.f, gap[nt][1] - lv[i][1]);
         }
+      }
     if (!__any_sync(kFull, rise)) return;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float f[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float ms = -INFINITY, mv = -INFINITY;
+        float ms = ref_s[nt][e], mv = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          ms = fmaxf(ms, fmaxf(s[i][nt][e], s[i][nt][e + 2]));
-          mv = fmaxf(mv, fmaxf(s[i][nt][e] + lv[i][0], s[i][nt][e + 2] + lv[i][1]));
-        }
+        for (int i = 0; i < N; ++i) ms = fmaxf(ms, fmaxf(s[i][nt][e], s[i][nt][e + 2]));
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) {
-          ms = fmaxf(ms, __shfl_xor_sync(kFull, ms, x));
-          mv = fmaxf(mv, __shfl_xor_sync(kFull, mv, x));
-        }
-        ms = fmaxf(ms, ref_s[nt][e]);
-        mv = fmaxf(mv, ref_v[nt][e]);
-        sum[nt][e] *= ex2(ref_s[nt][e] - ms);
-        f[e] = ex2(ref_v[nt][e] - mv);
+        for (int x = 4; x < 32; x <<= 1) ms = fmaxf(ms, __shfl_xor_sync(kFull, ms, x));
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          mv = fmaxf(mv, fmaxf(s[i][nt][e] - ms + lv[i][0], s[i][nt][e + 2] - ms + lv[i][1]));
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) mv = fmaxf(mv, __shfl_xor_sync(kFull, mv, x));
+        const float down = ref_s[nt][e] - ms, old = gap[nt][e] + down;
+        mv = fmaxf(mv, old);
+        sum[nt][e] *= ex2(down);
+        f[e] = ex2(old - mv);
         ref_s[nt][e] = ms;
-        ref_v[nt][e] = mv;
+        gap[nt][e] = mv;
       }
 #pragma unroll
       for (int n = 0; n < KS; ++n)
@@ -269,7 +278,7 @@ struct Rows {
         const float2 p = add2(y, make_float2(-ref_s[nt][0], -ref_s[nt][1]));
         l = add2(l, make_float2(ex2(p.x), ex2(p.y)));
         const float up = lv[x] + kLift;
-        const float2 q = add2(y, make_float2(up - ref_v[nt][0], up - ref_v[nt][1]));
+        const float2 q = add2(p, make_float2(up - gap[nt][0], up - gap[nt][1]));
         const float2 z = mul2(make_float2(ex2(q.x), ex2(q.y)), make_float2(vm[x], vm[x]));
         b[x][nt] = turn(pack_f16(z.x, z.y));  // the weights' one rounding: float16 feeds the product
       }
@@ -317,8 +326,9 @@ struct Rows {
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        sum[nt][e & 1] += ex2(s[0][nt][e] - ref_s[nt][e & 1]);
-        p[nt][e] = ex2(s[0][nt][e] - ref_v[nt][e & 1] + kLift);
+        const float x = s[0][nt][e] - ref_s[nt][e & 1];
+        sum[nt][e & 1] += ex2(x);
+        p[nt][e] = ex2(x + (kLift - gap[nt][e & 1]));
       }
       b0[nt] = turn(pack_bf16(p[nt][0], p[nt][1]));  // bf16, as the Values they meet
       b1[nt] = turn(pack_bf16(p[nt][2], p[nt][3]));
@@ -404,7 +414,7 @@ struct Rows {
         }
         // In two factors, of which the second is 1 but for Values below 2^-94: their scales and the lift may together be
         // below what one power of two holds.
-        const float x = ref_v[nt][e] - kLift - ref_s[nt][e];
+        const float x = gap[nt][e] - kLift;
         const float f = ex2(fmaxf(x, -100.f)), f2 = ex2(fminf(x + 100.f, 0.f));
 #pragma unroll
         for (int n = 0; n < KS; ++n)
