@@ -699,8 +699,9 @@ kk_status kk_qk_norm_rope(int32_t dtype, int32_t num_nodes, int32_t num_q_heads,
  * results below 2^-6 as long as the scales are this call's (a power of two
  * changes no mantissa); a caller's own may be 0, below 0 or no powers of two:
  * older tokens keep what they stood for. What is not finite becomes NaN. Nothing
- * behind a request's last token is written. No page may be in two requests'
- * tables. k or v may be NULL with its cache NULL (Keys or Values alone).
+ * behind a request's last token is written. Every page that receives tokens
+ * belongs to one request alone (full pages may be in several tables, as
+ * kk_pages_fork leaves them). k or v may be NULL with its cache NULL (Keys or Values alone).
  */
 kk_status kk_kv8_write(const kk_kcache_desc* kc, float* k_scale, const kk_kcache_desc* vc, float* v_scale,
                        const kk_block_table* bt, int32_t layer, int32_t num_layers, int32_t dtype, const kk_rows* k,
