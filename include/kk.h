@@ -663,10 +663,11 @@ typedef struct kk_rope {
  * alone. q (nullable with num_q_heads 0), k (nullable with num_kv_heads 0) and v
  * are read; q_out may be q and k_out k (the same address and strides), other
  * outputs overlap no input. dtype: KK_BF16 or KK_F32, the caches' too. D is 32,
- * 64, 128 or 256. A request whose table disagrees with seq_lens or holds a bad
- * page, or with more nodes than tokens, is reported through the device error
- * word, and its nodes are not written to the cache; without positions their
- * position is 0.
+ * 64, 128 or 256. A request whose table disagrees with seq_lens, or with more
+ * nodes than tokens, is reported through the device error word, and its nodes are
+ * not written to the cache; without positions their position is 0. A page out of
+ * range is reported too: the nodes that it would receive are not written, the
+ * others are, and all have their position.
  */
 kk_status kk_qk_norm_rope(int32_t dtype, int32_t num_nodes, int32_t num_q_heads, int32_t num_kv_heads, int32_t D,
                           const kk_rows* q, const kk_rows* k, const kk_rows* v, const void* q_weight,
