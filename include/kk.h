@@ -637,8 +637,9 @@ typedef struct kk_rows {
  * head_dim; 0: none) in pairs (i, i + rotary_dim/2), or (2i, 2i + 1) when
  * interleaved: pair (a, b) at position p becomes (a c - b s, b c + a s) with c =
  * scale * cos(p * inv_freq[i]), s = scale * sin(p * inv_freq[i]) (inv_freq:
- * device float [rotary_dim/2], finite). The angle is exact in inv_freq's float32
- * values however far the position is, up to the rounding of its sine and cosine.
+ * device float [rotary_dim/2], at most 2^32 in magnitude). The angle is exact in
+ * inv_freq's float32 values however far the position is, up to the rounding of
+ * its sine and cosine.
  */
 typedef struct kk_rope {
   const float* inv_freq;
