@@ -316,14 +316,14 @@ constexpr long long kTcWork = 72 << 10;
 // The same over an 8-bit cache, where the loaders' conversions, which are the same
 // for 1 row as for 256, bound the tensor-memory kernel: from 80 rows on (8 requests
 // of up to 32768 tokens, 4 KV heads, groups of 7, few rows / tensor memory, us: 9
-// nodes 145 / 163, 16 nodes 211 / 170, 36 nodes 434 / 177, 64 nodes 744 / 447; up to
-// 8192 tokens 50 / 55, 67 / 64, 127 / 68, 211 / 132; up to 1024 tokens 25 / 27,
-// 29 / 28, 47 / 37, 77 / 43; 64 dims and up to 32768 93 / 111, 133 / 113 at 9 and 16
-// nodes), and where tokens x tiles, counted as above, pass 48 K, since it takes longer
-// to start (D = 128, tokens x tiles: 2 K x 15 22.6 / 23.1, 2 K x 27 28.8 / 24.6,
-// 4 K x 6 18.5 / 20.5, 4 K x 15 29.4 / 24.6, 8 K x 5 18.9 / 20.5, 8 K x 6 24.6 / 22.6;
-// D = 64: 18.5 / 17.3, 22.6 / 18.5, 14.4 / 17.5, 22.6 / 18.5, 16.4 / 18.5,
-// 18.5 / 18.5).
+// nodes 141 / 155, 16 nodes 205 / 163, 36 nodes 419 / 173, 64 nodes 717 / 418; up to
+// 8192 tokens 49 / 51, 66 / 59, 124 / 65, 207 / 123; up to 1024 tokens 25 / 25,
+// 29 / 27, 47 / 37, 77 / 41; 64 dims and up to 32768 94 / 113, 137 / 113, 277 / 121,
+// 473 / 297), and where tokens x tiles, counted as above, pass 48 K, since it takes longer
+// to start (D = 128, tokens x tiles: 2 K x 15 22.6 / 22.6, 2 K x 27 30.4 / 24.6,
+// 4 K x 6 18.5 / 21.6, 4 K x 15 30.0 / 24.6, 8 K x 5 19.5 / 22.6, 8 K x 6 24.6 / 22.6;
+// D = 64: 18.5 / 16.6, 22.6 / 18.5, 14.4 / 18.5, 22.6 / 18.5, 16.4 / 18.5,
+// 19.5 / 18.5).
 constexpr int kTcRows8 = 80;
 constexpr long long kTcWork8 = 48 << 10;
 // From where the mma kernel's tiles have 32 rows (layouts that do not suit the

@@ -36,10 +36,12 @@
 // L2), 77 % of a copy's time for them. A call costs about 20 us before its first
 // and after its last step (places, queries, the join).
 //
-// Over an 8-bit cache (K8) four loader warps read the codes, 32 tokens of a tile
-// each and a tile ahead in registers, and lay them out as bf16 values times their
+// Over an 8-bit cache (K8) four loader warps copy the codes, 32 tokens of a tile
+// each, into shared memory a tile ahead, and lay them out as bf16 values times their
 // scale where the copies of a bf16 cache would have put them (exact while scales
-// are powers of two); everything else is the same.
+// are powers of two); everything else is the same. 8 requests of up to 32768
+// tokens and 16, 36, 64 nodes: 163, 173, 418 us (448 rows are a pair of row tiles
+// and another, and every pair widens the codes again).
 #pragma once
 #include <cuda.h>
 
@@ -731,8 +733,9 @@ __global__ void __launch_bounds__(tc_threads<K8>(), 1)
       };
       // The codes of the warp's tokens go through shared memory a tile ahead, a row's pieces by neighbouring lanes (a
       // lane reads what it copied itself); the scale of each lane's own token waits in a register. 8 requests of up
-      // to 32768 tokens, 9 nodes: 160 us; 220 with one register buffer for K and V, 335 with one for each (128
-      // registers a thread: the conversions ran one after the other), 245 with a bulk copy for every row.
+      // to 32768 tokens and 9 nodes, brought here for comparison (the few-rows kernel has them): 155 us; when this was
+      // chosen 160, with one register buffer for K and V 220, with one for each 335 (128 registers a thread: the
+      // conversions ran one after the other), with a bulk copy for every row 245.
       unsigned char* raw = s_v + VS * C::kTile + lw * (C::kRaw / 4) + lane * 16;
       struct Ahead {
         float scale;

@@ -8,16 +8,17 @@
 // their codes move with it. A scale of the caller's own that is no power of two
 // costs its item a second round of stores, with exact divisions. One warp takes
 // an item of few tokens (a decode step: the item is one row), a block of eight
-// warps one of many. The new tokens stay in registers between the two passes, up to 8 vectors of 16 bytes
-// a thread (a page of 128 tokens of 128 bf16 dims in a block); larger items
-// read them again, from L2.
+// warps one of many. The new tokens stay in registers between the two passes, up
+// to 8 vectors of 16 bytes a thread (a page of 128 tokens of 128 bf16 dims in a
+// block); larger items read them again, from L2.
 //
 // Measured: one token of 8 requests in 28 layers of 4 heads of 128 dims 6.2 us
-// (a launch and a chain of four loads); prompts of 22.5 K tokens, one layer (69 MB read
-// and written), 13.2 us, 5.2 TB/s, with the codes written to L2. Two and a half
-// rounds of blocks, each a chain of look-ups, loads and a block-wide maximum,
-// are what is left; magnitudes as packed integers and 64 registers, four blocks
-// an SM instead of two, took it there from 22.5.
+// (a launch and a chain of four loads); prompts of 22.5 K tokens, one layer (69 MB
+// read and written), 16 us on new inputs each time, 4.3 TB/s (13.4 where a call
+// repeats on the same, its codes in L2). Two and a half rounds of blocks, each a
+// chain of look-ups, loads and a block-wide maximum, are what is left; magnitudes
+// as packed integers and 64 registers, four blocks an SM instead of two, took the
+// repeated call there from 22.5.
 #include "kk_device.cuh"
 #include "kk_pdl.cuh"
 #include "kk_write8.cuh"
@@ -196,7 +197,10 @@ __global__ void __launch_bounds__(kThreads, 4) write8_kernel(const Write8Args a)
         return keep_side(y, fmaf(-y, by, x * up));
       });
   }
-  if (had && old != now) {  // the page's older codes, in terms of the new scale
+  // The page's older codes, in terms of the new scale. In a decode step a warp does this by itself, a word a lane at a
+  // time: pages of 128 tokens, half full, 8.9 us a call where no scale grows, 21 where one does, 36 where all do (pages
+  // of 16: 8.9, 9.0, 11.4).
+  if (had && old != now) {
     const float f = old == -now ? -1.f : old * inv;  // else `now` is the new tokens' power of two
     for (int i = tid; i < had * (D / 4); i += NTH) {
       uint32_t* p = reinterpret_cast<uint32_t*>(codes + (i / (D / 4)) * x.dT + (i % (D / 4)) * 4);
